@@ -73,6 +73,7 @@ enum {
     MOE_ERR_CUDA = -6,          /* a CUDA runtime call or launch failed */
     MOE_ERR_TENSOR_MAP = -7,    /* TMA descriptor could not be encoded */
     MOE_ERR_DEVICE = -8,        /* current device is not an sm_103 GPU */
+    MOE_ERR_PAGE = -9,          /* device: a page, sequence or position outside the paged cache */
     MOE_ERR_TIMEOUT = -100      /* device: a bounded wait ran out (-100 - site) */
 };
 
@@ -460,6 +461,108 @@ int gqa_decode_attention(const void *q, const void *k_cache, const void *v_cache
 int gqa_decode_attention_per_head(const void *q, const void *k_cache, const void *v_cache, int32_t Hq,
                                   int32_t Hkv, int32_t D, int32_t L, int32_t L_cap, float scale, void *out,
                                   void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------ attention sub-layer
+ * The operators either side of and inside the attention of a decoding step
+ * for a batch, whose result is the `attn` that the decoder-block calls take:
+ * projections on int4 weights, a paged key-value cache, and attention over it.
+ * bf16 tensors throughout, like the layer calls; sums, softmax statistics and
+ * merges in fp32.  Strides count elements and are multiples of 8; pointers are
+ * device memory of the current device owned by the caller, 16-byte aligned
+ * (int32 arrays and inv_freq: 4-byte aligned).  No synchronisation; work enqueued on `stream`.
+ */
+
+/*
+ * y[b][n] = sum_k x[b][k] (scale[n][k / group] q[n][k] + bias[n][k / group])
+ * for 1 <= B <= 64 tokens and one int4 matrix [N][K] in the format of
+ * pack_int4 (scale and bias rows at the padded pitch).  The weights are not
+ * rounded to bf16; sums in fp32, y rounded once to bf16 (y_fp32 = 0) or
+ * written as fp32 (y_fp32 = 1).  x: [B] rows of K bf16, row stride x_stride
+ * (>= K); y: [B] rows of N, row stride y_stride (>= N, any).  y must not
+ * overlap x.  N >= 1, group in {32, 64, 128}, K % group == 0, K <= 32768 (else
+ * MOE_ERR_SHAPE); B outside 1..64 is MOE_ERR_TOKENS.  No workspace: calls on
+ * several streams do not meet.
+ */
+int int4_linear(const moe_qweight *w, int32_t N, int32_t K, int32_t group, const void *x, int64_t x_stride, int32_t B,
+                void *y, int64_t y_stride, int32_t y_fp32, cudaStream_t stream);
+
+/*
+ * A paged key-value cache: two pools of n_pages pages, element (page, head,
+ * position in the page, dimension) at page * page_stride + head * head_stride
+ * + position * pos_stride + dimension of k and of v.  Both orders of heads and
+ * positions inside a page, and pools that share one buffer, are strides.
+ * D in {64, 128}, page_size a power of two in 16 .. 65536, n_pages >= 1,
+ * 1 <= Hkv <= 256; strides positive multiples of 8 below 2^39, pos_stride and
+ * head_stride >= D (else MOE_ERR_SHAPE).  A page table row lists the pages of
+ * a sequence in order of position.
+ *
+ * Page tables, lengths and positions live on the device and may change
+ * between replays of a captured graph.  The kernels check them: a page number
+ * outside [0, n_pages) or a position past the table is never followed, and
+ * MOE_ERR_PAGE is recorded in the status word (moe_read_device_status); the
+ * results of the rows concerned are then undefined.
+ */
+typedef struct {
+    void *k, *v;
+    int32_t n_pages, page_size, Hkv, D;
+    int64_t page_stride, head_stride, pos_stride;
+} gqa_pages;
+
+/*
+ * Append T tokens to the cache and rotate them by their positions.  Token t
+ * goes to position index[t] of sequence seq[t] (both int32, device): page
+ * page_table[seq][index / page_size] (int32 [n_seq][table_ld], device), row
+ * index % page_size.  Its rotary position is p = index[t] + pos_offset (the
+ * length of a shared prefix, or 0), and with angles a_i = p * inv_freq[i]
+ * (inv_freq fp32 [rot / 2], device; the product taken exactly, far positions
+ * included) the pairs (x_i, x_{i + rot/2}) of each head, or with
+ * interleaved = 1 (x_{2i}, x_{2i+1}), become
+ *   (x cos a - y sin a, y cos a + x sin a)    fp32, rounded once to bf16;
+ * dimensions rot .. D-1 stay.  Keys go to the cache rotated, values as they
+ * are, and queries rotated to q_out (q and q_out may be NULL together, then
+ * Hq is ignored; q_out may be q itself).  rot is 0 (no rotation, inv_freq
+ * NULL) or a multiple of 16 up to D.  q, k, v, q_out: rows of Hq or Hkv heads
+ * of D, row strides given.  A token with seq[t] < 0 or index[t] < 0 is
+ * padding: nothing of it is written.  The tokens of one call go to different
+ * places; if two share one, the cache holds a mix of both.  status: the first
+ * word of a workspace or any zeroed int32, or NULL (errors then stay
+ * unrecorded).  1 <= T <= 2^24 (else MOE_ERR_TOKENS), 1 <= Hq <= 256,
+ * 0 <= pos_offset <= 2^30.
+ */
+int gqa_append(const gqa_pages *cache, const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+               int64_t v_stride, int32_t T, int32_t Hq, const int32_t *seq, const int32_t *index,
+               const int32_t *page_table, int32_t n_seq, int32_t table_ld, int32_t pos_offset, const float *inv_freq,
+               int32_t rot, int32_t interleaved, void *q_out, int64_t q_out_stride, int32_t *status,
+               cudaStream_t stream);
+
+/* Workspace bytes of gqa_paged_attention for up to B rows, Hq query heads and
+ * up to prefix_len shared positions; 0 if unsupported.  To be zero-filled
+ * once before first use (moe_workspace_init clears what has to be). */
+size_t gqa_paged_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t prefix_len);
+
+/*
+ * Attention of B rows (one query token each) over a prefix that all rows
+ * share and each row's own positions: with the keys of positions
+ * 0 .. prefix_len - 1 of prefix_pages (int32, device, NULL if prefix_len is 0)
+ * followed by those of positions 0 .. seq_len[b] - 1 of page_table[b]
+ * (int32 [B][table_ld]; seq_len int32 [B]; the row's own new key among them),
+ * and key-value head h / (Hq / Hkv) for query head h,
+ *   out[b][h] = softmax(scale * q[b][h] . keys) values     fp32, bf16 out.
+ * The prefix is read once for the whole batch.  A row without any position
+ * (seq_len 0, no prefix) gives zeros; a row with seq_len < 0 is padding, its
+ * out is left as it was.  What the pages hold behind a sequence's last
+ * position has no influence, NaN included.  Several rows may name the same
+ * pages (draft tokens of one sequence: the same table row, growing lengths).
+ * q, out: rows of Hq heads of D at the given row strides; out may be q.
+ * Supported: Hq % Hkv == 0, Hq / Hkv <= 8, Hq <= 256 (MOE_ERR_SHAPE),
+ * 1 <= B <= 1024, prefix_len 0 .. 2^26, table_ld >= 1 with table_ld *
+ * page_size <= 2^26 (MOE_ERR_TOKENS).  The workspace is this call's alone
+ * while it runs: calls that may overlap take one each.
+ */
+int gqa_paged_attention(const gqa_pages *cache, const void *q, int64_t q_stride, int32_t B, int32_t Hq,
+                        const int32_t *prefix_pages, int32_t prefix_len, const int32_t *page_table, int32_t table_ld,
+                        const int32_t *seq_len, float scale, void *out, int64_t out_stride, void *ws, size_t ws_bytes,
+                        cudaStream_t stream);
 
 /* Human-readable text for a status code. */
 const char *moe_status_string(int code);

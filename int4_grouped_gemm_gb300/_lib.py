@@ -23,6 +23,7 @@ MOE_ERR_WORKSPACE = -5
 MOE_ERR_CUDA = -6
 MOE_ERR_TENSOR_MAP = -7
 MOE_ERR_DEVICE = -8
+MOE_ERR_PAGE = -9
 MOE_ERR_TIMEOUT = -100
 
 
@@ -47,6 +48,11 @@ class moe_routing_views(ctypes.Structure):
 class moe_batch_views(ctypes.Structure):
     _fields_ = [(n, c_i64) for n in ("logits", "slots", "slot_w", "h")] + \
         [("S_max", c_i32), ("logit_ld", c_i32), ("max_tokens", c_i32)]
+
+
+class gqa_pages(ctypes.Structure):
+    _fields_ = [("k", c_p), ("v", c_p), ("n_pages", c_i32), ("page_size", c_i32), ("Hkv", c_i32), ("D", c_i32),
+                ("page_stride", c_i64), ("head_stride", c_i64), ("pos_stride", c_i64)]
 
 
 MOE_DECODE_PHASES = 8
@@ -95,6 +101,12 @@ SIGNATURES = {
                                             c_p, c_sz, c_p]),
     "gqa_decode_attention_per_head": (ctypes.c_int, [c_p, c_p, c_p, c_i32, c_i32, c_i32, c_i32, c_i32,
                                                      ctypes.c_float, c_p, c_p, c_sz, c_p]),
+    "int4_linear": (ctypes.c_int, [c_p, c_i32, c_i32, c_i32, c_p, c_i64, c_i32, c_p, c_i64, c_i32, c_p]),
+    "gqa_append": (ctypes.c_int, [c_p, c_p, c_i64, c_p, c_i64, c_p, c_i64, c_i32, c_i32, c_p, c_p, c_p, c_i32, c_i32,
+                                  c_i32, c_p, c_i32, c_i32, c_p, c_i64, c_p, c_p]),
+    "gqa_paged_workspace_bytes": (c_sz, [c_i32, c_i32, c_i32, c_i32, c_i32]),
+    "gqa_paged_attention": (ctypes.c_int, [c_p, c_p, c_i64, c_i32, c_i32, c_p, c_i32, c_p, c_i32, c_p, ctypes.c_float,
+                                           c_p, c_i64, c_p, c_sz, c_p]),
 }
 
 
@@ -327,3 +339,53 @@ def gqa_decode_attention(q, k_cache, v_cache, L: int, scale: float, out, ws, per
     fn = load().gqa_decode_attention_per_head if per_head else load().gqa_decode_attention
     _check(fn(_ptr(q), _ptr(k_cache), _ptr(v_cache), Hq, Hkv, D, L, L_cap, float(scale), _ptr(out), _ptr(ws),
               ws.numel() * ws.element_size(), _stream(stream)), "gqa_decode_attention")
+
+
+# ---------------------------------------------------- attention sub-layer
+
+
+def check_device(what: str, *tensors):
+    """Every tensor on the current device (the library launches there)."""
+    import torch
+    cur = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != cur):
+            raise ValueError(f"{what}: a tensor on {t.device}, the current device is cuda:{cur}")
+
+
+def _row(t) -> int:
+    """Elements from one row of t to the next (a single row has no next: its own length)."""
+    return t.stride(0) if t.shape[0] > 1 else t[0].numel()
+
+
+def int4_linear(w: moe_qweight, N: int, K: int, group: int, x, y, stream=None):
+    """y [B, N] (bf16 or fp32) = x [B, K] (bf16) times the int4 matrix w [N, K] transposed, 1 <= B <= 64."""
+    import torch
+    _check(load().int4_linear(ctypes.byref(w), N, K, group, _ptr(x), _row(x), x.shape[0], _ptr(y), _row(y),
+                              int(y.dtype == torch.float32), _stream(stream)), "int4_linear")
+
+
+def gqa_append(cache: gqa_pages, q, k, v, seq, index, page_table, pos_offset: int, inv_freq, interleaved: bool, q_out,
+               status=None, stream=None):
+    """q [T, Hq, D] or None, k, v [T, Hkv, D] bf16; seq, index [T], page_table [n_seq, ld] int32; inv_freq fp32
+    [rot / 2] or None; q_out [T, Hq, D] or None; status: an int32-aligned device tensor or None."""
+    n_seq, ld = page_table.shape
+    _check(load().gqa_append(ctypes.byref(cache), _ptr(q), 0 if q is None else _row(q), _ptr(k), _row(k),
+                             _ptr(v), _row(v), k.shape[0], 0 if q is None else q.shape[1], _ptr(seq), _ptr(index),
+                             _ptr(page_table), n_seq, ld, pos_offset, _ptr(inv_freq),
+                             0 if inv_freq is None else 2 * inv_freq.numel(), int(interleaved), _ptr(q_out),
+                             0 if q_out is None else _row(q_out), _ptr(status), _stream(stream)), "gqa_append")
+
+
+def gqa_paged_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, prefix_len: int) -> int:
+    return int(load().gqa_paged_workspace_bytes(B, Hq, Hkv, D, prefix_len))
+
+
+def gqa_paged_attention(cache: gqa_pages, q, prefix_pages, prefix_len: int, page_table, seq_len, scale: float, out,
+                        ws, stream=None):
+    """q, out [B, Hq, D] bf16; prefix_pages int32 or None; page_table [B, ld], seq_len [B] int32."""
+    B, Hq, _ = q.shape
+    _check(load().gqa_paged_attention(ctypes.byref(cache), _ptr(q), _row(q), B, Hq, _ptr(prefix_pages),
+                                      prefix_len, _ptr(page_table), page_table.shape[1], _ptr(seq_len), float(scale),
+                                      _ptr(out), _row(out), _ptr(ws), ws.numel() * ws.element_size(),
+                                      _stream(stream)), "gqa_paged_attention")

@@ -1,0 +1,157 @@
+"""The attention sub-layer of a decoding step, on top of the C ABI.
+
+``PagedCache`` wraps two page pools (``gqa_append``, ``gqa_paged_attention``);
+``AttentionLayer`` puts int4 projections (``moe.linear``) around it, and its
+result is the ``attn`` of ``PackedLayer.decode_batch_block``.
+"""
+from __future__ import annotations
+
+import math
+from typing import Optional
+
+import torch
+
+from . import _lib
+from .moe import QMatrix, linear
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _heads(t: torch.Tensor, name: str, T: Optional[int], D: int):
+    """[T, heads, D] bf16 whose rows are contiguous (rows themselves may be strided)."""
+    _need(t.dim() == 3 and t.dtype == torch.bfloat16 and t.shape[2] == D and (T is None or t.shape[0] == T),
+          f"{name}: [T, heads, {D}] in bf16")
+    _need(t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == D), f"{name}: the heads of a row must be contiguous")
+
+
+def _ints(t: torch.Tensor, name: str, *shape):
+    _need(t.dtype == torch.int32 and t.is_contiguous() and t.dim() == len(shape) and
+          all(n is None or n == m for n, m in zip(shape, t.shape)), f"{name}: int32 {list(shape)}, contiguous")
+
+
+class PagedCache:
+    """A paged key-value cache over two pools [n_pages, Hkv, page_size, D] in
+    bf16 (any order of heads and positions in memory: pass a transposed view;
+    both pools in the same layout).  The pools stay the caller's."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        _need(k.dim() == 4 and k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16 and k.shape == v.shape,
+              "PagedCache: two bf16 pools [n_pages, Hkv, page_size, D]")
+        _need(k.stride() == v.stride() and k.stride(3) == 1, "PagedCache: both pools in one layout, D innermost")
+        _need(k.device == v.device, "PagedCache: both pools on one device")
+        self.k, self.v = k, v
+        self.n_pages, self.Hkv, self.page_size, self.D = k.shape
+        # a dimension of size 1 has no stride of its own
+        page, head, pos = (s if n > 1 else self.D for s, n in zip(k.stride(), k.shape[:3]))
+        self.desc = _lib.gqa_pages(k.data_ptr(), v.data_ptr(), self.n_pages, self.page_size, self.Hkv, self.D, page,
+                                   head, pos)
+        # where append records errors found on the device
+        self.status = torch.zeros(4, dtype=torch.int32, device=k.device)
+
+    @classmethod
+    def empty(cls, n_pages: int, Hkv: int, page_size: int, D: int, device="cuda") -> "PagedCache":
+        pool = torch.empty(2, n_pages, Hkv, page_size, D, dtype=torch.bfloat16, device=device)
+        return cls(pool[0], pool[1])
+
+    def append(self, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, seq: torch.Tensor,
+               index: torch.Tensor, page_table: torch.Tensor, inv_freq: Optional[torch.Tensor], pos_offset: int = 0,
+               interleaved: bool = False, q_out: Optional[torch.Tensor] = None, stream=None):
+        """Rotate q and k by position index + pos_offset, write k and v to
+        position index[t] of sequence seq[t]; returns the rotated q."""
+        T = k.shape[0]
+        _heads(k, "k", T, self.D)
+        _heads(v, "v", T, self.D)
+        _need(k.shape[1] == self.Hkv and v.shape[1] == self.Hkv, f"k, v: {self.Hkv} heads")
+        _ints(seq, "seq", T)
+        _ints(index, "index", T)
+        _ints(page_table, "page_table", None, None)
+        if inv_freq is not None:
+            _need(inv_freq.dtype == torch.float32 and inv_freq.dim() == 1 and inv_freq.is_contiguous(),
+                  "inv_freq: fp32 [rot / 2]")
+        if q is None:
+            _need(q_out is None, "q_out without q")
+        else:
+            _heads(q, "q", T, self.D)
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            _heads(q_out, "q_out", T, self.D)
+            _need(q_out.shape == q.shape, "q_out: the shape of q")
+        _lib.check_device("append", self.k, q, k, v, seq, index, page_table, inv_freq, q_out)
+        _lib.gqa_append(self.desc, q, k, v, seq, index, page_table, pos_offset, inv_freq, interleaved, q_out,
+                        self.status, stream)
+        return q_out
+
+    def workspace(self, B: int, Hq: int, prefix_len: int = 0) -> torch.Tensor:
+        """Scratch of attend for up to B rows, Hq heads and prefix_len shared
+        positions; calls that may overlap take one each."""
+        n = _lib.gqa_paged_workspace_bytes(B, Hq, self.Hkv, self.D, prefix_len)
+        if n == 0:
+            raise _lib.MoEError(_lib.MOE_ERR_SHAPE, "gqa_paged_workspace_bytes")
+        return torch.zeros(n, dtype=torch.uint8, device=self.k.device)
+
+    def attend(self, q: torch.Tensor, page_table: torch.Tensor, seq_len: torch.Tensor,
+               prefix_pages: Optional[torch.Tensor] = None, prefix_len: int = 0, scale: Optional[float] = None,
+               out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """out [B, Hq, D]: row b's query attends to the shared prefix (read
+        once for all rows), then to the first seq_len[b] positions of
+        page_table[b].  scale: 1 / sqrt(D) unless given."""
+        B = q.shape[0]
+        _heads(q, "q", B, self.D)
+        _ints(page_table, "page_table", B, None)
+        _ints(seq_len, "seq_len", B)
+        if prefix_len:
+            _need(prefix_pages is not None, "prefix_len without prefix_pages")
+            _ints(prefix_pages, "prefix_pages", None)
+            _need(prefix_len <= prefix_pages.numel() * self.page_size, "prefix_pages: too few for prefix_len")
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        _heads(out, "out", B, self.D)
+        _need(out.shape == q.shape, "out: the shape of q")
+        if ws is None:
+            ws = self.workspace(B, q.shape[1], prefix_len)
+        _lib.check_device("attend", self.k, q, page_table, seq_len, prefix_pages, out, ws)
+        _lib.gqa_paged_attention(self.desc, q, prefix_pages if prefix_len else None, prefix_len, page_table, seq_len,
+                                 1.0 / math.sqrt(self.D) if scale is None else scale, out, ws, stream)
+        return out
+
+
+class AttentionLayer:
+    """int4 projections around a paged cache: qkv [(Hq + 2 Hkv) D, H] and
+    out [H, Hq D], both QMatrix (pack_matrix), and the rotation."""
+
+    def __init__(self, qkv: QMatrix, out: QMatrix, Hq: int, Hkv: int, D: int, inv_freq: Optional[torch.Tensor],
+                 interleaved: bool = False):
+        _need(qkv.rows == (Hq + 2 * Hkv) * D and out.K == Hq * D and out.rows == qkv.K, "AttentionLayer: shapes")
+        self.qkv, self.out, self.Hq, self.Hkv, self.D = qkv, out, Hq, Hkv, D
+        self.inv_freq, self.interleaved = inv_freq, interleaved
+
+    def project(self, x: torch.Tensor, stream=None):
+        """Queries, keys and values [T, heads, D] of 1 to 64 tokens (views of one buffer)."""
+        y = linear(self.qkv, x, stream=stream).view(x.shape[0], self.Hq + 2 * self.Hkv, self.D)
+        return y[:, :self.Hq], y[:, self.Hq:self.Hq + self.Hkv], y[:, self.Hq + self.Hkv:]
+
+    def decode(self, x: torch.Tensor, cache: PagedCache, seq: torch.Tensor, index: torch.Tensor,
+               page_table: torch.Tensor, seq_len: torch.Tensor, ws: torch.Tensor,
+               prefix_pages: Optional[torch.Tensor] = None, prefix_len: int = 0, stream=None) -> torch.Tensor:
+        """One step of B rows: x [B, H] (normalised) -> attn [B, H].  Row b's
+        new token goes to position index[b] of page table row seq[b]; it
+        attends to the prefix and the first seq_len[b] positions of row b
+        (seq_len = index + 1 for a plain step)."""
+        q, k, v = self.project(x, stream)
+        # every launch goes to `stream`: q_out, o and attn are made while it is current
+        with torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else _nothing():
+            q = cache.append(q, k, v, seq, index, page_table, self.inv_freq, prefix_len, self.interleaved,
+                             stream=stream)
+            o = cache.attend(q, page_table, seq_len, prefix_pages, prefix_len, ws=ws, stream=stream)
+            return linear(self.out, o.view(x.shape[0], self.Hq * self.D), stream=stream)
+
+
+class _nothing:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *a):
+        return False

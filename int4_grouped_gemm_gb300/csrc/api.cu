@@ -8,6 +8,8 @@
 #include "attention.cuh"
 #include "block.cuh"
 #include "kernels.cuh"
+#include "linear.cuh"
+#include "paged.cuh"
 #include "small_batch.cuh"
 
 
@@ -755,6 +757,174 @@ int gqa_decode_attention_per_head(const void *q, const void *k_cache, const void
     return gqa_run(q, k_cache, v_cache, Hq, Hkv, D, L, L_cap, scale, out, ws, ws_bytes, false, stream);
 }
 
+// ------------------------------------------------ attention sub-layer
+
+int int4_linear(const moe_qweight *w, int32_t N, int32_t K, int32_t group, const void *x, int64_t x_stride, int32_t B,
+                void *y, int64_t y_stride, int32_t y_fp32, cudaStream_t stream) {
+    if (!w) return MOE_ERR_NULL;
+    int rc;
+    if ((rc = check_ptr(w->q)) || (rc = check_ptr(w->scale)) || (rc = check_ptr(w->bias)) || (rc = check_ptr(x)) ||
+        (rc = check_ptr(y)))
+        return rc;
+    if (group != 32 && group != 64 && group != 128) return MOE_ERR_SHAPE;
+    if (N < 1 || K < group || K > kLinearMaxK || K % group != 0) return MOE_ERR_SHAPE;
+    if (x_stride < K || x_stride % 8 != 0 || y_stride < N || (y_fp32 != 0 && y_fp32 != 1)) return MOE_ERR_SHAPE;
+    if (B < 1 || B > kLinearMaxB) return MOE_ERR_TOKENS;
+    DeviceInfo *dev = nullptr;
+    if ((rc = current_device(dev))) return rc;
+    LinearArgs a{};
+    a.q = w->q;
+    a.s = w->scale;
+    a.b = w->bias;
+    a.x = static_cast<const __nv_bfloat16 *>(x);
+    a.y = y;
+    a.x_stride = x_stride;
+    a.y_stride = y_stride;
+    a.N = N;
+    a.K = K;
+    a.G = group;
+    a.ldg = ld_groups(K, group);
+    a.B = B;
+    a.y_fp32 = y_fp32;
+    return cuda_rc(launch_linear(a, dev->num_sms, stream));
+}
+
+// int32 and fp32 arrays of the paged calls: element-aligned, so that slices of
+// tables and lengths serve as they are
+static int check_ptr4(const void *p) {
+    if (!p) return MOE_ERR_NULL;
+    return (reinterpret_cast<uintptr_t>(p) & 3u) == 0 ? MOE_OK : MOE_ERR_ALIGN;
+}
+
+static bool good_stride(int64_t s, int64_t least) { return s >= least && s % 8 == 0 && s < (int64_t(1) << 39); }
+
+static int check_pages(const gqa_pages *c, Pages &p) {
+    if (!c) return MOE_ERR_NULL;
+    int rc;
+    if ((rc = check_ptr(c->k)) || (rc = check_ptr(c->v))) return rc;
+    if (c->D != 64 && c->D != 128) return MOE_ERR_SHAPE;
+    if (c->page_size < 16 || c->page_size > 65536 || (c->page_size & (c->page_size - 1)) != 0) return MOE_ERR_SHAPE;
+    if (c->n_pages < 1 || c->Hkv < 1 || c->Hkv > 256) return MOE_ERR_SHAPE;
+    if (!good_stride(c->page_stride, 8) || !good_stride(c->head_stride, c->D) || !good_stride(c->pos_stride, c->D))
+        return MOE_ERR_SHAPE;
+    p.k = static_cast<__nv_bfloat16 *>(c->k);
+    p.v = static_cast<__nv_bfloat16 *>(c->v);
+    p.page_stride = c->page_stride;
+    p.head_stride = c->head_stride;
+    p.pos_stride = c->pos_stride;
+    p.n_pages = c->n_pages;
+    p.page_shift = 0;
+    while ((1 << p.page_shift) < c->page_size) ++p.page_shift;
+    p.Hkv = c->Hkv;
+    p.D = c->D;
+    return MOE_OK;
+}
+
+int gqa_append(const gqa_pages *cache, const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+               int64_t v_stride, int32_t T, int32_t Hq, const int32_t *seq, const int32_t *index,
+               const int32_t *page_table, int32_t n_seq, int32_t table_ld, int32_t pos_offset, const float *inv_freq,
+               int32_t rot, int32_t interleaved, void *q_out, int64_t q_out_stride, int32_t *status,
+               cudaStream_t stream) {
+    AppendArgs a{};
+    int rc = check_pages(cache, a.c);
+    if (rc) return rc;
+    if ((rc = check_ptr(k)) || (rc = check_ptr(v)) || (rc = check_ptr4(seq)) || (rc = check_ptr4(index)) ||
+        (rc = check_ptr4(page_table)))
+        return rc;
+    const int D = a.c.D;
+    if (rot < 0 || rot > D || rot % 16 != 0 || (interleaved != 0 && interleaved != 1)) return MOE_ERR_SHAPE;
+    if (rot && (rc = check_ptr4(inv_freq))) return rc;
+    if ((q == nullptr) != (q_out == nullptr)) return MOE_ERR_NULL;
+    if (q) {
+        if ((rc = check_ptr(q)) || (rc = check_ptr(q_out))) return rc;
+        if (Hq < 1 || Hq > 256) return MOE_ERR_SHAPE;
+        if (!good_stride(q_stride, static_cast<int64_t>(Hq) * D) ||
+            !good_stride(q_out_stride, static_cast<int64_t>(Hq) * D))
+            return MOE_ERR_SHAPE;
+        if (q == q_out && q_stride != q_out_stride) return MOE_ERR_SHAPE;
+    }
+    if (!good_stride(k_stride, static_cast<int64_t>(a.c.Hkv) * D) ||
+        !good_stride(v_stride, static_cast<int64_t>(a.c.Hkv) * D))
+        return MOE_ERR_SHAPE;
+    if (status && (reinterpret_cast<uintptr_t>(status) & 3u)) return MOE_ERR_ALIGN;
+    if (T < 1 || T > (1 << 24) || n_seq < 1 || table_ld < 1 || pos_offset < 0 || pos_offset > (1 << 30))
+        return MOE_ERR_TOKENS;
+    DeviceInfo *dev = nullptr;
+    if ((rc = current_device(dev))) return rc;
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.k = static_cast<const __nv_bfloat16 *>(k);
+    a.v = static_cast<const __nv_bfloat16 *>(v);
+    a.q_out = static_cast<__nv_bfloat16 *>(q_out);
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.qo_stride = q_out_stride;
+    a.seq = seq;
+    a.index = index;
+    a.table = page_table;
+    a.inv_freq = inv_freq;
+    a.status = status;
+    a.T = T;
+    a.Hq = q ? Hq : 0;
+    a.n_seq = n_seq;
+    a.table_ld = table_ld;
+    a.pos_offset = pos_offset;
+    a.rot = rot;
+    a.interleaved = interleaved;
+    return cuda_rc(launch_append(a, dev->num_sms, stream));
+}
+
+static int check_paged_shape(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t prefix_len) {
+    if (D != 64 && D != 128) return MOE_ERR_SHAPE;
+    if (Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > 8 || Hq > 256) return MOE_ERR_SHAPE;
+    if (B < 1 || B > 1024 || prefix_len < 0 || prefix_len > (1 << 26)) return MOE_ERR_TOKENS;
+    return MOE_OK;
+}
+
+size_t gqa_paged_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t prefix_len) {
+    if (check_paged_shape(B, Hq, Hkv, D, prefix_len) != MOE_OK) return 0;
+    return paged_workspace_bytes(B, Hq, Hkv, D, prefix_len, kGqaMaxSms);
+}
+
+int gqa_paged_attention(const gqa_pages *cache, const void *q, int64_t q_stride, int32_t B, int32_t Hq,
+                        const int32_t *prefix_pages, int32_t prefix_len, const int32_t *page_table, int32_t table_ld,
+                        const int32_t *seq_len, float scale, void *out, int64_t out_stride, void *ws, size_t ws_bytes,
+                        cudaStream_t stream) {
+    PagedArgs a{};
+    int rc = check_pages(cache, a.c);
+    if (rc) return rc;
+    if ((rc = check_ptr(q)) || (rc = check_ptr4(page_table)) || (rc = check_ptr4(seq_len)) || (rc = check_ptr(out)) ||
+        (rc = check_ptr(ws)))
+        return rc;
+    if ((rc = check_paged_shape(B, Hq, a.c.Hkv, a.c.D, prefix_len))) return rc;
+    if (prefix_len > 0 && (rc = check_ptr4(prefix_pages))) return rc;
+    if (table_ld < 1 || static_cast<int64_t>(table_ld) * cache->page_size > (1 << 26)) return MOE_ERR_TOKENS;
+    if (!good_stride(q_stride, static_cast<int64_t>(Hq) * a.c.D) ||
+        !good_stride(out_stride, static_cast<int64_t>(Hq) * a.c.D))
+        return MOE_ERR_SHAPE;
+    if (q == out && q_stride != out_stride) return MOE_ERR_SHAPE;
+    if (!(scale == scale) || scale > 1e30f || scale < -1e30f) return MOE_ERR_SHAPE;
+    DeviceInfo *dev = nullptr;
+    if ((rc = current_device(dev))) return rc;
+    if (dev->num_sms > kGqaMaxSms) return MOE_ERR_DEVICE;
+    if (ws_bytes < paged_workspace_bytes(B, Hq, a.c.Hkv, a.c.D, prefix_len, dev->num_sms)) return MOE_ERR_WORKSPACE;
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.out = static_cast<__nv_bfloat16 *>(out);
+    a.q_stride = q_stride;
+    a.out_stride = out_stride;
+    a.prefix_pages = prefix_pages;
+    a.table = page_table;
+    a.seq_len = seq_len;
+    a.status = static_cast<int *>(ws);
+    a.B = B;
+    a.Hq = Hq;
+    a.group = Hq / a.c.Hkv;
+    a.prefix_len = prefix_len;
+    a.table_ld = table_ld;
+    a.scale = scale;
+    return cuda_rc(launch_paged(a, ws, dev->num_sms, stream));
+}
+
 const char *moe_status_string(int code) {
     switch (code) {
         case MOE_OK: return "ok";
@@ -766,6 +936,7 @@ const char *moe_status_string(int code) {
         case MOE_ERR_CUDA: return "CUDA runtime error or failed launch";
         case MOE_ERR_TENSOR_MAP: return "TMA descriptor could not be encoded";
         case MOE_ERR_DEVICE: return "current device is not an sm_103 GPU";
+        case MOE_ERR_PAGE: return "device: a page, sequence or position outside the paged cache";
         default: break;
     }
     if (code <= MOE_ERR_TIMEOUT && code > MOE_ERR_TIMEOUT - 100) return "device: a bounded wait ran out";
