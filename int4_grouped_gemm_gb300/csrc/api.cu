@@ -921,8 +921,7 @@ int gqa_paged_attention(const gqa_pages *cache, const void *q, int64_t q_stride,
     a.group = Hq / a.c.Hkv;
     a.prefix_len = prefix_len;
     a.table_ld = table_ld;
-    a.scale = scale;
-    return cuda_rc(launch_paged(a, ws, dev->num_sms, stream));
+    return cuda_rc(launch_paged(a, scale, ws, dev->num_sms, stream));
 }
 
 const char *moe_status_string(int code) {

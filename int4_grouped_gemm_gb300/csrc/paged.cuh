@@ -28,6 +28,10 @@ struct AppendArgs {
     int T, Hq, n_seq, table_ld, pos_offset, rot, interleaved;
 };
 
+// Partial results of the attention, merged by the combine kernel.  A flat list
+// of tiles is cut into ncta even pieces; piece c of the list and item i of it
+// (a row's key-value head, or a block of rows of the prefix) that meet have
+// partial slot c + i, which no other pair has (both only grow along the list).
 struct PagedArgs {
     Pages c;
     const __nv_bfloat16 *q;          // [B][Hq][D], row stride q_stride
@@ -35,12 +39,18 @@ struct PagedArgs {
     int64_t q_stride, out_stride;
     const int *prefix_pages, *table, *seq_len;
     int *status;
+    int64_t *starts;                 // [B + 1]: 16-position tiles of the rows before b
+    float2 *own_ml;                  // [slot][8 heads]: running maximum (log2) and sum
+    float *own_o;                    // [slot][D / 4][8 heads][4]: unnormalised output
     int B, Hq, group, prefix_len, table_ld;
-    float scale;
+    int join;                        // the prefix is read as the start of every row
+    int ncta;                        // blocks of the own-position kernel
+    int negate;                      // scale < 0: the queries' signs are flipped instead
+    float scale_log2;                // |scale| log2(e)
 };
 
 cudaError_t launch_append(const AppendArgs &a, int num_sms, cudaStream_t s);
 size_t paged_workspace_bytes(int B, int Hq, int Hkv, int D, int prefix_len, int num_sms);
-cudaError_t launch_paged(const PagedArgs &a, void *ws, int num_sms, cudaStream_t s);
+cudaError_t launch_paged(PagedArgs &a, float scale, void *ws, int num_sms, cudaStream_t s);
 
 }  // namespace moe
