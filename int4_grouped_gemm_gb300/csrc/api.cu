@@ -63,6 +63,21 @@ static int encode_2d(CUtensorMap *map, CUtensorMapDataType type, int elem_bytes,
     return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_TENSOR_MAP;
 }
 
+// One page pool as a tensor (dimension, position in the page, head, page), in
+// boxes of 64 dimensions and `rows` positions.
+static int encode_pages(CUtensorMap *map, const void *ptr, const Pages &c, uint32_t rows) {
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.D), cuuint64_t(1) << c.page_shift, static_cast<cuuint64_t>(c.Hkv),
+                          static_cast<cuuint64_t>(c.n_pages)};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.pos_stride) * 2, static_cast<cuuint64_t>(c.head_stride) * 2,
+                             static_cast<cuuint64_t>(c.page_stride) * 2};
+    cuuint32_t box[4] = {64, rows, 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_TENSOR_MAP;
+}
+
 static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 static int check_ptr(const void *p) {
@@ -921,7 +936,13 @@ int gqa_paged_attention(const gqa_pages *cache, const void *q, int64_t q_stride,
     a.group = Hq / a.c.Hkv;
     a.prefix_len = prefix_len;
     a.table_ld = table_ld;
-    return cuda_rc(launch_paged(a, scale, ws, dev->num_sms, stream));
+    a.wait_limit = g_wait_limit;
+    CUtensorMap maps[2];
+    if (!paged_joins(B, prefix_len)) {
+        const uint32_t rows = cache->page_size < 128 ? cache->page_size : 128;
+        if ((rc = encode_pages(&maps[0], a.c.k, a.c, rows)) || (rc = encode_pages(&maps[1], a.c.v, a.c, rows))) return rc;
+    }
+    return cuda_rc(launch_paged(a, maps, scale, ws, dev->num_sms, stream));
 }
 
 const char *moe_status_string(int code) {

@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
     const int mi = lane >> 3, rr = lane & 7;
     const int kpos = (mi >> 1) * 8 + rr, kch = mi & 1;
     const int vpos = (mi & 1) * 8 + rr, vch = mi >> 1;
-    const uint32_t flip = a.negate ? 0x80008000u : 0u;
+    const uint32_t flip = a.negate ? 0x80008000u : 0u, keep = a.zero_q ? 0u : 0xFFFFFFFFu;
 
     int i = 0;
     for (int64_t f = f0; f < f1;) {
@@ -302,8 +302,8 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
                 a.q + b * a.q_stride + static_cast<int64_t>(kv * a.group + (real ? g8 : 0)) * D);
 #pragma unroll
             for (int kd = 0; kd < KD; ++kd) {
-                qa[kd][0] = real ? __ldg(qrow + kd * 8 + c) ^ flip : 0u;
-                qa[kd][1] = real ? __ldg(qrow + kd * 8 + c + 4) ^ flip : 0u;
+                qa[kd][0] = real ? (__ldg(qrow + kd * 8 + c) & keep) ^ flip : 0u;
+                qa[kd][1] = real ? (__ldg(qrow + kd * 8 + c + 4) & keep) ^ flip : 0u;
             }
         }
         float o[NT][4];
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
 // Merge the partials of one (row, key-value head): grid (B Hkv, D / 32), thread
 // (part of the partials, 4 dimensions, head).  First the weights 2^(m_i - M) of
 // all partials per head, then the sums with every load independent.
-constexpr int kMergeMax = 512;  // partials of one row (two pieces lists of at most 256)
+constexpr int kMergeMax = 768;  // partials of one row: at most 256 of its own, 512 of the prefix
 
 __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ PagedArgs a) {
     __shared__ float s_w[8][kMergeMax + 1];
@@ -444,21 +444,37 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
         n_own = piece_of(W, np, s0 * Hkv + (kv + 1) * nt - 1) - c0 + 1;
     }
     const int64_t slot0 = static_cast<int64_t>(c0) + static_cast<int64_t>(b) * Hkv + kv;
+    // the prefix's partials of head h's row: first index, count, step
+    const int step = a.prefix_two ? 2 : 1;
+    auto prefix_parts = [&](int h, int64_t &first, int &row) {
+        if (a.prefix_ncta == 0 || h >= a.group) return 0;
+        const int g = b * a.group + h, blk = g / (step * 128);
+        const int64_t item = static_cast<int64_t>(kv) * a.prefix_blocks + blk;
+        const int64_t ntile = (a.prefix_len + 127) / 128, Wp = ntile * Hkv * a.prefix_blocks;
+        const int p0 = piece_of(Wp, a.prefix_ncta, item * ntile), p1 = piece_of(Wp, a.prefix_ncta, (item + 1) * ntile - 1);
+        row = g & 127;
+        first = (p0 + item) * 2 + (a.prefix_two ? (g >> 7) & 1 : 0);
+        return (p1 - p0 + 1) * (3 - step);
+    };
     {
         const int h = warp;  // warp h: head h's weights
+        int64_t first = 0;
+        int row = 0;
+        const int n_pre = prefix_parts(h, first, row);
+        const float2 *own = a.own_ml + slot0 * 8 + h, *pre = a.prefix_ml + first * 128 + row;
         float M = -INFINITY;
-        for (int i = lane; i < n_own; i += 32) {
-            const float2 v = __ldcg(a.own_ml + (slot0 + i) * 8 + h);
-            s_w[h][i] = v.x;
-            M = fmaxf(M, v.x);
+        for (int i = lane; i < n_own + n_pre; i += 32) {
+            const float v = i < n_own ? __ldcg(own + i * 8).x : __ldcg(pre + static_cast<int64_t>(i - n_own) * step * 128).x;
+            s_w[h][i] = v;
+            M = fmaxf(M, v);
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
         float den = 0.f;
-        for (int i = lane; i < n_own; i += 32) {
-            const float w = s_w[h][i] == -INFINITY ? 0.f : exp2f(s_w[h][i] - M);
+        for (int i = lane; i < n_own + n_pre; i += 32) {
+            const float v = s_w[h][i], w = v == -INFINITY ? 0.f : exp2f(v - M);
             s_w[h][i] = w;
-            den += w * __ldcg(a.own_ml + (slot0 + i) * 8 + h).y;
+            den += w * (i < n_own ? __ldcg(own + i * 8).y : __ldcg(pre + static_cast<int64_t>(i - n_own) * step * 128).y);
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
@@ -467,17 +483,25 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
     __syncthreads();
     const int h = tid & 7, dq = (tid >> 3) & 7, part = tid >> 6;
     const int d4 = blockIdx.y * 8 + dq;
+    int64_t first = 0;
+    int row = 0;
+    const int n_pre = prefix_parts(h, first, row);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    // a partial without weight may never have been written: it is not added
+    auto add = [&](float w, const float4 &v) {
+        acc.x = w > 0.f ? fmaf(w, v.x, acc.x) : acc.x;
+        acc.y = w > 0.f ? fmaf(w, v.y, acc.y) : acc.y;
+        acc.z = w > 0.f ? fmaf(w, v.z, acc.z) : acc.z;
+        acc.w = w > 0.f ? fmaf(w, v.w, acc.w) : acc.w;
+    };
     const float *src = a.own_o + (slot0 * (D / 4) + d4) * 32 + h * 4;
 #pragma unroll 8
-    for (int i = part; i < n_own; i += 4) {
-        const float w = s_w[h][i];
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + static_cast<int64_t>(i) * D * 8));
-        acc.x = fmaf(w, v.x, acc.x);
-        acc.y = fmaf(w, v.y, acc.y);
-        acc.z = fmaf(w, v.z, acc.z);
-        acc.w = fmaf(w, v.w, acc.w);
-    }
+    for (int i = part; i < n_own; i += 4)
+        add(s_w[h][i], __ldcg(reinterpret_cast<const float4 *>(src + static_cast<int64_t>(i) * D * 8)));
+    const float *psrc = a.prefix_o + (first * (D / 4) + d4) * 512 + row * 4;
+#pragma unroll 8
+    for (int i = part; i < n_pre; i += 4)
+        add(s_w[h][n_own + i], __ldcg(reinterpret_cast<const float4 *>(psrc + static_cast<int64_t>(i) * step * D * 128)));
     s_red[part][tid & 63] = acc;
     __syncthreads();
     if (part == 0 && h < a.group) {
@@ -499,23 +523,32 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
 
 // ------------------------------------------------------------------- host
 
+// One row's prefix is read once either way, and without the prefix kernel
+// there is a launch less.
+bool paged_joins(int B, int prefix_len) { return B == 1 || prefix_len == 0; }
+
+static int prefix_row_blocks(int rows) { return rows <= 128 ? 1 : (rows + 255) / 256; }
+
 struct PagedLayout {
-    size_t starts, own_ml, own_o, total;
+    size_t starts, own_ml, own_o, prefix_ml, prefix_o, total;
 };
 
-static PagedLayout paged_layout(int B, int Hkv, int D, int num_sms) {
+static PagedLayout paged_layout(int B, int Hq, int Hkv, int D, int prefix_len, int num_sms) {
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     PagedLayout L{};
     const size_t slots = static_cast<size_t>(num_sms) + static_cast<size_t>(B) * Hkv;
     L.starts = kCtrlBytes;
     L.own_ml = L.starts + up((B + 1) * sizeof(int64_t));
     L.own_o = L.own_ml + up(slots * 8 * sizeof(float2));
-    L.total = L.own_o + slots * 8 * D * sizeof(float);
+    L.prefix_ml = L.own_o + up(slots * 8 * D * sizeof(float));
+    const size_t parts = paged_joins(B, prefix_len) ? 0 : 2 * (num_sms + static_cast<size_t>(Hkv) * prefix_row_blocks(B * (Hq / Hkv)));
+    L.prefix_o = L.prefix_ml + up(parts * 128 * sizeof(float2));
+    L.total = L.prefix_o + parts * 128 * D * sizeof(float);
     return L;
 }
 
-size_t paged_workspace_bytes(int B, int, int Hkv, int D, int, int num_sms) {
-    return paged_layout(B, Hkv, D, num_sms).total;
+size_t paged_workspace_bytes(int B, int Hq, int Hkv, int D, int prefix_len, int num_sms) {
+    return paged_layout(B, Hq, Hkv, D, prefix_len, num_sms).total;
 }
 
 template <int D>
@@ -523,22 +556,35 @@ static cudaError_t launch_own(const PagedArgs &a, cudaStream_t s) {
     constexpr int smem = own_smem_bytes(D);
     cudaError_t e = cudaFuncSetAttribute(paged_own_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    // beside a prefix kernel its blocks take over the SMs as that one's end
+    if (a.prefix_ncta) return launch_dependent(paged_own_kernel<D>, dim3(a.ncta), dim3(kOwnThreads), smem, s, a);
     paged_own_kernel<D><<<a.ncta, kOwnThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
 
-cudaError_t launch_paged(PagedArgs &a, float scale, void *ws, int num_sms, cudaStream_t s) {
+cudaError_t launch_paged(PagedArgs &a, const CUtensorMap *maps, float scale, void *ws, int num_sms, cudaStream_t s) {
     char *w = static_cast<char *>(ws);
-    const PagedLayout L = paged_layout(a.B, a.c.Hkv, a.c.D, num_sms);
+    const PagedLayout L = paged_layout(a.B, a.Hq, a.c.Hkv, a.c.D, a.prefix_len, num_sms);
     a.starts = reinterpret_cast<int64_t *>(w + L.starts);
     a.own_ml = reinterpret_cast<float2 *>(w + L.own_ml);
     a.own_o = reinterpret_cast<float *>(w + L.own_o);
+    a.prefix_ml = reinterpret_cast<float2 *>(w + L.prefix_ml);
+    a.prefix_o = reinterpret_cast<float *>(w + L.prefix_o);
     a.ncta = num_sms;
-    a.join = 1;
     a.negate = scale < 0.f;
-    a.scale_log2 = fabsf(scale) * 1.4426950408889634f;
-    const cudaError_t e = a.c.D == 64 ? launch_own<64>(a, s) : launch_own<128>(a, s);
-    if (e != cudaSuccess) return e;
+    a.zero_q = scale == 0.f;
+    a.scale_log2 = scale == 0.f ? 1.f : fabsf(scale) * 1.4426950408889634f;
+    a.join = paged_joins(a.B, a.prefix_len);
+    cudaError_t e;
+    if (!a.join) {
+        const int rows = a.B * a.group;
+        a.prefix_two = rows > 128;
+        a.prefix_blocks = prefix_row_blocks(rows);
+        const int64_t tiles = static_cast<int64_t>(a.c.Hkv) * a.prefix_blocks * ((a.prefix_len + 127) / 128);
+        a.prefix_ncta = tiles < num_sms ? static_cast<int>(tiles) : num_sms;
+        if ((e = launch_prefix(maps[0], maps[1], a, s)) != cudaSuccess) return e;
+    }
+    if ((e = a.c.D == 64 ? launch_own<64>(a, s) : launch_own<128>(a, s)) != cudaSuccess) return e;
     return launch_dependent(paged_combine_kernel, dim3(a.B * a.c.Hkv, a.c.D / 32), dim3(256), 0, s, a);
 }
 

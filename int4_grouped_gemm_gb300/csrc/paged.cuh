@@ -40,17 +40,25 @@ struct PagedArgs {
     const int *prefix_pages, *table, *seq_len;
     int *status;
     int64_t *starts;                 // [B + 1]: 16-position tiles of the rows before b
+    float2 *prefix_ml;               // [2 slot + sub][128 rows]: as own_ml
+    float *prefix_o;                 // [2 slot + sub][D / 4][128 rows][4]
     float2 *own_ml;                  // [slot][8 heads]: running maximum (log2) and sum
     float *own_o;                    // [slot][D / 4][8 heads][4]: unnormalised output
     int B, Hq, group, prefix_len, table_ld;
     int join;                        // the prefix is read as the start of every row
     int ncta;                        // blocks of the own-position kernel
+    int prefix_two, prefix_blocks;   // prefix: 256-row blocks (else one of 128), blocks a key-value head
+    int prefix_ncta;                 // blocks of the prefix kernel, 0 without one
     int negate;                      // scale < 0: the queries' signs are flipped instead
+    int zero_q;                      // scale = 0: the queries are taken as zeros, with scale_log2 = 1
+    long long wait_limit;
     float scale_log2;                // |scale| log2(e)
 };
 
 cudaError_t launch_append(const AppendArgs &a, int num_sms, cudaStream_t s);
+cudaError_t launch_prefix(const CUtensorMap &k, const CUtensorMap &v, const PagedArgs &a, cudaStream_t s);
+bool paged_joins(int B, int prefix_len);  // the prefix is read per row instead of by the prefix kernel
 size_t paged_workspace_bytes(int B, int Hq, int Hkv, int D, int prefix_len, int num_sms);
-cudaError_t launch_paged(PagedArgs &a, float scale, void *ws, int num_sms, cudaStream_t s);
+cudaError_t launch_paged(PagedArgs &a, const CUtensorMap *maps, float scale, void *ws, int num_sms, cudaStream_t s);
 
 }  // namespace moe
