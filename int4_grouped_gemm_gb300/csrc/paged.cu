@@ -65,19 +65,24 @@ cudaError_t launch_append(const AppendArgs &a, int, cudaStream_t s) {
 //
 // Row b, query head h, key-value head g = h / group: o = softmax(scale q . K) V
 // over the prefix and the row's own positions, by the online softmax: over any
-// part of the positions a running maximum m, sum l = sum 2^(s - m) and output
-// O = sum 2^(s - m) v (scores in units of log2), and parts merge as
+// part of the positions a reference m (here the maximum), sum l = sum 2^(s - m)
+// and output O = sum 2^(s - m) v (scores in units of log2), and parts merge as
 // m = max m_i, l = sum 2^(m_i - m) l_i, O likewise.
 //
 // paged_own_kernel: every key and value is read once for the (at most 8) query
 // heads that share it, so the work is bound by those bytes.  The rows' positions
 // are cut into tiles of 16 (never across a page), all tiles of all rows and
-// key-value heads form one list, and each of the (one per SM) blocks takes an
-// even piece of it, whatever the lengths: a batch of one long and many short
-// rows fills the GPU like one row does.  Within a block, warp w takes tiles w,
-// w + 8, ... of the piece through its own ring of cp.async stages (24 KB), which
-// runs on across the items of the piece; at an item's end the warps' (m, l, O)
-// are merged in shared memory and written as one partial.
+// key-value heads (items) form one list, and the list is cut into even pieces,
+// whatever the lengths: a batch of one long and many short rows fills the GPU
+// like one row does.  Two ways, by the average item (the kernel sees the
+// lengths, the host does not):
+//   long items   a piece per block; warp w takes tiles w, w + 8, ... of it, and
+//                at an item's end the warps' (m, l, O) are merged in shared
+//                memory into one partial (about a microsecond an item)
+//   short items  (up to 32 tiles on average) a piece per warp, which writes a
+//                partial of its own for each item: no block-wide barriers
+// Each warp streams its tiles through its own ring of cp.async stages (24 KB),
+// which runs on across the items of the piece.
 //   scores   mma.sync m16n8k16, the heads as M, 16 positions as N
 //   output   O += P V, P from the score registers, rounded to bf16; l sums the
 //            rounded values, so that a weight's rounding cancels where one
@@ -85,7 +90,9 @@ cudaError_t launch_append(const AppendArgs &a, int, cudaStream_t s) {
 constexpr int kOwnWarps = 8;
 constexpr int kOwnThreads = kOwnWarps * 32;
 constexpr int kPosTile = 16;
-constexpr int kOwnMinTiles = kOwnWarps;  // tiles a block takes at least: one per warp
+constexpr int kShortItem = 32;   // tiles of an average item up to which pieces go to warps
+constexpr int kBlockTiles = 8;   // tiles that a block's piece has at least (one per warp) ...
+constexpr int kWarpTiles = 4;    // ... and a warp's, if there are fewer items than pieces
 
 __host__ __device__ constexpr int own_stages(int D) { return D == 128 ? 3 : 6; }
 __host__ __device__ constexpr int own_stage_bytes(int D) { return 2 * kPosTile * D * 2; }
@@ -130,16 +137,6 @@ __device__ __forceinline__ int own_len(const PagedArgs &a, int b, bool &over) {
     return n < 0 ? 0 : over ? static_cast<int>(room) : n;
 }
 
-// First tile of piece c of W tiles cut into n pieces, and the piece of tile f.
-__device__ __forceinline__ int64_t piece_start(int64_t W, int n, int c) { return W * c / n; }
-__device__ __forceinline__ int piece_of(int64_t W, int n, int64_t f) {
-    return static_cast<int>(((f + 1) * n - 1) / W);
-}
-__device__ __forceinline__ int own_pieces(int64_t W, int ncta) {
-    const int64_t most = (W + kOwnMinTiles - 1) / kOwnMinTiles;
-    return most < ncta ? static_cast<int>(most) : ncta;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_constant__ PagedArgs a) {
     constexpr int KD = D / 16;          // MMA k-steps of the scores
@@ -154,15 +151,18 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
     int *s_valid = reinterpret_cast<int *>(ml + kOwnWarps * 8);               // [warp][stage]
     int64_t *s_start = reinterpret_cast<int64_t *>(s_valid + kOwnWarps * NS);  // [B + 1]
     __shared__ int64_t s_warp[kOwnWarps];
+    __shared__ int s_rows[kOwnWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g8 = lane >> 2, c = lane & 3;
     pdl_trigger();
     const int Hkv = a.c.Hkv, ps = a.c.page_shift;
     const int ntp = a.join ? tiles16(a.prefix_len) : 0;
 
-    // tiles of the rows before each row (four rows a thread, then a scan)
+    // tiles of the rows before each row (four rows a thread, then a scan), and
+    // the number of rows that have any
     {
         int64_t n[4], sum = 0;
+        int filled = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int b = tid * 4 + i;
@@ -174,14 +174,19 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
                 if (over && blockIdx.x == 0) record_status(a.status, MOE_ERR_PAGE);
             }
             sum += n[i];
+            filled += n[i] > 0;
         }
         int64_t scan = sum;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int64_t v = __shfl_up_sync(0xffffffffu, scan, off);
             if (lane >= off) scan += v;
+            filled += __shfl_xor_sync(0xffffffffu, filled, off);
         }
-        if (lane == 31) s_warp[warp] = scan;
+        if (lane == 31) {
+            s_warp[warp] = scan;
+            s_rows[warp] = filled;
+        }
         __syncthreads();
         scan -= sum;
         for (int w = 0; w < warp; ++w) scan += s_warp[w];
@@ -201,12 +206,27 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
         __syncthreads();
     }
     const int64_t W = s_start[a.B] * Hkv;
-    const int np = own_pieces(W, a.ncta);
-    if (static_cast<int>(blockIdx.x) >= np) {
-        pdl_wait();
-        return;
-    }
-    const int64_t f0 = piece_start(W, np, blockIdx.x), f1 = piece_start(W, np, blockIdx.x + 1);
+    int64_t items = 0;
+#pragma unroll
+    for (int w = 0; w < kOwnWarps; ++w) items += s_rows[w];
+    items *= Hkv;
+    // tiles of a piece: as many pieces as there are blocks or warps, or fewer
+    // where that leaves less than an item or a few tiles for each
+    const bool by_warp = W <= kShortItem * items;
+    int64_t most = by_warp ? (W + kWarpTiles - 1) / kWarpTiles : (W + kBlockTiles - 1) / kBlockTiles;
+    most = most > items ? most : items;
+    const int64_t cap = by_warp ? a.ncta * kOwnWarps : a.ncta;
+    most = most < cap ? most : cap;
+    const int64_t per = most ? (W + most - 1) / most : 0;
+    if (blockIdx.x == 0 && tid == 0) a.starts[a.B + 1] = per;
+
+    // this warp's piece, and its tiles in it: first + stride i, i < my_n.  Pieces
+    // of warps go round the blocks, so that a few of them meet no other
+    const int piece = by_warp ? warp * a.ncta + blockIdx.x : blockIdx.x;
+    const int64_t f0 = piece * per < W ? piece * per : W, f1 = f0 + per < W ? f0 + per : W;
+    const int stride = by_warp ? 1 : kOwnWarps;
+    const int64_t first = by_warp ? f0 : f0 + warp;
+    const int my_n = f1 > first ? static_cast<int>((f1 - first + stride - 1) / stride) : 0;
 
     // the row of tile f: the last one that starts at or before it
     auto row_of = [&](int64_t f) {
@@ -221,16 +241,14 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
         return lo;
     };
 
-    // this warp's i-th tile is f0 + warp + 8 i; lane j describes tile 32 k + j:
-    // where its first key is, and how many positions it has (none if the page
-    // is outside the pool)
-    const int my_n = f1 - f0 > warp ? static_cast<int>((f1 - f0 - warp + kOwnWarps - 1) / kOwnWarps) : 0;
+    // lane j describes tile 32 k + j of this warp: where its first key is, and
+    // how many positions it has (none if the page is outside the pool)
     int64_t d_at = 0;
     int d_valid = 0;
     auto describe = [&](int i) {
         d_valid = 0;
         if (i >= my_n) return;
-        const int64_t f = f0 + warp + static_cast<int64_t>(kOwnWarps) * i;
+        const int64_t f = first + static_cast<int64_t>(stride) * i;
         const int b = row_of(f);
         const int64_t nt = s_start[b + 1] - s_start[b];
         const int64_t in_row = f - s_start[b] * Hkv;
@@ -285,33 +303,37 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
     const int vpos = (mi & 1) * 8 + rr, vch = mi >> 1;
     const uint32_t flip = a.negate ? 0x80008000u : 0u, keep = a.zero_q ? 0u : 0xFFFFFFFFu;
 
-    int i = 0;
-    for (int64_t f = f0; f < f1;) {
-        const int b = row_of(f);
-        const int64_t nt = s_start[b + 1] - s_start[b];
-        const int kv = static_cast<int>((f - s_start[b] * Hkv) / nt);
-        const int64_t item_end = s_start[b] * Hkv + (kv + 1) * nt;
-        const int64_t end = item_end < f1 ? item_end : f1;
-
-        // the group's queries as the A operand: thread (g8, c) holds
-        // q[g8][16 kd + 2c, +1] and [16 kd + 2c + 8, +9]
-        uint32_t qa[KD][2];
-        {
-            const bool real = g8 < a.group;
-            const uint32_t *qrow = reinterpret_cast<const uint32_t *>(
-                a.q + b * a.q_stride + static_cast<int64_t>(kv * a.group + (real ? g8 : 0)) * D);
+    // the item's queries as the A operand: thread (g8, c) holds
+    // q[g8][16 kd + 2c, +1] and [16 kd + 2c + 8, +9]
+    uint32_t qa[KD][2];
+    auto load_q = [&](int b, int kv) {
+        const bool real = g8 < a.group;
+        const uint32_t *qrow = reinterpret_cast<const uint32_t *>(
+            a.q + b * a.q_stride + static_cast<int64_t>(kv * a.group + (real ? g8 : 0)) * D);
 #pragma unroll
-            for (int kd = 0; kd < KD; ++kd) {
-                qa[kd][0] = real ? (__ldg(qrow + kd * 8 + c) & keep) ^ flip : 0u;
-                qa[kd][1] = real ? (__ldg(qrow + kd * 8 + c + 4) & keep) ^ flip : 0u;
-            }
+        for (int kd = 0; kd < KD; ++kd) {
+            qa[kd][0] = real ? (__ldg(qrow + kd * 8 + c) & keep) ^ flip : 0u;
+            qa[kd][1] = real ? (__ldg(qrow + kd * 8 + c + 4) & keep) ^ flip : 0u;
         }
+    };
+
+    int i = 0, b = 0, kv = 0;
+    int64_t nt = 0, end = 0;  // tiles of the row's items, end of this one
+    if (f0 < f1) {
+        b = row_of(f0);
+        nt = s_start[b + 1] - s_start[b];
+        kv = static_cast<int>((f0 - s_start[b] * Hkv) / nt);
+        end = s_start[b] * Hkv + (kv + 1) * nt;
+        load_q(b, kv);
+    }
+    for (int64_t f = f0; f < f1;) {
+        const int64_t stop = end < f1 ? end : f1;
         float o[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
         float m_run = -INFINITY, l_run = 0.f;
 
-        for (; f0 + warp + static_cast<int64_t>(kOwnWarps) * i < end; ++i) {
+        for (; first + static_cast<int64_t>(stride) * i < stop; ++i) {
             cp_async_wait<NS - 1>();
             __syncwarp();
             const uint32_t sk = ring + (i % NS) * STAGE, sv = sk + kPosTile * ROW;
@@ -359,11 +381,32 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
             cp_async_commit();
         }
 
+        const int64_t slot = static_cast<int64_t>(piece) + static_cast<int64_t>(b) * Hkv + kv;
+        // the next item; its queries are on their way while this one is written
+        f = stop;
+        if (f < f1) {
+            if (++kv == Hkv) {
+                kv = 0;
+                do ++b;
+                while (s_start[b + 1] == s_start[b]);
+                nt = s_start[b + 1] - s_start[b];
+            }
+            end += nt;
+            load_q(b, kv);
+        }
+
+        float l_sum = l_run + __shfl_xor_sync(0xffffffffu, l_run, 1);
+        l_sum += __shfl_xor_sync(0xffffffffu, l_sum, 2);
+        if (by_warp) {
+            float *dst = a.own_o + slot * (8 * D) + (c >> 1) * 32 + g8 * 4 + (c & 1) * 2;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) *reinterpret_cast<float2 *>(dst + n * 64) = make_float2(o[n][0], o[n][1]);
+            if (c == 0) a.own_ml[slot * 8 + g8] = make_float2(m_run, l_sum);
+            continue;
+        }
         // merge the eight warps: every warp scales its output to the common
         // maximum, the upper four hand theirs to the lower four, these add and
         // leave four sums, which the block adds in order
-        float l_sum = l_run + __shfl_xor_sync(0xffffffffu, l_run, 1);
-        l_sum += __shfl_xor_sync(0xffffffffu, l_sum, 2);
         if (c == 0) {
             mm[warp * 8 + g8] = m_run;  // -inf: no tile of this item
             ml[warp * 8 + g8] = l_sum;
@@ -390,7 +433,6 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
             }
         }
         __syncthreads();
-        const int64_t slot = static_cast<int64_t>(blockIdx.x) + static_cast<int64_t>(b) * Hkv + kv;
         {
             const int h = tid & 7;
             for (int d4 = tid >> 3; d4 < D / 4; d4 += kOwnThreads / 8) {
@@ -416,104 +458,120 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
             }
         }
         __syncthreads();  // the merge buffers are free for the next item
-        f = end;
     }
     cp_async_wait<0>();
     pdl_wait();  // a kernel before this one that still runs is complete before this one is
 }
 
 // Merge the partials of one (row, key-value head): grid (B Hkv, D / 32), thread
-// (part of the partials, 4 dimensions, head).  First the weights 2^(m_i - M) of
-// all partials per head, then the sums with every load independent.
-constexpr int kMergeMax = 768;  // partials of one row: at most 256 of its own, 512 of the prefix
-
+// (quarter of the partials, 4 dimensions, head).  Every thread runs the online
+// merge over its partials, eight at a time (their loads independent), the
+// quarters meet in shared memory.
 __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ PagedArgs a) {
-    __shared__ float s_w[8][kMergeMax + 1];
-    __shared__ float s_inv[8];
-    __shared__ float4 s_red[4][64];
+    __shared__ float4 s_acc[4][64];
+    __shared__ float2 s_ml[4][64];
     pdl_wait();
     const int Hkv = a.c.Hkv, D = a.c.D;
     const int b = blockIdx.x / Hkv, kv = blockIdx.x % Hkv;
-    if (a.seq_len[b] < 0) return;  // padding: out stays as it is
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t W = a.starts[a.B] * Hkv, s0 = a.starts[b], nt = a.starts[b + 1] - s0;
-    int c0 = 0, n_own = 0;
-    if (nt > 0) {
-        const int np = own_pieces(W, a.ncta);
-        c0 = piece_of(W, np, s0 * Hkv + kv * nt);
-        n_own = piece_of(W, np, s0 * Hkv + (kv + 1) * nt - 1) - c0 + 1;
-    }
-    const int64_t slot0 = static_cast<int64_t>(c0) + static_cast<int64_t>(b) * Hkv + kv;
-    // the prefix's partials of head h's row: first index, count, step
-    const int step = a.prefix_two ? 2 : 1;
-    auto prefix_parts = [&](int h, int64_t &first, int &row) {
-        if (a.prefix_ncta == 0 || h >= a.group) return 0;
-        const int g = b * a.group + h, blk = g / (step * 128);
-        const int64_t item = static_cast<int64_t>(kv) * a.prefix_blocks + blk;
-        const int64_t ntile = (a.prefix_len + 127) / 128, Wp = ntile * Hkv * a.prefix_blocks;
-        const int p0 = piece_of(Wp, a.prefix_ncta, item * ntile), p1 = piece_of(Wp, a.prefix_ncta, (item + 1) * ntile - 1);
-        row = g & 127;
-        first = (p0 + item) * 2 + (a.prefix_two ? (g >> 7) & 1 : 0);
-        return (p1 - p0 + 1) * (3 - step);
-    };
-    {
-        const int h = warp;  // warp h: head h's weights
-        int64_t first = 0;
-        int row = 0;
-        const int n_pre = prefix_parts(h, first, row);
-        const float2 *own = a.own_ml + slot0 * 8 + h, *pre = a.prefix_ml + first * 128 + row;
-        float M = -INFINITY;
-        for (int i = lane; i < n_own + n_pre; i += 32) {
-            const float v = i < n_own ? __ldcg(own + i * 8).x : __ldcg(pre + static_cast<int64_t>(i - n_own) * step * 128).x;
-            s_w[h][i] = v;
-            M = fmaxf(M, v);
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-        float den = 0.f;
-        for (int i = lane; i < n_own + n_pre; i += 32) {
-            const float v = s_w[h][i], w = v == -INFINITY ? 0.f : exp2f(v - M);
-            s_w[h][i] = w;
-            den += w * (i < n_own ? __ldcg(own + i * 8).y : __ldcg(pre + static_cast<int64_t>(i - n_own) * step * 128).y);
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
-        if (lane == 0) s_inv[h] = M == -INFINITY ? 0.f : 1.0f / den;
-    }
-    __syncthreads();
-    const int h = tid & 7, dq = (tid >> 3) & 7, part = tid >> 6;
+    const int tid = threadIdx.x, h = tid & 7, dq = (tid >> 3) & 7, part = tid >> 6;
     const int d4 = blockIdx.y * 8 + dq;
-    int64_t first = 0;
-    int row = 0;
-    const int n_pre = prefix_parts(h, first, row);
+    const int len = a.seq_len[b];
+    const int64_t s0 = a.starts[b], nt = a.starts[b + 1] - s0, per = a.starts[a.B + 1];
+    if (len < 0) return;  // padding: out stays as it is
+
+    // its own partials: those of the pieces that its tiles lie in
+    int n_own = 0;
+    const float2 *own_ml = a.own_ml;
+    const float *own_o = a.own_o;
+    if (nt > 0) {
+        const int64_t f = s0 * Hkv + kv * nt, p0 = f / per;
+        n_own = static_cast<int>((f + nt - 1) / per - p0) + 1;
+        const int64_t slot = p0 + static_cast<int64_t>(b) * Hkv + kv;
+        own_ml += slot * 8 + h;
+        own_o += (slot * (D / 4) + d4) * 32 + h * 4;
+    }
+    // the prefix's partials of head h's row
+    int n_pre = 0;
+    int64_t step = 1;
+    const float2 *pre_ml = a.prefix_ml;
+    const float *pre_o = a.prefix_o;
+    if (a.prefix_ncta && h < a.group) {
+        const int g = b * a.group + h, sub = a.prefix_two ? (g >> 7) & 1 : 0;
+        const int64_t item = static_cast<int64_t>(kv) * a.prefix_blocks + (a.prefix_two ? g >> 8 : 0);
+        const int64_t f = item * a.prefix_tiles, p0 = f / a.prefix_per;
+        n_pre = static_cast<int>((f + a.prefix_tiles - 1) / a.prefix_per - p0) + 1;
+        if (a.prefix_two)
+            step = 2;
+        else
+            n_pre *= 2;  // a partial of the even and one of the odd tiles
+        const int64_t slot = 2 * (p0 + item) + sub;
+        pre_ml += slot * 128 + (g & 127);
+        pre_o += (slot * (D / 4) + d4) * 512 + (g & 127) * 4;
+    }
+    const int n = n_own + n_pre;
+    float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    // a partial without weight may never have been written: it is not added
-    auto add = [&](float w, const float4 &v) {
-        acc.x = w > 0.f ? fmaf(w, v.x, acc.x) : acc.x;
-        acc.y = w > 0.f ? fmaf(w, v.y, acc.y) : acc.y;
-        acc.z = w > 0.f ? fmaf(w, v.z, acc.z) : acc.z;
-        acc.w = w > 0.f ? fmaf(w, v.w, acc.w) : acc.w;
-    };
-    const float *src = a.own_o + (slot0 * (D / 4) + d4) * 32 + h * 4;
-#pragma unroll 8
-    for (int i = part; i < n_own; i += 4)
-        add(s_w[h][i], __ldcg(reinterpret_cast<const float4 *>(src + static_cast<int64_t>(i) * D * 8)));
-    const float *psrc = a.prefix_o + (first * (D / 4) + d4) * 512 + row * 4;
-#pragma unroll 8
-    for (int i = part; i < n_pre; i += 4)
-        add(s_w[h][n_own + i], __ldcg(reinterpret_cast<const float4 *>(psrc + static_cast<int64_t>(i) * step * D * 128)));
-    s_red[part][tid & 63] = acc;
+    for (int i0 = part; i0 < n; i0 += 32) {
+        float2 t[8];
+        float4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + 4 * j;
+            t[j] = make_float2(-INFINITY, 0.f);
+            v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < n_own) {
+                t[j] = __ldcg(own_ml + i * 8);
+                v[j] = __ldcg(reinterpret_cast<const float4 *>(own_o + static_cast<int64_t>(i) * D * 8));
+            } else if (i < n) {
+                t[j] = __ldcg(pre_ml + (i - n_own) * step * 128);
+                v[j] = __ldcg(reinterpret_cast<const float4 *>(pre_o + (i - n_own) * step * D * 128));
+            }
+        }
+        float mx = m;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mx = fmaxf(mx, t[j].x);
+        if (mx == -INFINITY) continue;
+        const float corr = exp2f(m - mx);
+        m = mx;
+        l *= corr;
+        acc = make_float4(acc.x * corr, acc.y * corr, acc.z * corr, acc.w * corr);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            // a partial without a tile (-inf) may never have been written
+            const bool has = t[j].x != -INFINITY;
+            const float w = exp2f(t[j].x - mx);
+            l += has ? w * t[j].y : 0.f;
+            acc.x += has ? w * v[j].x : 0.f;
+            acc.y += has ? w * v[j].y : 0.f;
+            acc.z += has ? w * v[j].z : 0.f;
+            acc.w += has ? w * v[j].w : 0.f;
+        }
+    }
+    s_acc[part][tid & 63] = acc;
+    s_ml[part][tid & 63] = make_float2(m, l);
     __syncthreads();
     if (part == 0 && h < a.group) {
+        float2 t[4];
+        float mx = -INFINITY, den = 0.f;
 #pragma unroll
-        for (int i = 1; i < 4; ++i) {
-            const float4 v = s_red[i][tid];
-            acc.x += v.x;
-            acc.y += v.y;
-            acc.z += v.z;
-            acc.w += v.w;
+        for (int i = 0; i < 4; ++i) {
+            t[i] = s_ml[i][tid];
+            mx = fmaxf(mx, t[i].x);
         }
-        const float inv = s_inv[h];
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (mx != -INFINITY) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float w = exp2f(t[i].x - mx);
+                const float4 v = s_acc[i][tid];
+                den += w * t[i].y;
+                acc.x += w * v.x;
+                acc.y += w * v.y;
+                acc.z += w * v.z;
+                acc.w += w * v.w;
+            }
+        }
+        const float inv = mx == -INFINITY ? 0.f : 1.0f / den;  // no position at all: zeros
         uint2 r;
         r.x = bf16_pair(acc.x * inv, acc.y * inv);
         r.y = bf16_pair(acc.z * inv, acc.w * inv);
@@ -536,9 +594,9 @@ struct PagedLayout {
 static PagedLayout paged_layout(int B, int Hq, int Hkv, int D, int prefix_len, int num_sms) {
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     PagedLayout L{};
-    const size_t slots = static_cast<size_t>(num_sms) + static_cast<size_t>(B) * Hkv;
+    const size_t slots = static_cast<size_t>(num_sms) * kOwnWarps + static_cast<size_t>(B) * Hkv;
     L.starts = kCtrlBytes;
-    L.own_ml = L.starts + up((B + 1) * sizeof(int64_t));
+    L.own_ml = L.starts + up((B + 2) * sizeof(int64_t));
     L.own_o = L.own_ml + up(slots * 8 * sizeof(float2));
     L.prefix_ml = L.own_o + up(slots * 8 * D * sizeof(float));
     const size_t parts = paged_joins(B, prefix_len) ? 0 : 2 * (num_sms + static_cast<size_t>(Hkv) * prefix_row_blocks(B * (Hq / Hkv)));
@@ -580,8 +638,10 @@ cudaError_t launch_paged(PagedArgs &a, const CUtensorMap *maps, float scale, voi
         const int rows = a.B * a.group;
         a.prefix_two = rows > 128;
         a.prefix_blocks = prefix_row_blocks(rows);
-        const int64_t tiles = static_cast<int64_t>(a.c.Hkv) * a.prefix_blocks * ((a.prefix_len + 127) / 128);
-        a.prefix_ncta = tiles < num_sms ? static_cast<int>(tiles) : num_sms;
+        a.prefix_tiles = (a.prefix_len + 127) / 128;
+        const int64_t tiles = static_cast<int64_t>(a.c.Hkv) * a.prefix_blocks * a.prefix_tiles;
+        a.prefix_per = static_cast<int>((tiles + num_sms - 1) / num_sms);
+        a.prefix_ncta = static_cast<int>((tiles + a.prefix_per - 1) / a.prefix_per);
         if ((e = launch_prefix(maps[0], maps[1], a, s)) != cudaSuccess) return e;
     }
     if ((e = a.c.D == 64 ? launch_own<64>(a, s) : launch_own<128>(a, s)) != cudaSuccess) return e;

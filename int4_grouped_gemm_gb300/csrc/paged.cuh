@@ -28,9 +28,9 @@ struct AppendArgs {
     int T, Hq, n_seq, table_ld, pos_offset, rot, interleaved;
 };
 
-// Partial results of the attention, merged by the combine kernel.  A flat list
-// of tiles is cut into ncta even pieces; piece c of the list and item i of it
-// (a row's key-value head, or a block of rows of the prefix) that meet have
+// Partial results of the attention, merged by the combine kernel.  A list of
+// tiles is cut into pieces of `per` tiles; piece c and item i of the list (a
+// row's key-value head, or a block of rows of the prefix) that meet have
 // partial slot c + i, which no other pair has (both only grow along the list).
 struct PagedArgs {
     Pages c;
@@ -39,7 +39,7 @@ struct PagedArgs {
     int64_t q_stride, out_stride;
     const int *prefix_pages, *table, *seq_len;
     int *status;
-    int64_t *starts;                 // [B + 1]: 16-position tiles of the rows before b
+    int64_t *starts;                 // [B + 1]: 16-position tiles of the rows before b; [B + 1] tiles of a piece
     float2 *prefix_ml;               // [2 slot + sub][128 rows]: as own_ml
     float *prefix_o;                 // [2 slot + sub][D / 4][128 rows][4]
     float2 *own_ml;                  // [slot][8 heads]: running maximum (log2) and sum
@@ -48,7 +48,8 @@ struct PagedArgs {
     int join;                        // the prefix is read as the start of every row
     int ncta;                        // blocks of the own-position kernel
     int prefix_two, prefix_blocks;   // prefix: 256-row blocks (else one of 128), blocks a key-value head
-    int prefix_ncta;                 // blocks of the prefix kernel, 0 without one
+    int prefix_tiles, prefix_per;    // 128-position tiles of the prefix, tiles of a piece
+    int prefix_ncta;                 // pieces and blocks of the prefix kernel, 0 without one
     int negate;                      // scale < 0: the queries' signs are flipped instead
     int zero_q;                      // scale = 0: the queries are taken as zeros, with scale_log2 = 1
     long long wait_limit;

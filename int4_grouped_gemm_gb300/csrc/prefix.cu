@@ -260,10 +260,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     pdl_trigger();
 
     // this block's piece of the list; item = (key-value head, block of rows)
-    const int ntile = (a.prefix_len + kPos - 1) / kPos, nblk = a.prefix_blocks;
+    const int ntile = a.prefix_tiles, nblk = a.prefix_blocks;
     const int rows = a.B * a.group;
     const int64_t W = static_cast<int64_t>(a.c.Hkv) * nblk * ntile;
-    const int64_t f0 = W * blockIdx.x / a.prefix_ncta, f1 = W * (blockIdx.x + 1) / a.prefix_ncta;
+    const int64_t f0 = static_cast<int64_t>(blockIdx.x) * a.prefix_per, f1 = f0 + a.prefix_per < W ? f0 + a.prefix_per : W;
     const int item0 = static_cast<int>(f0 / ntile), tile0 = static_cast<int>(f0 % ntile);
     const int count = static_cast<int>(f1 - f0);  // tiles of this piece
     const int per_block = two ? 2 * kRows : kRows;
