@@ -20,6 +20,17 @@ struct LinearArgs {
     int64_t x_stride, y_stride;
     int N, K, G, ldg, B;
     int y_fp32;
+    // filled in by launch_linear: blocks of a cluster (they split K), units of
+    // 128 k in a chunk of tokens, buffers for chunks
+    int split, chunk_units, x_buffers;
+
+    __device__ __forceinline__ int rank_of(int block) const { return block % split; }
+    __device__ __forceinline__ void store(int t, int n, float v) const {
+        if (y_fp32)
+            static_cast<float *>(y)[t * y_stride + n] = v;
+        else
+            static_cast<__nv_bfloat16 *>(y)[t * y_stride + n] = __float2bfloat16_rn(v);
+    }
 };
 
 cudaError_t launch_linear(const LinearArgs &a, int num_sms, cudaStream_t s);

@@ -118,11 +118,6 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
                  : "r"(addr));
 }
 
-// 16 bytes from global to shared memory, or zeros (the source is then not read).
-__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, bool valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     return bf162_as_u32(__floats2bfloat162_rn(lo, hi));
 }
