@@ -20,16 +20,17 @@
 // buffers.
 #include "linear.cuh"
 
+#include <algorithm>
+
 namespace moe {
 
 constexpr int kLinWarps = 8;
 constexpr int kLinThreads = kLinWarps * 32;
 constexpr int kUnit = 128;                       // k of a stage
-constexpr int kLinStages = 8;
 constexpr int kNibBytes = 16 * kUnit / 2;        // codes of a stage
 constexpr int kScaleBytes = 16 * 8;              // up to four groups of 16 rows
 constexpr int kStageBytes = kNibBytes + 2 * kScaleBytes;
-constexpr int kRingBytes = kLinWarps * kLinStages * kStageBytes;
+__host__ __device__ constexpr int ring_bytes(int stages) { return kLinWarps * stages * kStageBytes; }
 
 __device__ __forceinline__ void cp_async_n(uint32_t dst, const void *src, int bytes, bool valid) {
     if (bytes == 16)
@@ -59,7 +60,7 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <int G, int NT, int RW>
+template <int G, int NT, int RW, int kLinStages>
 __global__ void __launch_bounds__(kLinThreads, NT <= 2 ? 2 : 1) int4_linear_kernel(const LinearArgs a) {
     constexpr int KW = kLinWarps / RW;
     constexpr int B8 = NT * 8;                    // token rows of the buffers
@@ -73,8 +74,8 @@ __global__ void __launch_bounds__(kLinThreads, NT <= 2 ? 2 : 1) int4_linear_kern
     const uint32_t ring = smem_u32(smem) + warp * kLinStages * kStageBytes;
     const int cu = a.chunk_units;                 // units of a chunk of tokens
     const int xpitch = cu * kUnit * 2 + XPAD;     // bytes
-    const int xbytes = B8 * xpitch, gbytes = cu * GPU_ * B8 * 4;
-    uint8_t *xbuf = smem + kRingBytes;            // [buffers][tokens][chunk], then group sums [buffers][group][tokens]
+    const int xbytes = a.B * xpitch, gbytes = cu * GPU_ * B8 * 4;
+    uint8_t *xbuf = smem + ring_bytes(kLinStages);            // [buffers][tokens][chunk], then group sums [buffers][group][tokens]
     uint8_t *gbuf = xbuf + a.x_buffers * xbytes;
     float *red = reinterpret_cast<float *>(gbuf + a.x_buffers * gbytes);  // sums across warps or blocks
     pdl_wait();
@@ -87,56 +88,55 @@ __global__ void __launch_bounds__(kLinThreads, NT <= 2 ? 2 : 1) int4_linear_kern
     const int first_block = blockIdx.x / a.split, row_step = gridDim.x / a.split;
     const int row_blocks = (a.N + 16 * RW - 1) / (16 * RW);
 
-    // this warp's units run through all its row blocks and chunks; `next` is
-    // the one to be requested
-    struct Pos {
-        int rb, ch, i;  // block of rows, chunk, unit of the warp's share of the chunk
-    };
+    // this warp's share of a chunk: units [from, to)
     auto share = [&](int ch, int &from, int &to) {
         const int n = min(cu, u1 - u0 - ch * cu);
         from = u0 + ch * cu + n * kw / KW;
         to = u0 + ch * cu + n * (kw + 1) / KW;
     };
-    auto settle = [&](Pos &p) {  // skip empty shares; false at the end
-        while (p.rb < row_blocks) {
-            int from, to;
-            share(p.ch, from, to);
-            if (p.i < to - from) return true;
-            p.i = 0;
-            if (++p.ch == nchunk) {
-                p.ch = 0;
-                p.rb += row_step;
-            }
-        }
-        return false;
-    };
-    Pos next{first_block, 0, 0};
+    // the requests run ahead through the same units: block of rows, chunk, unit
+    // and end of the share, and this lane's sources.  Lane l copies the 16-byte
+    // pieces l and l + 32 of the codes' [16 rows][4 pieces], and row l % 16's
+    // scales (lanes 0-15) or biases
     const int ldw = a.K / 8;
+    int n_rb = first_block, n_ch = 0, n_u, n_to;
+    share(0, n_u, n_to);
+    const uint32_t *n_q = nullptr;
+    const uint16_t *n_s = nullptr;
+    bool n_row0 = false, n_row1 = false, n_srow = false;
+    auto aim = [&]() {
+        const int row = (n_rb * RW + rw) * 16;
+        const int r = row + (lane >> 2), rs = row + (lane & 15);
+        n_row0 = r < a.N;
+        n_row1 = r + 8 < a.N;
+        n_srow = rs < a.N;
+        n_q = a.q + static_cast<int64_t>(n_row0 ? r : 0) * ldw + n_u * (kUnit / 8) + 4 * (lane & 3);
+        n_s = (lane < 16 ? a.s : a.b) + static_cast<int64_t>(n_srow ? rs : 0) * a.ldg;
+    };
+    aim();
+    uint32_t d_q, d_s;  // destinations in a stage
+    {
+        const int r = lane >> 2, sw = ((r >> 1) & 1) * 2 + ((r >> 2) & 1);
+        d_q = ring + r * 64 + (((lane & 3) ^ sw) << 4);
+        d_s = ring + kNibBytes + (lane >> 4) * kScaleBytes + (lane & 15) * 8;
+    }
     auto issue = [&](int st) {
-        if (!settle(next)) return;
-        int from, to;
-        share(next.ch, from, to);
-        const int u = from + next.i++;
-        const int row0 = (next.rb * RW + rw) * 16;
-        const uint32_t dst = ring + st * kStageBytes;
-        // codes: lane's 16-byte pieces lane and lane + 32 of [16 rows][4 pieces]
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = (lane >> 2) + 8 * i, p = lane & 3;
-            const bool ok = row0 + r < a.N && u * kUnit + 32 * p < a.K;
-            const uint32_t *src = a.q + (ok ? static_cast<int64_t>(row0 + r) * ldw + u * (kUnit / 8) + 4 * p : 0);
-            const int sw = ((r >> 1) & 1) * 2 + ((r >> 2) & 1);
-            cp_async_n(dst + r * 64 + ((p ^ sw) << 4), src, 16, ok);
+        while (n_u == n_to) {  // the share is through: the next chunk, the next block of rows
+            if (n_rb >= row_blocks) return;
+            if (++n_ch == nchunk) {
+                n_ch = 0;
+                n_rb += row_step;
+                if (n_rb >= row_blocks) return;
+            }
+            share(n_ch, n_u, n_to);
+            aim();
         }
-        // scales (lanes 0-15) and biases of the unit's groups
-        {
-            const int r = lane & 15;
-            const bool ok = row0 + r < a.N;
-            const uint16_t *base = lane < 16 ? a.s : a.b;
-            const int g0 = GPU_ == 1 ? u & ~1 : u * GPU_;
-            const uint16_t *src = base + (ok ? static_cast<int64_t>(row0 + r) * a.ldg + g0 : 0);
-            cp_async_n(dst + kNibBytes + (lane >> 4) * kScaleBytes + r * 8, src, SB, ok);
-        }
+        const bool k_ok = n_u * kUnit + 32 * (lane & 3) < a.K;
+        cp_async_n(d_q + st * kStageBytes, n_q, 16, n_row0 && k_ok);
+        cp_async_n(d_q + st * kStageBytes + 8 * 64, n_row1 ? n_q + 8 * static_cast<int64_t>(ldw) : n_q, 16, n_row1 && k_ok);
+        cp_async_n(d_s + st * kStageBytes, n_s + (GPU_ == 1 ? n_u & ~1 : n_u * GPU_), SB, n_srow);
+        n_q += kUnit / 8;
+        ++n_u;
     };
 #pragma unroll
     for (int i = 0; i < kLinStages - 1; ++i) {
@@ -144,27 +144,32 @@ __global__ void __launch_bounds__(kLinThreads, NT <= 2 ? 2 : 1) int4_linear_kern
         cp_async_commit();
     }
 
-    // chunk ch of the tokens into a buffer, with its group sums: thread = 16
-    // bytes of a token row, the lanes of a group add up their elements
+    // chunk ch of the tokens into a buffer (all copies in flight together), then
+    // its group sums: a thread takes 16 bytes of a token row, the lanes of a
+    // group add up their elements
     auto load_x = [&](int ch, int buf) {
         const int k0 = (u0 + ch * cu) * kUnit;
-        const int n = min(cu, u1 - u0 - ch * cu) * (kUnit / 8);  // 16-byte pieces of a row
+        const int n = min(cu, u1 - u0 - ch * cu) * (kUnit / 8);  // 16-byte pieces of a row, a multiple of 16
         uint8_t *xd = xbuf + buf * xbytes;
         float *gd = reinterpret_cast<float *>(gbuf + buf * gbytes);
-        for (int i = tid; i < a.B * n; i += kLinThreads) {       // n is a multiple of 16
-            const int t = i / n, p = i - t * n;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (k0 + 8 * p < a.K) v = *reinterpret_cast<const uint4 *>(a.x + t * a.x_stride + k0 + 8 * p);
-            *reinterpret_cast<uint4 *>(xd + t * xpitch + p * 16) = v;
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            float sum = 0.f;
+        for (int t = warp; t < a.B; t += kLinWarps)
+            for (int p = lane; p < n; p += 32)
+                cp_async_n(smem_u32(xd + t * xpitch + p * 16), a.x + t * a.x_stride + min(k0 + 8 * p, a.K - 8), 16,
+                           k0 + 8 * p < a.K);
+        cp_async_wait_all();
+        __syncwarp();
+        for (int t = warp; t < a.B; t += kLinWarps)
+            for (int p = lane; p < n; p += 32) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(xd + t * xpitch + p * 16);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                float sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sum += __uint_as_float(w[j] << 16) + __uint_as_float(w[j] & 0xFFFF0000u);
-            const unsigned mask = 0xFFFFu << (lane & 16);        // 16 lanes are in or out together
+                for (int j = 0; j < 4; ++j) sum += __uint_as_float(w[j] << 16) + __uint_as_float(w[j] & 0xFFFF0000u);
+                const unsigned mask = 0xFFFFu << (lane & 16);  // 16 lanes are in or out together
 #pragma unroll
-            for (int off = 1; off < G / 8; off <<= 1) sum += __shfl_xor_sync(mask, sum, off);
-            if (p % (G / 8) == 0) gd[(p / (G / 8)) * B8 + t] = sum;
-        }
+                for (int off = 1; off < G / 8; off <<= 1) sum += __shfl_xor_sync(mask, sum, off);
+                if (p % (G / 8) == 0) gd[(p / (G / 8)) * B8 + t] = sum;
+            }
     };
     load_x(0, 0);
     __syncthreads();
@@ -177,7 +182,11 @@ __global__ void __launch_bounds__(kLinThreads, NT <= 2 ? 2 : 1) int4_linear_kern
         for (int ch = 0; ch < nchunk; ++ch) {
             int from, to;
             share(ch, from, to);
-            const uint32_t xs = smem_u32(xbuf + buf * xbytes) + g8 * xpitch;
+            // (columns past the batch repeat its last token: they are not stored)
+            const uint32_t xs = smem_u32(xbuf + buf * xbytes);
+            uint32_t xrow[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) xrow[n] = xs + min(n * 8 + g8, a.B - 1) * xpitch;
             const float *gs = reinterpret_cast<const float *>(gbuf + buf * gbytes) + 2 * c;
             const int base = u0 + ch * cu;
             for (int u = from; u < to; ++u) {
@@ -228,7 +237,7 @@ __global__ void __launch_bounds__(kLinThreads, NT <= 2 ? 2 : 1) int4_linear_kern
                                 uint32_t x0, x1, x2, x3;
                                 asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                                              : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3)
-                                             : "r"(xs + n * 8 * xpitch + ul * (kUnit * 2) + (w0 + w) * 16));
+                                             : "r"(xrow[n] + ul * (kUnit * 2) + (w0 + w) * 16));
                                 mma_16816(d[n], af[0], x0, x1);
                                 mma_16816(d[n], af[1], x2, x3);
                             }
@@ -236,10 +245,13 @@ __global__ void __launch_bounds__(kLinThreads, NT <= 2 ? 2 : 1) int4_linear_kern
                     }
                     // the group's scale and bias of rows g8 and g8 + 8
                     const int gi = GPU_ == 1 ? (u & 1) : gr;
-                    const uint16_t *ss = reinterpret_cast<const uint16_t *>(sp + kNibBytes + g8 * 8) + gi;
-                    const float s0 = bf16_bits_to_float(ss[0]), s1 = bf16_bits_to_float(ss[8 * 4]);
-                    const float z0 = fmaf(-128.f, s0, bf16_bits_to_float(ss[kScaleBytes / 2]));
-                    const float z1 = fmaf(-128.f, s1, bf16_bits_to_float(ss[kScaleBytes / 2 + 8 * 4]));
+                    const uint32_t *ss = reinterpret_cast<const uint32_t *>(sp + kNibBytes + g8 * 8) + (gi >> 1);
+                    auto pick = [&](uint32_t pair) {
+                        return __uint_as_float((gi & 1) ? pair & 0xFFFF0000u : pair << 16);
+                    };
+                    const float s0 = pick(ss[0]), s1 = pick(ss[16]);
+                    const float z0 = fmaf(-128.f, s0, pick(ss[kScaleBytes / 4]));
+                    const float z1 = fmaf(-128.f, s1, pick(ss[kScaleBytes / 4 + 16]));
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const float2 X = *reinterpret_cast<const float2 *>(gs + (ul * GPU_ + gr) * B8 + n * 8);
@@ -312,37 +324,13 @@ __global__ void __launch_bounds__(kLinThreads, NT <= 2 ? 2 : 1) int4_linear_kern
     cp_async_wait<0>();
 }
 
-template <int G, int NT, int RW>
-static cudaError_t launch_t(LinearArgs a, int num_sms, cudaStream_t s) {
-    constexpr int KW = kLinWarps / RW, B8 = NT * 8;
-    const int units = (a.K + kUnit - 1) / kUnit;
-    const int row_blocks = (a.N + 16 * RW - 1) / (16 * RW);
-    // split K over a cluster while that leaves every warp two units and the
-    // GPU is not yet full
-    a.split = 1;
-    while (a.split < 8 && row_blocks * a.split * 2 <= num_sms + num_sms / 4 && units / (a.split * 2) >= 2 * KW) a.split *= 2;
-    const int share = (units + a.split - 1) / a.split;
-    // all of the block's tokens if they fit, else two chunks that do
-    constexpr int per_unit = B8 * (kUnit * 2 + kUnit / G * 4);
-    constexpr int room = 96 * 1024;
-    if (share * per_unit <= room) {
-        a.chunk_units = share;
-        a.x_buffers = 1;
-    } else {
-        a.chunk_units = room / 2 / per_unit / KW * KW;
-        a.x_buffers = 2;
-    }
-    constexpr int XPAD = G == 32 ? 64 : 16;
-    const int xbytes = B8 * (a.chunk_units * kUnit * 2 + XPAD), gbytes = a.chunk_units * (kUnit / G) * B8 * 4;
-    const int red = KW > 1 || a.split > 1 ? RW * KW * B8 * 16 * 4 : 0;
-    const int smem = kRingBytes + a.x_buffers * (xbytes + gbytes) + red;
-    auto kernel = int4_linear_kernel<G, NT, RW>;
+template <int G, int NT, int RW, int kLinStages>
+static cudaError_t launch_s(LinearArgs a, int blocks, int smem, cudaStream_t s) {
+    auto kernel = int4_linear_kernel<G, NT, RW, kLinStages>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int per_sm = smem <= 113 * 1024 && NT <= 2 ? 2 : 1;
-    int groups = row_blocks < num_sms * per_sm / a.split ? row_blocks : num_sms * per_sm / a.split;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(groups * a.split);
+    cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(kLinThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -357,15 +345,48 @@ static cudaError_t launch_t(LinearArgs a, int num_sms, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+template <int G, int NT, int RW>
+static cudaError_t launch_t(LinearArgs a, int num_sms, cudaStream_t s) {
+    constexpr int KW = kLinWarps / RW, B8 = NT * 8;
+    const int units = (a.K + kUnit - 1) / kUnit;
+    const int row_blocks = (a.N + 16 * RW - 1) / (16 * RW);
+    // split K over a cluster while that leaves every warp two units and the
+    // GPU is not yet full
+    a.split = 1;
+    while (a.split < 8 && row_blocks * a.split * 2 <= num_sms + num_sms / 4 && units / (a.split * 2) >= 2 * KW) a.split *= 2;
+    const int share = (units + a.split - 1) / a.split;
+    // all of the block's tokens if they fit, else two chunks that do
+    const int per_unit = a.B * kUnit * 2 + B8 * (kUnit / G) * 4;
+    constexpr int room = 96 * 1024;
+    if (share * per_unit <= room) {
+        a.chunk_units = share;
+        a.x_buffers = 1;
+    } else {
+        a.chunk_units = room / 2 / per_unit / KW * KW;
+        a.x_buffers = 2;
+    }
+    constexpr int XPAD = G == 32 ? 64 : 16;
+    const int xbytes = a.B * (a.chunk_units * kUnit * 2 + XPAD), gbytes = a.chunk_units * (kUnit / G) * B8 * 4;
+    const int red = KW > 1 || a.split > 1 ? RW * KW * B8 * 16 * 4 : 0;
+    const int rest = a.x_buffers * (xbytes + gbytes) + red;
+    // two blocks a SM if their rings fit with eight or four stages
+    constexpr int half = 113 * 1024;
+    const bool two8 = NT <= 2 && rest + ring_bytes(8) <= half, two4 = NT <= 2 && rest + ring_bytes(4) <= half;
+    const int per_sm = two8 || two4 ? 2 : 1;
+    const int groups = std::min(row_blocks, num_sms * per_sm / a.split);
+    if (two4 && !two8) return launch_s<G, NT, RW, 4>(a, groups * a.split, rest + ring_bytes(4), s);
+    return launch_s<G, NT, RW, 8>(a, groups * a.split, rest + ring_bytes(8), s);
+}
+
 template <int G>
 static cudaError_t launch_g(const LinearArgs &a, int num_sms, cudaStream_t s) {
-    if (a.B <= 8) return launch_t<G, 1, 1>(a, num_sms, s);
     if (a.B <= 16) return launch_t<G, 2, 8>(a, num_sms, s);
     if (a.B <= 32) return launch_t<G, 4, 8>(a, num_sms, s);
     return launch_t<G, 8, 8>(a, num_sms, s);
 }
 
 cudaError_t launch_linear(const LinearArgs &a, int num_sms, cudaStream_t s) {
+    if (a.B <= kFewTokens) return launch_linear_few(a, num_sms, s);
     if (a.G == 32) return launch_g<32>(a, num_sms, s);
     if (a.G == 64) return launch_g<64>(a, num_sms, s);
     return launch_g<128>(a, num_sms, s);

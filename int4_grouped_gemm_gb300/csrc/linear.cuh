@@ -11,6 +11,7 @@ namespace moe {
 
 constexpr int kLinearMaxB = 64;      // tokens of one call
 constexpr int kLinearMaxK = 32768;
+constexpr int kFewTokens = 8;        // up to here launch_linear_few
 
 struct LinearArgs {
     const uint32_t *q;         // [N][K/8]
@@ -33,6 +34,7 @@ struct LinearArgs {
     }
 };
 
+cudaError_t launch_linear_few(const LinearArgs &a, int num_sms, cudaStream_t s);
 cudaError_t launch_linear(const LinearArgs &a, int num_sms, cudaStream_t s);
 
 }  // namespace moe
