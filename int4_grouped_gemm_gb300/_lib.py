@@ -342,27 +342,46 @@ def gqa_decode_attention(q, k_cache, v_cache, L: int, scale: float, out, ws, per
 
 
 # ---------------------------------------------------- attention sub-layer
+#
+# These calls run in a microsecond or a few on the GPU, so their host side is
+# kept short: one query per tensor, and the stream handle straight from the
+# current device's.
 
 
-def check_device(what: str, *tensors):
-    """Every tensor on the current device (the library launches there)."""
+def current_device() -> int:
     import torch
-    cur = torch.cuda.current_device() if torch.cuda.is_available() else None
+    return torch._C._cuda_getDevice()
+
+
+def _stream_on(stream, device: int) -> int:
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(device)
+    return int(getattr(stream, "cuda_stream", stream))
+
+
+def check_device(what: str, *tensors) -> int:
+    """Every tensor on the current device (the library launches there); returns it."""
+    import torch
+    cur = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != cur):
+        if t is not None and t.get_device() != cur:
             raise ValueError(f"{what}: a tensor on {t.device}, the current device is cuda:{cur}")
+    return cur
 
 
 def _row(t) -> int:
     """Elements from one row of t to the next (a single row has no next: its own length)."""
-    return t.stride(0) if t.shape[0] > 1 else t[0].numel()
+    n = t.shape[0]
+    return t.stride(0) if n > 1 else t.numel()
 
 
 def int4_linear(w: moe_qweight, N: int, K: int, group: int, x, y, stream=None):
     """y [B, N] (bf16 or fp32) = x [B, K] (bf16) times the int4 matrix w [N, K] transposed, 1 <= B <= 64."""
-    import torch
-    _check(load().int4_linear(ctypes.byref(w), N, K, group, _ptr(x), _row(x), x.shape[0], _ptr(y), _row(y),
-                              int(y.dtype == torch.float32), _stream(stream)), "int4_linear")
+    rc = load().int4_linear(ctypes.byref(w), N, K, group, x.data_ptr(), _row(x), x.shape[0], y.data_ptr(), _row(y),
+                            y.element_size() == 4, _stream_on(stream, x.get_device()))
+    if rc:
+        raise MoEError(rc, "int4_linear")
 
 
 def gqa_append(cache: gqa_pages, q, k, v, seq, index, page_table, pos_offset: int, inv_freq, interleaved: bool, q_out,
@@ -370,11 +389,15 @@ def gqa_append(cache: gqa_pages, q, k, v, seq, index, page_table, pos_offset: in
     """q [T, Hq, D] or None, k, v [T, Hkv, D] bf16; seq, index [T], page_table [n_seq, ld] int32; inv_freq fp32
     [rot / 2] or None; q_out [T, Hq, D] or None; status: an int32-aligned device tensor or None."""
     n_seq, ld = page_table.shape
-    _check(load().gqa_append(ctypes.byref(cache), _ptr(q), 0 if q is None else _row(q), _ptr(k), _row(k),
-                             _ptr(v), _row(v), k.shape[0], 0 if q is None else q.shape[1], _ptr(seq), _ptr(index),
-                             _ptr(page_table), n_seq, ld, pos_offset, _ptr(inv_freq),
-                             0 if inv_freq is None else 2 * inv_freq.numel(), int(interleaved), _ptr(q_out),
-                             0 if q_out is None else _row(q_out), _ptr(status), _stream(stream)), "gqa_append")
+    rc = load().gqa_append(ctypes.byref(cache), None if q is None else q.data_ptr(), 0 if q is None else _row(q),
+                           k.data_ptr(), _row(k), v.data_ptr(), _row(v), k.shape[0], 0 if q is None else q.shape[1],
+                           seq.data_ptr(), index.data_ptr(), page_table.data_ptr(), n_seq, ld, pos_offset,
+                           None if inv_freq is None else inv_freq.data_ptr(),
+                           0 if inv_freq is None else 2 * inv_freq.shape[0], interleaved,
+                           None if q_out is None else q_out.data_ptr(), 0 if q_out is None else _row(q_out),
+                           None if status is None else status.data_ptr(), _stream_on(stream, k.get_device()))
+    if rc:
+        raise MoEError(rc, "gqa_append")
 
 
 def gqa_paged_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, prefix_len: int) -> int:
@@ -385,7 +408,10 @@ def gqa_paged_attention(cache: gqa_pages, q, prefix_pages, prefix_len: int, page
                         ws, stream=None):
     """q, out [B, Hq, D] bf16; prefix_pages int32 or None; page_table [B, ld], seq_len [B] int32."""
     B, Hq, _ = q.shape
-    _check(load().gqa_paged_attention(ctypes.byref(cache), _ptr(q), _row(q), B, Hq, _ptr(prefix_pages),
-                                      prefix_len, _ptr(page_table), page_table.shape[1], _ptr(seq_len), float(scale),
-                                      _ptr(out), _row(out), _ptr(ws), ws.numel() * ws.element_size(),
-                                      _stream(stream)), "gqa_paged_attention")
+    rc = load().gqa_paged_attention(ctypes.byref(cache), q.data_ptr(), _row(q), B, Hq,
+                                    None if prefix_pages is None else prefix_pages.data_ptr(), prefix_len,
+                                    page_table.data_ptr(), page_table.shape[1], seq_len.data_ptr(), scale,
+                                    out.data_ptr(), _row(out), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                    _stream_on(stream, q.get_device()))
+    if rc:
+        raise MoEError(rc, "gqa_paged_attention")

@@ -20,16 +20,20 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _heads(t: torch.Tensor, name: str, T: Optional[int], D: int):
+def _heads(t: torch.Tensor, name: str, T: int, heads: Optional[int], D: int):
     """[T, heads, D] bf16 whose rows are contiguous (rows themselves may be strided)."""
-    _need(t.dim() == 3 and t.dtype == torch.bfloat16 and t.shape[2] == D and (T is None or t.shape[0] == T),
-          f"{name}: [T, heads, {D}] in bf16")
-    _need(t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == D), f"{name}: the heads of a row must be contiguous")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or t.dtype != torch.bfloat16 or shape[0] != T or shape[2] != D or \
+            (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name}: [{T}, {'heads' if heads is None else heads}, {D}] in bf16")
+    if stride[2] != 1 or (shape[1] > 1 and stride[1] != D):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
 
 
-def _ints(t: torch.Tensor, name: str, *shape):
-    _need(t.dtype == torch.int32 and t.is_contiguous() and t.dim() == len(shape) and
-          all(n is None or n == m for n, m in zip(shape, t.shape)), f"{name}: int32 {list(shape)}, contiguous")
+def _ints(t: torch.Tensor, name: str, n: Optional[int], dims: int):
+    shape = t.shape
+    if t.dtype != torch.int32 or len(shape) != dims or (n is not None and shape[0] != n) or not t.is_contiguous():
+        raise ValueError(f"{name}: int32, contiguous, {dims} dimension(s)" + ("" if n is None else f", the first {n}"))
 
 
 class PagedCache:
@@ -62,23 +66,21 @@ class PagedCache:
         """Rotate q and k by position index + pos_offset, write k and v to
         position index[t] of sequence seq[t]; returns the rotated q."""
         T = k.shape[0]
-        _heads(k, "k", T, self.D)
-        _heads(v, "v", T, self.D)
-        _need(k.shape[1] == self.Hkv and v.shape[1] == self.Hkv, f"k, v: {self.Hkv} heads")
-        _ints(seq, "seq", T)
-        _ints(index, "index", T)
-        _ints(page_table, "page_table", None, None)
-        if inv_freq is not None:
-            _need(inv_freq.dtype == torch.float32 and inv_freq.dim() == 1 and inv_freq.is_contiguous(),
-                  "inv_freq: fp32 [rot / 2]")
+        _heads(k, "k", T, self.Hkv, self.D)
+        _heads(v, "v", T, self.Hkv, self.D)
+        _ints(seq, "seq", T, 1)
+        _ints(index, "index", T, 1)
+        _ints(page_table, "page_table", None, 2)
+        if inv_freq is not None and (inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or
+                                     not inv_freq.is_contiguous()):
+            raise ValueError("inv_freq: fp32 [rot / 2]")
         if q is None:
             _need(q_out is None, "q_out without q")
         else:
-            _heads(q, "q", T, self.D)
+            _heads(q, "q", T, None, self.D)
             if q_out is None:
                 q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            _heads(q_out, "q_out", T, self.D)
-            _need(q_out.shape == q.shape, "q_out: the shape of q")
+            _heads(q_out, "q_out", T, q.shape[1], self.D)
         _lib.check_device("append", self.k, q, k, v, seq, index, page_table, inv_freq, q_out)
         _lib.gqa_append(self.desc, q, k, v, seq, index, page_table, pos_offset, inv_freq, interleaved, q_out,
                         self.status, stream)
@@ -98,20 +100,19 @@ class PagedCache:
         """out [B, Hq, D]: row b's query attends to the shared prefix (read
         once for all rows), then to the first seq_len[b] positions of
         page_table[b].  scale: 1 / sqrt(D) unless given."""
-        B = q.shape[0]
-        _heads(q, "q", B, self.D)
-        _ints(page_table, "page_table", B, None)
-        _ints(seq_len, "seq_len", B)
+        B, Hq = q.shape[0], q.shape[1]
+        _heads(q, "q", B, None, self.D)
+        _ints(page_table, "page_table", B, 2)
+        _ints(seq_len, "seq_len", B, 1)
         if prefix_len:
             _need(prefix_pages is not None, "prefix_len without prefix_pages")
-            _ints(prefix_pages, "prefix_pages", None)
-            _need(prefix_len <= prefix_pages.numel() * self.page_size, "prefix_pages: too few for prefix_len")
+            _ints(prefix_pages, "prefix_pages", None, 1)
+            _need(prefix_len <= prefix_pages.shape[0] * self.page_size, "prefix_pages: too few for prefix_len")
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        _heads(out, "out", B, self.D)
-        _need(out.shape == q.shape, "out: the shape of q")
+        _heads(out, "out", B, Hq, self.D)
         if ws is None:
-            ws = self.workspace(B, q.shape[1], prefix_len)
+            ws = self.workspace(B, Hq, prefix_len)
         _lib.check_device("attend", self.k, q, page_table, seq_len, prefix_pages, out, ws)
         _lib.gqa_paged_attention(self.desc, q, prefix_pages if prefix_len else None, prefix_len, page_table, seq_len,
                                  1.0 / math.sqrt(self.D) if scale is None else scale, out, ws, stream)

@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kLinThreads, NT <= 2 ? 2 : 1) int4_linear_kern
 template <int G, int NT, int RW, int kLinStages>
 static cudaError_t launch_s(LinearArgs a, int blocks, int smem, cudaStream_t s) {
     auto kernel = int4_linear_kernel<G, NT, RW, kLinStages>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_smem<int4_linear_kernel<G, NT, RW, kLinStages>>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(blocks);

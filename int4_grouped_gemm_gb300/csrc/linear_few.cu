@@ -419,7 +419,7 @@ static cudaError_t launch_t(LinearArgs a, int num_sms, cudaStream_t s) {
     const int per_sm = smem <= kHalfSmem && WARPS == 8 ? 2 : 1;
     const int groups = std::min(row_blocks, std::max(1, num_sms * per_sm / a.split));
     auto kernel = linear_few_kernel<G, WARPS, RW>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_smem<linear_few_kernel<G, WARPS, RW>>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(groups * a.split);

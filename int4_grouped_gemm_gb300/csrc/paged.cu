@@ -14,51 +14,131 @@ __device__ __forceinline__ float2 angle_cs(int64_t pos, float f) {
     return r;
 }
 
-// One block per token: keys (and queries) rotated pair by pair, values copied.
-__global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
-    const int t = blockIdx.x;
-    const int seq = a.seq[t], idx = a.index[t];
-    if (seq < 0 || idx < 0) return;  // padding
-    const int ps = a.c.page_shift, D = a.c.D;
-    const bool in_table = seq < a.n_seq && (idx >> ps) < a.table_ld;
-    const int page = in_table ? a.table[static_cast<int64_t>(seq) * a.table_ld + (idx >> ps)] : -1;
-    if (page < 0 || page >= a.c.n_pages) {
-        if (threadIdx.x == 0) record_status(a.status, MOE_ERR_PAGE);
-        return;
+// A block takes a few tokens (one when there are few, so that every SM has a
+// share, up to eight).  First the tokens' places and their angles' cosines and
+// sines into shared memory, one per thread and pair, shared by all heads (the
+// fp64 products are what is dear there: the GPU's fp64 rate is 1/64 of its fp32
+// rate); then 16-byte pieces: of a rotated head the pair of pieces whose
+// elements turn into one another (halves: pieces j and j + rot / 16 of the
+// head; interleaved: a piece by itself), otherwise plain copies.  Bound by the
+// bytes: each is read and written once.
+constexpr int kAppendThreads = 256;
+constexpr int kAppendTokens = 8;
+
+__device__ __forceinline__ uint4 turn_piece(const uint4 &x, const float2 (&cs)[4]) {
+    // interleaved: (x0, x1) by cs[0], ...
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float a = __uint_as_float(w[j] << 16), b = __uint_as_float(w[j] & 0xFFFF0000u);
+        r[j] = bf162_as_u32(__floats2bfloat162_rn(a * cs[j].x - b * cs[j].y, b * cs[j].x + a * cs[j].y));
     }
-    const int64_t slot = page * a.c.page_stride + (idx & ((1 << ps) - 1)) * a.c.pos_stride;
-    const int Hq = a.q ? a.Hq : 0, half = D / 2;
-    for (int i = threadIdx.x; i < (Hq + a.c.Hkv) * half; i += blockDim.x) {
-        const int h = i / half, p = i % half;  // pair p of head h
-        const __nv_bfloat16 *src = h < Hq ? a.q + t * a.q_stride + h * D : a.k + t * a.k_stride + (h - Hq) * D;
-        __nv_bfloat16 *dst =
-            h < Hq ? a.q_out + t * a.qo_stride + h * D : a.c.k + slot + (h - Hq) * a.c.head_stride;
-        int i0 = 2 * p, i1 = 2 * p + 1;
-        const bool turn = p < a.rot / 2;
-        if (turn && !a.interleaved) {
-            i0 = p;
-            i1 = p + a.rot / 2;
-        }
-        const __nv_bfloat16 x0 = src[i0], x1 = src[i1];
-        if (turn) {
-            const float2 cs = angle_cs(static_cast<int64_t>(idx) + a.pos_offset, a.inv_freq[p]);
-            const float f0 = __bfloat162float(x0), f1 = __bfloat162float(x1);
-            dst[i0] = __float2bfloat16_rn(f0 * cs.x - f1 * cs.y);
-            dst[i1] = __float2bfloat16_rn(f1 * cs.x + f0 * cs.y);
-        } else {
-            dst[i0] = x0;
-            dst[i1] = x1;
-        }
-    }
-    for (int i = threadIdx.x; i < a.c.Hkv * D; i += blockDim.x) {
-        const int h = i / D, d = i % D;
-        a.c.v[slot + h * a.c.head_stride + d] = a.v[t * a.v_stride + i];
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+__device__ __forceinline__ void turn_halves(uint4 &x, uint4 &y, const float2 *cs) {
+    uint32_t *wx = reinterpret_cast<uint32_t *>(&x), *wy = reinterpret_cast<uint32_t *>(&y);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 c0 = cs[2 * j], c1 = cs[2 * j + 1];
+        const float a0 = __uint_as_float(wx[j] << 16), a1 = __uint_as_float(wx[j] & 0xFFFF0000u);
+        const float b0 = __uint_as_float(wy[j] << 16), b1 = __uint_as_float(wy[j] & 0xFFFF0000u);
+        wx[j] = bf162_as_u32(__floats2bfloat162_rn(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y));
+        wy[j] = bf162_as_u32(__floats2bfloat162_rn(b0 * c0.x + a0 * c0.y, b1 * c1.x + a1 * c1.y));
     }
 }
 
-cudaError_t launch_append(const AppendArgs &a, int, cudaStream_t s) {
-    append_kernel<<<a.T, 256, 0, s>>>(a);
-    return cudaGetLastError();
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs a, int per_block) {
+    constexpr int P = D / 8;  // 16-byte pieces of a head
+    __shared__ float2 s_cs[kAppendTokens][D / 2];
+    __shared__ int64_t s_slot[kAppendTokens];  // the token's place in the pools, -1: none
+    pdl_wait();
+    pdl_trigger();
+    const int tid = threadIdx.x;
+    const int t0 = blockIdx.x * per_block, nt = min(per_block, a.T - t0);
+    const int ps = a.c.page_shift, half = a.rot / 2;
+    if (tid < nt) {
+        const int seq = a.seq[t0 + tid], idx = a.index[t0 + tid];
+        int64_t slot = -1;
+        if (seq >= 0 && idx >= 0) {  // else padding
+            const bool in_table = seq < a.n_seq && (idx >> ps) < a.table_ld;
+            const int page = in_table ? a.table[static_cast<int64_t>(seq) * a.table_ld + (idx >> ps)] : -1;
+            if (page >= 0 && page < a.c.n_pages)
+                slot = page * a.c.page_stride + (idx & ((1 << ps) - 1)) * a.c.pos_stride;
+            else
+                record_status(a.status, MOE_ERR_PAGE);
+        }
+        s_slot[tid] = slot;
+    }
+    for (int i = tid; i < nt * half; i += kAppendThreads) {
+        const int t = i / half, p = i - t * half;
+        s_cs[t][p] = angle_cs(static_cast<int64_t>(a.index[t0 + t]) + a.pos_offset, a.inv_freq[p]);
+    }
+    __syncthreads();
+
+    // work items of a token: rotated heads (halves) HP = P / 2 pairs of pieces,
+    // else P pieces; queries, keys, then values (P plain pieces each, in pairs)
+    const int Hq = a.q ? a.Hq : 0, Hkv = a.c.Hkv;
+    constexpr int HP = P / 2;
+    const int per_token = (Hq + 2 * Hkv) * HP;
+    const int rp = a.rot / 16;  // pieces of a rotated half
+#pragma unroll 2
+    for (int i = tid; i < nt * per_token; i += kAppendThreads) {
+        const int t = i / per_token, r = i - t * per_token, h = r / HP, p = r % HP;
+        const int64_t slot = s_slot[t];
+        if (slot < 0) continue;
+        const __nv_bfloat16 *src;
+        __nv_bfloat16 *dst;
+        if (h < Hq) {
+            src = a.q + (t0 + t) * a.q_stride + h * D;
+            dst = a.q_out + (t0 + t) * a.qo_stride + h * D;
+        } else if (h < Hq + Hkv) {
+            src = a.k + (t0 + t) * a.k_stride + (h - Hq) * D;
+            dst = a.c.k + slot + (h - Hq) * a.c.head_stride;
+        } else {
+            src = a.v + (t0 + t) * a.v_stride + (h - Hq - Hkv) * D;
+            dst = a.c.v + slot + (h - Hq - Hkv) * a.c.head_stride;
+        }
+        // two pieces a thread: the pair of a rotation by halves, or neighbours
+        const bool rotated = h < Hq + Hkv;
+        int p0 = 2 * p, p1 = 2 * p + 1;
+        if (rotated && !a.interleaved) {
+            // pairs (j, j + rp) for j < rp, then the pieces that are not rotated:
+            // 2 rp, 2 rp + 1 and on, which 2 p, 2 p + 1 from p = rp on are
+            if (p < rp) {
+                p0 = p;
+                p1 = p + rp;
+            }
+        }
+        uint4 x = *reinterpret_cast<const uint4 *>(src + p0 * 8), y = *reinterpret_cast<const uint4 *>(src + p1 * 8);
+        if (rotated) {
+            if (!a.interleaved) {
+                if (p < rp) turn_halves(x, y, s_cs[t] + p * 8);
+            } else {
+                if (p0 * 8 < a.rot) {
+                    const float2 cs[4] = {s_cs[t][p0 * 4], s_cs[t][p0 * 4 + 1], s_cs[t][p0 * 4 + 2], s_cs[t][p0 * 4 + 3]};
+                    x = turn_piece(x, cs);
+                }
+                if (p1 * 8 < a.rot) {
+                    const float2 cs[4] = {s_cs[t][p1 * 4], s_cs[t][p1 * 4 + 1], s_cs[t][p1 * 4 + 2], s_cs[t][p1 * 4 + 3]};
+                    y = turn_piece(y, cs);
+                }
+            }
+        }
+        *reinterpret_cast<uint4 *>(dst + p0 * 8) = x;
+        *reinterpret_cast<uint4 *>(dst + p1 * 8) = y;
+    }
+}
+
+cudaError_t launch_append(const AppendArgs &a, int num_sms, cudaStream_t s) {
+    // as many tokens a block as leave every SM four blocks
+    int per = a.T / (4 * num_sms);
+    per = per < 1 ? 1 : per > kAppendTokens ? kAppendTokens : per;
+    const dim3 grid((a.T + per - 1) / per), block(kAppendThreads);
+    return a.c.D == 64 ? launch_dependent(append_kernel<64>, grid, block, 0, s, a, per)
+                       : launch_dependent(append_kernel<128>, grid, block, 0, s, a, per);
 }
 
 // ------------------------------------------------------------- attention
@@ -149,6 +229,10 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
     __shared__ int s_rows[kOwnWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g8 = lane >> 2, c = lane & 3;
+    // the first kernel of the call waits for what came before it; after a prefix
+    // kernel (which has waited) it need not wait for that one, and its blocks
+    // take over the SMs as that one's end
+    if (!a.prefix_ncta) pdl_wait();
     pdl_trigger();
     const int Hkv = a.c.Hkv, ps = a.c.page_shift;
     const int ntp = a.join ? tiles16(a.prefix_len) : 0;
@@ -466,6 +550,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
     __shared__ float4 s_acc[4][64];
     __shared__ float2 s_ml[4][64];
     pdl_wait();
+    pdl_trigger();
     const int Hkv = a.c.Hkv, D = a.c.D;
     const int b = blockIdx.x / Hkv, kv = blockIdx.x % Hkv;
     const int tid = threadIdx.x, h = tid & 7, dq = (tid >> 3) & 7, part = tid >> 6;
@@ -607,12 +692,9 @@ size_t paged_workspace_bytes(int B, int Hq, int Hkv, int D, int prefix_len, int 
 template <int D>
 static cudaError_t launch_own(const PagedArgs &a, cudaStream_t s) {
     constexpr int smem = own_smem_bytes(D);
-    cudaError_t e = cudaFuncSetAttribute(paged_own_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_smem<paged_own_kernel<D>>();
     if (e != cudaSuccess) return e;
-    // beside a prefix kernel its blocks take over the SMs as that one's end
-    if (a.prefix_ncta) return launch_dependent(paged_own_kernel<D>, dim3(a.ncta), dim3(kOwnThreads), smem, s, a);
-    paged_own_kernel<D><<<a.ncta, kOwnThreads, smem, s>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(paged_own_kernel<D>, dim3(a.ncta), dim3(kOwnThreads), smem, s, a);
 }
 
 cudaError_t launch_paged(PagedArgs &a, const CUtensorMap *maps, float scale, void *ws, int num_sms, cudaStream_t s) {

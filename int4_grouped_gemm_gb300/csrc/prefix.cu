@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s->tmem;
+    pdl_wait();
     pdl_trigger();
 
     // this block's piece of the list; item = (key-value head, block of rows)
@@ -622,10 +623,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
 template <int D>
 static cudaError_t launch_t(const CUtensorMap &k, const CUtensorMap &v, const PagedArgs &a, cudaStream_t s) {
     constexpr int smem = prefix_smem_bytes(D);
-    cudaError_t e = cudaFuncSetAttribute(prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_smem<prefix_kernel<D>>();
     if (e != cudaSuccess) return e;
-    prefix_kernel<D><<<a.prefix_ncta, kPrefixThreads, smem, s>>>(k, v, a);
-    return cudaGetLastError();
+    return launch_dependent(prefix_kernel<D>, dim3(a.prefix_ncta), dim3(kPrefixThreads), smem, s, k, v, a);
 }
 
 cudaError_t launch_prefix(const CUtensorMap &k, const CUtensorMap &v, const PagedArgs &a, cudaStream_t s) {

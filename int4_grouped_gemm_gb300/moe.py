@@ -53,18 +53,18 @@ def linear(w: QMatrix, x: torch.Tensor, y: Optional[torch.Tensor] = None, dtype=
     """y [B, N] = x [B, K] w^T for 1 to 64 tokens and one int4 matrix [N, K]
     (int4_linear); x bf16 with contiguous rows, y bf16 or fp32 (a new tensor of
     `dtype` unless given)."""
-    if w.q.dim() != 2 and w.q.numel() != w.rows * w.K // 8:
+    B, K = x.shape if x.dim() == 2 else (0, 0)
+    N = w.rows
+    if K != w.K or x.dtype != torch.bfloat16 or x.stride(1) != 1:
+        raise ValueError(f"linear: x [B, {w.K}] in bf16, its rows contiguous")
+    if w.q.numel() * 8 != N * K:
         raise ValueError("linear: one matrix [N, K], not a stack")
-    if x.dim() != 2 or x.shape[1] != w.K or x.dtype != torch.bfloat16:
-        raise ValueError(f"linear: x [B, {w.K}] in bf16")
     if y is None:
-        y = torch.empty(x.shape[0], w.rows, dtype=dtype, device=x.device)
-    if y.shape != (x.shape[0], w.rows) or y.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"linear: y [B, {w.rows}] in bf16 or fp32")
-    if x.stride(1) != 1 or (y.shape[1] > 1 and y.stride(1) != 1):
-        raise ValueError("linear: rows of x and y must be contiguous")
+        y = torch.empty(B, N, dtype=dtype, device=x.device)
+    if y.shape != (B, N) or y.dtype not in (torch.bfloat16, torch.float32) or (N > 1 and y.stride(1) != 1):
+        raise ValueError(f"linear: y [B, {N}] in bf16 or fp32, its rows contiguous")
     _lib.check_device("linear", x, y, w.q)
-    _lib.int4_linear(w.as_c(), w.rows, w.K, w.group, x, y, stream)
+    _lib.int4_linear(w.as_c(), N, K, w.group, x, y, stream)
     return y
 
 
