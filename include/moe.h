@@ -480,11 +480,13 @@ int gqa_decode_attention_per_head(const void *q, const void *k_cache, const void
  * written as fp32 (y_fp32 = 1).  x: [B] rows of K bf16, row stride x_stride
  * (>= K); y: [B] rows of N, row stride y_stride (>= N, any).  y must not
  * overlap x.  N >= 1, group in {32, 64, 128}, K % group == 0, K <= 32768 (else
- * MOE_ERR_SHAPE); B outside 1..64 is MOE_ERR_TOKENS.  No workspace: calls on
- * several streams do not meet.
+ * MOE_ERR_SHAPE); x_stride below 2^39; B outside 1..64 is MOE_ERR_TOKENS.  No
+ * workspace: calls on several streams do not meet.  status: where a device-side
+ * wait that ran out is recorded (the first word of a workspace or any zeroed
+ * int32), or NULL.
  */
 int int4_linear(const moe_qweight *w, int32_t N, int32_t K, int32_t group, const void *x, int64_t x_stride, int32_t B,
-                void *y, int64_t y_stride, int32_t y_fp32, cudaStream_t stream);
+                void *y, int64_t y_stride, int32_t y_fp32, int32_t *status, cudaStream_t stream);
 
 /*
  * A paged key-value cache: two pools of n_pages pages, element (page, head,

@@ -101,7 +101,7 @@ SIGNATURES = {
                                             c_p, c_sz, c_p]),
     "gqa_decode_attention_per_head": (ctypes.c_int, [c_p, c_p, c_p, c_i32, c_i32, c_i32, c_i32, c_i32,
                                                      ctypes.c_float, c_p, c_p, c_sz, c_p]),
-    "int4_linear": (ctypes.c_int, [c_p, c_i32, c_i32, c_i32, c_p, c_i64, c_i32, c_p, c_i64, c_i32, c_p]),
+    "int4_linear": (ctypes.c_int, [c_p, c_i32, c_i32, c_i32, c_p, c_i64, c_i32, c_p, c_i64, c_i32, c_p, c_p]),
     "gqa_append": (ctypes.c_int, [c_p, c_p, c_i64, c_p, c_i64, c_p, c_i64, c_i32, c_i32, c_p, c_p, c_p, c_i32, c_i32,
                                   c_i32, c_p, c_i32, c_i32, c_p, c_i64, c_p, c_p]),
     "gqa_paged_workspace_bytes": (c_sz, [c_i32, c_i32, c_i32, c_i32, c_i32]),
@@ -376,10 +376,11 @@ def _row(t) -> int:
     return t.stride(0) if n > 1 else t.numel()
 
 
-def int4_linear(w: moe_qweight, N: int, K: int, group: int, x, y, stream=None):
+def int4_linear(w: moe_qweight, N: int, K: int, group: int, x, y, status=None, stream=None):
     """y [B, N] (bf16 or fp32) = x [B, K] (bf16) times the int4 matrix w [N, K] transposed, 1 <= B <= 64."""
     rc = load().int4_linear(ctypes.byref(w), N, K, group, x.data_ptr(), _row(x), x.shape[0], y.data_ptr(), _row(y),
-                            y.element_size() == 4, _stream_on(stream, x.get_device()))
+                            y.element_size() == 4, None if status is None else status.data_ptr(),
+                            _stream_on(stream, x.get_device()))
     if rc:
         raise MoEError(rc, "int4_linear")
 

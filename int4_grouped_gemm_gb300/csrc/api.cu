@@ -53,9 +53,10 @@ static int current_device(DeviceInfo *&info) {
 }
 
 static int encode_2d(CUtensorMap *map, CUtensorMapDataType type, int elem_bytes, const void *ptr, uint64_t inner,
-                     uint64_t outer, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz) {
+                     uint64_t outer, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz,
+                     uint64_t pitch = 0) {  // elements from row to row (0: contiguous rows)
     cuuint64_t dims[2] = {inner, outer};
-    cuuint64_t strides[1] = {inner * static_cast<uint64_t>(elem_bytes)};
+    cuuint64_t strides[1] = {(pitch ? pitch : inner) * static_cast<uint64_t>(elem_bytes)};
     cuuint32_t box[2] = {box_inner, box_outer};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = g_encode(map, type, 2, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -775,7 +776,7 @@ int gqa_decode_attention_per_head(const void *q, const void *k_cache, const void
 // ------------------------------------------------ attention sub-layer
 
 int int4_linear(const moe_qweight *w, int32_t N, int32_t K, int32_t group, const void *x, int64_t x_stride, int32_t B,
-                void *y, int64_t y_stride, int32_t y_fp32, cudaStream_t stream) {
+                void *y, int64_t y_stride, int32_t y_fp32, int32_t *status, cudaStream_t stream) {
     if (!w) return MOE_ERR_NULL;
     int rc;
     if ((rc = check_ptr(w->q)) || (rc = check_ptr(w->scale)) || (rc = check_ptr(w->bias)) || (rc = check_ptr(x)) ||
@@ -783,8 +784,9 @@ int int4_linear(const moe_qweight *w, int32_t N, int32_t K, int32_t group, const
         return rc;
     if (group != 32 && group != 64 && group != 128) return MOE_ERR_SHAPE;
     if (N < 1 || K < group || K > kLinearMaxK || K % group != 0) return MOE_ERR_SHAPE;
-    if (x_stride < K || x_stride % 8 != 0 || y_stride < N || (y_fp32 != 0 && y_fp32 != 1)) return MOE_ERR_SHAPE;
+    if (x_stride < K || x_stride % 8 != 0 || x_stride >= (int64_t(1) << 39) || y_stride < N || (y_fp32 != 0 && y_fp32 != 1)) return MOE_ERR_SHAPE;
     if (B < 1 || B > kLinearMaxB) return MOE_ERR_TOKENS;
+    if (status && (reinterpret_cast<uintptr_t>(status) & 3u)) return MOE_ERR_ALIGN;
     DeviceInfo *dev = nullptr;
     if ((rc = current_device(dev))) return rc;
     LinearArgs a{};
@@ -801,7 +803,18 @@ int int4_linear(const moe_qweight *w, int32_t N, int32_t K, int32_t group, const
     a.ldg = ld_groups(K, group);
     a.B = B;
     a.y_fp32 = y_fp32;
-    return cuda_rc(launch_linear(a, dev->num_sms, stream));
+    a.status = status;
+    a.wait_limit = g_wait_limit;
+    if (B <= kFewTokens) return cuda_rc(launch_linear_few(a, dev->num_sms, stream));
+    CUtensorMap maps[4];
+    const auto SW0 = CU_TENSOR_MAP_SWIZZLE_NONE;
+    if ((rc = encode_2d(&maps[0], CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, w->q, K / 8, N, 16, 128, CU_TENSOR_MAP_SWIZZLE_64B)) ||
+        (rc = encode_2d(&maps[1], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->scale, a.ldg, N, 8, 128, SW0)) ||
+        (rc = encode_2d(&maps[2], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->bias, a.ldg, N, 8, 128, SW0)) ||
+        (rc = encode_2d(&maps[3], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, K, B, 64, linear_token_rows(B),
+                        CU_TENSOR_MAP_SWIZZLE_128B, x_stride)))
+        return rc;
+    return cuda_rc(launch_linear_many(maps, a, dev->num_sms, stream));
 }
 
 // int32 and fp32 arrays of the paged calls: element-aligned, so that slices of

@@ -21,9 +21,11 @@ struct LinearArgs {
     int64_t x_stride, y_stride;
     int N, K, G, ldg, B;
     int y_fp32;
-    // filled in by launch_linear: blocks of a cluster (they split K), units of
-    // 128 k in a chunk of tokens, buffers for chunks
-    int split, chunk_units, x_buffers;
+    int *status;               // may be NULL
+    long long wait_limit;
+    // filled in by the launches: blocks of a cluster (they share K); few tokens:
+    // units of k in a chunk of tokens
+    int split, chunk_units;
 
     __device__ __forceinline__ int rank_of(int block) const { return block % split; }
     __device__ __forceinline__ void store(int t, int n, float v) const {
@@ -34,7 +36,12 @@ struct LinearArgs {
     }
 };
 
+// 1 to 8 tokens.
 cudaError_t launch_linear_few(const LinearArgs &a, int num_sms, cudaStream_t s);
-cudaError_t launch_linear(const LinearArgs &a, int num_sms, cudaStream_t s);
+// 9 to 64 tokens; maps: codes (u32, boxes of 16 x 128 rows, 64-byte swizzle),
+// scales, biases (u16, 8 x 128 rows), tokens (bf16, 64 x linear_token_rows(B),
+// 128-byte swizzle).
+int linear_token_rows(int B);
+cudaError_t launch_linear_many(const CUtensorMap *maps, const LinearArgs &a, int num_sms, cudaStream_t s);
 
 }  // namespace moe

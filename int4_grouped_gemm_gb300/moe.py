@@ -49,10 +49,11 @@ def pack_matrix(w: torch.Tensor, group: int, stream=None) -> QMatrix:
 
 
 def linear(w: QMatrix, x: torch.Tensor, y: Optional[torch.Tensor] = None, dtype=torch.bfloat16,
-           stream=None) -> torch.Tensor:
+           status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y [B, N] = x [B, K] w^T for 1 to 64 tokens and one int4 matrix [N, K]
     (int4_linear); x bf16 with contiguous rows, y bf16 or fp32 (a new tensor of
-    `dtype` unless given)."""
+    `dtype` unless given).  status: a zeroed int32 device tensor that records a
+    device-side wait that ran out (moe_read_device_status), or None."""
     B, K = x.shape if x.dim() == 2 else (0, 0)
     N = w.rows
     if K != w.K or x.dtype != torch.bfloat16 or x.stride(1) != 1:
@@ -64,7 +65,7 @@ def linear(w: QMatrix, x: torch.Tensor, y: Optional[torch.Tensor] = None, dtype=
     if y.shape != (B, N) or y.dtype not in (torch.bfloat16, torch.float32) or (N > 1 and y.stride(1) != 1):
         raise ValueError(f"linear: y [B, {N}] in bf16 or fp32, its rows contiguous")
     _lib.check_device("linear", x, y, w.q)
-    _lib.int4_linear(w.as_c(), N, K, w.group, x, y, stream)
+    _lib.int4_linear(w.as_c(), N, K, w.group, x, y, status, stream)
     return y
 
 

@@ -18,16 +18,18 @@ def test_linear_refusals(lib):
     from int4_grouped_gemm_gb300 import _lib
     w = _lib.moe_qweight(256, 512, 768)
 
-    def call(w=w, N=64, K=128, group=64, x=P(1024), xs=128, B=4, y=P(2048), ys=64, fp32=0):
-        return lib.int4_linear(None if w is None else ctypes.byref(w), N, K, group, x, xs, B, y, ys, fp32, None)
+    def call(w=w, N=64, K=128, group=64, x=P(1024), xs=128, B=4, y=P(2048), ys=64, fp32=0, status=None):
+        return lib.int4_linear(None if w is None else ctypes.byref(w), N, K, group, x, xs, B, y, ys, fp32, status, None)
 
     assert call(w=None) == _lib.MOE_ERR_NULL
     assert call(w=_lib.moe_qweight(256, 0, 768)) == _lib.MOE_ERR_NULL
     assert call(w=_lib.moe_qweight(256, 520, 768)) == _lib.MOE_ERR_ALIGN
     assert call(x=None) == _lib.MOE_ERR_NULL
     assert call(y=P(2056)) == _lib.MOE_ERR_ALIGN
+    assert call(status=P(6)) == _lib.MOE_ERR_ALIGN
     for bad in (dict(group=16), dict(group=48), dict(K=96), dict(K=0), dict(K=32832, xs=32832), dict(N=0), dict(N=-5),
-                dict(xs=127), dict(xs=129), dict(xs=120), dict(ys=63), dict(fp32=2)):
+                dict(xs=127), dict(xs=129), dict(xs=120), dict(ys=63), dict(fp32=2),
+                dict(xs=1 << 39)):
         assert call(**bad) == _lib.MOE_ERR_SHAPE, bad
     for B in (0, -1, 65):
         assert call(B=B) == _lib.MOE_ERR_TOKENS
