@@ -6,20 +6,23 @@
 // tcgen05.mma, the tokens as they are the N side, and each group of weights
 // has a sum of its own, D = sum (128 + q) x; then, in fp32 registers,
 //   y += s D + (z - 128 s) X,   X = sum of the group's x
-// X comes out of the same MMA: the last of the 128 rows of a tile is not a
-// weight row but ones, so that a tile has 127 weight rows and D's row 127 is X.
-// The codes go straight into tensor memory, where the MMA reads its first
-// operand from: a thread unpacks one row's 64 codes in registers and stores
-// them to its lane.  What is in shared memory is only what TMA brings: packed
-// codes, scales, and tokens.
+// X comes out of the same MMA: the last of each 32 rows of a tile is not a
+// weight row but ones, so that a tile has 4 x 31 weight rows and the last lane of
+// every epilogue warp finds X in its row of D.  The codes go straight into tensor
+// memory, where the MMA reads its first operand from: a thread unpacks one row's
+// 128 codes in registers and stores them to its lane.  What is in shared memory
+// is only what TMA brings: packed codes, scales, and tokens.
 //
-//   warps 0-7    epilogue, warp w: rows 32 (w % 4) .., token half w / 4: D from
+//   epilogue     warps 0-7, warp w: rows 32 (w % 4) .., token half w / 4: D from
 //                tensor memory, y in registers
-//   warps 8-11   unpacking, a thread per row
-//   warp 12      TMA loads
-//   warp 13      MMA issue
+//   unpacking    warps 8-15, a thread per row, two sets of four in turn
+//   loads, MMA   warps 16 and 17 (18 and 19 complete the warpgroup)
 //
-// Blocks take tiles of 127 rows in turn.  If there are too few tiles for the
+// A barrier wait costs its role about 130 cycles however early the other side
+// was, so the steps are 128 k with one wait of each kind (steps of 64 k with a
+// separate barrier for X took 1,200 cycles each: 136 us for 64 x 2048 x 131072).
+//
+// Blocks take tiles of 124 rows in turn.  If there are too few tiles for the
 // GPU, a cluster of up to four blocks shares K and adds up through distributed
 // shared memory.  Every wait is bounded.
 #include <algorithm>
@@ -29,25 +32,32 @@
 namespace moe {
 namespace many {
 
-constexpr int kRows = 127;                 // weight rows of a tile
-constexpr int kEpiWarps = 8, kDeqWarp = 8, kTmaWarp = 12, kMmaWarp = 13, kThreads = 14 * 32;
-constexpr int kUnit = 128;                 // k of a stage of codes
-constexpr int kW = 6, kX = 8, kS = 3;      // stages: codes (128 k), tokens (64 k), scales (8 groups)
-constexpr int kA = 4, kD = 4;              // buffers in tensor memory: codes (64 k, 32 columns), group sums
+constexpr int kRows = 124;                 // weight rows of a tile: 31 in each 32 lanes
+constexpr int kEpiWarps = 8, kDeqWarp = 8, kTmaWarp = 16, kMmaWarp = 17, kThreads = 20 * 32;
+// Registers a thread: an epilogue thread of 64 tokens holds 32 sums and 32 of
+// D.  The launch gives 96 to each of the 640 threads (61,440 in all); epilogue,
+// unpacking and the rest then hold 128, 72 and 80 (32,768 + 18,432 + 10,240).
+constexpr int kLaunchRegs = 96, kEpiRegs = 128, kDeqRegs = 72, kRestRegs = 80;
+static_assert(256 * kEpiRegs + 256 * kDeqRegs + 128 * kRestRegs <= kThreads * kLaunchRegs, "shares of the launch's registers");
+constexpr int kUnit = 128;                 // k of a step
+constexpr int kW = 6, kS = 3;              // stages: codes, scales (8 groups)
+constexpr int kX = 6, kA = 3;              // stages: tokens in shared memory, codes in tensor memory (64 columns)
+constexpr int kD = 2;                      // buffers of group sums, two groups each (128 columns)
 constexpr int kWBytes = 128 * kUnit / 2, kSBytes = 128 * 8 * 2;
-constexpr uint32_t kTmemCols = 512;        // kD * 64 + kA * 32 = 384, rounded up
+constexpr uint32_t kTmemCols = 512;        // kD * 128 + kA * 64 = 448, rounded up
 
-__host__ __device__ constexpr int x_bytes(int tok) { return tok * 128; }
+__host__ __device__ constexpr int x_bytes(int tok) { return 2 * tok * 128; }  // two boxes of 64 k
 
 struct Ctl {
-    uint64_t w_full[kW], w_empty[kW], x_full[kX], x_empty[kX], s_full[kS], s_empty[kS];
-    uint64_t a_full[kA], a_empty[kA], d_full[kD], d_empty[kD];
-    uint64_t sum_full[2][kD];              // X of the token half is in shared memory
+    uint64_t w_full[kW], w_empty[kW], x_full[kX], s_full[kS], s_empty[kS];
+    uint64_t a_full[kA], used[kX];         // codes are in tensor memory; the step's MMAs are complete
+    uint64_t d_full[kD], d_empty[kD];
     uint64_t drain;
-    alignas(16) float sums[kD][64];        // X
+    alignas(16) float sums[kEpiWarps][32]; // X, each warp's own
     uint32_t tmem;
     int abort;
 };
+static_assert(offsetof(Ctl, sums) % 16 == 0, "X is read in 16-byte pieces");
 
 // More than half of a SM's: one block at a time, since each takes all of the
 // tensor memory.
@@ -57,7 +67,6 @@ __host__ __device__ constexpr int smem_bytes(int tok) {
     return n > least ? n : least;
 }
 static_assert(smem_bytes(64) <= kBlockSmem, "one block per SM");
-static_assert(offsetof(Ctl, sums) % 16 == 0, "X is read in 16-byte pieces");
 
 struct Maps {
     CUtensorMap q, s, b, x;
@@ -81,6 +90,20 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const 
     return __all_sync(0xffffffffu, wait(bar, parity, a, s, site));
 }
 
+// Shared memory by its own address: through a plain pointer these become generic
+// accesses, with several times the latency.
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t at, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+
 // (w & mask) | set in one instruction
 __device__ __forceinline__ uint32_t mask_set(uint32_t w, uint32_t mask, uint32_t set) {
     uint32_t r;
@@ -101,6 +124,21 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// N columns of this warp's lanes; the registers are valid after tmem_wait.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t *r) {
+    if constexpr (N == 32)
+        tmem_ld32(at, r);
+    else if constexpr (N == 16)
+        tmem_ld16_now(at, r);
+    else
+        tmem_ld8_now(at, r);
+}
+template <int N>
+__device__ __forceinline__ void tmem_wait(uint32_t *r) {
+    if constexpr (N == 32) tmem_wait32(r);
+}
+
 // A ring position: stage and phase parity.
 template <int N>
 struct Ring {
@@ -117,11 +155,12 @@ template <int G, int TOK>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_many_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LinearArgs a) {
     constexpr int TW = TOK / 2;                        // tokens of an epilogue warp
-    constexpr int HG = G == 32 ? 2 : 1;                // groups that end in a 64-k half (128: one in two halves)
+    constexpr int GU = kUnit / G;                      // groups of a step
+    constexpr int DG = GU < 2 ? GU : 2, DU = GU / DG;  // groups of a buffer of sums, buffers of a step
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sX = base, *sW = sX + kX * x_bytes(TOK), *sS = sW + kW * kWBytes;
-    float *red = reinterpret_cast<float *>(sS + kS * 2 * kSBytes);  // [token][128 rows]
+    float *red = reinterpret_cast<float *>(sS + kS * 2 * kSBytes);  // [token][128 lanes]
     Ctl *s = reinterpret_cast<Ctl *>(red + TOK * 128);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -129,23 +168,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&s->w_full[i], 1);
             mbar_init(&s->w_empty[i], 4);
         }
-        for (int i = 0; i < kX; ++i) {
-            mbar_init(&s->x_full[i], 1);
-            mbar_init(&s->x_empty[i], 1);
-        }
         for (int i = 0; i < kS; ++i) {
             mbar_init(&s->s_full[i], 1);
             mbar_init(&s->s_empty[i], kEpiWarps);
         }
-        for (int i = 0; i < kA; ++i) {
-            mbar_init(&s->a_full[i], 4);
-            mbar_init(&s->a_empty[i], 1);
+        for (int i = 0; i < kX; ++i) {
+            mbar_init(&s->x_full[i], 1);
+            mbar_init(&s->used[i], 1);
         }
+        for (int i = 0; i < kA; ++i) mbar_init(&s->a_full[i], 4);
         for (int i = 0; i < kD; ++i) {
             mbar_init(&s->d_full[i], 1);
             mbar_init(&s->d_empty[i], kEpiWarps);
-            mbar_init(&s->sum_full[0][i], 1);
-            mbar_init(&s->sum_full[1][i], 1);
         }
         mbar_init(&s->drain, 1);
         s->abort = 0;
@@ -165,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s->tmem;                     // group sums, then codes
-    const uint32_t tA = tmem + kD * 64;
+    const uint32_t tA = tmem + kD * 128;
     pdl_wait();
     pdl_trigger();
 
@@ -174,17 +208,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tiles = (a.N + kRows - 1) / kRows, step = gridDim.x / a.split;
     const int first = blockIdx.x / a.split;
 
+    if (warp >= kTmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
     if (warp == kTmaWarp) {
         if (lane == 0) {
             Ring<kW> w;
             Ring<kX> x;
             Ring<kS> sc;
-            uint32_t n_w = 0, n_x = 0, n_s = 0;
+            uint32_t n_w = 0, n_s = 0;
             bool ok = true;
             for (int tile = first; tile < tiles && ok; tile += step) {
                 int block = -1;
                 for (int u = u0; u < u1 && ok; ++u) {
-                    const int need = u * (kUnit / 32) * 32 / G / 8;  // block of 8 groups that the unit's lie in
+                    const int need = u * GU / 8;       // block of 8 groups that the unit's lie in
                     if (need != block) {
                         block = need;
                         ok = wait(&s->s_empty[sc.i], sc.ph ^ 1, a, s, 40);
@@ -202,17 +238,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_2d(sW + w.i * kWBytes, &maps.q, &s->w_full[w.i], u * (kUnit / 8), tile * kRows);
                     w.next();
                     ++n_w;
-                    for (int h = 0; h < 2 && ok; ++h) {
-                        ok = wait(&s->x_empty[x.i], x.ph ^ 1, a, s, 42);
-                        if (!ok) break;
-                        mbar_arrive_expect_tx(&s->x_full[x.i], x_bytes(TOK));
-                        tma_load_2d(sX + x.i * x_bytes(TOK), &maps.x, &s->x_full[x.i], u * kUnit + h * 64, 0);
-                        x.next();
-                        ++n_x;
-                    }
+                    ok = wait(&s->used[x.i], x.ph ^ 1, a, s, 42);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&s->x_full[x.i], x_bytes(TOK));
+                    tma_load_2d(sX + x.i * x_bytes(TOK), &maps.x, &s->x_full[x.i], u * kUnit, 0);
+                    tma_load_2d(sX + x.i * x_bytes(TOK) + TOK * 128, &maps.x, &s->x_full[x.i], u * kUnit + 64, 0);
+                    x.next();
                 }
             }
-            // no copy of this block is in flight when it ends
+            // no copy of this block is in flight when it ends (one token stage per
+            // code stage, but for the last one after a timeout)
+            const uint32_t n_x = ok ? n_w : n_w > 0 ? n_w - 1 : 0;
             for (uint32_t i = n_w > kW ? n_w - kW : 0; i < n_w; ++i) mbar_wait(&s->w_full[i % kW], (i / kW) & 1, a.wait_limit);
             for (uint32_t i = n_x > kX ? n_x - kX : 0; i < n_x; ++i) mbar_wait(&s->x_full[i % kX], (i / kX) & 1, a.wait_limit);
             for (uint32_t i = n_s > kS ? n_s - kS : 0; i < n_s; ++i) mbar_wait(&s->s_full[i % kS], (i / kS) & 1, a.wait_limit);
@@ -226,32 +262,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             Ring<kD> db;
             bool ok = true;
             for (int tile = first; tile < tiles && ok; tile += step) {
-                for (int h = 2 * u0; h < 2 * u1 && ok; ++h) {  // 64 k each
+                for (int u = u0; u < u1 && ok; ++u) {
                     ok = wait(&s->x_full[x.i], x.ph, a, s, 43) && wait(&s->a_full[ab.i], ab.ph, a, s, 44);
                     if (!ok) break;
-                    const uint32_t xa = smem_u32(sX + x.i * x_bytes(TOK)), at = tA + ab.i * 32;
+                    const uint32_t xa = smem_u32(sX + x.i * x_bytes(TOK)), at = tA + ab.i * 64;
 #pragma unroll
-                    for (int g = 0; g < HG; ++g) {
-                        if (G < 128 || (h & 1) == 0) {
-                            ok = wait(&s->d_empty[db.i], db.ph ^ 1, a, s, 45);
-                            if (!ok) break;
-                        }
+                    for (int du = 0; du < DU; ++du) {
+                        ok = wait(&s->d_empty[db.i], db.ph ^ 1, a, s, 45);
+                        if (!ok) break;
                         tc_fence_after();
-                        const uint32_t dt = tmem + db.i * 64;
+                        const uint32_t dt = tmem + db.i * 128;
 #pragma unroll
-                        for (int kk = g * (4 / HG); kk < (g + 1) * (4 / HG); ++kk)
-                            umma_bf16_ts(dt, at + kk * 8, sdesc_k128(xa + kk * 32), idesc,
-                                         kk != g * (4 / HG) || (G == 128 && (h & 1)));
-                        if (G < 128 || (h & 1)) {
-                            umma_commit(&s->d_full[db.i]);
-                            db.next();
+                        for (int i = 0; i < 8 / DU; ++i) {
+                            const int kk = du * (8 / DU) + i, g = i / (8 / DU / DG);  // 16 k, group of the buffer
+                            umma_bf16_ts(dt + g * 64, at + kk * 8, sdesc_k128(xa + (kk / 4) * (TOK * 128) + (kk % 4) * 32),
+                                         idesc, i % (8 / DU / DG) != 0);
                         }
+                        umma_commit(&s->d_full[db.i]);
+                        db.next();
                     }
                     if (!ok) break;
-                    umma_commit(&s->a_empty[ab.i]);
-                    umma_commit(&s->x_empty[x.i]);
-                    ab.next();
+                    umma_commit(&s->used[x.i]);
                     x.next();
+                    ab.next();
                 }
             }
             // every MMA issued here is complete before tensor memory is freed
@@ -259,51 +292,64 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait(&s->drain, 0, a.wait_limit);
         }
         __syncwarp();
+    }
     } else if (warp >= kDeqWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDeqRegs));
         // ------------------------------------------------------- unpacking
-        const int r = (warp & 3) * 32 + lane;
-        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        // the two sets of four warps take the steps in turn
+        const int quarter = warp & 3, set_of = (warp - kDeqWarp) >> 2;
+        const int r = quarter * 31 + min(lane, 30);    // row of the tile
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const int rot = (r >> 1) & 3;                  // 64-byte swizzle of the row's 16-byte pieces
-        // (w & mask) | set: 128 + q as a bf16 pair, or ones in the last row
-        const uint32_t mask = r == kRows ? 0u : 0x000F000Fu, set = r == kRows ? 0x3F803F80u : 0x43004300u;
-        Ring<kW> w;
-        Ring<kA> ab;
+        const uint32_t w_addr = smem_u32(sW);
+        // (w & mask) | set: 128 + q as a bf16 pair, or ones in the last lane
+        const uint32_t mask = lane == 31 ? 0u : 0x000F000Fu, set = lane == 31 ? 0x3F803F80u : 0x43004300u;
+        uint32_t n = 0;                                // steps of the block so far
         bool ok = true;
         for (int tile = first; tile < tiles && ok; tile += step) {
-            for (int u = u0; u < u1 && ok; ++u) {
-                ok = warp_wait(&s->w_full[w.i], w.ph, a, s, 46);
+            for (int u = u0; u < u1; ++u, ++n) {
+                if (static_cast<int>(n & 1) != set_of) continue;
+                const uint32_t ws = n % kW, as = n % kA;
+                ok = warp_wait(&s->w_full[ws], (n / kW) & 1, a, s, 46);
                 if (!ok) break;
-                const uint8_t *row = sW + w.i * kWBytes + r * 64;
+                const uint32_t row = w_addr + ws * kWBytes + r * 64;
+                uint4 v[4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint4 v0 = *reinterpret_cast<const uint4 *>(row + (((2 * h) ^ rot) << 4));
-                    const uint4 v1 = *reinterpret_cast<const uint4 *>(row + (((2 * h + 1) ^ rot) << 4));
-                    const uint32_t q[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-                    uint32_t p[32];
+                for (int i = 0; i < 4; ++i) v[i] = lds128(row + ((i ^ rot) << 4));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s->w_empty[ws]);
+                bool free = false;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    uint32_t p[16];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) p[4 * i + j] = mask_set(q[i] >> (4 * j), mask, set);
-                    ok = warp_wait(&s->a_empty[ab.i], ab.ph ^ 1, a, s, 47);
-                    if (!ok) break;
-                    tc_fence_after();
-                    tmem_st16((tA + ab.i * 32) | lanes, p);
-                    tmem_st16((tA + ab.i * 32 + 16) | lanes, p + 16);
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&s->a_full[ab.i]);
-                    ab.next();
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) p[4 * e + j] = mask_set(q[e] >> (4 * j), mask, set);
+                    if (!free) {
+                        // the MMAs of the step that had this buffer before
+                        if (n >= kA) ok = warp_wait(&s->used[(n - kA) % kX], ((n - kA) / kX) & 1, a, s, 47);
+                        if (!ok) break;
+                        free = true;
+                        tc_fence_after();
+                    }
+                    tmem_st16((tA + as * 64 + i * 16) | lanes, p);
                 }
                 if (!ok) break;
-                if (lane == 0) mbar_arrive(&s->w_empty[w.i]);
-                w.next();
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s->a_full[as]);
             }
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
         // -------------------------------------------------------- epilogue
-        const int half = warp >> 2, r = (warp & 3) * 32 + lane;
-        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const int half = warp >> 2, quarter = warp & 3;
+        const int r = quarter * 31 + min(lane, 30);    // row of the tile (the last lane: X)
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t sums = smem_u32(s->sums[warp]), s_addr = smem_u32(sS) + r * 16;
         Ring<kS> sc;
         Ring<kD> db;
         bool ok = true;
@@ -313,16 +359,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < TW / 2; ++i) y[i] = 0;
             int block = -1;
             uint4 sv = make_uint4(0u, 0u, 0u, 0u), bv = sv;
-            const int g0 = u0 * kUnit / G, g1 = u1 * kUnit / G;
-            for (int g = g0; g < g1 && ok; ++g) {
+            for (int g = u0 * GU; g < u1 * GU && ok; g += DG) {
                 if (g / 8 != block) {
                     // the row's scales and biases of eight groups
                     block = g / 8;
                     ok = warp_wait(&s->s_full[sc.i], sc.ph, a, s, 48);
                     if (!ok) break;
-                    const uint8_t *src = sS + sc.i * 2 * kSBytes + r * 16;
-                    sv = *reinterpret_cast<const uint4 *>(src);
-                    bv = *reinterpret_cast<const uint4 *>(src + kSBytes);
+                    sv = lds128(s_addr + sc.i * 2 * kSBytes);
+                    bv = lds128(s_addr + sc.i * 2 * kSBytes + kSBytes);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s->s_empty[sc.i]);
                     sc.next();
@@ -330,48 +374,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = warp_wait(&s->d_full[db.i], db.ph, a, s, 49);
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t d[TW];
-                const uint32_t at = (tmem + db.i * 64 + half * TW) | lanes;
-                if constexpr (TW == 32) {
-                    tmem_ld32(at, d);
-                    tmem_wait32(d);
-                } else if constexpr (TW == 16) {
-                    tmem_ld16_now(at, d);
-                } else {
-                    tmem_ld8_now(at, d);
-                }
-                float *sums = s->sums[db.i] + half * TW;
-                if (r == kRows) {
+                const int pair = (g & 7) >> 1;
+                const uint32_t sw = pair == 0 ? sv.x : pair == 1 ? sv.y : pair == 2 ? sv.z : sv.w;
+                const uint32_t bw = pair == 0 ? bv.x : pair == 1 ? bv.y : pair == 2 ? bv.z : bv.w;
 #pragma unroll
-                    for (int i = 0; i < TW; i += 4)
-                        *reinterpret_cast<uint4 *>(sums + i) = make_uint4(d[i], d[i + 1], d[i + 2], d[i + 3]);
-                    mbar_arrive(&s->sum_full[half][db.i]);
-                }
-                __syncwarp();
-                ok = warp_wait(&s->sum_full[half][db.i], db.ph, a, s, 50);
-                if (!ok) break;
-                const int gi = g & 7;
-                const uint32_t sw = (gi >> 1) == 0 ? sv.x : (gi >> 1) == 1 ? sv.y : (gi >> 1) == 2 ? sv.z : sv.w;
-                const uint32_t bw = (gi >> 1) == 0 ? bv.x : (gi >> 1) == 1 ? bv.y : (gi >> 1) == 2 ? bv.z : bv.w;
-                const float scale = __uint_as_float(gi & 1 ? sw & 0xFFFF0000u : sw << 16);
-                const float bias = fmaf(-128.f, scale, __uint_as_float(gi & 1 ? bw & 0xFFFF0000u : bw << 16));
-                const uint64_t s2 = pack2(__float_as_uint(scale), __float_as_uint(scale));
-                const uint64_t b2 = pack2(__float_as_uint(bias), __float_as_uint(bias));
+                for (int dg = 0; dg < DG; ++dg) {
+                    uint32_t d[TW];
+                    tmem_ld<TW>((tmem + db.i * 128 + dg * 64 + half * TW) | lanes, d);
+                    tmem_wait<TW>(d);
+                    tc_fence_before();
+                    __syncwarp();  // (also: the previous group's X has been read)
+                    if (dg == DG - 1 && lane == 0) mbar_arrive(&s->d_empty[db.i]);
+                    if (lane == 31) {
 #pragma unroll
-                for (int i = 0; i < TW / 4; ++i) {
-                    const uint4 X = *reinterpret_cast<const uint4 *>(sums + 4 * i);
-                    y[2 * i] = fma2(s2, pack2(d[4 * i], d[4 * i + 1]), fma2(b2, pack2(X.x, X.y), y[2 * i]));
-                    y[2 * i + 1] = fma2(s2, pack2(d[4 * i + 2], d[4 * i + 3]), fma2(b2, pack2(X.z, X.w), y[2 * i + 1]));
+                        for (int i = 0; i < TW; i += 4) sts128(sums + 4 * i, d[i], d[i + 1], d[i + 2], d[i + 3]);
+                    }
+                    __syncwarp();
+                    const bool high = DG == 2 ? dg == 1 : (g & 1);
+                    const float scale = __uint_as_float(high ? sw & 0xFFFF0000u : sw << 16);
+                    const float bias = fmaf(-128.f, scale, __uint_as_float(high ? bw & 0xFFFF0000u : bw << 16));
+                    const uint64_t s2 = pack2(__float_as_uint(scale), __float_as_uint(scale));
+                    const uint64_t b2 = pack2(__float_as_uint(bias), __float_as_uint(bias));
+#pragma unroll
+                    for (int i = 0; i < TW / 4; ++i) {
+                        const uint4 X = lds128(sums + 16 * i);
+                        y[2 * i] = fma2(s2, pack2(d[4 * i], d[4 * i + 1]), fma2(b2, pack2(X.x, X.y), y[2 * i]));
+                        y[2 * i + 1] =
+                            fma2(s2, pack2(d[4 * i + 2], d[4 * i + 3]), fma2(b2, pack2(X.z, X.w), y[2 * i + 1]));
+                    }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s->d_empty[db.i]);
                 db.next();
             }
             if (a.split == 1) {
                 if (!ok) break;
                 const int row = tile * kRows + r;
-                if (r < kRows && row < a.N) {
+                if (lane < 31 && row < a.N) {
 #pragma unroll
                     for (int i = 0; i < TW / 2; ++i) {
                         const float2 v = unpack2(y[i]);
@@ -385,8 +422,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < TW / 2; ++i) {
                 const float2 v = unpack2(y[i]);
-                red[(half * TW + 2 * i) * 128 + r] = v.x;
-                red[(half * TW + 2 * i + 1) * 128 + r] = v.y;
+                const uint32_t at = smem_u32(red) + ((half * TW + 2 * i) * 128 + quarter * 32 + lane) * 4;
+                sts32(at, v.x);
+                sts32(at + 512, v.y);
             }
         }
     }
@@ -402,10 +440,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         cluster_sync();
         const int per = (a.B + a.split - 1) / a.split, t0 = rank * per, t1 = min(a.B, t0 + per);
         for (int i = tid; i < (t1 - t0) * 128; i += kThreads) {
-            const int t = t0 + i / 128, r = i % 128, row = first * kRows + r;
-            if (r >= kRows || row >= a.N) continue;
+            const int t = t0 + i / 128, l = i % 128, row = first * kRows + l / 32 * 31 + l % 32;
+            if (l % 32 == 31 || row >= a.N) continue;
             float sum = 0.f;
-            for (int p = 0; p < a.split; ++p) sum += dsmem_ld(smem_u32(red + t * 128 + r), p);
+            for (int p = 0; p < a.split; ++p) sum += dsmem_ld(smem_u32(red + t * 128 + l), p);
             a.store(t, row, sum);
         }
         cluster_sync();
