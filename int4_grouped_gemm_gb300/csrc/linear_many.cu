@@ -19,8 +19,11 @@
 //   loads, MMA   warps 16 and 17 (18 and 19 complete the warpgroup)
 //
 // A barrier wait costs its role about 130 cycles however early the other side
-// was, so the steps are 128 k with one wait of each kind (steps of 64 k with a
-// separate barrier for X took 1,200 cycles each: 136 us for 64 x 2048 x 131072).
+// was, so the work goes in steps of 128 k (groups of 32: 64 k) and all that a
+// step's MMAs need comes in on one barrier (`ready`: tokens by TMA, codes from
+// the unpacking warps, the buffer of sums given back by the epilogue), all that
+// waits for them on one other (`done`).  With a barrier for each and steps of 64
+// k, 64 x 2048 x 131072 took 136 us, with steps of 128 k 104.
 //
 // Blocks take tiles of 124 rows in turn.  If there are too few tiles for the
 // GPU, a cluster of up to four blocks shares K and adds up through distributed
@@ -39,34 +42,33 @@ constexpr int kEpiWarps = 8, kDeqWarp = 8, kTmaWarp = 16, kMmaWarp = 17, kThread
 // unpacking and the rest then hold 128, 72 and 80 (32,768 + 18,432 + 10,240).
 constexpr int kLaunchRegs = 96, kEpiRegs = 128, kDeqRegs = 72, kRestRegs = 80;
 static_assert(256 * kEpiRegs + 256 * kDeqRegs + 128 * kRestRegs <= kThreads * kLaunchRegs, "shares of the launch's registers");
-constexpr int kUnit = 128;                 // k of a step
 constexpr int kW = 6, kS = 3;              // stages: codes, scales (8 groups)
 constexpr int kX = 6, kA = 3;              // stages: tokens in shared memory, codes in tensor memory (64 columns)
 constexpr int kD = 2;                      // buffers of group sums, two groups each (128 columns)
-constexpr int kWBytes = 128 * kUnit / 2, kSBytes = 128 * 8 * 2;
+constexpr int kSBytes = 128 * 8 * 2;
 constexpr uint32_t kTmemCols = 512;        // kD * 128 + kA * 64 = 448, rounded up
+__host__ __device__ constexpr int step_k(int G) { return G == 32 ? 64 : 128; }
+__host__ __device__ constexpr int w_bytes(int G) { return 128 * step_k(G) / 2; }
 
-__host__ __device__ constexpr int x_bytes(int tok) { return 2 * tok * 128; }  // two boxes of 64 k
+__host__ __device__ constexpr int x_bytes(int G, int tok) { return step_k(G) / 64 * tok * 128; }  // boxes of 64 k
 
 struct Ctl {
-    uint64_t w_full[kW], w_empty[kW], x_full[kX], s_full[kS], s_empty[kS];
-    uint64_t a_full[kA], used[kX];         // codes are in tensor memory; the step's MMAs are complete
-    uint64_t d_full[kD], d_empty[kD];
+    uint64_t w_full[kW], w_empty[kW], s_full[kS], s_empty[kS];
+    uint64_t ready[kX], done[kX];          // a step's operands and sums are there; its MMAs are complete
     uint64_t drain;
-    alignas(16) float sums[kEpiWarps][32]; // X, each warp's own
     uint32_t tmem;
     int abort;
 };
-static_assert(offsetof(Ctl, sums) % 16 == 0, "X is read in 16-byte pieces");
 
 // More than half of a SM's: one block at a time, since each takes all of the
 // tensor memory.
-__host__ __device__ constexpr int smem_bytes(int tok) {
+__host__ __device__ constexpr int smem_bytes(int G, int tok) {
     constexpr int least = kBlockSmem / 2 + 1024;
-    const int n = kX * x_bytes(tok) + kW * kWBytes + kS * 2 * kSBytes + tok * 128 * 4 + static_cast<int>(sizeof(Ctl)) + 1024;
+    const int n = kX * x_bytes(G, tok) + kW * w_bytes(G) + kS * 2 * kSBytes + tok * 128 * 4 +
+                  static_cast<int>(sizeof(Ctl)) + 1024;
     return n > least ? n : least;
 }
-static_assert(smem_bytes(64) <= kBlockSmem, "one block per SM");
+static_assert(smem_bytes(64, 64) <= kBlockSmem, "one block per SM");
 
 struct Maps {
     CUtensorMap q, s, b, x;
@@ -96,9 +98,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
     return v;
-}
-__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 __device__ __forceinline__ void sts32(uint32_t at, float v) {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
@@ -155,11 +154,11 @@ template <int G, int TOK>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_many_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LinearArgs a) {
     constexpr int TW = TOK / 2;                        // tokens of an epilogue warp
-    constexpr int GU = kUnit / G;                      // groups of a step
-    constexpr int DG = GU < 2 ? GU : 2, DU = GU / DG;  // groups of a buffer of sums, buffers of a step
+    constexpr int KS = step_k(G), GU = KS / G;         // k and groups (one or two) of a step
+    constexpr int XB = x_bytes(G, TOK), WB = w_bytes(G), WROW = KS / 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *sX = base, *sW = sX + kX * x_bytes(TOK), *sS = sW + kW * kWBytes;
+    uint8_t *sX = base, *sW = sX + kX * XB, *sS = sW + kW * WB;
     float *red = reinterpret_cast<float *>(sS + kS * 2 * kSBytes);  // [token][128 lanes]
     Ctl *s = reinterpret_cast<Ctl *>(red + TOK * 128);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -173,13 +172,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&s->s_empty[i], kEpiWarps);
         }
         for (int i = 0; i < kX; ++i) {
-            mbar_init(&s->x_full[i], 1);
-            mbar_init(&s->used[i], 1);
-        }
-        for (int i = 0; i < kA; ++i) mbar_init(&s->a_full[i], 4);
-        for (int i = 0; i < kD; ++i) {
-            mbar_init(&s->d_full[i], 1);
-            mbar_init(&s->d_empty[i], kEpiWarps);
+            mbar_init(&s->ready[i], 1 + 4 + kEpiWarps);  // the loads' own arrival, unpacking warps, epilogue warps
+            mbar_init(&s->done[i], 1);
         }
         mbar_init(&s->drain, 1);
         s->abort = 0;
@@ -203,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     pdl_trigger();
 
-    const int units = (a.K + kUnit - 1) / kUnit, rank = a.rank_of(blockIdx.x);
+    const int units = (a.K + KS - 1) / KS, rank = a.rank_of(blockIdx.x);
     const int u0 = units * rank / a.split, u1 = units * (rank + 1) / a.split;
     const int tiles = (a.N + kRows - 1) / kRows, step = gridDim.x / a.split;
     const int first = blockIdx.x / a.split;
@@ -215,12 +209,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             Ring<kW> w;
             Ring<kX> x;
             Ring<kS> sc;
-            uint32_t n_w = 0, n_s = 0;
+            uint32_t n_w = 0, n_s = 0, n_x = 0;
             bool ok = true;
             for (int tile = first; tile < tiles && ok; tile += step) {
                 int block = -1;
                 for (int u = u0; u < u1 && ok; ++u) {
-                    const int need = u * GU / 8;       // block of 8 groups that the unit's lie in
+                    const int need = u * GU / 8;       // block of 8 groups that the step's lie in
                     if (need != block) {
                         block = need;
                         ok = wait(&s->s_empty[sc.i], sc.ph ^ 1, a, s, 40);
@@ -234,23 +228,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     ok = wait(&s->w_empty[w.i], w.ph ^ 1, a, s, 41);
                     if (!ok) break;
-                    mbar_arrive_expect_tx(&s->w_full[w.i], kWBytes);
-                    tma_load_2d(sW + w.i * kWBytes, &maps.q, &s->w_full[w.i], u * (kUnit / 8), tile * kRows);
+                    mbar_arrive_expect_tx(&s->w_full[w.i], WB);
+                    tma_load_2d(sW + w.i * WB, &maps.q, &s->w_full[w.i], u * (KS / 8), tile * kRows);
                     w.next();
                     ++n_w;
-                    ok = wait(&s->used[x.i], x.ph ^ 1, a, s, 42);
+                    // the slot's previous step (kX before this one) is complete
+                    ok = wait(&s->done[x.i], x.ph ^ 1, a, s, 42);
                     if (!ok) break;
-                    mbar_arrive_expect_tx(&s->x_full[x.i], x_bytes(TOK));
-                    tma_load_2d(sX + x.i * x_bytes(TOK), &maps.x, &s->x_full[x.i], u * kUnit, 0);
-                    tma_load_2d(sX + x.i * x_bytes(TOK) + TOK * 128, &maps.x, &s->x_full[x.i], u * kUnit + 64, 0);
+                    mbar_arrive_expect_tx(&s->ready[x.i], XB);
+#pragma unroll
+                    for (int i = 0; i < KS / 64; ++i)
+                        tma_load_2d(sX + x.i * XB + i * TOK * 128, &maps.x, &s->ready[x.i], u * KS + i * 64, 0);
                     x.next();
+                    ++n_x;
                 }
             }
-            // no copy of this block is in flight when it ends (one token stage per
-            // code stage, but for the last one after a timeout)
-            const uint32_t n_x = ok ? n_w : n_w > 0 ? n_w - 1 : 0;
+            // no copy of this block is in flight when it ends.  (The tokens' phases
+            // also wait for other arrivals, which after a timeout elsewhere may
+            // not come: the wait then runs out, long after the copies landed.)
             for (uint32_t i = n_w > kW ? n_w - kW : 0; i < n_w; ++i) mbar_wait(&s->w_full[i % kW], (i / kW) & 1, a.wait_limit);
-            for (uint32_t i = n_x > kX ? n_x - kX : 0; i < n_x; ++i) mbar_wait(&s->x_full[i % kX], (i / kX) & 1, a.wait_limit);
+            for (uint32_t i = n_x > kX ? n_x - kX : 0; i < n_x; ++i)
+                if (!mbar_wait(&s->ready[i % kX], (i / kX) & 1, a.wait_limit)) break;
             for (uint32_t i = n_s > kS ? n_s - kS : 0; i < n_s; ++i) mbar_wait(&s->s_full[i % kS], (i / kS) & 1, a.wait_limit);
         }
         __syncwarp();
@@ -258,33 +256,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
             constexpr uint32_t idesc = idesc_bf16(128, TOK);
             Ring<kX> x;
-            Ring<kA> ab;
-            Ring<kD> db;
+            uint32_t ab = 0, db = 0;
             bool ok = true;
+            const uint32_t x_addr = smem_u32(sX);
             for (int tile = first; tile < tiles && ok; tile += step) {
-                for (int u = u0; u < u1 && ok; ++u) {
-                    ok = wait(&s->x_full[x.i], x.ph, a, s, 43) && wait(&s->a_full[ab.i], ab.ph, a, s, 44);
+                for (int u = u0; u < u1; ++u) {
+                    ok = wait(&s->ready[x.i], x.ph, a, s, 43);
                     if (!ok) break;
-                    const uint32_t xa = smem_u32(sX + x.i * x_bytes(TOK)), at = tA + ab.i * 64;
+                    tc_fence_after();
+                    const uint32_t xa = x_addr + x.i * XB, at = tA + ab * 64, dt = tmem + db * 128;
 #pragma unroll
-                    for (int du = 0; du < DU; ++du) {
-                        ok = wait(&s->d_empty[db.i], db.ph ^ 1, a, s, 45);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t dt = tmem + db.i * 128;
-#pragma unroll
-                        for (int i = 0; i < 8 / DU; ++i) {
-                            const int kk = du * (8 / DU) + i, g = i / (8 / DU / DG);  // 16 k, group of the buffer
-                            umma_bf16_ts(dt + g * 64, at + kk * 8, sdesc_k128(xa + (kk / 4) * (TOK * 128) + (kk % 4) * 32),
-                                         idesc, i % (8 / DU / DG) != 0);
-                        }
-                        umma_commit(&s->d_full[db.i]);
-                        db.next();
-                    }
-                    if (!ok) break;
-                    umma_commit(&s->used[x.i]);
+                    for (int kk = 0; kk < KS / 16; ++kk)
+                        umma_bf16_ts(dt + kk / (G / 16) * 64, at + kk * 8, sdesc_k128(xa + (kk / 4) * (TOK * 128) + (kk % 4) * 32),
+                                     idesc, kk % (G / 16) != 0);
+                    umma_commit(&s->done[x.i]);
                     x.next();
-                    ab.next();
+                    ab = ab + 1 == kA ? 0 : ab + 1;
+                    db ^= 1;
                 }
             }
             // every MMA issued here is complete before tensor memory is freed
@@ -300,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quarter = warp & 3, set_of = (warp - kDeqWarp) >> 2;
         const int r = quarter * 31 + min(lane, 30);    // row of the tile
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        const int rot = (r >> 1) & 3;                  // 64-byte swizzle of the row's 16-byte pieces
+        const int rot = KS == 128 ? (r >> 1) & 3 : (r >> 2) & 1;  // swizzle of the row's 16-byte pieces
         const uint32_t w_addr = smem_u32(sW);
         // (w & mask) | set: 128 + q as a bf16 pair, or ones in the last lane
         const uint32_t mask = lane == 31 ? 0u : 0x000F000Fu, set = lane == 31 ? 0x3F803F80u : 0x43004300u;
@@ -312,15 +300,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t ws = n % kW, as = n % kA;
                 ok = warp_wait(&s->w_full[ws], (n / kW) & 1, a, s, 46);
                 if (!ok) break;
-                const uint32_t row = w_addr + ws * kWBytes + r * 64;
-                uint4 v[4];
+                const uint32_t row = w_addr + ws * WB + r * WROW;
+                uint4 v[KS / 32];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = lds128(row + ((i ^ rot) << 4));
+                for (int i = 0; i < KS / 32; ++i) v[i] = lds128(row + ((i ^ rot) << 4));
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s->w_empty[ws]);
                 bool free = false;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < KS / 32; ++i) {
                     const uint32_t q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                     uint32_t p[16];
 #pragma unroll
@@ -329,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int j = 0; j < 4; ++j) p[4 * e + j] = mask_set(q[e] >> (4 * j), mask, set);
                     if (!free) {
                         // the MMAs of the step that had this buffer before
-                        if (n >= kA) ok = warp_wait(&s->used[(n - kA) % kX], ((n - kA) / kX) & 1, a, s, 47);
+                        if (n >= kA) ok = warp_wait(&s->done[(n - kA) % kX], ((n - kA) / kX) & 1, a, s, 47);
                         if (!ok) break;
                         free = true;
                         tc_fence_after();
@@ -340,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s->a_full[as]);
+                if (lane == 0) mbar_arrive(&s->ready[n % kX]);
             }
         }
     } else {
@@ -349,17 +337,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int half = warp >> 2, quarter = warp & 3;
         const int r = quarter * 31 + min(lane, 30);    // row of the tile (the last lane: X)
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t sums = smem_u32(s->sums[warp]), s_addr = smem_u32(sS) + r * 16;
+        const uint32_t s_addr = smem_u32(sS) + r * 16;
         Ring<kS> sc;
-        Ring<kD> db;
+        Ring<kX> x;                                    // step
+        uint32_t ahead = kD, db = 0;                   // slot of the step that gets this one's buffer of sums
         bool ok = true;
+        // the first steps find their buffers free
+        if (lane == 0)
+            for (int i = 0; i < kD; ++i) mbar_arrive(&s->ready[i]);
         for (int tile = first; tile < tiles; tile += step) {
             uint64_t y[TW / 2];
 #pragma unroll
             for (int i = 0; i < TW / 2; ++i) y[i] = 0;
             int block = -1;
             uint4 sv = make_uint4(0u, 0u, 0u, 0u), bv = sv;
-            for (int g = u0 * GU; g < u1 * GU && ok; g += DG) {
+            for (int g = u0 * GU; g < u1 * GU && ok; g += GU) {
                 if (g / 8 != block) {
                     // the row's scales and biases of eight groups
                     block = g / 8;
@@ -371,39 +363,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive(&s->s_empty[sc.i]);
                     sc.next();
                 }
-                ok = warp_wait(&s->d_full[db.i], db.ph, a, s, 49);
+                ok = warp_wait(&s->done[x.i], x.ph, a, s, 49);
                 if (!ok) break;
                 tc_fence_after();
+                uint32_t d[GU][TW];
+#pragma unroll
+                for (int gu = 0; gu < GU; ++gu) tmem_ld<TW>((tmem + db * 128 + gu * 64 + half * TW) | lanes, d[gu]);
+#pragma unroll
+                for (int gu = 0; gu < GU; ++gu) tmem_wait<TW>(d[gu]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s->ready[ahead]);
+                x.next();
+                ahead = ahead + 1 == kX ? 0 : ahead + 1;
+                db ^= 1;
                 const int pair = (g & 7) >> 1;
                 const uint32_t sw = pair == 0 ? sv.x : pair == 1 ? sv.y : pair == 2 ? sv.z : sv.w;
                 const uint32_t bw = pair == 0 ? bv.x : pair == 1 ? bv.y : pair == 2 ? bv.z : bv.w;
 #pragma unroll
-                for (int dg = 0; dg < DG; ++dg) {
-                    uint32_t d[TW];
-                    tmem_ld<TW>((tmem + db.i * 128 + dg * 64 + half * TW) | lanes, d);
-                    tmem_wait<TW>(d);
-                    tc_fence_before();
-                    __syncwarp();  // (also: the previous group's X has been read)
-                    if (dg == DG - 1 && lane == 0) mbar_arrive(&s->d_empty[db.i]);
-                    if (lane == 31) {
-#pragma unroll
-                        for (int i = 0; i < TW; i += 4) sts128(sums + 4 * i, d[i], d[i + 1], d[i + 2], d[i + 3]);
-                    }
-                    __syncwarp();
-                    const bool high = DG == 2 ? dg == 1 : (g & 1);
+                for (int gu = 0; gu < GU; ++gu) {
+                    const bool high = GU == 2 ? gu == 1 : (g & 1);
                     const float scale = __uint_as_float(high ? sw & 0xFFFF0000u : sw << 16);
                     const float bias = fmaf(-128.f, scale, __uint_as_float(high ? bw & 0xFFFF0000u : bw << 16));
                     const uint64_t s2 = pack2(__float_as_uint(scale), __float_as_uint(scale));
                     const uint64_t b2 = pack2(__float_as_uint(bias), __float_as_uint(bias));
+                    const uint32_t *e = d[gu];
 #pragma unroll
                     for (int i = 0; i < TW / 4; ++i) {
-                        const uint4 X = lds128(sums + 16 * i);
-                        y[2 * i] = fma2(s2, pack2(d[4 * i], d[4 * i + 1]), fma2(b2, pack2(X.x, X.y), y[2 * i]));
+                        // X is the last lane's D
+                        uint4 X;
+                        X.x = __shfl_sync(0xffffffffu, e[4 * i], 31);
+                        X.y = __shfl_sync(0xffffffffu, e[4 * i + 1], 31);
+                        X.z = __shfl_sync(0xffffffffu, e[4 * i + 2], 31);
+                        X.w = __shfl_sync(0xffffffffu, e[4 * i + 3], 31);
+                        y[2 * i] = fma2(s2, pack2(e[4 * i], e[4 * i + 1]), fma2(b2, pack2(X.x, X.y), y[2 * i]));
                         y[2 * i + 1] =
-                            fma2(s2, pack2(d[4 * i + 2], d[4 * i + 3]), fma2(b2, pack2(X.z, X.w), y[2 * i + 1]));
+                            fma2(s2, pack2(e[4 * i + 2], e[4 * i + 3]), fma2(b2, pack2(X.z, X.w), y[2 * i + 1]));
                     }
                 }
-                db.next();
             }
             if (a.split == 1) {
                 if (!ok) break;
@@ -452,8 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int G, int TOK>
 static cudaError_t launch_t(const Maps &maps, LinearArgs a, int num_sms, cudaStream_t s) {
-    const int units = (a.K + kUnit - 1) / kUnit, tiles = (a.N + kRows - 1) / kRows;
-    // share K in a cluster while there are two units for each block and all
+    const int units = (a.K + step_k(G) - 1) / step_k(G), tiles = (a.N + kRows - 1) / kRows;
+    // share K in a cluster while there are two steps for each block and all
     // clusters run at once (one tile each)
     a.split = 1;
     while (a.split < 4 && tiles * a.split * 2 <= num_sms * 7 / 8 && units >= a.split * 4) a.split *= 2;
@@ -463,7 +460,7 @@ static cudaError_t launch_t(const Maps &maps, LinearArgs a, int num_sms, cudaStr
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(a.split > 1 ? tiles * a.split : std::min(tiles, num_sms));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes(TOK);
+    cfg.dynamicSmemBytes = smem_bytes(G, TOK);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -485,6 +482,7 @@ static cudaError_t launch_g(const Maps &m, const LinearArgs &a, int num_sms, cud
 
 }  // namespace many
 
+int linear_code_words(int G) { return many::step_k(G) / 8; }
 int linear_token_rows(int B) { return B <= 16 ? 16 : B <= 32 ? 32 : 64; }
 
 cudaError_t launch_linear_many(const CUtensorMap *maps, const LinearArgs &a, int num_sms, cudaStream_t s) {
