@@ -1,11 +1,13 @@
 // y[b][n] = sum_k x[b][k] (s[n][k/G] q[n][k] + z[n][k/G]) for 9 to 64 tokens on the
 // fifth-generation tensor cores.
 //
-// As with few tokens no weight is rounded: the codes themselves, 128 + q in
-// bf16 (one shift or one mask-and-set a pair), are the M = 128 side of
-// tcgen05.mma, the tokens as they are the N side, and each group of weights
-// has a sum of its own, D = sum (128 + q) x; then, in fp32 registers,
-//   y += s D + (z - 128 s) X,   X = sum of the group's x
+// As with few tokens no weight is rounded: the codes themselves, exact in bf16
+// (128 + q by a shift and a mask-and-set a pair, less 128), are the M = 128 side
+// of tcgen05.mma, the tokens as they are the N side, and each group of weights
+// has a sum of its own, D = sum q x; then, in fp32 registers,
+//   y += s D + z X,   X = sum of the group's x
+// (With 128 + q as the operand and z - 128 s the subtraction is saved, but D is
+// 17 times as large and y off by 2e-6 instead of 2e-7.)
 // X comes out of the same MMA: the last of each 32 rows of a tile is not a
 // weight row but ones, so that a tile has 4 x 31 weight rows and the last lane of
 // every epilogue warp finds X in its row of D.  The codes go straight into tensor
@@ -290,8 +292,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const int rot = KS == 128 ? (r >> 1) & 3 : (r >> 2) & 1;  // swizzle of the row's 16-byte pieces
         const uint32_t w_addr = smem_u32(sW);
-        // (w & mask) | set: 128 + q as a bf16 pair, or ones in the last lane
-        const uint32_t mask = lane == 31 ? 0u : 0x000F000Fu, set = lane == 31 ? 0x3F803F80u : 0x43004300u;
+        // (w & mask) | set: 128 + q as a bf16 pair, or 129 in the last lane
+        const uint32_t mask = lane == 31 ? 0u : 0x000F000Fu, set = lane == 31 ? 0x43014301u : 0x43004300u;
+        const __nv_bfloat162 c128 = u32_as_bf162(0x43004300u);
         uint32_t n = 0;                                // steps of the block so far
         bool ok = true;
         for (int tile = first; tile < tiles && ok; tile += step) {
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) p[4 * e + j] = mask_set(q[e] >> (4 * j), mask, set);
+                        for (int j = 0; j < 4; ++j) p[4 * e + j] = bf162_as_u32(__hsub2(u32_as_bf162(mask_set(q[e] >> (4 * j), mask, set)), c128));
                     if (!free) {
                         // the MMAs of the step that had this buffer before
                         if (n >= kA) ok = warp_wait(&s->done[(n - kA) % kX], ((n - kA) / kX) & 1, a, s, 47);
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int gu = 0; gu < GU; ++gu) {
                     const bool high = GU == 2 ? gu == 1 : (g & 1);
                     const float scale = __uint_as_float(high ? sw & 0xFFFF0000u : sw << 16);
-                    const float bias = fmaf(-128.f, scale, __uint_as_float(high ? bw & 0xFFFF0000u : bw << 16));
+                    const float bias = __uint_as_float(high ? bw & 0xFFFF0000u : bw << 16);
                     const uint64_t s2 = pack2(__float_as_uint(scale), __float_as_uint(scale));
                     const uint64_t b2 = pack2(__float_as_uint(bias), __float_as_uint(bias));
                     const uint32_t *e = d[gu];
