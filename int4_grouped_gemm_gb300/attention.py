@@ -6,6 +6,7 @@ result is the ``attn`` of ``PackedLayer.decode_batch_block``.
 """
 from __future__ import annotations
 
+import ctypes
 import math
 from typing import Optional
 
@@ -20,20 +21,28 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _heads(t: torch.Tensor, name: str, T: int, heads: Optional[int], D: int):
-    """[T, heads, D] bf16 whose rows are contiguous (rows themselves may be strided)."""
+def _heads(t: torch.Tensor, name: str, T: int, heads: Optional[int], D: int, device: int) -> int:
+    """[T, heads, D] bf16 whose rows are contiguous (rows themselves may be
+    strided), on the current device; elements from one row to the next."""
     shape, stride = t.shape, t.stride()
     if len(shape) != 3 or t.dtype != torch.bfloat16 or shape[0] != T or shape[2] != D or \
             (heads is not None and shape[1] != heads):
         raise ValueError(f"{name}: [{T}, {'heads' if heads is None else heads}, {D}] in bf16")
     if stride[2] != 1 or (shape[1] > 1 and stride[1] != D):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, the current device is cuda:{device}")
+    return stride[0] if T > 1 else shape[1] * D
 
 
-def _ints(t: torch.Tensor, name: str, n: Optional[int], dims: int):
+def _ints(t: torch.Tensor, name: str, n: Optional[int], dims: int, device: int) -> int:
+    """A contiguous int32 array on the current device; its address."""
     shape = t.shape
     if t.dtype != torch.int32 or len(shape) != dims or (n is not None and shape[0] != n) or not t.is_contiguous():
         raise ValueError(f"{name}: int32, contiguous, {dims} dimension(s)" + ("" if n is None else f", the first {n}"))
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, the current device is cuda:{device}")
+    return t.data_ptr()
 
 
 class PagedCache:
@@ -52,8 +61,11 @@ class PagedCache:
         page, head, pos = (s if n > 1 else self.D for s, n in zip(k.stride(), k.shape[:3]))
         self.desc = _lib.gqa_pages(k.data_ptr(), v.data_ptr(), self.n_pages, self.page_size, self.Hkv, self.D, page,
                                    head, pos)
+        self._device = k.get_device()
         # where append records errors found on the device
         self.status = torch.zeros(4, dtype=torch.int32, device=k.device)
+        self._ref, self._status_at = ctypes.byref(self.desc), self.status.data_ptr()
+        self._scale = 1.0 / math.sqrt(self.D)
 
     @classmethod
     def empty(cls, n_pages: int, Hkv: int, page_size: int, D: int, device="cuda") -> "PagedCache":
@@ -65,26 +77,42 @@ class PagedCache:
                interleaved: bool = False, q_out: Optional[torch.Tensor] = None, stream=None):
         """Rotate q and k by position index + pos_offset, write k and v to
         position index[t] of sequence seq[t]; returns the rotated q."""
-        T = k.shape[0]
-        _heads(k, "k", T, self.Hkv, self.D)
-        _heads(v, "v", T, self.Hkv, self.D)
-        _ints(seq, "seq", T, 1)
-        _ints(index, "index", T, 1)
-        _ints(page_table, "page_table", None, 2)
-        if inv_freq is not None and (inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or
-                                     not inv_freq.is_contiguous()):
-            raise ValueError("inv_freq: fp32 [rot / 2]")
+        if stream is not None and q is not None and q_out is None:
+            with _lib.on_stream(stream):
+                return self.append(q, k, v, seq, index, page_table, inv_freq, pos_offset, interleaved)
+        T, D, dev = k.shape[0], self.D, self._check_device("append")
+        ks = _heads(k, "k", T, self.Hkv, D, dev)
+        vs = _heads(v, "v", T, self.Hkv, D, dev)
+        seq_at, index_at = _ints(seq, "seq", T, 1, dev), _ints(index, "index", T, 1, dev)
+        table_at = _ints(page_table, "page_table", None, 2, dev)
+        rot, freq_at = 0, None
+        if inv_freq is not None:
+            if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous() or \
+                    inv_freq.get_device() != dev:
+                raise ValueError("inv_freq: fp32 [rot / 2], contiguous, on the current device")
+            rot, freq_at = 2 * inv_freq.shape[0], inv_freq.data_ptr()
+        Hq = qs = os = 0
+        q_at = out_at = None
         if q is None:
             _need(q_out is None, "q_out without q")
         else:
-            _heads(q, "q", T, None, self.D)
+            qs = _heads(q, "q", T, None, D, dev)
+            Hq = q.shape[1]
             if q_out is None:
                 q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            _heads(q_out, "q_out", T, q.shape[1], self.D)
-        _lib.check_device("append", self.k, q, k, v, seq, index, page_table, inv_freq, q_out)
-        _lib.gqa_append(self.desc, q, k, v, seq, index, page_table, pos_offset, inv_freq, interleaved, q_out,
-                        self.status, stream)
+            os = _heads(q_out, "q_out", T, Hq, D, dev)
+            q_at, out_at = q.data_ptr(), q_out.data_ptr()
+        n_seq, ld = page_table.shape
+        _lib.check(_lib.load().gqa_append(self._ref, q_at, qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq, seq_at,
+                                          index_at, table_at, n_seq, ld, pos_offset, freq_at, rot, interleaved, out_at,
+                                          os, self._status_at, _lib.stream_on(stream, dev)), "gqa_append")
         return q_out
+
+    def _check_device(self, what: str) -> int:
+        cur = _lib.current_device()
+        if cur != self._device:
+            raise ValueError(f"{what}: the cache is on cuda:{self._device}, the current device is cuda:{cur}")
+        return cur
 
     def workspace(self, B: int, Hq: int, prefix_len: int = 0) -> torch.Tensor:
         """Scratch of attend for up to B rows, Hq heads and prefix_len shared
@@ -100,22 +128,29 @@ class PagedCache:
         """out [B, Hq, D]: row b's query attends to the shared prefix (read
         once for all rows), then to the first seq_len[b] positions of
         page_table[b].  scale: 1 / sqrt(D) unless given."""
-        B, Hq = q.shape[0], q.shape[1]
-        _heads(q, "q", B, None, self.D)
-        _ints(page_table, "page_table", B, 2)
-        _ints(seq_len, "seq_len", B, 1)
+        if stream is not None and (out is None or ws is None):
+            with _lib.on_stream(stream):
+                return self.attend(q, page_table, seq_len, prefix_pages, prefix_len, scale, out, ws)
+        B, Hq, dev = q.shape[0], q.shape[1], self._check_device("attend")
+        qs = _heads(q, "q", B, None, self.D, dev)
+        table_at = _ints(page_table, "page_table", B, 2, dev)
+        len_at = _ints(seq_len, "seq_len", B, 1, dev)
+        prefix_at = None
         if prefix_len:
             _need(prefix_pages is not None, "prefix_len without prefix_pages")
-            _ints(prefix_pages, "prefix_pages", None, 1)
+            prefix_at = _ints(prefix_pages, "prefix_pages", None, 1, dev)
             _need(prefix_len <= prefix_pages.shape[0] * self.page_size, "prefix_pages: too few for prefix_len")
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        _heads(out, "out", B, Hq, self.D)
+        os = _heads(out, "out", B, Hq, self.D, dev)
         if ws is None:
             ws = self.workspace(B, Hq, prefix_len)
-        _lib.check_device("attend", self.k, q, page_table, seq_len, prefix_pages, out, ws)
-        _lib.gqa_paged_attention(self.desc, q, prefix_pages if prefix_len else None, prefix_len, page_table, seq_len,
-                                 1.0 / math.sqrt(self.D) if scale is None else scale, out, ws, stream)
+        _need(ws.get_device() == dev and ws.is_contiguous(), "ws: contiguous, on the current device")
+        _lib.check(_lib.load().gqa_paged_attention(self._ref, q.data_ptr(), qs, B, Hq, prefix_at, prefix_len, table_at,
+                                                   page_table.shape[1], len_at,
+                                                   self._scale if scale is None else scale, out.data_ptr(), os,
+                                                   ws.data_ptr(), ws.numel() * ws.element_size(),
+                                                   _lib.stream_on(stream, dev)), "gqa_paged_attention")
         return out
 
 
@@ -131,7 +166,10 @@ class AttentionLayer:
 
     def project(self, x: torch.Tensor, stream=None):
         """Queries, keys and values [T, heads, D] of 1 to 64 tokens (views of one buffer)."""
-        y = linear(self.qkv, x, stream=stream).view(x.shape[0], self.Hq + 2 * self.Hkv, self.D)
+        return self._split(linear(self.qkv, x, stream=stream))
+
+    def _split(self, y: torch.Tensor):
+        y = y.view(y.shape[0], self.Hq + 2 * self.Hkv, self.D)
         return y[:, :self.Hq], y[:, self.Hq:self.Hq + self.Hkv], y[:, self.Hq + self.Hkv:]
 
     def decode(self, x: torch.Tensor, cache: PagedCache, seq: torch.Tensor, index: torch.Tensor,
@@ -140,19 +178,14 @@ class AttentionLayer:
         """One step of B rows: x [B, H] (normalised) -> attn [B, H].  Row b's
         new token goes to position index[b] of page table row seq[b]; it
         attends to the prefix and the first seq_len[b] positions of row b
-        (seq_len = index + 1 for a plain step)."""
-        q, k, v = self.project(x, stream)
-        # every launch goes to `stream`: q_out, o and attn are made while it is current
-        with torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else _nothing():
-            q = cache.append(q, k, v, seq, index, page_table, self.inv_freq, prefix_len, self.interleaved,
-                             stream=stream)
-            o = cache.attend(q, page_table, seq_len, prefix_pages, prefix_len, ws=ws, stream=stream)
-            return linear(self.out, o.view(x.shape[0], self.Hq * self.D), stream=stream)
-
-
-class _nothing:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *a):
-        return False
+        (seq_len = index + 1 for a plain step; both negative: padding, whose
+        attn row means nothing)."""
+        if stream is not None:
+            with _lib.on_stream(stream):
+                return self.decode(x, cache, seq, index, page_table, seq_len, ws, prefix_pages, prefix_len)
+        qkv = linear(self.qkv, x)
+        q, k, v = self._split(qkv)
+        # queries, rotated queries and the attention's output share their place
+        cache.append(q, k, v, seq, index, page_table, self.inv_freq, prefix_len, self.interleaved, q_out=q)
+        cache.attend(q, page_table, seq_len, prefix_pages, prefix_len, out=q, ws=ws)
+        return linear(self.out, qkv[:, :self.Hq * self.D])

@@ -28,7 +28,7 @@
 // k, 64 x 2048 x 131072 took 136 us, with steps of 128 k 104.
 //
 // Blocks take tiles of 124 rows in turn.  If there are too few tiles for the
-// GPU, a cluster of up to four blocks shares K and adds up through distributed
+// GPU, a cluster of up to eight blocks shares K and adds up through distributed
 // shared memory.  Every wait is bounded.
 #include <algorithm>
 
@@ -456,7 +456,7 @@ static cudaError_t launch_t(const Maps &maps, LinearArgs a, int num_sms, cudaStr
     // share K in a cluster while there are two steps for each block and all
     // clusters run at once (one tile each)
     a.split = 1;
-    while (a.split < 4 && tiles * a.split * 2 <= num_sms * 7 / 8 && units >= a.split * 4) a.split *= 2;
+    while (a.split < 8 && tiles * (a.split + 1) <= num_sms * 7 / 8 && units >= (a.split + 1) * 2) ++a.split;
     const auto kernel = linear_many_kernel<G, TOK>;
     const cudaError_t e = allow_smem<linear_many_kernel<G, TOK>>();
     if (e != cudaSuccess) return e;
