@@ -543,12 +543,18 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
 }
 
 // Merge the partials of one (row, key-value head): grid (B Hkv, D / 32), thread
-// (quarter of the partials, 4 dimensions, head).  Every thread runs the online
-// merge over its partials, eight at a time (their loads independent), the
-// quarters meet in shared memory.
-__global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ PagedArgs a) {
-    __shared__ float4 s_acc[4][64];
-    __shared__ float2 s_ml[4][64];
+// (one of kParts shares of the partials, 4 dimensions, head).  Every thread runs
+// the online merge over its partials, four at a time (their loads
+// independent), the shares meet in shared memory.  Bound by latency, so there
+// are as many shares as keep the GPU's threads busy: 128 rows without a prefix
+// take 13 us in all with 2 shares and 18 with 8, one row of 32768 positions 21
+// and 14.
+constexpr int kBatch = 4;
+
+template <int kParts>
+__global__ void __launch_bounds__(kParts * 64, 16 / kParts) paged_combine_kernel(const __grid_constant__ PagedArgs a) {
+    __shared__ float4 s_acc[kParts][64];
+    __shared__ float2 s_ml[kParts][64];
     pdl_wait();
     pdl_trigger();
     const int Hkv = a.c.Hkv, D = a.c.D;
@@ -591,12 +597,12 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
     const int n = n_own + n_pre;
     float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = part; i0 < n; i0 += 32) {
-        float2 t[8];
-        float4 v[8];
+    for (int i0 = part; i0 < n; i0 += kParts * kBatch) {
+        float2 t[kBatch];
+        float4 v[kBatch];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int i = i0 + 4 * j;
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + kParts * j;
             t[j] = make_float2(-INFINITY, 0.f);
             v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (i < n_own) {
@@ -609,14 +615,14 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
         }
         float mx = m;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) mx = fmaxf(mx, t[j].x);
+        for (int j = 0; j < kBatch; ++j) mx = fmaxf(mx, t[j].x);
         if (mx == -INFINITY) continue;
         const float corr = exp2f(m - mx);
         m = mx;
         l *= corr;
         acc = make_float4(acc.x * corr, acc.y * corr, acc.z * corr, acc.w * corr);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kBatch; ++j) {
             // a partial without a tile (-inf) may never have been written
             const bool has = t[j].x != -INFINITY;
             const float w = exp2f(t[j].x - mx);
@@ -631,17 +637,17 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
     s_ml[part][tid & 63] = make_float2(m, l);
     __syncthreads();
     if (part == 0 && h < a.group) {
-        float2 t[4];
+        float2 t[kParts];
         float mx = -INFINITY, den = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kParts; ++i) {
             t[i] = s_ml[i][tid];
             mx = fmaxf(mx, t[i].x);
         }
         acc = make_float4(0.f, 0.f, 0.f, 0.f);
         if (mx != -INFINITY) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kParts; ++i) {
                 const float w = exp2f(t[i].x - mx);
                 const float4 v = s_acc[i][tid];
                 den += w * t[i].y;
@@ -722,7 +728,12 @@ cudaError_t launch_paged(PagedArgs &a, const CUtensorMap *maps, float scale, voi
         if ((e = launch_prefix(maps[0], maps[1], a, s)) != cudaSuccess) return e;
     }
     if ((e = a.c.D == 64 ? launch_own<64>(a, s) : launch_own<128>(a, s)) != cudaSuccess) return e;
-    return launch_dependent(paged_combine_kernel, dim3(a.B * a.c.Hkv, a.c.D / 32), dim3(256), 0, s, a);
+    const dim3 grid(a.B * a.c.Hkv, a.c.D / 32);
+    const int blocks = a.B * a.c.Hkv * (a.c.D / 32);
+    if (blocks >= 4 * num_sms) return launch_dependent(paged_combine_kernel<2>, grid, dim3(2 * 64), 0, s, a);
+    if (blocks >= 2 * num_sms) return launch_dependent(paged_combine_kernel<4>, grid, dim3(4 * 64), 0, s, a);
+    if (blocks >= num_sms / 2) return launch_dependent(paged_combine_kernel<8>, grid, dim3(8 * 64), 0, s, a);
+    return launch_dependent(paged_combine_kernel<16>, grid, dim3(16 * 64), 0, s, a);
 }
 
 }  // namespace moe
