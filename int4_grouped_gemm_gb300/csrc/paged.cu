@@ -162,7 +162,11 @@ cudaError_t launch_append(const AppendArgs &a, int num_sms, cudaStream_t s) {
 //   short items  (up to 32 tiles on average) a piece per warp, which writes a
 //                partial of its own for each item: no block-wide barriers
 // Each warp streams its tiles through its own ring of cp.async stages (24 KB),
-// which runs on across the items of the piece.
+// which runs on across the items of the piece.  Alone, block (or warp) n takes
+// piece n.  Behind a prefix kernel the pieces are taken in turn from a counter:
+// a few SMs are left to this kernel from the start, its first blocks work through
+// the pieces there while the prefix is under way, and blocks that come late find
+// nothing left and go.  (Which block took a piece does not show in the result.)
 //   scores   mma.sync m16n8k16, the heads as M, 16 positions as N
 //   output   O += P V, P from the score registers, rounded to bf16; l sums the
 //            rounded values, so that a weight's rounding cancels where one
@@ -227,6 +231,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
     int64_t *s_start = reinterpret_cast<int64_t *>(s_valid + kOwnWarps * NS);  // [B + 1]
     __shared__ int64_t s_warp[kOwnWarps];
     __shared__ int s_rows[kOwnWarps];
+    __shared__ int s_piece;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g8 = lane >> 2, c = lane & 3;
     // the first kernel of the call waits for what came before it; after a prefix
@@ -234,6 +239,15 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
     // take over the SMs as that one's end
     if (!a.prefix_ncta) pdl_wait();
     pdl_trigger();
+    if (a.prefix_ncta) {
+        // everything taken already?
+        if (tid == 0) s_piece = __ldcg(a.pieces) > 0 && __ldcg(a.pieces + 1) >= __ldcg(a.pieces);
+        __syncthreads();
+        if (s_piece) {
+            pdl_wait();
+            return;
+        }
+    }
     const int Hkv = a.c.Hkv, ps = a.c.page_shift;
     const int ntp = a.join ? tiles16(a.prefix_len) : 0;
 
@@ -297,15 +311,18 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
     const int64_t cap = by_warp ? a.ncta * kOwnWarps : a.ncta;
     most = most < cap ? most : cap;
     const int64_t per = most ? (W + most - 1) / most : 0;
-    if (blockIdx.x == 0 && tid == 0) a.starts[a.B + 1] = per;
-
-    // this warp's piece, and its tiles in it: first + stride i, i < my_n.  Pieces
-    // of warps go round the blocks, so that a few of them meet no other
-    const int piece = by_warp ? warp * a.ncta + blockIdx.x : blockIdx.x;
-    const int64_t f0 = piece * per < W ? piece * per : W, f1 = f0 + per < W ? f0 + per : W;
+    const int n_pieces = per ? static_cast<int>((W + per - 1) / per) : 0;
+    if (blockIdx.x == 0 && tid == 0) {
+        a.starts[a.B + 1] = per;
+        if (a.prefix_ncta) __stcg(a.pieces, n_pieces);
+    }
     const int stride = by_warp ? 1 : kOwnWarps;
-    const int64_t first = by_warp ? f0 : f0 + warp;
-    const int my_n = f1 > first ? static_cast<int>((f1 - first + stride - 1) / stride) : 0;
+    // this warp's piece, and its tiles in it: first + stride i, i < my_n.  Without
+    // a prefix kernel the pieces of warps go round the blocks, so that a few of
+    // them meet no other
+    int piece = by_warp ? warp * a.ncta + blockIdx.x : blockIdx.x;
+    int64_t f0 = 0, f1 = 0, first = 0;
+    int my_n = 0;
 
     // the row of tile f: the last one that starts at or before it
     auto row_of = [&](int64_t f) {
@@ -370,12 +387,6 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
             cp16_or_zero(dst + kPosTile * ROW, a.c.v + src, ok);
         }
     };
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        if (i < my_n) issue(i);
-        cp_async_commit();
-    }
-
     // ldmatrix lane roles: matrix mi = lane / 8, row rr = lane % 8
     const int mi = lane >> 3, rr = lane & 7;
     const int kpos = (mi >> 1) * 8 + rr, kch = mi & 1;
@@ -396,15 +407,33 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
         }
     };
 
-    int i = 0, b = 0, kv = 0;
-    int64_t nt = 0, end = 0;  // tiles of the row's items, end of this one
-    if (f0 < f1) {
-        b = row_of(f0);
-        nt = s_start[b + 1] - s_start[b];
-        kv = static_cast<int>((f0 - s_start[b] * Hkv) / nt);
-        end = s_start[b] * Hkv + (kv + 1) * nt;
-        load_q(b, kv);
+    for (bool more = true; more; more = a.prefix_ncta != 0) {
+    if (a.prefix_ncta) {
+        if (by_warp) {
+            if (lane == 0) piece = atomicAdd(a.pieces + 1, 1);
+            piece = __shfl_sync(0xffffffffu, piece, 0);
+        } else {
+            __syncthreads();  // the piece before has been read by every warp
+            if (tid == 0) s_piece = atomicAdd(a.pieces + 1, 1);
+            __syncthreads();
+            piece = s_piece;
+        }
     }
+    if (piece >= n_pieces) break;
+    f0 = piece * per;
+    f1 = f0 + per < W ? f0 + per : W;
+    first = by_warp ? f0 : f0 + warp;
+    my_n = f1 > first ? static_cast<int>((f1 - first + stride - 1) / stride) : 0;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+        if (j < my_n) issue(j);
+        cp_async_commit();
+    }
+    int i = 0, b = row_of(f0);
+    int64_t nt = s_start[b + 1] - s_start[b];  // tiles of the row's items
+    int kv = static_cast<int>((f0 - s_start[b] * Hkv) / nt);
+    int64_t end = s_start[b] * Hkv + (kv + 1) * nt;  // end of this item
+    load_q(b, kv);
     for (int64_t f = f0; f < f1;) {
         const int64_t stop = end < f1 ? end : f1;
         float o[NT][4];
@@ -538,6 +567,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
         }
         __syncthreads();  // the merge buffers are free for the next item
     }
+    }
     cp_async_wait<0>();
     pdl_wait();  // a kernel before this one that still runs is complete before this one is
 }
@@ -563,6 +593,7 @@ __global__ void __launch_bounds__(kParts * 64, 16 / kParts) paged_combine_kernel
     const int d4 = blockIdx.y * 8 + dq;
     const int len = a.seq_len[b];
     const int64_t s0 = a.starts[b], nt = a.starts[b + 1] - s0, per = a.starts[a.B + 1];
+    if (a.prefix_ncta && blockIdx.x == 0 && blockIdx.y == 0 && tid < 2) a.pieces[tid] = 0;  // for the next call
     if (len < 0) return;  // padding: out stays as it is
 
     // its own partials: those of the pieces that its tiles lie in
@@ -711,6 +742,7 @@ cudaError_t launch_paged(PagedArgs &a, const CUtensorMap *maps, float scale, voi
     a.own_o = reinterpret_cast<float *>(w + L.own_o);
     a.prefix_ml = reinterpret_cast<float2 *>(w + L.prefix_ml);
     a.prefix_o = reinterpret_cast<float *>(w + L.prefix_o);
+    a.pieces = reinterpret_cast<int *>(w) + 8;  // in the control block, zero between calls
     a.ncta = num_sms;
     a.negate = scale < 0.f;
     a.zero_q = scale == 0.f;
@@ -723,7 +755,10 @@ cudaError_t launch_paged(PagedArgs &a, const CUtensorMap *maps, float scale, voi
         a.prefix_blocks = prefix_row_blocks(rows);
         a.prefix_tiles = (a.prefix_len + 127) / 128;
         const int64_t tiles = static_cast<int64_t>(a.c.Hkv) * a.prefix_blocks * a.prefix_tiles;
+        // (short pieces one tile longer: that costs 1.4 us and leaves SMs for the
+        // rows' own positions)
         a.prefix_per = static_cast<int>((tiles + num_sms - 1) / num_sms);
+        if (a.prefix_per >= 2 && a.prefix_per <= 8) ++a.prefix_per;
         a.prefix_ncta = static_cast<int>((tiles + a.prefix_per - 1) / a.prefix_per);
         if ((e = launch_prefix(maps[0], maps[1], a, s)) != cudaSuccess) return e;
     }

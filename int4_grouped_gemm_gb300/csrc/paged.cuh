@@ -44,6 +44,7 @@ struct PagedArgs {
     float *prefix_o;                 // [2 slot + sub][D / 4][128 rows][4]
     float2 *own_ml;                  // [slot][8 heads]: running maximum (log2) and sum
     float *own_o;                    // [slot][D / 4][8 heads][4]: unnormalised output
+    int *pieces;                     // behind a prefix kernel: pieces of own positions in all (0: not known yet), taken
     int B, Hq, group, prefix_len, table_ld;
     int join;                        // the prefix is read as the start of every row
     int ncta;                        // blocks of the own-position kernel

@@ -337,9 +337,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 constexpr int CH = D / 8;
                 const int ch = tid % CH, h0 = kv * a.group;
                 uint8_t *dst = sQ + (ch / 8) * HALF;
-#pragma unroll 4
+                // (g / group by a 16-bit reciprocal: exact for g < 8192, group <= 8)
+                const uint32_t recip = (65536 + a.group - 1) / a.group;
+#pragma unroll 2
                 for (int row = tid / CH; row < per_block; row += 256 / CH) {
-                    const int g = blk * per_block + row, b = g < rows ? g / a.group : 0, h = g < rows ? g % a.group : 0;
+                    const int g = blk * per_block + row;
+                    const int b = g < rows ? static_cast<int>((g * recip) >> 16) : 0, h = g < rows ? g - b * a.group : 0;
                     cp16_or_zero(smem_u32(dst + (row / kRows) * QSUB + (row % kRows) * 128 + (((ch % 8) ^ (row & 7)) << 4)),
                                  a.q + b * a.q_stride + static_cast<int64_t>(h0 + h) * D + ch * 8, g < rows);
                 }
