@@ -163,10 +163,11 @@ cudaError_t launch_append(const AppendArgs &a, int num_sms, cudaStream_t s) {
 //                partial of its own for each item: no block-wide barriers
 // Each warp streams its tiles through its own ring of cp.async stages (24 KB),
 // which runs on across the items of the piece.  Alone, block (or warp) n takes
-// piece n.  Behind a prefix kernel the pieces are taken in turn from a counter:
-// a few SMs are left to this kernel from the start, its first blocks work through
-// the pieces there while the prefix is under way, and blocks that come late find
-// nothing left and go.  (Which block took a piece does not show in the result.)
+// piece n.  Behind a prefix kernel the first blocks, on the SMs that it leaves
+// free, start with a piece each, and the other pieces are taken from a counter:
+// the first blocks work through them while the prefix is under way, and blocks
+// that come late find nothing left and go.  (Which block took a piece does not
+// show in the result.)
 //   scores   mma.sync m16n8k16, the heads as M, 16 positions as N
 //   output   O += P V, P from the score registers, rounded to bf16; l sums the
 //            rounded values, so that a weight's rounding cancels where one
@@ -239,9 +240,9 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
     // take over the SMs as that one's end
     if (!a.prefix_ncta) pdl_wait();
     pdl_trigger();
-    if (a.prefix_ncta) {
+    if (a.prefix_ncta && static_cast<int>(blockIdx.x) >= a.own_first) {
         // everything taken already?
-        if (tid == 0) s_piece = __ldcg(a.pieces) > 0 && __ldcg(a.pieces + 1) >= __ldcg(a.pieces);
+        if (tid == 0) s_piece = __ldcg(a.pieces) > 0 && __ldcg(a.pieces + 1) >= __ldcg(a.pieces) - 1;
         __syncthreads();
         if (s_piece) {
             pdl_wait();
@@ -312,15 +313,16 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
     most = most < cap ? most : cap;
     const int64_t per = most ? (W + most - 1) / most : 0;
     const int n_pieces = per ? static_cast<int>((W + per - 1) / per) : 0;
+    const int given = a.prefix_ncta ? (by_warp ? a.own_first * kOwnWarps : a.own_first) : n_pieces;  // not by the counter
     if (blockIdx.x == 0 && tid == 0) {
         a.starts[a.B + 1] = per;
-        if (a.prefix_ncta) __stcg(a.pieces, n_pieces);
+        if (a.prefix_ncta) __stcg(a.pieces, max(n_pieces - given, 0) + 1);
     }
     const int stride = by_warp ? 1 : kOwnWarps;
-    // this warp's piece, and its tiles in it: first + stride i, i < my_n.  Without
-    // a prefix kernel the pieces of warps go round the blocks, so that a few of
-    // them meet no other
-    int piece = by_warp ? warp * a.ncta + blockIdx.x : blockIdx.x;
+    // this warp's piece, and its tiles in it: first + stride i, i < my_n.  The
+    // pieces of warps go round the blocks, so that a few of them meet no other
+    const int spread = a.prefix_ncta ? a.own_first : a.ncta;
+    int piece = by_warp ? warp * spread + blockIdx.x : blockIdx.x;
     int64_t f0 = 0, f1 = 0, first = 0;
     int my_n = 0;
 
@@ -407,14 +409,15 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
         }
     };
 
-    for (bool more = true; more; more = a.prefix_ncta != 0) {
-    if (a.prefix_ncta) {
+    for (bool given_one = static_cast<int>(blockIdx.x) < spread;; given_one = false) {
+    if (!given_one) {
+        if (!a.prefix_ncta) break;
         if (by_warp) {
-            if (lane == 0) piece = atomicAdd(a.pieces + 1, 1);
+            if (lane == 0) piece = given + atomicAdd(a.pieces + 1, 1);
             piece = __shfl_sync(0xffffffffu, piece, 0);
         } else {
             __syncthreads();  // the piece before has been read by every warp
-            if (tid == 0) s_piece = atomicAdd(a.pieces + 1, 1);
+            if (tid == 0) s_piece = given + atomicAdd(a.pieces + 1, 1);
             __syncthreads();
             piece = s_piece;
         }
@@ -760,6 +763,7 @@ cudaError_t launch_paged(PagedArgs &a, const CUtensorMap *maps, float scale, voi
         a.prefix_per = static_cast<int>((tiles + num_sms - 1) / num_sms);
         if (a.prefix_per >= 2 && a.prefix_per <= 8) ++a.prefix_per;
         a.prefix_ncta = static_cast<int>((tiles + a.prefix_per - 1) / a.prefix_per);
+        a.own_first = num_sms - a.prefix_ncta;
         if ((e = launch_prefix(maps[0], maps[1], a, s)) != cudaSuccess) return e;
     }
     if ((e = a.c.D == 64 ? launch_own<64>(a, s) : launch_own<128>(a, s)) != cudaSuccess) return e;

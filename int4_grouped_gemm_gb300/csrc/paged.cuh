@@ -44,10 +44,12 @@ struct PagedArgs {
     float *prefix_o;                 // [2 slot + sub][D / 4][128 rows][4]
     float2 *own_ml;                  // [slot][8 heads]: running maximum (log2) and sum
     float *own_o;                    // [slot][D / 4][8 heads][4]: unnormalised output
-    int *pieces;                     // behind a prefix kernel: pieces of own positions in all (0: not known yet), taken
+    int *pieces;                     // behind a prefix kernel: pieces to be taken from the counter + 1 (0: not known
+                                     // yet), and the counter
     int B, Hq, group, prefix_len, table_ld;
     int join;                        // the prefix is read as the start of every row
     int ncta;                        // blocks of the own-position kernel
+    int own_first;                   // of them, those that find a SM while the prefix kernel runs
     int prefix_two, prefix_blocks;   // prefix: 256-row blocks (else one of 128), blocks a key-value head
     int prefix_tiles, prefix_per;    // 128-position tiles of the prefix, tiles of a piece
     int prefix_ncta;                 // pieces and blocks of the prefix kernel, 0 without one
