@@ -3,22 +3,28 @@
 
 namespace moe {
 
-// The rotation angle pos * f as the cosine and sine of its fraction of a
-// turn.  The turns are taken in fp64 (pos up to 2^31 times f / 2 pi leaves
-// 2^-52 * 2^28 = 2^-24 of a turn at most), only the fraction in fp32.
-__device__ __forceinline__ float2 angle_cs(int64_t pos, float f) {
-    const double turns = static_cast<double>(pos) * (static_cast<double>(f) * 0.15915494309189533577);
-    const float frac = static_cast<float>(turns - rint(turns));
+// The rotation angle pos * f as the cosine and sine of its fraction of a turn.
+// f / 2 pi, less whole turns, is kept as a 64-bit fraction (made in fp64, off by
+// 2^-53 of a turn at most for f below 2 pi), so that its product with a position
+// loses whole turns by itself and is off by 2^-22 of a turn at position 2^31, and
+// at any nearer position by less than the fp32 fraction's own rounding.
+__device__ __forceinline__ uint64_t turn_fraction(float f) {
+    double r = static_cast<double>(f) * 0.15915494309189533577;
+    r -= rint(r);
+    return static_cast<uint64_t>(__double2ll_rn(r * 18446744073709551616.0));  // 2^64
+}
+__device__ __forceinline__ float2 angle_cs(uint32_t pos, uint64_t f) {
+    const uint32_t frac = __umulhi(static_cast<uint32_t>(f), pos) + static_cast<uint32_t>(f >> 32) * pos;
     float2 r;
-    sincospif(2.0f * frac, &r.y, &r.x);
+    sincospif(static_cast<float>(static_cast<int32_t>(frac)) * 0x1p-31f, &r.y, &r.x);
     return r;
 }
 
 // A block takes a few tokens (one when there are few, so that every SM has a
 // share, up to eight).  First the tokens' places and their angles' cosines and
-// sines into shared memory, one per thread and pair, shared by all heads (the
-// fp64 products are what is dear there: the GPU's fp64 rate is 1/64 of its fp32
-// rate); then 16-byte pieces: of a rotated head the pair of pieces whose
+// sines into shared memory, one per thread and pair, shared by all heads (fp64
+// only once per pair and block: its rate is 1/64 of fp32's, and with a product
+// per angle a prompt of 8192 tokens took 21 us); then 16-byte pieces: of a rotated head the pair of pieces whose
 // elements turn into one another (halves: pieces j and j + rot / 16 of the
 // head; interleaved: a piece by itself), otherwise plain copies.  Bound by the
 // bytes: each is read and written once.
@@ -54,6 +60,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     constexpr int P = D / 8;  // 16-byte pieces of a head
     __shared__ float2 s_cs[kAppendTokens][D / 2];
     __shared__ int64_t s_slot[kAppendTokens];  // the token's place in the pools, -1: none
+    __shared__ uint64_t s_turn[D / 2];
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x;
@@ -72,9 +79,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         }
         s_slot[tid] = slot;
     }
+    if (tid >= kAppendThreads - half) s_turn[tid - (kAppendThreads - half)] = turn_fraction(a.inv_freq[tid - (kAppendThreads - half)]);
+    __syncthreads();
     for (int i = tid; i < nt * half; i += kAppendThreads) {
         const int t = i / half, p = i - t * half;
-        s_cs[t][p] = angle_cs(static_cast<int64_t>(a.index[t0 + t]) + a.pos_offset, a.inv_freq[p]);
+        s_cs[t][p] = angle_cs(static_cast<uint32_t>(a.index[t0 + t]) + static_cast<uint32_t>(a.pos_offset), s_turn[p]);
     }
     __syncthreads();
 
