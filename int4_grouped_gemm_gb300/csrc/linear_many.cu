@@ -2,11 +2,12 @@
 // fifth-generation tensor cores.
 //
 // As with few tokens no weight is rounded: the codes themselves, exact in bf16
-// (128 + q by a shift and a mask-and-set a pair, less 128), are the M = 128 side
-// of tcgen05.mma, the tokens as they are the N side, and each group of weights
-// has a sum of its own, D = sum q x; then, in fp32 registers,
-//   y += s D + z X,   X = sum of the group's x
-// (With 128 + q as the operand and z - 128 s the subtraction is saved, but D is
+// as q 2^-12 (128 + q by a shift and a mask-and-set a pair, then one fused
+// multiply-add), are the M = 128 side of tcgen05.mma, the tokens as they are the N
+// side, and each group of weights has a sum of its own, D = sum q x 2^-12 (the
+// power keeps it finite for any finite token); then, in fp32 registers,
+//   y += (2^12 s) D + (2^12 z) X,   X = sum of the group's x 2^-12
+// (With 128 + q as the operand and z - 128 s the multiply-add is saved, but D is
 // 17 times as large and y off by 2e-6 instead of 2e-7.)
 // X comes out of the same MMA: the last of each 32 rows of a tile is not a
 // weight row but ones, so that a tile has 4 x 31 weight rows and the last lane of
@@ -292,9 +293,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const int rot = KS == 128 ? (r >> 1) & 3 : (r >> 2) & 1;  // swizzle of the row's 16-byte pieces
         const uint32_t w_addr = smem_u32(sW);
-        // (w & mask) | set: 128 + q as a bf16 pair, or 129 in the last lane
+        // (w & mask) | set: 128 + q as a bf16 pair, or 129 in the last lane; then
+        // (128 + q) 2^-12 - 2^-5, exactly
         const uint32_t mask = lane == 31 ? 0u : 0x000F000Fu, set = lane == 31 ? 0x43014301u : 0x43004300u;
-        const __nv_bfloat162 c128 = u32_as_bf162(0x43004300u);
+        const __nv_bfloat162 down = u32_as_bf162(0x39803980u), off = u32_as_bf162(0xBD00BD00u);
         uint32_t n = 0;                                // steps of the block so far
         bool ok = true;
         for (int tile = first; tile < tiles && ok; tile += step) {
@@ -317,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) p[4 * e + j] = bf162_as_u32(__hsub2(u32_as_bf162(mask_set(q[e] >> (4 * j), mask, set)), c128));
+                        for (int j = 0; j < 4; ++j) p[4 * e + j] = bf162_as_u32(__hfma2(u32_as_bf162(mask_set(q[e] >> (4 * j), mask, set)), down, off));
                     if (!free) {
                         // the MMAs of the step that had this buffer before
                         if (n >= kA) ok = warp_wait(&s->done[(n - kA) % kX], ((n - kA) / kX) & 1, a, s, 47);
@@ -386,8 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int gu = 0; gu < GU; ++gu) {
                     const bool high = GU == 2 ? gu == 1 : (g & 1);
-                    const float scale = __uint_as_float(high ? sw & 0xFFFF0000u : sw << 16);
-                    const float bias = __uint_as_float(high ? bw & 0xFFFF0000u : bw << 16);
+                    const float scale = 4096.f * __uint_as_float(high ? sw & 0xFFFF0000u : sw << 16);
+                    const float bias = 4096.f * __uint_as_float(high ? bw & 0xFFFF0000u : bw << 16);
                     const uint64_t s2 = pack2(__float_as_uint(scale), __float_as_uint(scale));
                     const uint64_t b2 = pack2(__float_as_uint(bias), __float_as_uint(bias));
                     const uint32_t *e = d[gu];

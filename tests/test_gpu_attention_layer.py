@@ -129,6 +129,56 @@ def test_linear_of_packed_weights_repeats_and_replays():
     assert (a.double() - ref).abs().max() < 0.1 * ref.abs().max()
 
 
+@pytest.mark.parametrize("B", [1, 5, 8, 9, 16, 40])
+def test_linear_a_broken_token_stays_alone(B):
+    """NaN and infinity in one token (a padding row, say) leave the others'
+    results as they are, bit for bit."""
+    g = gen(40 + B)
+    m, w = make_int4(g, 150, 256, 64)
+    x = randn(g, B, 256).cuda()
+    want = moe.linear(m, x, dtype=torch.float32)
+    for bad in (float("nan"), float("inf")):
+        broken = x.clone()
+        broken[B // 2, 17] = bad
+        got = moe.linear(m, broken, dtype=torch.float32)
+        for b in range(B):
+            if b == B // 2:
+                assert not torch.isfinite(got[b]).any()
+            else:
+                assert torch.equal(got[b], want[b])
+
+
+@pytest.mark.parametrize("B", [1, 3, 12])
+@pytest.mark.parametrize("top", [1e-38, 1e-20, 1e20, 3e38])
+def test_linear_tokens_of_any_magnitude(B, top):
+    """Tokens whose largest element is tiny, huge or subnormal (the few-token
+    kernel scales by powers of two), and tokens that span 30 binary orders."""
+    g = gen(50)
+    m, w = make_int4(g, 40, 128, 32)
+    w = w * (1.0 if top < 1e30 else 1e-3)     # (the largest results would not be finite)
+    if top >= 1e30:
+        s = m.scale.view(torch.bfloat16).float() * 1e-3
+        z = m.bias.view(torch.bfloat16).float() * 1e-3
+        m = moe.QMatrix(m.q, s.to(torch.bfloat16).view(torch.int16), z.to(torch.bfloat16).view(torch.int16), 40, 128, 32)
+        qs = torch.zeros(40, 128, dtype=torch.float64)
+        words = m.q.cpu().long() & 0xFFFFFFFF
+        for e in range(8):
+            qs[:, e::8] = ((words >> (4 * (e // 2 + 4 * (e % 2)))) & 15).double()
+        sc = m.scale.cpu().view(torch.bfloat16)[:, :4].double().repeat_interleave(32, 1)
+        zc = m.bias.cpu().view(torch.bfloat16)[:, :4].double().repeat_interleave(32, 1)
+        w = qs * sc + zc
+    x = randn(g, B, 128).double()
+    x = x / x.abs().max(1, keepdim=True).values * top
+    x[:, ::3] *= 2.0 ** -15
+    x[:, 1::3] *= 2.0 ** -30
+    x = x.to(torch.bfloat16)
+    y = moe.linear(m, x.cuda(), dtype=torch.float32).cpu().double()
+    want = x.double() @ w.t()
+    # and an element below 2^-31 of the token's largest is off by 2^-40 of that
+    tol = linear_bound(x, w, 128) + x.abs().double().max(1, keepdim=True).values * 2.0 ** -40 * w.abs().sum(1) + 1e-43
+    assert ((y - want).abs() <= tol).all()
+
+
 # ------------------------------------------------------------------- append
 
 
@@ -246,6 +296,62 @@ def test_append_padding_and_bad_places():
     assert torch.equal(vp[1, :, 1], v[0]) and torch.equal(vp[2, :, 15], v[7])
     vp[1, :, 1] = kp[1, :, 1] = vp[2, :, 15] = kp[2, :, 15] = 1.0
     assert (kp == 1).all() and (vp == 1).all()
+
+
+def test_append_on_a_side_stream_and_replayed():
+    """A captured append follows the positions of the moment."""
+    g = gen(33)
+    kp, vp = pools(5, 2, 16, 64, True, fill=0.0)
+    cache = attention.PagedCache(kp, vp)
+    q, k, v = (randn(g, 2, h, 64).cuda() for h in (4, 2, 2))
+    table = torch.tensor([[3, 1], [4, 2]], dtype=torch.int32).cuda()
+    seq = torch.tensor([0, 1], dtype=torch.int32).cuda()
+    index = torch.tensor([0, 0], dtype=torch.int32).cuda()
+    inv = (1e4 ** (-torch.arange(0, 64, 2).double() / 64)).float().cuda()
+    out = torch.zeros_like(q)
+    cache.append(q, k, v, seq, index, table, inv, q_out=out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.append(q, k, v, seq, index, table, inv, q_out=out)
+    for i, j in ((5, 31), (16, 2)):
+        index.copy_(torch.tensor([i, j], dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = rotate64(q.cpu(), torch.tensor([i, j]), inv.cpu(), False)
+        assert ((out.cpu().double() - want).abs() <= rotate_tol(q.cpu(), want, 64, False)).all()
+        for t, at in ((0, i), (1, j)):
+            assert torch.equal(vp[table[t, at // 16], :, at % 16], v[t])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    again = cache.append(q, k, v, seq, index, table, inv, stream=side)
+    side.synchronize()
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("f", [0.0, 1.0, -0.75, 3.0, 100.0, 1e-7, 2 ** -20])
+def test_append_angles_of_any_frequency_far_out(f):
+    """cos and sin of p f by the exact product, p up to 2^31 - 1, f of either
+    sign and beyond a turn per position."""
+    g = gen(34)
+    kp, vp = pools(1, 1, 65536, 64, True)
+    cache = attention.PagedCache(kp, vp)
+    T = 200
+    index = torch.randint(0, 65536, (T,), generator=g)
+    index = torch.unique(index)
+    T = len(index)
+    k = randn(g, T, 1, 64).cuda()
+    inv = torch.full((8,), f)
+    zero = torch.zeros(T, dtype=torch.int32).cuda()
+    for off in (0, 1 << 20, 1 << 30):
+        cache.append(None, k, k, zero, index.int().cuda(), torch.zeros(1, 1, dtype=torch.int32).cuda(), inv.cuda(),
+                     pos_offset=off)
+        # fp64's own cos of a large angle is exact to the product's rounding,
+        # 2^-53 of it: 2^-22 of a radian at 2^31, like the kernel's
+        want = rotate64(k.cpu(), index + off, inv, False)
+        got = kp[0, :, index.cuda()].transpose(0, 1).cpu().double()
+        tol = rotate_tol(k.cpu(), want, 16, False)
+        tol[..., :16] += abs(f) * (index + off).double()[:, None, None] * 2 ** -52 * 8
+        assert ((got - want).abs() <= tol).all()
 
 
 def test_append_without_queries_and_beyond_32_bit_offsets():
@@ -371,6 +477,18 @@ ATTEND = [  # B, Hq, Hkv, D, page, prefix, lens, heads_first
     (100, 32, 4, 64, 64, 1500, [i for i in range(100)], False),
     (9, 56, 8, 128, 1024, 3000, [40, 0, 1, 2, 16, 15, 1025, 900, 7], True),
     (300, 8, 1, 128, 16, 260, [i % 40 for i in range(300)], True),
+    # long among short (pieces per warp), short among long (pieces per block)
+    (41, 8, 1, 128, 16, 0, [9000] + [1] * 40, True),
+    (5, 16, 2, 64, 32, 0, [6000, 1, 5000, 0, 7], False),
+    (41, 8, 1, 64, 16, 200, [2000] + [2] * 40, False),
+    (6, 16, 2, 128, 64, 300, [4000, 3, 2500, -1, 0, 700], True),
+    # the most rows: 8192 of the prefix, 32 blocks of 256
+    (1024, 8, 1, 64, 16, 130, [1 + i % 3 for i in range(1024)], True),
+    (1023, 1, 1, 128, 16, 0, [i % 20 for i in range(1023)], True),
+    # a page of the largest size, and one that holds the whole prefix
+    (2, 8, 1, 64, 65536, 1000, [900, 5], True),
+    # padding at both ends and between
+    (20, 16, 2, 128, 16, 64, [-1, -1, 30, -1, 5] + [-1] * 14 + [17], True),
 ]
 
 
@@ -378,10 +496,13 @@ ATTEND = [  # B, Hq, Hkv, D, page, prefix, lens, heads_first
 def test_attend_against_64_bits(B, Hq, Hkv, D, page, prefix, lens, hf):
     s = Setup(B, Hq, Hkv, D, page, prefix, lens, hf, seed=B + Hq + prefix)
     ws = s.cache.workspace(B, Hq, prefix)
-    out = s.run(ws=ws)
+    # (padding rows keep what out held)
+    out = s.run(out=torch.full_like(s.q, 3.0), ws=ws)
     assert _lib.moe_read_device_status(ws) == 0
     s.check(out)
-    assert torch.equal(out, s.run(ws=ws))   # the same bits again, in the workspace as it is now
+    assert (out[s.seq_len < 0] == 3).all()
+    # the same bits again, in the workspace as it is now
+    assert torch.equal(out, s.run(out=torch.full_like(s.q, 3.0), ws=ws))
 
 
 @pytest.mark.parametrize("k_std,scale", [(6.0, None), (1.0, 0.0), (1.0, -0.3), (30.0, None)])
@@ -498,6 +619,72 @@ def test_attend_replays_with_new_lengths_and_on_two_streams():
         s.run(out=ob, ws=ws2, stream=b)
     torch.cuda.synchronize()
     assert torch.equal(oa, full) and torch.equal(ob, full)
+
+
+def test_attend_pools_that_share_a_buffer_and_offsets_past_32_bits():
+    """Keys and values of a page side by side; pages 2^29 elements apart, so
+    that the prefix's and the rows' pages lie past 2^32 elements."""
+    Hkv, page, D, n_pages = 2, 16, 64, 10
+    stride = 1 << 29
+    buf = torch.full((9 * stride + 2 * Hkv * page * D,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    both = buf.as_strided((n_pages, 2, Hkv, page, D), (stride, Hkv * page * D, page * D, D, 1))
+    cache = attention.PagedCache(both[:, 0], both[:, 1])
+    g = gen(30)
+    P, lens = 21, [18, 3, 0]
+    k, v = randn(g, Hkv, P + 18 + 3, D).cuda(), randn(g, Hkv, P + 18 + 3, D).cuda()
+    prefix = torch.tensor([9, 1], dtype=torch.int32).cuda()
+    table = torch.tensor([[8, 7], [6, 0], [0, 0]], dtype=torch.int32).cuda()
+    Setup._fill(both[:, 0], both[:, 1], prefix, k[:, :P], v[:, :P], page)
+    Setup._fill(both[:, 0], both[:, 1], table[0], k[:, P:P + 18], v[:, P:P + 18], page)
+    Setup._fill(both[:, 0], both[:, 1], table[1, :1], k[:, P + 18:], v[:, P + 18:], page)
+    q = randn(g, 3, 8, D).cuda()
+    out = cache.attend(q, table, torch.tensor(lens, dtype=torch.int32).cuda(), prefix, P)
+    for b, part in enumerate((slice(P, P + 18), slice(P + 18, None), slice(0, 0))):
+        kk, vv = (torch.cat((t[:, :P], t[:, part]), 1).double() for t in (k, v))
+        want = attend64(q[b:b + 1].double(), kk[None], vv[None], 1 / 8)[0]
+        assert ((out[b].double() - want).abs() <= attend_tol(want, vv)).all()
+
+
+def test_attend_slices_of_tables_and_lengths():
+    """Lengths and page lists that start at any int32, as slices do."""
+    s = Setup(7, 8, 1, 128, 16, 100, [5, 30, 0, 1, 16, 17, 50], seed=31)
+    full = s.run().clone()
+    lens = torch.cat((torch.zeros(1, dtype=torch.int32, device="cuda"), s.seq_len))[1:]
+    pages = torch.cat((torch.zeros(3, dtype=torch.int32, device="cuda"), s.prefix_pages))[3:]
+    table = torch.cat((torch.zeros(1, dtype=torch.int32, device="cuda"), s.table.flatten()))[1:].view(7, -1)
+    assert lens.data_ptr() % 16 and pages.data_ptr() % 16 and table.data_ptr() % 16
+    out = s.cache.attend(s.q, table, lens, pages, 100)
+    assert torch.equal(out, full)
+
+
+def test_attend_many_calls_back_to_back():
+    """Calls that follow one another without a pause, of changing shapes in one
+    workspace: kernels of one overlap the end of the one before."""
+    a = Setup(30, 16, 2, 128, 16, 500, [i for i in range(30)], seed=32)
+    b = Setup(3, 16, 2, 128, 16, 0, [900, 20, 1], seed=33)
+    c = Setup(8, 16, 2, 128, 16, 3000, [1] * 8, seed=34)
+    ws = a.cache.workspace(30, 16, 3000)
+    want = [s.run().clone() for s in (a, b, c)]
+    outs = [[torch.zeros_like(w) for w in want] for _ in range(20)]
+    for o in outs:
+        for s, t in zip((a, b, c), o):
+            s.run(out=t, ws=ws)
+    torch.cuda.synchronize()
+    for o in outs:
+        for t, w in zip(o, want):
+            assert torch.equal(t, w)
+    assert _lib.moe_read_device_status(ws) == 0
+
+
+def test_attend_on_a_side_stream_with_its_own_allocations():
+    s = Setup(4, 16, 2, 128, 16, 200, [9, 90, 0, 33], seed=35)
+    want = s.run().clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = [s.run(stream=side) for _ in range(5)]
+    side.synchronize()
+    for o in outs:
+        assert torch.equal(o, want)
 
 
 def test_one_workspace_serves_smaller_calls_in_turn():
