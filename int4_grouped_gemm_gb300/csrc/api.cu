@@ -810,8 +810,8 @@ int int4_linear(const moe_qweight *w, int32_t N, int32_t K, int32_t group, const
     const auto SW0 = CU_TENSOR_MAP_SWIZZLE_NONE;
     if ((rc = encode_2d(&maps[0], CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, w->q, K / 8, N, linear_code_words(group), 128,
                         group == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B)) ||
-        (rc = encode_2d(&maps[1], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->scale, a.ldg, N, 8, 128, SW0)) ||
-        (rc = encode_2d(&maps[2], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->bias, a.ldg, N, 8, 128, SW0)) ||
+        (rc = encode_2d(&maps[1], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->scale, K / group, N, 16, 128, SW0, a.ldg)) ||
+        (rc = encode_2d(&maps[2], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->bias, K / group, N, 16, 128, SW0, a.ldg)) ||
         (rc = encode_2d(&maps[3], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, K, B, 64, linear_token_rows(B),
                         CU_TENSOR_MAP_SWIZZLE_128B, x_stride)))
         return rc;

@@ -6,29 +6,35 @@
 // multiply-add), are the M = 128 side of tcgen05.mma, the tokens as they are the N
 // side, and each group of weights has a sum of its own, D = sum q x 2^-12 (the
 // power keeps it finite for any finite token); then, in fp32 registers,
-//   y += (2^12 s) D + (2^12 z) X,   X = sum of the group's x 2^-12
-// (With 128 + q as the operand and z - 128 s the multiply-add is saved, but D is
-// 17 times as large and y off by 2e-6 instead of 2e-7.)
-// X comes out of the same MMA: the last of each 32 rows of a tile is not a
-// weight row but ones, so that a tile has 4 x 31 weight rows and the last lane of
-// every epilogue warp finds X in its row of D.  The codes go straight into tensor
-// memory, where the MMA reads its first operand from: a thread unpacks one row's
-// 128 codes in registers and stores them to its lane.  What is in shared memory
-// is only what TMA brings: packed codes, scales, and tokens.
+//   y += (2^12 s) D
+// (With 128 + q as the operand and z - 128 s for z, D is 17 times as large and y
+// off by 2e-6 instead of 2e-7.)  The codes go straight into tensor memory, where
+// the MMA reads its first operand from: a thread unpacks one row's 128 codes in
+// registers and stores them to its lane.  What is in shared memory is only what
+// TMA brings (packed codes, scales, tokens) and the token sums.
+//
+// The biases are a small product of their own, sum_g z[n][g] X[b][g] with
+// X = sum of the group's x: for each 16 groups (a chunk) the row's 16 biases,
+// copied to tensor memory as they are, times X as three bf16 parts (24 bits), three MMAs
+// of K = 16 (and a fourth for sums that bf16 cannot hold).  X is the same
+// for every tile of rows, so that it is made once per block, while the first
+// tile's tokens pass by, where shared memory has room for all its chunks.  (With
+// X from a row of ones in every tile and one multiply-add more a value, the
+// epilogue's shuffles set the pace: 64 x 2048 x 131072 took 94 us.)
 //
 //   epilogue     warps 0-7, warp w: rows 32 (w % 4) .., token half w / 4: D from
 //                tensor memory, y in registers
 //   unpacking    warps 8-15, a thread per row, two sets of four in turn
-//   loads, MMA   warps 16 and 17 (18 and 19 complete the warpgroup)
+//   16, 17, 18   loads of weights, MMA, loads of tokens
+//   token sums   warps 20-23
 //
 // A barrier wait costs its role about 130 cycles however early the other side
 // was, so the work goes in steps of 128 k (groups of 32: 64 k) and all that a
 // step's MMAs need comes in on one barrier (`ready`: tokens by TMA, codes from
 // the unpacking warps, the buffer of sums given back by the epilogue), all that
-// waits for them on one other (`done`).  With a barrier for each and steps of 64
-// k, 64 x 2048 x 131072 took 136 us, with steps of 128 k 104.
+// waits for them on one other (`done`).
 //
-// Blocks take tiles of 124 rows in turn.  If there are too few tiles for the
+// Blocks take tiles of 128 rows in turn.  If there are too few tiles for the
 // GPU, a cluster of up to eight blocks shares K and adds up through distributed
 // shared memory.  Every wait is bounded.
 #include <algorithm>
@@ -38,18 +44,23 @@
 namespace moe {
 namespace many {
 
-constexpr int kRows = 124;                 // weight rows of a tile: 31 in each 32 lanes
-constexpr int kEpiWarps = 8, kDeqWarp = 8, kTmaWarp = 16, kMmaWarp = 17, kThreads = 20 * 32;
-// Registers a thread: an epilogue thread of 64 tokens holds 32 sums and 32 of
-// D.  The launch gives 96 to each of the 640 threads (61,440 in all); epilogue,
-// unpacking and the rest then hold 128, 72 and 80 (32,768 + 18,432 + 10,240).
-constexpr int kLaunchRegs = 96, kEpiRegs = 128, kDeqRegs = 72, kRestRegs = 80;
-static_assert(256 * kEpiRegs + 256 * kDeqRegs + 128 * kRestRegs <= kThreads * kLaunchRegs, "shares of the launch's registers");
-constexpr int kW = 6, kS = 3;              // stages: codes, scales (8 groups)
-constexpr int kX = 6, kA = 3;              // stages: tokens in shared memory, codes in tensor memory (64 columns)
+constexpr int kRows = 128;                 // weight rows of a tile
+constexpr int kEpiWarps = 8, kDeqWarp = 8, kWWarp = 16, kMmaWarp = 17, kXWarp = 18, kSumWarp = 20, kSumWarps = 4;
+constexpr int kThreads = 24 * 32;
+// Registers a thread: an epilogue thread of 64 tokens holds 32 sums and 64 of D.
+// The launch gives 80 to each of the 768 threads (61,440 in all); epilogue,
+// unpacking and the rest then hold 120, 64 and 56 (30,720 + 16,384 + 14,336).
+constexpr int kLaunchRegs = 80, kEpiRegs = 120, kDeqRegs = 64, kRestRegs = 56;
+static_assert(256 * kEpiRegs + 256 * kDeqRegs + 256 * kRestRegs <= kThreads * kLaunchRegs, "shares of the launch's registers");
+constexpr int kW = 6, kS = 2;              // stages: codes, scales (a chunk of 16 groups)
+constexpr int kX = 6, kA = 2;              // stages: tokens in shared memory, codes in tensor memory (64 columns)
 constexpr int kD = 2;                      // buffers of group sums, two groups each (128 columns)
-constexpr int kSBytes = 128 * 8 * 2;
-constexpr uint32_t kTmemCols = 512;        // kD * 128 + kA * 64 = 448, rounded up
+constexpr int kChunk = 16, kC = 8;         // groups of a chunk, chunks of token sums in shared memory
+constexpr int kSBytes = 128 * kChunk * 2;
+// Columns: group sums, codes, the bias products (64), a chunk's biases (2 x 8).
+constexpr uint32_t kColA = kD * 128, kColZ = kColA + kA * 64, kColBias = kColZ + 64;
+static_assert(kColBias + 16 <= 512, "tensor memory");
+constexpr uint32_t kTmemCols = 512;        // 464, rounded up
 __host__ __device__ constexpr int step_k(int G) { return G == 32 ? 64 : 128; }
 __host__ __device__ constexpr int w_bytes(int G) { return 128 * step_k(G) / 2; }
 
@@ -58,6 +69,8 @@ __host__ __device__ constexpr int x_bytes(int G, int tok) { return step_k(G) / 6
 struct Ctl {
     uint64_t w_full[kW], w_empty[kW], s_full[kS], s_empty[kS];
     uint64_t ready[kX], done[kX];          // a step's operands and sums are there; its MMAs are complete
+    uint64_t z_full;                       // a chunk's biases are in tensor memory, its products' place is free
+    uint64_t sums_full[kC], x_read[kX];    // a chunk's token sums are there; a stage of tokens has been added up
     uint64_t drain;
     uint32_t tmem;
     int abort;
@@ -67,11 +80,12 @@ struct Ctl {
 // tensor memory.
 __host__ __device__ constexpr int smem_bytes(int G, int tok) {
     constexpr int least = kBlockSmem / 2 + 1024;
-    const int n = kX * x_bytes(G, tok) + kW * w_bytes(G) + kS * 2 * kSBytes + tok * 128 * 4 +
+    const int n = kX * x_bytes(G, tok) + kW * w_bytes(G) + kS * 2 * kSBytes + kC * tok * 128 +
                   static_cast<int>(sizeof(Ctl)) + 1024;
     return n > least ? n : least;
 }
 static_assert(smem_bytes(64, 64) <= kBlockSmem, "one block per SM");
+static_assert(kX * x_bytes(32, 64) >= 64 * 128 * 4, "the cluster's sums lie over the tokens");
 
 struct Maps {
     CUtensorMap q, s, b, x;
@@ -101,6 +115,17 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
     return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts16(uint32_t at, uint16_t v) {
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(v) : "memory");
+}
+__device__ __forceinline__ void sts128_zero(uint32_t at) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
 }
 __device__ __forceinline__ void sts32(uint32_t at, float v) {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
@@ -162,8 +187,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sX = base, *sW = sX + kX * XB, *sS = sW + kW * WB;
-    float *red = reinterpret_cast<float *>(sS + kS * 2 * kSBytes);  // [token][128 lanes]
-    Ctl *s = reinterpret_cast<Ctl *>(red + TOK * 128);
+    uint8_t *sT = sS + kS * 2 * kSBytes;               // token sums: chunks of [token][4 parts][16 groups]
+    Ctl *s = reinterpret_cast<Ctl *>(sT + kC * TOK * 128);
+    float *red = reinterpret_cast<float *>(sX);        // [token][128 lanes], when the last tokens have been read
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < kW; ++i) {
@@ -178,11 +204,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&s->ready[i], 1 + 4 + kEpiWarps);  // the loads' own arrival, unpacking warps, epilogue warps
             mbar_init(&s->done[i], 1);
         }
+        mbar_init(&s->z_full, kEpiWarps);
+        for (int i = 0; i < kC; ++i) mbar_init(&s->sums_full[i], kSumWarps);
+        for (int i = 0; i < kX; ++i) mbar_init(&s->x_read[i], kSumWarps);
         mbar_init(&s->drain, 1);
         s->abort = 0;
         fence_mbar_init();
     }
-    if (warp == kTmaWarp && lane == 0) {
+    if (warp == kWWarp && lane == 0) {
         prefetch_tmap(&maps.q);
         prefetch_tmap(&maps.s);
         prefetch_tmap(&maps.b);
@@ -196,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s->tmem;                     // group sums, then codes
-    const uint32_t tA = tmem + kD * 128;
+    const uint32_t tA = tmem + kColA, tZ = tmem + kColZ, tB = tmem + kColBias;
     pdl_wait();
     pdl_trigger();
 
@@ -204,28 +233,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int u0 = units * rank / a.split, u1 = units * (rank + 1) / a.split;
     const int tiles = (a.N + kRows - 1) / kRows, step = gridDim.x / a.split;
     const int first = blockIdx.x / a.split;
+    // The token sums are the same for every tile: made in the first one, if all
+    // chunks of this block's k have a place, else in each.
+    const int c0 = u0 * GU / kChunk;
+    const bool once = (u1 * GU - 1) / kChunk - c0 < kC;
+    // the last step of a chunk
+    auto ends = [&](int u) { return u == u1 - 1 || (u + 1) * GU % kChunk == 0; };
 
-    if (warp >= kTmaWarp) {
+    if (warp >= kWWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
-    if (warp == kTmaWarp) {
-        if (lane == 0) {
+    if (warp == kWWarp) {
+        if (elect_one()) {
             Ring<kW> w;
-            Ring<kX> x;
             Ring<kS> sc;
-            uint32_t n_w = 0, n_s = 0, n_x = 0;
+            uint32_t n_w = 0, n_s = 0;
             bool ok = true;
             for (int tile = first; tile < tiles && ok; tile += step) {
-                int block = -1;
-                for (int u = u0; u < u1 && ok; ++u) {
-                    const int need = u * GU / 8;       // block of 8 groups that the step's lie in
-                    if (need != block) {
-                        block = need;
+                for (int u = u0; u < u1; ++u) {
+                    if (u == u0 || u * GU % kChunk == 0) {
                         ok = wait(&s->s_empty[sc.i], sc.ph ^ 1, a, s, 40);
                         if (!ok) break;
                         mbar_arrive_expect_tx(&s->s_full[sc.i], 2 * kSBytes);
                         uint8_t *dst = sS + sc.i * 2 * kSBytes;
-                        tma_load_2d(dst, &maps.s, &s->s_full[sc.i], block * 8, tile * kRows);
-                        tma_load_2d(dst + kSBytes, &maps.b, &s->s_full[sc.i], block * 8, tile * kRows);
+                        const int g = u * GU / kChunk * kChunk;
+                        tma_load_2d(dst, &maps.s, &s->s_full[sc.i], g, tile * kRows);
+                        tma_load_2d(dst + kSBytes, &maps.b, &s->s_full[sc.i], g, tile * kRows);
                         sc.next();
                         ++n_s;
                     }
@@ -235,8 +267,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_2d(sW + w.i * WB, &maps.q, &s->w_full[w.i], u * (KS / 8), tile * kRows);
                     w.next();
                     ++n_w;
-                    // the slot's previous step (kX before this one) is complete
+                }
+            }
+            // no copy of this block is in flight when it ends
+            for (uint32_t i = n_w > kW ? n_w - kW : 0; i < n_w; ++i) mbar_wait(&s->w_full[i % kW], (i / kW) & 1, a.wait_limit);
+            for (uint32_t i = n_s > kS ? n_s - kS : 0; i < n_s; ++i) mbar_wait(&s->s_full[i % kS], (i / kS) & 1, a.wait_limit);
+        }
+        __syncwarp();
+    } else if (warp == kXWarp) {
+        if (elect_one()) {
+            Ring<kX> x;
+            uint32_t n_x = 0;
+            bool ok = true;
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                for (int u = u0; u < u1; ++u) {
+                    // the slot's previous step (kX before this one) is complete, and
+                    // its tokens have been added up
                     ok = wait(&s->done[x.i], x.ph ^ 1, a, s, 42);
+                    if (ok && (!once || n_x < static_cast<uint32_t>(u1 - u0 + kX))) ok = wait(&s->x_read[x.i], x.ph ^ 1, a, s, 44);
                     if (!ok) break;
                     mbar_arrive_expect_tx(&s->ready[x.i], XB);
 #pragma unroll
@@ -246,32 +294,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++n_x;
                 }
             }
-            // no copy of this block is in flight when it ends.  (The tokens' phases
-            // also wait for other arrivals, which after a timeout elsewhere may
-            // not come: the wait then runs out, long after the copies landed.)
-            for (uint32_t i = n_w > kW ? n_w - kW : 0; i < n_w; ++i) mbar_wait(&s->w_full[i % kW], (i / kW) & 1, a.wait_limit);
+            // nor one of these.  (The phases also wait for other arrivals, which after
+            // a timeout elsewhere may not come: the wait then runs out, long after
+            // the copies landed.)
             for (uint32_t i = n_x > kX ? n_x - kX : 0; i < n_x; ++i)
                 if (!mbar_wait(&s->ready[i % kX], (i / kX) & 1, a.wait_limit)) break;
-            for (uint32_t i = n_s > kS ? n_s - kS : 0; i < n_s; ++i) mbar_wait(&s->s_full[i % kS], (i / kS) & 1, a.wait_limit);
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
         if (elect_one()) {
             constexpr uint32_t idesc = idesc_bf16(128, TOK);
             Ring<kX> x;
-            uint32_t ab = 0, db = 0;
+            uint32_t ab = 0, db = 0, chunk = 0;        // chunks of the block so far
             bool ok = true;
-            const uint32_t x_addr = smem_u32(sX);
+            // (a descriptor's address field counts 16 bytes)
+            const uint64_t x_desc = sdesc_k128(smem_u32(sX)), t_desc = sdesc_k128(smem_u32(sT));
             for (int tile = first; tile < tiles && ok; tile += step) {
                 for (int u = u0; u < u1; ++u) {
                     ok = wait(&s->ready[x.i], x.ph, a, s, 43);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t xa = x_addr + x.i * XB, at = tA + ab * 64, dt = tmem + db * 128;
+                    const uint64_t xd = x_desc + x.i * (XB / 16);
+                    const uint32_t at = tA + ab * 64, dt = tmem + db * 128;
 #pragma unroll
                     for (int kk = 0; kk < KS / 16; ++kk)
-                        umma_bf16_ts(dt + kk / (G / 16) * 64, at + kk * 8, sdesc_k128(xa + (kk / 4) * (TOK * 128) + (kk % 4) * 32),
+                        umma_bf16_ts(dt + kk / (G / 16) * 64, at + kk * 8, xd + (kk / 4) * (TOK * 8) + (kk % 4) * 2,
                                      idesc, kk % (G / 16) != 0);
+                    if (ends(u)) {
+                        // the chunk's biases times the three parts of its token sums, and 2^12
+                        // times the biases times what was too large for those
+                        const uint32_t slot = once ? u * GU / kChunk - c0 : chunk % kC;
+                        ok = wait(&s->z_full, chunk & 1, a, s, 45);
+                        if (ok && (!once || tile == first)) ok = wait(&s->sums_full[slot], once ? 0 : (chunk / kC) & 1, a, s, 50);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int part = 0; part < 4; ++part)
+                            umma_bf16_ts(tZ, tB + part / 3 * 8, t_desc + slot * (TOK * 8) + part * 2, idesc, part != 0);
+                        ++chunk;
+                    }
                     umma_commit(&s->done[x.i]);
                     x.next();
                     ab = ab + 1 == kA ? 0 : ab + 1;
@@ -283,19 +344,84 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait(&s->drain, 0, a.wait_limit);
         }
         __syncwarp();
+    } else if (warp >= kSumWarp) {
+        // ----------------------------------------------------- token sums
+        // Two lanes a token (TOK of the 64 pairs): each adds up 64 k of a step
+        // (groups of 32: one of two groups, groups of 128: half of one).
+        const int pair = (tid - kSumWarp * 32) >> 1, h = tid & 1, t = min(pair, TOK - 1);
+        const bool mine = pair < TOK;
+        const uint32_t x_row = smem_u32(sX) + t * 128, t_row = smem_u32(sT) + t * 128;
+        const uint32_t sw = (t & 7) << 4;              // 128-byte swizzle
+        Ring<kX> x;
+        uint32_t chunk = 0;
+        bool ok = true;
+        for (int tile = first; tile < tiles && ok; tile += step) {
+            if (once && tile != first) break;
+            for (int u = u0; u < u1; ++u) {
+                ok = warp_wait(&s->ready[x.i], x.ph, a, s, 52);
+                if (!ok) break;
+                const uint32_t dst = t_row + chunk % kC * (TOK * 128);
+                if (mine && (u == u0 || u * GU % kChunk == 0)) {
+                    // groups that this block has no share of count as zero.  (The
+                    // chunk that had the place before was multiplied long since:
+                    // the sums of step n - 2, of another chunk, have been read.)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sts128_zero(dst + (((4 * h + i) << 4) ^ sw));
+                }
+                __syncwarp();
+                const uint32_t src = x_row + x.i * XB + (KS == 128 ? h * (TOK * 128) : 0);
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < KS / 16; ++i) {
+                    // the pair's pieces fall on different banks
+                    const uint4 v = lds128(src + ((KS == 128 ? (i ^ 4 * h) << 4 : (4 * h + i) << 4) ^ sw));
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        sum[j] = fmaf(__uint_as_float(w[j] << 16), 0x1p-7f, sum[j]);
+                        sum[j] = fmaf(__uint_as_float(w[j] & 0xFFFF0000u), 0x1p-7f, sum[j]);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s->x_read[x.i]);
+                float X = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                if constexpr (GU == 1) X += __shfl_xor_sync(0xffffffffu, X, 1);
+                // X 2^-7, exact down to the smallest token and finite up to the largest.
+                // X in three parts of 8 bits is exact to 2^-25; one that is too large
+                // for that has 2^-12 of its first 8 bits in the fourth place.
+                if (mine && (GU == 2 || h == 0)) {
+                    float top = 0.f;
+                    if (fabsf(X) >= 0x1p118f) top = __bfloat162float(__float2bfloat16_rn(X * 0x1p-5f));
+                    X = fmaf(top, -32.f, X) * 128.f;
+                    const int at = (GU == 2 ? 2 * u + h : u) % kChunk * 2;
+#pragma unroll
+                    for (int part = 0; part < 3; ++part) {
+                        const __nv_bfloat16 b = __float2bfloat16_rn(X);
+                        sts16(dst + ((part * 32 + at) ^ sw), __bfloat16_as_ushort(b));
+                        X -= __bfloat162float(b);
+                    }
+                    if (top != 0.f) sts16(dst + ((96 + at) ^ sw), __bfloat16_as_ushort(__float2bfloat16_rn(top)));
+                }
+                if (ends(u)) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s->sums_full[chunk % kC]);
+                    ++chunk;
+                }
+                x.next();
+            }
+        }
     }
     } else if (warp >= kDeqWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDeqRegs));
         // ------------------------------------------------------- unpacking
         // the two sets of four warps take the steps in turn
         const int quarter = warp & 3, set_of = (warp - kDeqWarp) >> 2;
-        const int r = quarter * 31 + min(lane, 30);    // row of the tile
+        const int r = quarter * 32 + lane;             // row of the tile
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const int rot = KS == 128 ? (r >> 1) & 3 : (r >> 2) & 1;  // swizzle of the row's 16-byte pieces
         const uint32_t w_addr = smem_u32(sW);
-        // (w & mask) | set: 128 + q as a bf16 pair, or 129 in the last lane; then
-        // (128 + q) 2^-12 - 2^-5, exactly
-        const uint32_t mask = lane == 31 ? 0u : 0x000F000Fu, set = lane == 31 ? 0x43014301u : 0x43004300u;
+        // 128 + q as a bf16 pair, then (128 + q) 2^-12 - 2^-5, exactly
         const __nv_bfloat162 down = u32_as_bf162(0x39803980u), off = u32_as_bf162(0xBD00BD00u);
         uint32_t n = 0;                                // steps of the block so far
         bool ok = true;
@@ -319,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) p[4 * e + j] = bf162_as_u32(__hfma2(u32_as_bf162(mask_set(q[e] >> (4 * j), mask, set)), down, off));
+                        for (int j = 0; j < 4; ++j) p[4 * e + j] = bf162_as_u32(__hfma2(u32_as_bf162(mask_set(q[e] >> (4 * j), 0x000F000Fu, 0x43004300u)), down, off));
                     if (!free) {
                         // the MMAs of the step that had this buffer before
                         if (n >= kA) ok = warp_wait(&s->done[(n - kA) % kX], ((n - kA) / kX) & 1, a, s, 47);
@@ -340,9 +466,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
         // -------------------------------------------------------- epilogue
         const int half = warp >> 2, quarter = warp & 3;
-        const int r = quarter * 31 + min(lane, 30);    // row of the tile (the last lane: X)
+        const int r = quarter * 32 + lane;             // row of the tile
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t s_addr = smem_u32(sS) + r * 16;
+        const uint32_t s_addr = smem_u32(sS) + r * (kChunk * 2);
         Ring<kS> sc;
         Ring<kX> x;                                    // step
         uint32_t ahead = kD, db = 0;                   // slot of the step that gets this one's buffer of sums
@@ -354,20 +480,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t y[TW / 2];
 #pragma unroll
             for (int i = 0; i < TW / 2; ++i) y[i] = 0;
-            int block = -1;
-            uint4 sv = make_uint4(0u, 0u, 0u, 0u), bv = sv;
-            for (int g = u0 * GU; g < u1 * GU && ok; g += GU) {
-                if (g / 8 != block) {
-                    // the row's scales and biases of eight groups
-                    block = g / 8;
+            for (int u = u0; u < u1; ++u) {
+                if (u == u0 || u * GU % kChunk == 0) {
+                    // the row's biases of the chunk are the first operand of its bias
+                    // products.  (The last chunk's are complete, and have been read.)
                     ok = warp_wait(&s->s_full[sc.i], sc.ph, a, s, 48);
                     if (!ok) break;
-                    sv = lds128(s_addr + sc.i * 2 * kSBytes);
-                    bv = lds128(s_addr + sc.i * 2 * kSBytes + kSBytes);
+                    if (half == 0) {
+                        const uint32_t at = s_addr + sc.i * 2 * kSBytes + kSBytes;
+                        const uint4 lo = lds128(at), hi = lds128(at + 16);
+                        uint32_t b[16] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                        // (2^12 z stays finite, as its factor is mostly zero)
+                        const __nv_bfloat162 most = u32_as_bf162(0x7F7F7F7Fu), least = u32_as_bf162(0xFF7FFF7Fu);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            b[8 + i] = bf162_as_u32(__hmax2(least, __hmin2(most, __hmul2(u32_as_bf162(b[i]), u32_as_bf162(0x45804580u)))));
+                        tmem_st16(tB | lanes, b);
+                        tmem_st_wait();
+                    }
+                    tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&s->s_empty[sc.i]);
-                    sc.next();
+                    if (lane == 0) mbar_arrive(&s->z_full);
                 }
+                const uint32_t pair = lds32(s_addr + sc.i * 2 * kSBytes + (u * GU % kChunk >> 1) * 4);
                 ok = warp_wait(&s->done[x.i], x.ph, a, s, 49);
                 if (!ok) break;
                 tc_fence_after();
@@ -382,52 +517,55 @@ __global__ void __launch_bounds__(kThreads, 1)
                 x.next();
                 ahead = ahead + 1 == kX ? 0 : ahead + 1;
                 db ^= 1;
-                const int pair = (g & 7) >> 1;
-                const uint32_t sw = pair == 0 ? sv.x : pair == 1 ? sv.y : pair == 2 ? sv.z : sv.w;
-                const uint32_t bw = pair == 0 ? bv.x : pair == 1 ? bv.y : pair == 2 ? bv.z : bv.w;
 #pragma unroll
                 for (int gu = 0; gu < GU; ++gu) {
-                    const bool high = GU == 2 ? gu == 1 : (g & 1);
-                    const float scale = 4096.f * __uint_as_float(high ? sw & 0xFFFF0000u : sw << 16);
-                    const float bias = 4096.f * __uint_as_float(high ? bw & 0xFFFF0000u : bw << 16);
+                    const bool high = GU == 2 ? gu == 1 : (u & 1);
+                    const float scale = 4096.f * __uint_as_float(high ? pair & 0xFFFF0000u : pair << 16);
                     const uint64_t s2 = pack2(__float_as_uint(scale), __float_as_uint(scale));
-                    const uint64_t b2 = pack2(__float_as_uint(bias), __float_as_uint(bias));
-                    const uint32_t *e = d[gu];
 #pragma unroll
-                    for (int i = 0; i < TW / 4; ++i) {
-                        // X is the last lane's D
-                        uint4 X;
-                        X.x = __shfl_sync(0xffffffffu, e[4 * i], 31);
-                        X.y = __shfl_sync(0xffffffffu, e[4 * i + 1], 31);
-                        X.z = __shfl_sync(0xffffffffu, e[4 * i + 2], 31);
-                        X.w = __shfl_sync(0xffffffffu, e[4 * i + 3], 31);
-                        y[2 * i] = fma2(s2, pack2(e[4 * i], e[4 * i + 1]), fma2(b2, pack2(X.x, X.y), y[2 * i]));
-                        y[2 * i + 1] =
-                            fma2(s2, pack2(e[4 * i + 2], e[4 * i + 3]), fma2(b2, pack2(X.z, X.w), y[2 * i + 1]));
-                    }
+                    for (int i = 0; i < TW / 2; ++i) y[i] = fma2(s2, pack2(d[gu][2 * i], d[gu][2 * i + 1]), y[i]);
+                }
+                if (ends(u)) {
+                    uint32_t z[TW];
+                    tmem_ld<TW>((tZ + half * TW) | lanes, z);
+                    tmem_wait<TW>(z);
+#pragma unroll
+                    for (int i = 0; i < TW / 2; ++i) y[i] = add2(y[i], pack2(z[2 * i], z[2 * i + 1]));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s->s_empty[sc.i]);
+                    sc.next();
                 }
             }
-            if (a.split == 1) {
-                if (!ok) break;
-                const int row = tile * kRows + r;
-                if (lane < 31 && row < a.N) {
+            if (!ok) break;
+            const int row = tile * kRows + r, t0 = half * TW;
+            if (a.split > 1) {
+                const uint32_t at = smem_u32(red) + (t0 * 128 + r) * 4;
 #pragma unroll
-                    for (int i = 0; i < TW / 2; ++i) {
-                        const float2 v = unpack2(y[i]);
-                        const int t = half * TW + 2 * i;
-                        if (t < a.B) a.store(t, row, v.x);
-                        if (t + 1 < a.B) a.store(t + 1, row, v.y);
-                    }
+                for (int i = 0; i < TW / 2; ++i) {
+                    const float2 v = unpack2(y[i]);
+                    sts32(at + i * 1024, v.x);
+                    sts32(at + i * 1024 + 512, v.y);
                 }
                 continue;
             }
+            // the MMAs of the next tile wait for these warps: a loop without branches
+            // for each type (through LinearArgs::store, a tile's end took 6500 cycles)
+            const int nt = row < a.N ? a.B - t0 : 0;
+            auto put = [&](auto *out, auto narrow) {
+                out += t0 * a.y_stride + row;
 #pragma unroll
-            for (int i = 0; i < TW / 2; ++i) {
-                const float2 v = unpack2(y[i]);
-                const uint32_t at = smem_u32(red) + ((half * TW + 2 * i) * 128 + quarter * 32 + lane) * 4;
-                sts32(at, v.x);
-                sts32(at + 512, v.y);
-            }
+                for (int i = 0; i < TW / 2; ++i) {
+                    const float2 v = unpack2(y[i]);
+                    if (2 * i < nt) *out = narrow(v.x);
+                    out += a.y_stride;
+                    if (2 * i + 1 < nt) *out = narrow(v.y);
+                    out += a.y_stride;
+                }
+            };
+            if (a.y_fp32)
+                put(static_cast<float *>(a.y), [](float v) { return v; });
+            else
+                put(static_cast<__nv_bfloat16 *>(a.y), [](float v) { return __float2bfloat16_rn(v); });
         }
     }
 
@@ -442,8 +580,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         cluster_sync();
         const int per = (a.B + a.split - 1) / a.split, t0 = rank * per, t1 = min(a.B, t0 + per);
         for (int i = tid; i < (t1 - t0) * 128; i += kThreads) {
-            const int t = t0 + i / 128, l = i % 128, row = first * kRows + l / 32 * 31 + l % 32;
-            if (l % 32 == 31 || row >= a.N) continue;
+            const int t = t0 + i / 128, l = i % 128, row = first * kRows + l;
+            if (row >= a.N) continue;
             float sum = 0.f;
             for (int p = 0; p < a.split; ++p) sum += dsmem_ld(smem_u32(red + t * 128 + l), p);
             a.store(t, row, sum);
