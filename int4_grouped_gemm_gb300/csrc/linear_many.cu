@@ -109,6 +109,14 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const 
     return __all_sync(0xffffffffu, wait(bar, parity, a, s, site));
 }
 
+// By predicate, without a branch.
+__device__ __forceinline__ void first_lane_arrives(int lane, uint64_t *bar) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(
+                     smem_u32(bar)),
+                 "r"(lane)
+                 : "memory");
+}
+
 // Shared memory by its own address: through a plain pointer these become generic
 // accesses, with several times the latency.
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
@@ -383,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s->x_read[x.i]);
+                first_lane_arrives(lane, &s->x_read[x.i]);
                 float X = (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 if constexpr (GU == 1) X += __shfl_xor_sync(0xffffffffu, X, 1);
                 // X 2^-7, exact down to the smallest token and finite up to the largest.
@@ -405,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ends(u)) {
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&s->sums_full[chunk % kC]);
+                    first_lane_arrives(lane, &s->sums_full[chunk % kC]);
                     ++chunk;
                 }
                 x.next();
@@ -436,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < KS / 32; ++i) v[i] = lds128(row + ((i ^ rot) << 4));
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s->w_empty[ws]);
+                first_lane_arrives(lane, &s->w_empty[ws]);
                 bool free = false;
 #pragma unroll
                 for (int i = 0; i < KS / 32; ++i) {
@@ -459,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s->ready[n % kX]);
+                first_lane_arrives(lane, &s->ready[n % kX]);
             }
         }
     } else {
@@ -500,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&s->z_full);
+                    first_lane_arrives(lane, &s->z_full);
                 }
                 const uint32_t pair = lds32(s_addr + sc.i * 2 * kSBytes + (u * GU % kChunk >> 1) * 4);
                 ok = warp_wait(&s->done[x.i], x.ph, a, s, 49);
@@ -513,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int gu = 0; gu < GU; ++gu) tmem_wait<TW>(d[gu]);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s->ready[ahead]);
+                first_lane_arrives(lane, &s->ready[ahead]);
                 x.next();
                 ahead = ahead + 1 == kX ? 0 : ahead + 1;
                 db ^= 1;
@@ -532,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < TW / 2; ++i) y[i] = add2(y[i], pack2(z[2 * i], z[2 * i + 1]));
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&s->s_empty[sc.i]);
+                    first_lane_arrives(lane, &s->s_empty[sc.i]);
                     sc.next();
                 }
             }
