@@ -808,8 +808,11 @@ int int4_linear(const moe_qweight *w, int32_t N, int32_t K, int32_t group, const
     if (B <= kFewTokens) return cuda_rc(launch_linear_few(a, dev->num_sms, stream));
     CUtensorMap maps[4];
     const auto SW0 = CU_TENSOR_MAP_SWIZZLE_NONE;
-    if ((rc = encode_2d(&maps[0], CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, w->q, K / 8, N, linear_code_words(group), 128,
-                        group == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B)) ||
+    const int words = linear_code_words(group, B);
+    if ((rc = encode_2d(&maps[0], CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, w->q, K / 8, N, words, 128,
+                        words == 8    ? CU_TENSOR_MAP_SWIZZLE_32B
+                        : words == 16 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                      : CU_TENSOR_MAP_SWIZZLE_128B)) ||
         (rc = encode_2d(&maps[1], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->scale, K / group, N, 16, 128, SW0, a.ldg)) ||
         (rc = encode_2d(&maps[2], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->bias, K / group, N, 16, 128, SW0, a.ldg)) ||
         (rc = encode_2d(&maps[3], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, K, B, 64, linear_token_rows(B),

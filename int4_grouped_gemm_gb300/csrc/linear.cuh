@@ -38,11 +38,11 @@ struct LinearArgs {
 
 // 1 to 8 tokens.
 cudaError_t launch_linear_few(const LinearArgs &a, int num_sms, cudaStream_t s);
-// 9 to 64 tokens; maps: codes (u32, boxes of linear_code_words(G) x 128 rows,
-// swizzled over their width), scales, biases (u16, 8 x 128 rows), tokens (bf16, 64 x linear_token_rows(B),
-// 128-byte swizzle).
+// 9 to 64 tokens; maps: codes (u32, boxes of linear_code_words(G, B) x 128 rows,
+// swizzled over their width), scales, biases (u16, 16 x 128 rows), tokens (bf16,
+// 64 x linear_token_rows(B), 128-byte swizzle).
 int linear_token_rows(int B);
-int linear_code_words(int G);
+int linear_code_words(int G, int B);
 cudaError_t launch_linear_many(const CUtensorMap *maps, const LinearArgs &a, int num_sms, cudaStream_t s);
 
 }  // namespace moe

@@ -29,7 +29,7 @@
 //   token sums   warps 20-23
 //
 // A barrier wait costs its role about 130 cycles however early the other side
-// was, so the work goes in steps of 128 k (groups of 32: 64 k) and all that a
+// was, so the work goes in steps of 64 to 256 k and all that a
 // step's MMAs need comes in on one barrier (`ready`: tokens by TMA, codes from
 // the unpacking warps, the buffer of sums given back by the epilogue), all that
 // waits for them on one other (`done`).
@@ -52,22 +52,31 @@ constexpr int kThreads = 24 * 32;
 // unpacking and the rest then hold 120, 64 and 56 (30,720 + 16,384 + 14,336).
 constexpr int kLaunchRegs = 80, kEpiRegs = 120, kDeqRegs = 64, kRestRegs = 56;
 static_assert(256 * kEpiRegs + 256 * kDeqRegs + 256 * kRestRegs <= kThreads * kLaunchRegs, "shares of the launch's registers");
-constexpr int kW = 6, kS = 2;              // stages: codes, scales (a chunk of 16 groups)
-constexpr int kX = 6, kA = 2;              // stages: tokens in shared memory, codes in tensor memory (64 columns)
-constexpr int kD = 2;                      // buffers of group sums, two groups each (128 columns)
+constexpr int kMaxW = 6, kS = 2;           // stages: codes (at most), scales (a chunk of 16 groups)
+constexpr int kX = 6, kA = 2;              // stages: tokens in shared memory, codes in tensor memory
+constexpr int kD = 2;                      // buffers of a step's group sums
 constexpr int kChunk = 16, kC = 8;         // groups of a chunk, chunks of token sums in shared memory
 constexpr int kSBytes = 128 * kChunk * 2;
-// Columns: group sums, codes, the bias products (64), a chunk's biases (2 x 8).
-constexpr uint32_t kColA = kD * 128, kColZ = kColA + kA * 64, kColBias = kColZ + 64;
-static_assert(kColBias + 16 <= 512, "tensor memory");
-constexpr uint32_t kTmemCols = 512;        // 464, rounded up
-__host__ __device__ constexpr int step_k(int G) { return G == 32 ? 64 : 128; }
-__host__ __device__ constexpr int w_bytes(int G) { return 128 * step_k(G) / 2; }
-
-__host__ __device__ constexpr int x_bytes(int G, int tok) { return step_k(G) / 64 * tok * 128; }  // boxes of 64 k
+// k of a step: the longer, the fewer waits; tensor memory has to hold two steps'
+// codes (a column for each two k) and group sums.
+__host__ __device__ constexpr int step_k(int G, int tok) {
+    return tok == 16 ? (G == 32 ? 128 : 256) : tok == 32 ? (G == 128 ? 256 : 128) : (G == 32 ? 64 : 128);
+}
+// Columns: group sums, codes, the bias products, a chunk's biases (2 x 8).
+__host__ __device__ constexpr int d_cols(int G, int tok) { return step_k(G, tok) / G * tok; }
+__host__ __device__ constexpr int tmem_cols(int G, int tok) { return kD * d_cols(G, tok) + kA * step_k(G, tok) / 2 + tok + 16; }
+constexpr uint32_t kTmemCols = 512;
+static_assert(tmem_cols(32, 16) <= 512 && tmem_cols(64, 16) <= 512 && tmem_cols(128, 16) <= 512 && tmem_cols(32, 32) <= 512 &&
+                  tmem_cols(64, 32) <= 512 && tmem_cols(128, 32) <= 512 && tmem_cols(32, 64) <= 512 &&
+                  tmem_cols(64, 64) <= 512 && tmem_cols(128, 64) <= 512,
+              "tensor memory");
+__host__ __device__ constexpr int w_bytes(int G, int tok) { return 128 * step_k(G, tok) / 2; }
+__host__ __device__ constexpr int x_bytes(int G, int tok) { return step_k(G, tok) / 64 * tok * 128; }  // boxes of 64 k
+// stages of codes: about 48 KB
+__host__ __device__ constexpr int w_stages(int G, int tok) { return step_k(G, tok) == 256 ? 4 : 6; }
 
 struct Ctl {
-    uint64_t w_full[kW], w_empty[kW], s_full[kS], s_empty[kS];
+    uint64_t w_full[kMaxW], w_empty[kMaxW], s_full[kS], s_empty[kS];
     uint64_t ready[kX], done[kX];          // a step's operands and sums are there; its MMAs are complete
     uint64_t z_full;                       // a chunk's biases are in tensor memory, its products' place is free
     uint64_t sums_full[kC], x_read[kX];    // a chunk's token sums are there; a stage of tokens has been added up
@@ -80,12 +89,14 @@ struct Ctl {
 // tensor memory.
 __host__ __device__ constexpr int smem_bytes(int G, int tok) {
     constexpr int least = kBlockSmem / 2 + 1024;
-    const int n = kX * x_bytes(G, tok) + kW * w_bytes(G) + kS * 2 * kSBytes + kC * tok * 128 +
+    const int n = kX * x_bytes(G, tok) + w_stages(G, tok) * w_bytes(G, tok) + kS * 2 * kSBytes + kC * tok * 128 +
                   static_cast<int>(sizeof(Ctl)) + 1024;
     return n > least ? n : least;
 }
 static_assert(smem_bytes(64, 64) <= kBlockSmem, "one block per SM");
-static_assert(kX * x_bytes(32, 64) >= 64 * 128 * 4, "the cluster's sums lie over the tokens");
+static_assert(kX * x_bytes(32, 64) >= 64 * 128 * 4 && kX * x_bytes(32, 32) >= 32 * 128 * 4 &&
+                  kX * x_bytes(32, 16) >= 16 * 128 * 4,
+              "the cluster's sums lie over the tokens");
 
 struct Maps {
     CUtensorMap q, s, b, x;
@@ -190,8 +201,9 @@ template <int G, int TOK>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_many_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LinearArgs a) {
     constexpr int TW = TOK / 2;                        // tokens of an epilogue warp
-    constexpr int KS = step_k(G), GU = KS / G;         // k and groups (one or two) of a step
-    constexpr int XB = x_bytes(G, TOK), WB = w_bytes(G), WROW = KS / 2;
+    constexpr int KS = step_k(G, TOK), GU = KS / G;    // k and groups of a step
+    constexpr int XB = x_bytes(G, TOK), WB = w_bytes(G, TOK), WROW = KS / 2, kW = w_stages(G, TOK);
+    constexpr int DC = d_cols(G, TOK);                 // columns of a step's sums; of its codes: KS / 2
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sX = base, *sW = sX + kX * XB, *sS = sW + kW * WB;
@@ -233,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s->tmem;                     // group sums, then codes
-    const uint32_t tA = tmem + kColA, tZ = tmem + kColZ, tB = tmem + kColBias;
+    const uint32_t tA = tmem + kD * DC, tZ = tA + kA * KS / 2, tB = tZ + TOK;
     pdl_wait();
     pdl_trigger();
 
@@ -323,10 +335,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t xd = x_desc + x.i * (XB / 16);
-                    const uint32_t at = tA + ab * 64, dt = tmem + db * 128;
+                    const uint32_t at = tA + ab * (KS / 2), dt = tmem + db * DC;
 #pragma unroll
                     for (int kk = 0; kk < KS / 16; ++kk)
-                        umma_bf16_ts(dt + kk / (G / 16) * 64, at + kk * 8, xd + (kk / 4) * (TOK * 8) + (kk % 4) * 2,
+                        umma_bf16_ts(dt + kk / (G / 16) * TOK, at + kk * 8, xd + (kk / 4) * (TOK * 8) + (kk % 4) * 2,
                                      idesc, kk % (G / 16) != 0);
                     if (ends(u)) {
                         // the chunk's biases times the three parts of its token sums, and 2^12
@@ -354,8 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp >= kSumWarp) {
         // ----------------------------------------------------- token sums
-        // Two lanes a token (TOK of the 64 pairs): each adds up 64 k of a step
-        // (groups of 32: one of two groups, groups of 128: half of one).
+        // Two lanes a token (TOK of the 64 pairs).  Of each 128 k of a step a lane
+        // adds up 64 (of a step of 64, a group of 32).
         const int pair = (tid - kSumWarp * 32) >> 1, h = tid & 1, t = min(pair, TOK - 1);
         const bool mine = pair < TOK;
         const uint32_t x_row = smem_u32(sX) + t * 128, t_row = smem_u32(sT) + t * 128;
@@ -377,31 +389,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 4; ++i) sts128_zero(dst + (((4 * h + i) << 4) ^ sw));
                 }
                 __syncwarp();
-                const uint32_t src = x_row + x.i * XB + (KS == 128 ? h * (TOK * 128) : 0);
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                // the sum of 16 k after 16 k, the pair's pieces on different banks
+                auto add_up = [&](uint32_t src, int piece, int n) {
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < KS / 16; ++i) {
-                    // the pair's pieces fall on different banks
-                    const uint4 v = lds128(src + ((KS == 128 ? (i ^ 4 * h) << 4 : (4 * h + i) << 4) ^ sw));
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    for (int i = 0; i < n; ++i) {
+                        const uint4 v = lds128(src + (((piece ^ i) << 4) ^ sw));
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        sum[j] = fmaf(__uint_as_float(w[j] << 16), 0x1p-7f, sum[j]);
-                        sum[j] = fmaf(__uint_as_float(w[j] & 0xFFFF0000u), 0x1p-7f, sum[j]);
+                        for (int j = 0; j < 4; ++j) {
+                            sum[j] = fmaf(__uint_as_float(w[j] << 16), 0x1p-7f, sum[j]);
+                            sum[j] = fmaf(__uint_as_float(w[j] & 0xFFFF0000u), 0x1p-7f, sum[j]);
+                        }
                     }
-                }
-                __syncwarp();
-                first_lane_arrives(lane, &s->x_read[x.i]);
-                float X = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                if constexpr (GU == 1) X += __shfl_xor_sync(0xffffffffu, X, 1);
+                    return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                };
                 // X 2^-7, exact down to the smallest token and finite up to the largest.
                 // X in three parts of 8 bits is exact to 2^-25; one that is too large
                 // for that has 2^-12 of its first 8 bits in the fourth place.
-                if (mine && (GU == 2 || h == 0)) {
+                auto put = [&](float X, int group) {
+                    const int at = group % kChunk * 2;
                     float top = 0.f;
                     if (fabsf(X) >= 0x1p118f) top = __bfloat162float(__float2bfloat16_rn(X * 0x1p-5f));
                     X = fmaf(top, -32.f, X) * 128.f;
-                    const int at = (GU == 2 ? 2 * u + h : u) % kChunk * 2;
 #pragma unroll
                     for (int part = 0; part < 3; ++part) {
                         const __nv_bfloat16 b = __float2bfloat16_rn(X);
@@ -409,7 +419,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                         X -= __bfloat162float(b);
                     }
                     if (top != 0.f) sts16(dst + ((96 + at) ^ sw), __bfloat16_as_ushort(__float2bfloat16_rn(top)));
+                };
+                const uint32_t src = x_row + x.i * XB;
+                if constexpr (KS == 64) {
+                    const float X = add_up(src, 4 * h, 4);
+                    if (mine) put(X, 2 * u + h);
+                } else {
+#pragma unroll 1
+                    for (int b = 0; b < KS / 128; ++b) {
+                        const uint32_t box = src + (2 * b + h) * (TOK * 128);
+                        if constexpr (G == 32) {
+                            const float lo = add_up(box, 4 * h, 4), hi = add_up(box, 4 * (h ^ 1), 4);
+                            if (mine) put(lo, u * GU + 4 * b + 2 * h + h);
+                            if (mine) put(hi, u * GU + 4 * b + 2 * h + (h ^ 1));
+                        } else {
+                            float X = add_up(box, 4 * h, 8);
+                            if constexpr (G == 128) X += __shfl_xor_sync(0xffffffffu, X, 1);
+                            if (mine && (G == 64 || h == 0)) put(X, G == 64 ? u * GU + 2 * b + h : u * GU + b);
+                        }
+                    }
                 }
+                __syncwarp();
+                first_lane_arrives(lane, &s->x_read[x.i]);
                 if (ends(u)) {
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -427,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quarter = warp & 3, set_of = (warp - kDeqWarp) >> 2;
         const int r = quarter * 32 + lane;             // row of the tile
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        const int rot = KS == 128 ? (r >> 1) & 3 : (r >> 2) & 1;  // swizzle of the row's 16-byte pieces
+        const int rot = KS == 256 ? r & 7 : KS == 128 ? (r >> 1) & 3 : (r >> 2) & 1;  // swizzle of the row's 16-byte pieces
         const uint32_t w_addr = smem_u32(sW);
         // 128 + q as a bf16 pair, then (128 + q) 2^-12 - 2^-5, exactly
         const __nv_bfloat162 down = u32_as_bf162(0x39803980u), off = u32_as_bf162(0xBD00BD00u);
@@ -440,15 +471,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = warp_wait(&s->w_full[ws], (n / kW) & 1, a, s, 46);
                 if (!ok) break;
                 const uint32_t row = w_addr + ws * WB + r * WROW;
-                uint4 v[KS / 32];
-#pragma unroll
-                for (int i = 0; i < KS / 32; ++i) v[i] = lds128(row + ((i ^ rot) << 4));
-                __syncwarp();
-                first_lane_arrives(lane, &s->w_empty[ws]);
+                constexpr int kHeld = KS < 128 ? KS / 32 : 4;  // pieces in registers
+                uint4 v[kHeld];
                 bool free = false;
-#pragma unroll
+#pragma unroll kHeld
                 for (int i = 0; i < KS / 32; ++i) {
-                    const uint32_t q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    if (i % kHeld == 0) {
+#pragma unroll
+                        for (int e = 0; e < kHeld; ++e) v[e] = lds128(row + (((i + e) ^ rot) << 4));
+                        if (i + kHeld == KS / 32) {
+                            __syncwarp();
+                            first_lane_arrives(lane, &s->w_empty[ws]);
+                        }
+                    }
+                    const uint4 &c = v[i % kHeld];
+                    const uint32_t q[4] = {c.x, c.y, c.z, c.w};
                     uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -461,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         free = true;
                         tc_fence_after();
                     }
-                    tmem_st16((tA + as * 64 + i * 16) | lanes, p);
+                    tmem_st16((tA + as * (KS / 2) + i * 16) | lanes, p);
                 }
                 if (!ok) break;
                 tmem_st_wait();
@@ -510,13 +547,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     first_lane_arrives(lane, &s->z_full);
                 }
-                const uint32_t pair = lds32(s_addr + sc.i * 2 * kSBytes + (u * GU % kChunk >> 1) * 4);
+                uint32_t pair[(GU + 1) / 2];               // scales of two groups each
+#pragma unroll
+                for (int i = 0; i < (GU + 1) / 2; ++i)
+                    pair[i] = lds32(s_addr + sc.i * 2 * kSBytes + ((u * GU % kChunk >> 1) + i) * 4);
                 ok = warp_wait(&s->done[x.i], x.ph, a, s, 49);
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t d[GU][TW];
 #pragma unroll
-                for (int gu = 0; gu < GU; ++gu) tmem_ld<TW>((tmem + db * 128 + gu * 64 + half * TW) | lanes, d[gu]);
+                for (int gu = 0; gu < GU; ++gu) tmem_ld<TW>((tmem + db * DC + gu * TOK + half * TW) | lanes, d[gu]);
 #pragma unroll
                 for (int gu = 0; gu < GU; ++gu) tmem_wait<TW>(d[gu]);
                 tc_fence_before();
@@ -527,8 +567,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 db ^= 1;
 #pragma unroll
                 for (int gu = 0; gu < GU; ++gu) {
-                    const bool high = GU == 2 ? gu == 1 : (u & 1);
-                    const float scale = 4096.f * __uint_as_float(high ? pair & 0xFFFF0000u : pair << 16);
+                    const bool high = GU > 1 ? gu & 1 : u & 1;
+                    const float scale = 4096.f * __uint_as_float(high ? pair[gu / 2] & 0xFFFF0000u : pair[gu / 2] << 16);
                     const uint64_t s2 = pack2(__float_as_uint(scale), __float_as_uint(scale));
 #pragma unroll
                     for (int i = 0; i < TW / 2; ++i) y[i] = fma2(s2, pack2(d[gu][2 * i], d[gu][2 * i + 1]), y[i]);
@@ -600,11 +640,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int G, int TOK>
 static cudaError_t launch_t(const Maps &maps, LinearArgs a, int num_sms, cudaStream_t s) {
-    const int units = (a.K + step_k(G) - 1) / step_k(G), tiles = (a.N + kRows - 1) / kRows;
-    // share K in a cluster while there are two steps for each block and all
-    // clusters run at once (one tile each)
+    const int units = (a.K + step_k(G, TOK) - 1) / step_k(G, TOK), tiles = (a.N + kRows - 1) / kRows;
+    // share K in a cluster while there are two steps for each block (one of 256 k)
+    // and all clusters run at once (one tile each)
+    constexpr int least = step_k(G, TOK) == 256 ? 1 : 2;
     a.split = 1;
-    while (a.split < 8 && tiles * (a.split + 1) <= num_sms * 7 / 8 && units >= (a.split + 1) * 2) ++a.split;
+    while (a.split < 8 && tiles * (a.split + 1) <= num_sms * 7 / 8 && units >= (a.split + 1) * least) ++a.split;
     const auto kernel = linear_many_kernel<G, TOK>;
     const cudaError_t e = allow_smem<linear_many_kernel<G, TOK>>();
     if (e != cudaSuccess) return e;
@@ -633,8 +674,8 @@ static cudaError_t launch_g(const Maps &m, const LinearArgs &a, int num_sms, cud
 
 }  // namespace many
 
-int linear_code_words(int G) { return many::step_k(G) / 8; }
 int linear_token_rows(int B) { return B <= 16 ? 16 : B <= 32 ? 32 : 64; }
+int linear_code_words(int G, int B) { return many::step_k(G, linear_token_rows(B)) / 8; }
 
 cudaError_t launch_linear_many(const CUtensorMap *maps, const LinearArgs &a, int num_sms, cudaStream_t s) {
     const many::Maps m{maps[0], maps[1], maps[2], maps[3]};
