@@ -31,34 +31,38 @@ __device__ __forceinline__ float2 angle_cs(uint32_t pos, uint64_t f) {
 constexpr int kAppendThreads = 256;
 constexpr int kAppendTokens = 8;
 
-__device__ __forceinline__ uint4 turn_piece(const uint4 &x, const float2 (&cs)[4]) {
-    // interleaved: (x0, x1) by cs[0], ...
+// cs: (cos, sin) of two pairs of elements in each
+__device__ __forceinline__ uint4 turn_piece(const uint4 &x, const float4 &cs0, const float4 &cs1) {
+    // interleaved: (x0, x1) by the first, ...
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    const float c[4] = {cs0.x, cs0.z, cs1.x, cs1.z}, s[4] = {cs0.y, cs0.w, cs1.y, cs1.w};
     uint32_t r[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float a = __uint_as_float(w[j] << 16), b = __uint_as_float(w[j] & 0xFFFF0000u);
-        r[j] = bf162_as_u32(__floats2bfloat162_rn(a * cs[j].x - b * cs[j].y, b * cs[j].x + a * cs[j].y));
+        r[j] = bf162_as_u32(__floats2bfloat162_rn(a * c[j] - b * s[j], b * c[j] + a * s[j]));
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-__device__ __forceinline__ void turn_halves(uint4 &x, uint4 &y, const float2 *cs) {
+__device__ __forceinline__ void turn_halves(uint4 &x, uint4 &y, const float4 *cs, int step) {
     uint32_t *wx = reinterpret_cast<uint32_t *>(&x), *wy = reinterpret_cast<uint32_t *>(&y);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float2 c0 = cs[2 * j], c1 = cs[2 * j + 1];
+        const float4 c = cs[j * step];
         const float a0 = __uint_as_float(wx[j] << 16), a1 = __uint_as_float(wx[j] & 0xFFFF0000u);
         const float b0 = __uint_as_float(wy[j] << 16), b1 = __uint_as_float(wy[j] & 0xFFFF0000u);
-        wx[j] = bf162_as_u32(__floats2bfloat162_rn(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y));
-        wy[j] = bf162_as_u32(__floats2bfloat162_rn(b0 * c0.x + a0 * c0.y, b1 * c1.x + a1 * c1.y));
+        wx[j] = bf162_as_u32(__floats2bfloat162_rn(a0 * c.x - b0 * c.y, a1 * c.z - b1 * c.w));
+        wy[j] = bf162_as_u32(__floats2bfloat162_rn(b0 * c.x + a0 * c.y, b1 * c.z + a1 * c.w));
     }
 }
 
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs a, int per_block) {
     constexpr int P = D / 8;  // 16-byte pieces of a head
-    __shared__ float2 s_cs[kAppendTokens][D / 2];
+    // (cos, sin) of the pairs, those of 16 p, 16 p + 2, .. (two each) side by side for
+    // all p: threads with neighbouring pieces read neighbouring places
+    __shared__ float4 s_cs[kAppendTokens][D / 4];
     __shared__ int64_t s_slot[kAppendTokens];  // the token's place in the pools, -1: none
     __shared__ uint64_t s_turn[D / 2];
     pdl_wait();
@@ -83,7 +87,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     __syncthreads();
     for (int i = tid; i < nt * half; i += kAppendThreads) {
         const int t = i / half, p = i - t * half;
-        s_cs[t][p] = angle_cs(static_cast<uint32_t>(a.index[t0 + t]) + static_cast<uint32_t>(a.pos_offset), s_turn[p]);
+        reinterpret_cast<float2 *>(s_cs[t])[(p % 8 / 2 * (D / 16) + p / 8) * 2 + p % 2] = angle_cs(static_cast<uint32_t>(a.index[t0 + t]) + static_cast<uint32_t>(a.pos_offset), s_turn[p]);
     }
     __syncthreads();
 
@@ -124,16 +128,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         uint4 x = *reinterpret_cast<const uint4 *>(src + p0 * 8), y = *reinterpret_cast<const uint4 *>(src + p1 * 8);
         if (rotated) {
             if (!a.interleaved) {
-                if (p < rp) turn_halves(x, y, s_cs[t] + p * 8);
+                if (p < rp) turn_halves(x, y, s_cs[t] + p, HP);
             } else {
-                if (p0 * 8 < a.rot) {
-                    const float2 cs[4] = {s_cs[t][p0 * 4], s_cs[t][p0 * 4 + 1], s_cs[t][p0 * 4 + 2], s_cs[t][p0 * 4 + 3]};
-                    x = turn_piece(x, cs);
-                }
-                if (p1 * 8 < a.rot) {
-                    const float2 cs[4] = {s_cs[t][p1 * 4], s_cs[t][p1 * 4 + 1], s_cs[t][p1 * 4 + 2], s_cs[t][p1 * 4 + 3]};
-                    y = turn_piece(y, cs);
-                }
+                if (p0 * 8 < a.rot) x = turn_piece(x, s_cs[t][p], s_cs[t][HP + p]);
+                if (p1 * 8 < a.rot) y = turn_piece(y, s_cs[t][2 * HP + p], s_cs[t][3 * HP + p]);
             }
         }
         *reinterpret_cast<uint4 *>(dst + p0 * 8) = x;
