@@ -24,10 +24,12 @@ __device__ __forceinline__ float2 angle_cs(uint32_t pos, uint64_t f) {
 // share, up to eight).  First the tokens' places and their angles' cosines and
 // sines into shared memory, one per thread and pair, shared by all heads (fp64
 // only once per pair and block: its rate is 1/64 of fp32's, and with a product
-// per angle a prompt of 8192 tokens took 21 us); then 16-byte pieces: of a rotated head the pair of pieces whose
-// elements turn into one another (halves: pieces j and j + rot / 16 of the
-// head; interleaved: a piece by itself), otherwise plain copies.  Bound by the
-// bytes: each is read and written once.
+// per angle a prompt of 8192 tokens took 1.4 us more); then 16-byte pieces: of a
+// rotated head the pair of pieces whose elements turn into one another (halves:
+// pieces j and j + rot / 16 of the head; interleaved: a piece by itself),
+// otherwise plain copies.  Bound by the bytes, each read and written once, and at
+// few tokens by the three dependent reads (index, page, piece): 8192 tokens of
+// 16 + 2 x 2 heads of 128 take 17.9 us (84 MB, 4.7 TB/s), 8 tokens 2.1.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendTokens = 8;
 
@@ -57,7 +59,8 @@ __device__ __forceinline__ void turn_halves(uint4 &x, uint4 &y, const float4 *cs
     }
 }
 
-template <int D>
+// ITEMS: a thread's work items in flight together
+template <int D, int ITEMS>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs a, int per_block) {
     constexpr int P = D / 8;  // 16-byte pieces of a head
     // (cos, sin) of the pairs, those of 16 p, 16 p + 2, .. (two each) side by side for
@@ -97,45 +100,55 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     constexpr int HP = P / 2;
     const int per_token = (Hq + 2 * Hkv) * HP;
     const int rp = a.rot / 16;  // pieces of a rotated half
-#pragma unroll 2
-    for (int i = tid; i < nt * per_token; i += kAppendThreads) {
-        const int t = i / per_token, r = i - t * per_token, h = r / HP, p = r % HP;
-        const int64_t slot = s_slot[t];
-        if (slot < 0) continue;
-        const __nv_bfloat16 *src;
-        __nv_bfloat16 *dst;
-        if (h < Hq) {
-            src = a.q + (t0 + t) * a.q_stride + h * D;
-            dst = a.q_out + (t0 + t) * a.qo_stride + h * D;
-        } else if (h < Hq + Hkv) {
-            src = a.k + (t0 + t) * a.k_stride + (h - Hq) * D;
-            dst = a.c.k + slot + (h - Hq) * a.c.head_stride;
-        } else {
-            src = a.v + (t0 + t) * a.v_stride + (h - Hq - Hkv) * D;
-            dst = a.c.v + slot + (h - Hq - Hkv) * a.c.head_stride;
-        }
-        // two pieces a thread: the pair of a rotation by halves, or neighbours
-        const bool rotated = h < Hq + Hkv;
-        int p0 = 2 * p, p1 = 2 * p + 1;
-        if (rotated && !a.interleaved) {
-            // pairs (j, j + rp) for j < rp, then the pieces that are not rotated:
-            // 2 rp, 2 rp + 1 and on, which 2 p, 2 p + 1 from p = rp on are
-            if (p < rp) {
-                p0 = p;
-                p1 = p + rp;
-            }
-        }
-        uint4 x = *reinterpret_cast<const uint4 *>(src + p0 * 8), y = *reinterpret_cast<const uint4 *>(src + p1 * 8);
-        if (rotated) {
-            if (!a.interleaved) {
-                if (p < rp) turn_halves(x, y, s_cs[t] + p, HP);
+    for (int i0 = tid; i0 < nt * per_token; i0 += ITEMS * kAppendThreads) {
+        uint4 x[ITEMS], y[ITEMS];
+        __nv_bfloat16 *dst[ITEMS];
+        int tt[ITEMS], pp[ITEMS], p0[ITEMS], p1[ITEMS];
+        bool rotated[ITEMS];
+#pragma unroll
+        for (int e = 0; e < ITEMS; ++e) {
+            const int i = i0 + e * kAppendThreads, t = i / per_token, r = i - t * per_token, h = r / HP, p = r % HP;
+            dst[e] = nullptr;
+            if (i >= nt * per_token) continue;
+            const int64_t slot = s_slot[t];
+            if (slot < 0) continue;
+            const __nv_bfloat16 *src;
+            if (h < Hq) {
+                src = a.q + (t0 + t) * a.q_stride + h * D;
+                dst[e] = a.q_out + (t0 + t) * a.qo_stride + h * D;
+            } else if (h < Hq + Hkv) {
+                src = a.k + (t0 + t) * a.k_stride + (h - Hq) * D;
+                dst[e] = a.c.k + slot + (h - Hq) * a.c.head_stride;
             } else {
-                if (p0 * 8 < a.rot) x = turn_piece(x, s_cs[t][p], s_cs[t][HP + p]);
-                if (p1 * 8 < a.rot) y = turn_piece(y, s_cs[t][2 * HP + p], s_cs[t][3 * HP + p]);
+                src = a.v + (t0 + t) * a.v_stride + (h - Hq - Hkv) * D;
+                dst[e] = a.c.v + slot + (h - Hq - Hkv) * a.c.head_stride;
             }
+            // two pieces a thread: the pair of a rotation by halves, or neighbours
+            // (not rotated are 2 rp, 2 rp + 1 and on: 2 p, 2 p + 1 from p = rp on)
+            rotated[e] = h < Hq + Hkv;
+            const bool paired = rotated[e] && !a.interleaved && p < rp;
+            tt[e] = t;
+            pp[e] = p;
+            p0[e] = paired ? p : 2 * p;
+            p1[e] = paired ? p + rp : 2 * p + 1;
+            x[e] = *reinterpret_cast<const uint4 *>(src + p0[e] * 8);
+            y[e] = *reinterpret_cast<const uint4 *>(src + p1[e] * 8);
         }
-        *reinterpret_cast<uint4 *>(dst + p0 * 8) = x;
-        *reinterpret_cast<uint4 *>(dst + p1 * 8) = y;
+#pragma unroll
+        for (int e = 0; e < ITEMS; ++e) {
+            if (!dst[e]) continue;
+            const float4 *cs = s_cs[tt[e]] + pp[e];
+            if (rotated[e]) {
+                if (!a.interleaved) {
+                    if (pp[e] < rp) turn_halves(x[e], y[e], cs, HP);
+                } else {
+                    if (p0[e] * 8 < a.rot) x[e] = turn_piece(x[e], cs[0], cs[HP]);
+                    if (p1[e] * 8 < a.rot) y[e] = turn_piece(y[e], cs[2 * HP], cs[3 * HP]);
+                }
+            }
+            *reinterpret_cast<uint4 *>(dst[e] + p0[e] * 8) = x[e];
+            *reinterpret_cast<uint4 *>(dst[e] + p1[e] * 8) = y[e];
+        }
     }
 }
 
@@ -144,8 +157,15 @@ cudaError_t launch_append(const AppendArgs &a, int num_sms, cudaStream_t s) {
     int per = a.T / (4 * num_sms);
     per = per < 1 ? 1 : per > kAppendTokens ? kAppendTokens : per;
     const dim3 grid((a.T + per - 1) / per), block(kAppendThreads);
-    return a.c.D == 64 ? launch_dependent(append_kernel<64>, grid, block, 0, s, a, per)
-                       : launch_dependent(append_kernel<128>, grid, block, 0, s, a, per);
+    // two items of a thread in flight together if a block has more than one for each
+    // (prompt of 8192: 19 -> 17.9 us; four: 24; where there is one only, two in the
+    // code cost 0.8 of 4.3 us)
+    const int heads = (a.q ? a.Hq : 0) + 2 * a.c.Hkv;
+    if (per * heads * (a.c.D / 16) <= kAppendThreads)
+        return a.c.D == 64 ? launch_dependent(append_kernel<64, 1>, grid, block, 0, s, a, per)
+                           : launch_dependent(append_kernel<128, 1>, grid, block, 0, s, a, per);
+    return a.c.D == 64 ? launch_dependent(append_kernel<64, 2>, grid, block, 0, s, a, per)
+                       : launch_dependent(append_kernel<128, 2>, grid, block, 0, s, a, per);
 }
 
 // ------------------------------------------------------------- attention
