@@ -125,6 +125,22 @@ def load(path: str = LIB_PATH):
     return _lib
 
 
+_native = None
+
+
+def native():
+    """The module of the attention sub-layer's calls on torch tensors (built
+    beside the library; raises if it has not been)."""
+    global _native
+    if _native is None:
+        load()
+        import torch  # noqa: F401  (its libraries are the module's)
+
+        from . import _native as module
+        _native = module
+    return _native
+
+
 def status_string(code: int) -> str:
     return load().moe_status_string(int(code)).decode()
 
@@ -343,14 +359,8 @@ def gqa_decode_attention(q, k_cache, v_cache, L: int, scale: float, out, ws, per
 
 # ---------------------------------------------------- attention sub-layer
 #
-# These calls run in a microsecond or a few on the GPU, so their host side is
-# kept short: one query per tensor, and the stream handle straight from the
-# current device's.
-
-
-def current_device() -> int:
-    import torch
-    return torch._C._cuda_getDevice()
+# The calls themselves are made by the module native(); these wrappers are the C
+# calls as they stand, on raw descriptors.
 
 
 def stream_on(stream, device: int) -> int:
@@ -358,6 +368,11 @@ def stream_on(stream, device: int) -> int:
         import torch
         return torch._C._cuda_getCurrentRawStream(device)
     return int(getattr(stream, "cuda_stream", stream))
+
+
+def handle(stream):
+    """The raw handle of a torch stream (or of a handle); None stays None."""
+    return stream if stream is None else int(getattr(stream, "cuda_stream", stream))
 
 
 def on_stream(stream):
@@ -368,16 +383,6 @@ def on_stream(stream):
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
     return torch.cuda.stream(stream)
-
-
-def check_device(what: str, *tensors) -> int:
-    """Every tensor on the current device (the library launches there); returns it."""
-    import torch
-    cur = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
-    for t in tensors:
-        if t is not None and t.get_device() != cur:
-            raise ValueError(f"{what}: a tensor on {t.device}, the current device is cuda:{cur}")
-    return cur
 
 
 def check(rc: int, what: str):

@@ -21,30 +21,6 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _heads(t: torch.Tensor, name: str, T: int, heads: Optional[int], D: int, device: int) -> int:
-    """[T, heads, D] bf16 whose rows are contiguous (rows themselves may be
-    strided), on the current device; elements from one row to the next."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or t.dtype != torch.bfloat16 or shape[0] != T or shape[2] != D or \
-            (heads is not None and shape[1] != heads):
-        raise ValueError(f"{name}: [{T}, {'heads' if heads is None else heads}, {D}] in bf16")
-    if stride[2] != 1 or (shape[1] > 1 and stride[1] != D):
-        raise ValueError(f"{name}: the heads of a row must be contiguous")
-    if t.get_device() != device:
-        raise ValueError(f"{name}: on {t.device}, the current device is cuda:{device}")
-    return stride[0] if T > 1 else shape[1] * D
-
-
-def _ints(t: torch.Tensor, name: str, n: Optional[int], dims: int, device: int) -> int:
-    """A contiguous int32 array on the current device; its address."""
-    shape = t.shape
-    if t.dtype != torch.int32 or len(shape) != dims or (n is not None and shape[0] != n) or not t.is_contiguous():
-        raise ValueError(f"{name}: int32, contiguous, {dims} dimension(s)" + ("" if n is None else f", the first {n}"))
-    if t.get_device() != device:
-        raise ValueError(f"{name}: on {t.device}, the current device is cuda:{device}")
-    return t.data_ptr()
-
-
 class PagedCache:
     """A paged key-value cache over two pools [n_pages, Hkv, page_size, D] in
     bf16 (any order of heads and positions in memory: pass a transposed view;
@@ -64,7 +40,7 @@ class PagedCache:
         self._device = k.get_device()
         # where append records errors found on the device
         self.status = torch.zeros(4, dtype=torch.int32, device=k.device)
-        self._ref, self._status_at = ctypes.byref(self.desc), self.status.data_ptr()
+        self._at, self._status_at = ctypes.addressof(self.desc), self.status.data_ptr()
         self._scale = 1.0 / math.sqrt(self.D)
 
     @classmethod
@@ -80,39 +56,13 @@ class PagedCache:
         if stream is not None and q is not None and q_out is None:
             with _lib.on_stream(stream):
                 return self.append(q, k, v, seq, index, page_table, inv_freq, pos_offset, interleaved)
-        T, D, dev = k.shape[0], self.D, self._check_device("append")
-        ks = _heads(k, "k", T, self.Hkv, D, dev)
-        vs = _heads(v, "v", T, self.Hkv, D, dev)
-        seq_at, index_at = _ints(seq, "seq", T, 1, dev), _ints(index, "index", T, 1, dev)
-        table_at = _ints(page_table, "page_table", None, 2, dev)
-        rot, freq_at = 0, None
-        if inv_freq is not None:
-            if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous() or \
-                    inv_freq.get_device() != dev:
-                raise ValueError("inv_freq: fp32 [rot / 2], contiguous, on the current device")
-            rot, freq_at = 2 * inv_freq.shape[0], inv_freq.data_ptr()
-        Hq = qs = os = 0
-        q_at = out_at = None
-        if q is None:
-            _need(q_out is None, "q_out without q")
-        else:
-            qs = _heads(q, "q", T, None, D, dev)
-            Hq = q.shape[1]
-            if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            os = _heads(q_out, "q_out", T, Hq, D, dev)
-            q_at, out_at = q.data_ptr(), q_out.data_ptr()
-        n_seq, ld = page_table.shape
-        _lib.check(_lib.load().gqa_append(self._ref, q_at, qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq, seq_at,
-                                          index_at, table_at, n_seq, ld, pos_offset, freq_at, rot, interleaved, out_at,
-                                          os, self._status_at, _lib.stream_on(stream, dev)), "gqa_append")
+        if q_out is None and q is not None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        rc = _lib.native().append(self._at, self._device, self._status_at, q, k, v, seq, index, page_table, inv_freq,
+                                  pos_offset, interleaved, q_out, _lib.handle(stream))
+        if rc:
+            raise _lib.MoEError(rc, "gqa_append")
         return q_out
-
-    def _check_device(self, what: str) -> int:
-        cur = _lib.current_device()
-        if cur != self._device:
-            raise ValueError(f"{what}: the cache is on cuda:{self._device}, the current device is cuda:{cur}")
-        return cur
 
     def workspace(self, B: int, Hq: int, prefix_len: int = 0) -> torch.Tensor:
         """Scratch of attend for up to B rows, Hq heads and prefix_len shared
@@ -131,26 +81,14 @@ class PagedCache:
         if stream is not None and (out is None or ws is None):
             with _lib.on_stream(stream):
                 return self.attend(q, page_table, seq_len, prefix_pages, prefix_len, scale, out, ws)
-        B, Hq, dev = q.shape[0], q.shape[1], self._check_device("attend")
-        qs = _heads(q, "q", B, None, self.D, dev)
-        table_at = _ints(page_table, "page_table", B, 2, dev)
-        len_at = _ints(seq_len, "seq_len", B, 1, dev)
-        prefix_at = None
-        if prefix_len:
-            _need(prefix_pages is not None, "prefix_len without prefix_pages")
-            prefix_at = _ints(prefix_pages, "prefix_pages", None, 1, dev)
-            _need(prefix_len <= prefix_pages.shape[0] * self.page_size, "prefix_pages: too few for prefix_len")
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        os = _heads(out, "out", B, Hq, self.D, dev)
         if ws is None:
-            ws = self.workspace(B, Hq, prefix_len)
-        _need(ws.get_device() == dev and ws.is_contiguous(), "ws: contiguous, on the current device")
-        _lib.check(_lib.load().gqa_paged_attention(self._ref, q.data_ptr(), qs, B, Hq, prefix_at, prefix_len, table_at,
-                                                   page_table.shape[1], len_at,
-                                                   self._scale if scale is None else scale, out.data_ptr(), os,
-                                                   ws.data_ptr(), ws.numel() * ws.element_size(),
-                                                   _lib.stream_on(stream, dev)), "gqa_paged_attention")
+            ws = self.workspace(q.shape[0], q.shape[1], prefix_len)
+        rc = _lib.native().attend(self._at, self._device, q, page_table, seq_len, prefix_pages, prefix_len,
+                                  self._scale if scale is None else scale, out, ws, _lib.handle(stream))
+        if rc:
+            raise _lib.MoEError(rc, "gqa_paged_attention")
         return out
 
 

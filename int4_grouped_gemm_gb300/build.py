@@ -2,7 +2,9 @@
 
 Each .cu file compiles to an object in parallel, then one link step makes
 the shared library next to this file.  No cmake, no torch extension machinery:
-the library has a plain C ABI and is loaded with ctypes.
+the library has a plain C ABI and is loaded with ctypes.  Beside it stands
+_native.so, a Python module that makes the attention sub-layer's calls on torch
+tensors (host code against torch's headers and libraries).
 """
 from __future__ import annotations
 
@@ -17,6 +19,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmoe_gb300.so")
+BINDING = os.path.join(HERE, "_native.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.cu", "pack.cu", "routing.cu", "grouped_gemm.cu", "decode.cu", "small_batch.cu", "block.cu",
@@ -36,6 +39,22 @@ def _stale(obj: str, deps) -> bool:
         return True
     t = os.path.getmtime(obj)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _binding_flags():
+    """Flags of the compile and of the link of the Python module."""
+    import importlib.util
+    import sysconfig
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    # (torch's and CUDA's headers as system headers: their warnings are theirs)
+    compile_ = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-I" + os.path.join(ROOT, "include"),
+                "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(torch, "include"),
+                "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+                "-isystem", os.path.join(cuda, "include")]
+    link = ["-L" + HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(torch, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    return compile_, link
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -58,15 +77,23 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if force or _stale(o, [s, *headers, __file__]):
             jobs.append([nvcc(), *ARCH, *NVCC_FLAGS, *extra_flags, "-c", s, "-o", o])
 
+    # (of one torch version, like the module made from it)
+    import importlib.metadata
+    src = os.path.join(CSRC, "binding.cpp")
+    binding_obj = os.path.join(BUILD_DIR, "binding-" + importlib.metadata.version("torch") + ".o")
+    compile_, link = _binding_flags()
+    if force or _stale(binding_obj, [src, headers[-1], __file__]):
+        jobs.append(["g++", *compile_, "-c", src, "-o", binding_obj])
+
     def run(cmd):
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{cmd[0]} failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         return r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         for err in ex.map(run, jobs):
             if verbose and err:
                 print(err, file=sys.stderr)
@@ -74,6 +101,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"])
         os.replace(tmp, LIB)
+    if force or _stale(BINDING, [binding_obj, LIB]):
+        tmp = BINDING + f".tmp{os.getpid()}"
+        run(["g++", "-shared", "-o", tmp, binding_obj, *link])
+        os.replace(tmp, BINDING)
     return LIB
 
 

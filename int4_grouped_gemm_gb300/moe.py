@@ -7,7 +7,6 @@ provides device memory and streams here.
 """
 from __future__ import annotations
 
-import ctypes
 from dataclasses import dataclass
 from typing import Optional
 
@@ -35,14 +34,6 @@ class QMatrix:
     def as_c(self) -> moe_qweight:
         return moe_qweight(self.q.data_ptr(), self.scale.data_ptr(), self.bias.data_ptr())
 
-    def ref(self):
-        """A C reference to as_c(), made anew only when a tensor was replaced."""
-        of = self.__dict__.get("_of")
-        if of is None or of[0] is not self.q or of[1] is not self.scale or of[2] is not self.bias:
-            of = (self.q, self.scale, self.bias, ctypes.byref(self.as_c()))
-            self.__dict__["_of"] = of
-        return of[3]
-
 
 def pack_matrix(w: torch.Tensor, group: int, stream=None) -> QMatrix:
     """Quantise fp32 w [..., rows, K] on the GPU (pack_int4)."""
@@ -63,25 +54,14 @@ def linear(w: QMatrix, x: torch.Tensor, y: Optional[torch.Tensor] = None, dtype=
     (int4_linear); x bf16 with contiguous rows, y bf16 or fp32 (a new tensor of
     `dtype` unless given).  status: a zeroed int32 device tensor that records a
     device-side wait that ran out (moe_read_device_status), or None."""
-    xs = x.stride()
-    if len(xs) != 2 or x.shape[1] != w.K or x.dtype != torch.bfloat16 or xs[1] != 1:
-        raise ValueError(f"linear: x [B, {w.K}] in bf16, its rows contiguous")
-    if w.q.numel() * 8 != w.rows * w.K:
-        raise ValueError("linear: one matrix [N, K], not a stack")
-    B, N = x.shape[0], w.rows
     if y is None:
         if stream is not None:
             with _lib.on_stream(stream):
                 return linear(w, x, None, dtype, status)
-        y = torch.empty(B, N, dtype=dtype, device=x.device)
-    ys = y.stride()
-    if y.shape != (B, N) or y.dtype not in (torch.bfloat16, torch.float32) or (N > 1 and ys[1] != 1):
-        raise ValueError(f"linear: y [B, {N}] in bf16 or fp32, its rows contiguous")
-    dev = _lib.check_device("linear", x, y, w.q)
-    _lib.check(_lib.load().int4_linear(w.ref(), N, w.K, w.group, x.data_ptr(), xs[0] if B > 1 else w.K, B, y.data_ptr(),
-                                       ys[0] if B > 1 else N, y.dtype == torch.float32,
-                                       None if status is None else status.data_ptr(), _lib.stream_on(stream, dev)),
-               "int4_linear")
+        y = torch.empty(x.shape[0], w.rows, dtype=dtype, device=x.device)
+    rc = _lib.native().linear(w.q, w.scale, w.bias, w.rows, w.K, w.group, x, y, status, _lib.handle(stream))
+    if rc:
+        raise _lib.MoEError(rc, "int4_linear")
     return y
 
 
