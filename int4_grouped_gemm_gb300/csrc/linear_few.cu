@@ -23,9 +23,14 @@
 // (no sums across warps then).  If there are too few rows for the GPU, a
 // cluster of up to eight blocks shares K and adds up through distributed
 // shared memory.  Each warp streams its weights through its own ring of
-// cp.async stages (16 rows x 256 k and their scales).  The tokens' parts and
-// group sums are made once per block if they fit in shared memory, else chunk
-// by chunk for each block of rows.
+// cp.async stages (16 rows x 256 k and their scales).  The tokens as fp16 and
+// their group sums are made once per block if they fit in shared memory, else
+// chunk by chunk for each block of rows.
+//
+// Measured: 131072 x 4096 with one token 55 us, 5.2 TB/s of the 285 MB (ALU 51 %,
+// issue 66 % of their peaks; eight warps a SM and more in flight gain nothing);
+// 2560 x 2048 with one token 4.3 us and 2048 x 2048 with eight 5.6, which is the
+// tokens' way through shared memory, the ring's first stages and the cluster's sum.
 #include <cuda_fp16.h>
 
 #include <algorithm>

@@ -36,6 +36,12 @@
 //                    at the tensor core: 5,300 cycles for a tile of both) and
 //                    one's barrier waits and commits pass while the other issues
 //
+// Measured: 128 rows of 16 heads behind 131072 positions 97 us, 1.4 PFLOP/s (the
+// tensor pipe 67 % busy; the rest is each slot's wait from its scores to its first
+// weights, which the other slot's products do not quite cover); 32 rows behind
+// 32749 positions 13 us, where a piece has 1 or 2 tiles and its start and partial
+// are most of the time.
+//
 // A position outside the pool is loaded as zeros (the page coordinate lies
 // past the tensor map) and recorded.  Every wait is bounded.
 #include "paged.cuh"
