@@ -477,10 +477,12 @@ int gqa_decode_attention_per_head(const void *q, const void *k_cache, const void
  * for 1 <= B <= 64 tokens and one int4 matrix [N][K] in the format of
  * pack_int4 (scale and bias rows at the padded pitch).  The weights are not
  * rounded to bf16; sums in fp32, y rounded once to bf16 (y_fp32 = 0) or
- * written as fp32 (y_fp32 = 1).  x: [B] rows of K bf16, row stride x_stride
+ * written as fp32 (y_fp32 = 1); group sums and products stay finite for any
+ * finite token, and a token with an infinity or NaN leaves its own row of y
+ * infinite or NaN and the other rows alone.  x: [B] rows of K bf16, row stride x_stride
  * (>= K); y: [B] rows of N, row stride y_stride (>= N, any).  y must not
- * overlap x.  N >= 1, group in {32, 64, 128}, K % group == 0, K <= 32768 (else
- * MOE_ERR_SHAPE); x_stride below 2^39; B outside 1..64 is MOE_ERR_TOKENS.  No
+ * overlap x.  1 <= N <= 2^30, group in {32, 64, 128}, K % group == 0, K <= 32768,
+ * strides below 2^39 (else MOE_ERR_SHAPE); B outside 1..64 is MOE_ERR_TOKENS.  No
  * workspace: calls on several streams do not meet.  status: where a device-side
  * wait that ran out is recorded (the first word of a workspace or any zeroed
  * int32), or NULL.
@@ -539,7 +541,8 @@ int gqa_append(const gqa_pages *cache, const void *q, int64_t q_stride, const vo
 
 /* Workspace bytes of gqa_paged_attention for up to B rows, Hq query heads and
  * up to prefix_len shared positions; 0 if unsupported.  To be zero-filled
- * once before first use (moe_workspace_init clears what has to be). */
+ * once before first use (moe_workspace_init clears what has to be), and again
+ * after a call that returned a CUDA error or recorded MOE_ERR_TIMEOUT. */
 size_t gqa_paged_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t prefix_len);
 
 /*

@@ -783,8 +783,11 @@ int int4_linear(const moe_qweight *w, int32_t N, int32_t K, int32_t group, const
         (rc = check_ptr(y)))
         return rc;
     if (group != 32 && group != 64 && group != 128) return MOE_ERR_SHAPE;
-    if (N < 1 || K < group || K > kLinearMaxK || K % group != 0) return MOE_ERR_SHAPE;
-    if (x_stride < K || x_stride % 8 != 0 || x_stride >= (int64_t(1) << 39) || y_stride < N || (y_fp32 != 0 && y_fp32 != 1)) return MOE_ERR_SHAPE;
+    // (N: rows of a last tile past it still count in 32 bits)
+    if (N < 1 || N > (1 << 30) || K < group || K > kLinearMaxK || K % group != 0) return MOE_ERR_SHAPE;
+    if (x_stride < K || x_stride % 8 != 0 || x_stride >= (int64_t(1) << 39) || y_stride < N ||
+        y_stride >= (int64_t(1) << 39) || (y_fp32 != 0 && y_fp32 != 1))
+        return MOE_ERR_SHAPE;
     if (B < 1 || B > kLinearMaxB) return MOE_ERR_TOKENS;
     if (status && (reinterpret_cast<uintptr_t>(status) & 3u)) return MOE_ERR_ALIGN;
     DeviceInfo *dev = nullptr;

@@ -107,6 +107,11 @@ int linear(PyObject *const *v) {
     if (x.dim() != 2 || x.size(1) != K || x.scalar_type() != at::kBFloat16 || x.stride(1) != 1)
         value_error("linear: x [B, " + std::to_string(K) + "] in bf16, its rows contiguous");
     if (q.numel() * 8 != static_cast<int64_t>(N) * K) value_error("linear: one matrix [N, K], not a stack");
+    const int64_t pitch = group > 0 ? (K / group + 7) / 8 * 8 : 0;
+    if (q.scalar_type() != at::kInt || !q.is_contiguous()) value_error("linear: codes in int32, contiguous");
+    for (const at::Tensor *t : {&s, &b})
+        if (t->element_size() != 2 || !t->is_contiguous() || t->numel() != N * pitch)
+            value_error("linear: scales and biases [N, " + std::to_string(pitch) + "] in 16 bits, contiguous");
     const int64_t B = x.size(0);
     const bool fp32 = y.scalar_type() == at::kFloat;
     if (y.dim() != 2 || y.size(0) != B || y.size(1) != N || !(fp32 || y.scalar_type() == at::kBFloat16) ||
@@ -116,6 +121,8 @@ int linear(PyObject *const *v) {
     on_device(x, "linear: x", dev);
     on_device(y, "linear: y", dev);
     on_device(q, "linear: codes", dev);
+    on_device(s, "linear: scales", dev);
+    on_device(b, "linear: biases", dev);
     int32_t *status = nullptr;
     if (v[8] != Py_None) {
         const at::Tensor &t = tensor(v[8], "linear: status");

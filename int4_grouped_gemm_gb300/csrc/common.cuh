@@ -120,6 +120,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, long l
     return true;
 }
 
+// A block's wait for its own copies and MMAs in flight before it ends: about two
+// milliseconds at least, however short the caller's limit is, since what lands
+// after the block has gone would land in another one's shared memory.
+__device__ __forceinline__ bool mbar_drain(uint64_t *bar, uint32_t parity, long long limit) {
+    constexpr long long least = 1 << 22;
+    return mbar_wait(bar, parity, limit > least ? limit : least);
+}
+
 // -------------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap *map) {

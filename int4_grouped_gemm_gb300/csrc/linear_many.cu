@@ -295,8 +295,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // no copy of this block is in flight when it ends
-            for (uint32_t i = n_w > kW ? n_w - kW : 0; i < n_w; ++i) mbar_wait(&s->w_full[i % kW], (i / kW) & 1, a.wait_limit);
-            for (uint32_t i = n_s > kS ? n_s - kS : 0; i < n_s; ++i) mbar_wait(&s->s_full[i % kS], (i / kS) & 1, a.wait_limit);
+            for (uint32_t i = n_w > kW ? n_w - kW : 0; i < n_w; ++i) mbar_drain(&s->w_full[i % kW], (i / kW) & 1, a.wait_limit);
+            for (uint32_t i = n_s > kS ? n_s - kS : 0; i < n_s; ++i) mbar_drain(&s->s_full[i % kS], (i / kS) & 1, a.wait_limit);
         }
         __syncwarp();
     } else if (warp == kXWarp) {
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // a timeout elsewhere may not come: the wait then runs out, long after
             // the copies landed.)
             for (uint32_t i = n_x > kX ? n_x - kX : 0; i < n_x; ++i)
-                if (!mbar_wait(&s->ready[i % kX], (i / kX) & 1, a.wait_limit)) break;
+                if (!mbar_drain(&s->ready[i % kX], (i / kX) & 1, a.wait_limit)) break;
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // every MMA issued here is complete before tensor memory is freed
             umma_commit(&s->drain);
-            mbar_wait(&s->drain, 0, a.wait_limit);
+            mbar_drain(&s->drain, 0, a.wait_limit);
         }
         __syncwarp();
     } else if (warp >= kSumWarp) {

@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         }
         // no copy of this block is in flight when it ends
         for (uint32_t i = it > kKvStages ? it - kKvStages : 0; i < it; ++i)
-            mbar_wait(&s->kv_full[i % kKvStages], (i / kKvStages) & 1, a.wait_limit);
+            mbar_drain(&s->kv_full[i % kKvStages], (i / kKvStages) & 1, a.wait_limit);
     } else if (warp >= 9) {
         // -------------------------------------------------------- MMA issue
         // (one thread, elected rather than picked by lane number: the compiler
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             }
             // every MMA issued here is complete before tensor memory is freed
             umma_commit(&s->drain);
-            mbar_wait(&s->drain, 0, a.wait_limit);
+            mbar_drain(&s->drain, 0, a.wait_limit);
         }
         __syncwarp();
     } else {

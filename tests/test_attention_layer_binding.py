@@ -64,6 +64,30 @@ def test_linear_refuses_a_stack_and_no_tensor():
         moe.linear(matrix(), torch.zeros(2, 128, dtype=BF).to_sparse(), y=torch.zeros(2, 64))
 
 
+@pytest.mark.parametrize("name, t", [
+    ("scale", torch.zeros(64, 4, dtype=torch.int16)), ("bias", torch.zeros(32, 8, dtype=torch.int16)),
+    ("bias", torch.zeros(64, 8)), ("scale", torch.zeros(8, 64, dtype=torch.int16).t()),
+    ("q", torch.zeros(64, 8, dtype=torch.int64).repeat(1, 2)), ("q", torch.zeros(16, 64, dtype=torch.int32).t())])
+def test_linear_refuses_weights_of_another_layout(name, t):
+    """Fewer scales than the kernel reads would be a read past their end."""
+    w = matrix()
+    setattr(w, name, t)
+    with pytest.raises(ValueError, match="linear: (scales and biases|codes)"):
+        moe.linear(w, torch.zeros(2, 128, dtype=BF), y=torch.zeros(2, 64))
+
+
+def test_linear_refuses_rows_and_strides_past_its_index():
+    """Row numbers of the last tile and offsets of y would not fit their types."""
+    lib, w = _lib.load(), _lib.moe_qweight(256, 512, 768)
+    P = ctypes.c_void_p
+
+    def call(N, ys):
+        return lib.int4_linear(ctypes.byref(w), N, 128, 64, P(1024), 128, 4, P(2048), ys, 0, None, None)
+    assert call((1 << 30) + 1, 1 << 31) == _lib.MOE_ERR_SHAPE
+    assert call((1 << 31) - 1, 1 << 31) == _lib.MOE_ERR_SHAPE
+    assert call(64, 1 << 39) == _lib.MOE_ERR_SHAPE
+
+
 def test_a_cache_of_another_device():
     c = cache()
     k = torch.zeros(3, 2, 64, dtype=BF)
