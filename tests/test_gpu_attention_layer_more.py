@@ -113,3 +113,52 @@ def test_a_wait_that_runs_out_is_recorded_and_harmless():
     _lib.moe_workspace_init(ws)
     assert torch.equal(moe.linear(m, x, dtype=torch.float32), want)
     assert torch.equal(cache.attend(q, table, lens, prefix, 2000, ws=ws), out)
+
+
+@pytest.mark.parametrize("B, K, N, G", [(9, 32, 40, 32), (64, 32, 3, 32), (17, 32, 1, 32), (33, 64, 7, 64), (64, 64, 200, 32),
+                                        (12, 128, 5, 128), (64, 128, 1, 64), (25, 128, 129, 128), (16, 160, 64, 32),
+                                        (10, 32768, 8, 128), (64, 32768, 130, 32)])
+def test_linear_smallest_and_longest_k(B, K, N, G):
+    """One group of k, rows fewer than a box of any load, the longest k."""
+    m, w, x = case(B, K, N, G, 3 * B + K + N)
+    want = x.double() @ w.t()
+    y = moe.linear(m, x, dtype=torch.float32)
+    assert ((y.double() - want).abs() <= bound(x, w, K)).all()
+
+
+def test_append_ragged_numbers_of_heads():
+    """Blocks whose items are not a multiple of the threads' two in flight, rotated
+    in place: against the rotation in 64 bits."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    for T, Hq, Hkv, D, rot, inter in ((2500, 3, 1, 64, 48, False), (1300, 40, 5, 128, 128, True), (5000, 7, 7, 64, 16, True),
+                                      (700, 255, 1, 64, 64, False)):
+        n_pages = (T + 63) // 64
+        cache = attention.PagedCache.empty(n_pages, Hkv, 64, D)
+        cache.k.fill_(7.0)
+        cache.v.fill_(7.0)
+        q, k, v = (torch.randn(T, h, D, generator=g, device="cuda").to(torch.bfloat16) for h in (Hq, Hkv, Hkv))
+        table = torch.randperm(n_pages, generator=g, device="cuda").to(torch.int32).view(1, -1)
+        index = torch.randperm(T, generator=g, device="cuda").to(torch.int32)
+        freq = 10000.0 ** (-torch.arange(rot // 2, device="cuda") / (rot // 2))
+        ang = (index.double() + 5)[:, None, None] * freq.double()
+
+        def turned(x):
+            x = x.double()
+            a, b = (x[..., 0:rot:2], x[..., 1:rot:2]) if inter else (x[..., :rot // 2], x[..., rot // 2:rot])
+            c, s = a * ang.cos() - b * ang.sin(), b * ang.cos() + a * ang.sin()
+            y = x.clone()
+            if inter:
+                y[..., 0:rot:2], y[..., 1:rot:2] = c, s
+            else:
+                y[..., :rot // 2], y[..., rot // 2:rot] = c, s
+            return y
+        want_q, want_k = turned(q), turned(k)
+        out = cache.append(q, k, v, torch.zeros(T, dtype=torch.int32, device="cuda"), index, table, freq, 5, inter, q_out=q)
+        assert out is q
+        pages, off = table[0, index.long() // 64].long(), index.long() % 64
+        # cos and sin off by 2^-22 at most (angle and function in fp32), two
+        # products and a sum, then the rounding to bf16
+        for got, want in ((q, want_q), (cache.k[pages, :, off], want_k)):
+            mag = 12.0 * (2.0 ** -21 + 4 * FP32)       # of |a| + |b| <= 12: six deviations each
+            assert ((got.double() - want).abs() <= want.abs() * BF16 * 1.01 + mag).all()
+        assert torch.equal(cache.v[pages, :, off], v)
