@@ -9,8 +9,8 @@
 // one fused multiply-add a pair, on the other pipe, leaves q exactly.  (Unpacked
 // to bf16 pairs: 74 us for 131072 x 4096, whose bytes take 42; as fp8 bytes with
 // mma.sync e4m3 x e5m2, which this GPU expands to fp16 by itself: 59.)
-// The token is made fp16 exactly as well: scaled by a power of two, so that its
-// largest element lies in [2^14, 2^15), the 8 significant bits of an element fit
+// The token is made fp16 exactly as well: scaled by a power of two, so that the
+// largest element of the block's share lies in [2^14, 2^15), the 8 significant bits of an element fit
 // unless it is below 2^-31 of the largest, and then it is off by 2^-40 of that.
 // mma.sync m16n8k16 multiplies and adds in fp32.  Per group of weights, with
 // D = sum q x 2^e and X = 2^e sum x,
@@ -29,7 +29,7 @@
 //
 // Measured: 131072 x 4096 with one token 55 us, 5.2 TB/s of the 285 MB (ALU 51 %,
 // issue 66 % of their peaks; eight warps a SM and more in flight gain nothing);
-// 2560 x 2048 with one token 4.3 us and 2048 x 2048 with eight 5.6, which is the
+// 2560 x 2048 with one token 4.1 us and 2048 x 2048 with eight 4.9, which is the
 // tokens' way through shared memory, the ring's first stages and the cluster's sum.
 #include <cuda_fp16.h>
 
@@ -151,7 +151,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) linear_few_kernel(cons
     uint8_t *xbuf = smem + ring_bytes(WARPS);     // [token] rows of fp16
     float *gbuf = reinterpret_cast<float *>(xbuf + map.xbytes);                // [group][8 tokens]
     float *red = reinterpret_cast<float *>(xbuf + map.xbytes + map.gbytes);    // [RW][KW][token][16 rows]
-    int *s_exp = reinterpret_cast<int *>(xbuf + map.xbytes + map.gbytes + map.red);  // [token]
+    int *s_top = reinterpret_cast<int *>(xbuf + map.xbytes + map.gbytes + map.red);  // [token] largest |x| as bf16 bits
+    int *s_exp = s_top + 8;                        // [token] exponent of its scale
     pdl_wait();
     pdl_trigger();
 
@@ -228,64 +229,97 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) linear_few_kernel(cons
         cp_async_commit();
     }
 
-    // the tokens' scales: exponent of the largest element of the whole row, by
-    // as many warps a token as there are
-    {
-        const int wpt = WARPS / a.B;  // 1 or more: at most 8 tokens
-        const int t = warp / wpt, part = warp % wpt;
-        if (tid < 8) s_exp[tid] = 0;
-        __syncthreads();
-        if (t < a.B) {
-            uint32_t top = 0;  // largest |x| as bf16 bits (NaN and infinity above all)
-#pragma unroll 4
-            for (int p = part * 32 + lane; p < a.K / 8; p += wpt * 32) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(a.x + t * a.x_stride + 8 * p);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    // The tokens as fp16, scaled by a power of two each that this block's share of k
+    // alone decides (the sums leave the block at their own scale): a thread
+    // takes eight k of a token at a time.
+    const int shift = 14 + 127;  // x 2^e: the largest element to [2^14, 2^15); 2^e and 2^-e stay normal
+    auto exponent = [&](int top) { return top == 0 ? 0 : max(-112, min(126, shift - (top >> 7))); };
+    auto largest = [&](const uint4 &v) {  // largest |x| as bf16 bits (NaN and infinity above all)
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t top = 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
-            }
-            top = __reduce_max_sync(0xffffffffu, top);
-            if (lane == 0) atomicMax(&s_exp[t], static_cast<int>(top));
+        for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+        return top;
+    };
+    // piece p (of n, a multiple of 32) of token t of a chunk, and the group sums: the
+    // lanes of a group add up their elements
+    auto convert = [&](int t, int p, const uint4 &v, int exp) {
+        const float up = __uint_as_float(static_cast<uint32_t>(exp + 127) << 23);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t h[4];
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float f0 = __uint_as_float(w[j] << 16) * up, f1 = __uint_as_float(w[j] & 0xFFFF0000u) * up;
+            const __half2 hh = __floats2half2_rn(f0, f1);
+            h[j] = *reinterpret_cast<const uint32_t *>(&hh);
+            sum += f0 + f1;
         }
-        __syncthreads();
-        // x 2^e: the largest to [2^14, 2^15); 2^e and 2^-e stay normal
-        if (tid < a.B) {
-            const int top = s_exp[tid];
-            s_exp[tid] = top == 0 ? 0 : max(-112, min(126, 14 - ((top >> 7) - 127)));
-        }
-        __syncthreads();
-    }
-
-    // chunk ch of the tokens: scaled to fp16, and the group sums.  A thread takes
-    // eight k of a token, the lanes of a group add up their elements
+        *reinterpret_cast<uint4 *>(xbuf + t * map.pitch + p * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+        // (all 32 lanes: n is a multiple of 32)
+#pragma unroll
+        for (int off = 1; off < G / 8; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (p % (G / 8) == 0) gbuf[(p / (G / 8)) * 8 + t] = sum;
+    };
+    auto piece = [&](int t, int k) {
+        return k < a.K ? *reinterpret_cast<const uint4 *>(a.x + t * a.x_stride + k) : make_uint4(0u, 0u, 0u, 0u);
+    };
     auto load_x = [&](int ch) {
         const int k0 = (u0 + ch * cu) * kUnit;
-        const int n = min(cu, u1 - u0 - ch * cu) * (kUnit / 8);  // a multiple of 32
+        const int n = min(cu, u1 - u0 - ch * cu) * (kUnit / 8);
 #pragma unroll 4
         for (int i = tid; i < a.B * n; i += kThreads) {
             const int t = i / n, p = i - t * n;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (k0 + 8 * p < a.K) v = *reinterpret_cast<const uint4 *>(a.x + t * a.x_stride + k0 + 8 * p);
-            const float up = __uint_as_float(static_cast<uint32_t>(s_exp[t] + 127) << 23);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t h[4];
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float f0 = __uint_as_float(w[j] << 16) * up, f1 = __uint_as_float(w[j] & 0xFFFF0000u) * up;
-                const __half2 hh = __floats2half2_rn(f0, f1);
-                h[j] = *reinterpret_cast<const uint32_t *>(&hh);
-                sum += f0 + f1;
-            }
-            *reinterpret_cast<uint4 *>(xbuf + t * map.pitch + p * 16) = make_uint4(h[0], h[1], h[2], h[3]);
-            // (all 32 lanes: n is a multiple of 32)
-#pragma unroll
-            for (int off = 1; off < G / 8; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            if (p % (G / 8) == 0) gbuf[(p / (G / 8)) * 8 + t] = sum;
+            convert(t, p, piece(t, k0 + 8 * p), s_exp[t]);
         }
         __syncthreads();
     };
-    load_x(0);
+    {
+        // the largest elements, by as many warps a token as there are
+        constexpr int kHeld = 8;  // pieces that a lane keeps between the two passes
+        const int k0 = u0 * kUnit, n = (u1 - u0) * (kUnit / 8);
+        const int wpt = WARPS / a.B, t = warp / wpt, step = wpt * 32, p0 = warp % wpt * 32 + lane;  // 1 or more: at most 8 tokens
+        // (one piece has a way of its own: the other's code, not yet in the
+        // instruction cache, costs one token 0.4 of 4.3 us)
+        const bool one = nchunk == 1 && n <= step, held = nchunk == 1 && n <= kHeld * step;
+        if (tid < 8) s_top[tid] = s_exp[tid] = 0;
+        __syncthreads();
+        uint4 v[kHeld];
+        uint32_t top = 0;
+        if (t < a.B) {
+            if (one) {
+                v[0] = p0 < n ? piece(t, k0 + 8 * p0) : make_uint4(0u, 0u, 0u, 0u);
+                top = largest(v[0]);
+            } else if (held) {
+#pragma unroll
+                for (int j = 0; j < kHeld; ++j) v[j] = p0 + j * step < n ? piece(t, k0 + 8 * (p0 + j * step)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int j = 0; j < kHeld; ++j) top = max(top, largest(v[j]));
+            } else {
+#pragma unroll 4
+                for (int p = p0; p < n; p += step) top = max(top, largest(piece(t, k0 + 8 * p)));
+            }
+            top = __reduce_max_sync(0xffffffffu, top);
+            if (lane == 0) atomicMax(&s_top[t], static_cast<int>(top));
+        }
+        __syncthreads();
+        const int exp = t < a.B ? exponent(s_top[t]) : 0;
+        if (t < a.B && p0 == 0) s_exp[t] = exp;
+        if (one) {
+            if (t < a.B && p0 < n) convert(t, p0, v[0], exp);
+            __syncthreads();
+        } else if (held) {
+            if (t < a.B) {
+#pragma unroll
+                for (int j = 0; j < kHeld; ++j)
+                    if (p0 + j * step < n) convert(t, p0 + j * step, v[j], exp);
+            }
+            __syncthreads();
+        } else {
+            __syncthreads();
+            load_x(0);
+        }
+    }
 
     // the B operand's row of this lane (columns past the batch repeat its last
     // token: they are not stored)
@@ -371,10 +405,11 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) linear_few_kernel(cons
         if (RW < WARPS || a.split > 1) {
             // add up the warps of a row tile and the blocks of the cluster
             float *dst = red + (rw * KW + kw) * (8 * 16);
-            dst[(2 * c) * 16 + g8] = y[0];
-            dst[(2 * c + 1) * 16 + g8] = y[1];
-            dst[(2 * c) * 16 + g8 + 8] = y[2];
-            dst[(2 * c + 1) * 16 + g8 + 8] = y[3];
+            const float d0 = down(2 * c), d1 = down(2 * c + 1);
+            dst[(2 * c) * 16 + g8] = y[0] * d0;
+            dst[(2 * c + 1) * 16 + g8] = y[1] * d1;
+            dst[(2 * c) * 16 + g8 + 8] = y[2] * d0;
+            dst[(2 * c + 1) * 16 + g8 + 8] = y[3] * d1;
             if (a.split > 1)
                 cluster_sync();
             else
@@ -390,7 +425,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) linear_few_kernel(cons
                         sum += a.split > 1 ? dsmem_ld(smem_u32(src), sp) : *src;
                     }
                 }
-                if (row < a.N) a.store(t, row, sum * down(t));
+                if (row < a.N) a.store(t, row, sum);
             }
             if (a.split > 1)
                 cluster_sync();
