@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
         f1 = f0 + per < W ? f0 + per : W;
         first = by_warp ? f0 : f0 + warp;
         my_n = f1 > first ? static_cast<int>((f1 - first + stride - 1) / stride) : 0;
-#pragma unroll
+#pragma unroll 1
         for (int j = 0; j < NS; ++j) {
             if (j < my_n) issue(j);
             cp_async_commit();
