@@ -19,8 +19,8 @@
 // the tokens.
 //
 // A block of eight warps takes RW tiles of 16 rows, KW = 8 / RW warps share the
-// k of a tile: one tile for few rows (2048 rows occupy 128 SMs), eight for many
-// (no sums across warps then).  If there are too few rows for the GPU, a
+// k of a tile: one tile for few rows (2048 rows occupy 128 SMs), two or four for
+// more, eight for many (no sums across warps then).  If there are too few rows for the GPU, a
 // cluster of up to eight blocks shares K and adds up through distributed
 // shared memory.  Each warp streams its weights through its own ring of
 // cp.async stages (16 rows x 256 k and their scales).  The tokens as fp16 and
@@ -479,16 +479,19 @@ static cudaError_t launch_t(LinearArgs a, int num_sms, cudaStream_t s) {
 
 template <int G>
 static cudaError_t launch_g(const LinearArgs &a, int num_sms, cudaStream_t s) {
-    // row tiles a block: as many as still give every SM two blocks' worth of
-    // work several times over; where the tokens leave no room for two blocks of
-    // eight warps on a SM, one of sixteen
+    // row tiles a block: for many rows eight (where the tokens leave no room for two
+    // blocks of eight warps on a SM, one block of sixteen), else as few as let all
+    // blocks run at once, up to four (2048 -> 16384 with one token: one 10.2 us,
+    // four 8.2; 4096 -> 4096 with four tokens: one 7.3, two 6.8)
     const int tiles = (a.N + 15) / 16, units = (a.K + kUnit - 1) / kUnit;
     if (tiles >= 8 * 4 * num_sms) {
         if (smem_map<G, 8, 8>(a.B, units, 1).total > kHalfSmem) return launch_t<G, 16, 16>(a, num_sms, s);
         return launch_t<G, 8, 8>(a, num_sms, s);
     }
-    if (tiles >= 4 * 2 * num_sms) return launch_t<G, 8, 4>(a, num_sms, s);
-    return launch_t<G, 8, 1>(a, num_sms, s);
+    const int slots = num_sms * (smem_map<G, 8, 1>(a.B, units, 1).total <= kHalfSmem ? 2 : 1);
+    if (tiles <= slots) return launch_t<G, 8, 1>(a, num_sms, s);
+    if (tiles <= 2 * slots) return launch_t<G, 8, 2>(a, num_sms, s);
+    return launch_t<G, 8, 4>(a, num_sms, s);
 }
 
 }  // namespace few

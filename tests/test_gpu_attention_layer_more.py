@@ -162,3 +162,25 @@ def test_append_ragged_numbers_of_heads():
             mag = 12.0 * (2.0 ** -21 + 4 * FP32)       # of |a| + |b| <= 12: six deviations each
             assert ((got.double() - want).abs() <= want.abs() * BF16 * 1.01 + mag).all()
         assert torch.equal(cache.v[pages, :, off], v)
+
+
+@pytest.mark.parametrize("B, K, N, G", [
+    (1, 512, 6000, 64), (3, 512, 9700, 32), (8, 2048, 2500, 64), (8, 2080, 5000, 32),     # two tiles of rows a block
+    (1, 256, 12000, 128), (5, 1024, 11111, 64), (7, 4096, 5100, 64),                      # four
+    (8, 8192, 2000, 64), (3, 32768, 2600, 128), (8, 32768, 131, 64),                      # tokens in chunks; K in a cluster
+    (6, 1056, 16, 32), (8, 128, 1, 128),
+])
+def test_linear_few_tokens_tiles_and_shares(B, K, N, G):
+    m, w, x = case(B, K, N, G, B + K + N)
+    # (the padding of the rows of scales holds zeros here, as pack_int4 leaves it)
+    for t in (m.scale, m.bias):
+        t[:, K // G:] = 0
+    x[B // 2] *= 2.0 ** -60      # tokens of different magnitude, and one that grows along k
+    x[-1] = (x[-1].double() * 2.0 ** torch.linspace(-20, 0, K, device="cuda").double()).to(torch.bfloat16)
+    want = x.double() @ w.t()
+    err = bound(x, w, K)
+    # tokens as fp16: an element below 2^-31 of the largest is off by 2^-40 of that
+    err = err + x.abs().double().max(1, keepdim=True).values * 2.0 ** -40 * w.abs().sum(1)
+    y = moe.linear(m, x, dtype=torch.float32)
+    assert ((y.double() - want).abs() <= err).all()
+    assert torch.equal(y, moe.linear(m, x, dtype=torch.float32))
