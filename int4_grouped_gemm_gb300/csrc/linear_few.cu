@@ -19,8 +19,8 @@
 // the tokens.
 //
 // A block of eight warps takes RW tiles of 16 rows, KW = 8 / RW warps share the
-// k of a tile: one tile for few rows (2048 rows occupy 128 SMs), two or four for
-// more, eight for many (no sums across warps then).  If there are too few rows for the GPU, a
+// k of a tile: one or two tiles for few rows (2048 rows occupy 128 SMs), eight for
+// many (no sums across warps then) or for long tokens.  If there are too few rows for the GPU, a
 // cluster of up to eight blocks shares K and adds up through distributed
 // shared memory.  Each warp streams its weights through its own ring of
 // cp.async stages (16 rows x 256 k and their scales).  The tokens as fp16 and
@@ -449,9 +449,11 @@ static cudaError_t launch_t(LinearArgs a, int num_sms, cudaStream_t s) {
     const int units = (a.K + kUnit - 1) / kUnit;
     const int row_blocks = (a.N + 16 * RW - 1) / (16 * RW);
     // share K in a cluster while that leaves every warp a unit and the GPU is
-    // not yet full
+    // not yet full (clusters of other numbers than powers of two measured slower:
+    // they find fewer places)
+    const int most = RW == WARPS ? num_sms : num_sms + num_sms / 4;
     a.split = 1;
-    while (a.split < 8 && row_blocks * a.split * 2 <= num_sms + num_sms / 4 && units / (a.split * 2) >= KW) a.split *= 2;
+    while (a.split < 8 && row_blocks * a.split * 2 <= most && units / (a.split * 2) >= KW) a.split *= 2;
     // all of the block's tokens at once if that leaves room for them
     a.chunk_units = (units + a.split - 1) / a.split;
     while (smem_map<G, WARPS, RW>(a.B, a.chunk_units, a.split).total > kMaxSmem) a.chunk_units = (a.chunk_units + 1) / 2;
@@ -479,19 +481,21 @@ static cudaError_t launch_t(LinearArgs a, int num_sms, cudaStream_t s) {
 
 template <int G>
 static cudaError_t launch_g(const LinearArgs &a, int num_sms, cudaStream_t s) {
-    // row tiles a block: for many rows eight (where the tokens leave no room for two
-    // blocks of eight warps on a SM, one block of sixteen), else as few as let all
-    // blocks run at once, up to four (2048 -> 16384 with one token: one 10.2 us,
-    // four 8.2; 4096 -> 4096 with four tokens: one 7.3, two 6.8)
+    // row tiles a block.  A block converts all tokens of its k, so that many or
+    // long tokens take eight tiles a block and share K among more blocks instead
+    // (8 tokens 4096 -> 4096: one tile 10.6 us, two 10.2, eight 7.1; 8192 -> 4096:
+    // 19, 19, 10).  Else one if all blocks run at once, two if they do then, and
+    // eight for many rows (one token 2048 -> 3500, 6000, 16384: one tile 4.0, 5.7,
+    // 10.2; two 3.9, 5.4, 8.7; eight 4.5, 5.8, 7.4).  Where the tokens leave no room
+    // for two blocks of eight warps on a SM, very many rows take one of sixteen
     const int tiles = (a.N + 15) / 16, units = (a.K + kUnit - 1) / kUnit;
-    if (tiles >= 8 * 4 * num_sms) {
-        if (smem_map<G, 8, 8>(a.B, units, 1).total > kHalfSmem) return launch_t<G, 16, 16>(a, num_sms, s);
-        return launch_t<G, 8, 8>(a, num_sms, s);
-    }
-    const int slots = num_sms * (smem_map<G, 8, 1>(a.B, units, 1).total <= kHalfSmem ? 2 : 1);
-    if (tiles <= slots) return launch_t<G, 8, 1>(a, num_sms, s);
-    if (tiles <= 2 * slots) return launch_t<G, 8, 2>(a, num_sms, s);
-    return launch_t<G, 8, 4>(a, num_sms, s);
+    const bool room = smem_map<G, 8, 8>(a.B, units, 1).total <= kHalfSmem;
+    if (tiles >= 8 * 4 * num_sms && !room) return launch_t<G, 16, 16>(a, num_sms, s);
+    const int slots = num_sms * (room ? 2 : 1);
+    const bool tokens = a.B * a.K >= 8192 && tiles >= num_sms / 4;  // (for 131 rows of 32768: eight 17, one 10.7)
+    if (tokens || tiles > 2 * slots) return launch_t<G, 8, 8>(a, num_sms, s);
+    if (tiles > slots) return launch_t<G, 8, 2>(a, num_sms, s);
+    return launch_t<G, 8, 1>(a, num_sms, s);
 }
 
 }  // namespace few
