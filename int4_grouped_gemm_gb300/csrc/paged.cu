@@ -220,6 +220,7 @@ __host__ __device__ constexpr int own_smem_bytes(int D) {
     return own_ring_bytes(D) + own_merge_bytes(D) + 2 * kOwnWarps * 8 * 4 + kOwnWarps * own_stages(D) * 4 +
            (kMaxRows + 1) * 8;
 }
+static_assert(kOwnWarps == 8, "a shift by 3 divides by the warps");
 static_assert(own_smem_bytes(128) <= 227 * 1024 && own_smem_bytes(64) <= 227 * 1024, "one block per SM");
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -232,6 +233,12 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
+}
+
+// a / b of two numbers that are not negative: nearly always both fit 32 bits,
+// where a division takes a fraction of the instructions.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return (a | b) >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
 }
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
@@ -283,9 +290,31 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
     const int Hkv = a.c.Hkv, ps = a.c.page_shift;
     const int ntp = a.join ? tiles16(a.prefix_len) : 0;
 
-    // tiles of the rows before each row (four rows a thread, then a scan), and
-    // the number of rows that have any
-    {
+    // tiles of the rows before each row, and the number of rows that have any
+    int64_t items = 0;
+    if (a.B <= 31) {
+        // a row a lane, the same in every warp
+        int64_t n = 0;
+        if (lane < a.B) {
+            bool over;
+            const int len = own_len(a, lane, over);
+            n = a.seq_len[lane] < 0 ? 0 : ntp + tiles16(len);
+            if (over && blockIdx.x == 0 && warp == 0) record_status(a.status, MOE_ERR_PAGE);
+        }
+        items = __popc(__ballot_sync(0xffffffffu, n > 0));
+        int64_t scan = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, scan, off);
+            if (lane >= off) scan += v;
+        }
+        if (warp == 0 && lane <= a.B) {
+            s_start[lane] = scan - n;
+            if (blockIdx.x == 0) a.starts[lane] = scan - n;
+        }
+        __syncthreads();
+    } else {
+        // four rows a thread, then a scan
         int64_t n[4], sum = 0;
         int filled = 0;
 #pragma unroll
@@ -329,12 +358,11 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
             if (blockIdx.x == 0) a.starts[kMaxRows] = scan;
         }
         __syncthreads();
-    }
-    const int64_t W = s_start[a.B] * Hkv;
-    int64_t items = 0;
 #pragma unroll
-    for (int w = 0; w < kOwnWarps; ++w) items += s_rows[w];
+        for (int w = 0; w < kOwnWarps; ++w) items += s_rows[w];
+    }
     items *= Hkv;
+    const int64_t W = s_start[a.B] * Hkv;
     // tiles of a piece: as many pieces as there are blocks or warps, or fewer
     // where that leaves less than an item or a few tiles for each
     const bool by_warp = W <= kShortItem * items;
@@ -342,8 +370,8 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
     most = most > items ? most : items;
     const int64_t cap = by_warp ? a.ncta * kOwnWarps : a.ncta;
     most = most < cap ? most : cap;
-    const int64_t per = most ? (W + most - 1) / most : 0;
-    const int n_pieces = per ? static_cast<int>((W + per - 1) / per) : 0;
+    const int64_t per = most ? quotient(W + most - 1, most) : 0;
+    const int n_pieces = per ? static_cast<int>(quotient(W + per - 1, per)) : 0;
     const int given = a.prefix_ncta ? (by_warp ? a.own_first * kOwnWarps : a.own_first) : n_pieces;  // not by the counter
     if (blockIdx.x == 0 && tid == 0) {
         a.starts[a.B + 1] = per;
@@ -381,7 +409,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
         const int b = row_of(f);
         const int64_t nt = s_start[b + 1] - s_start[b];
         const int64_t in_row = f - s_start[b] * Hkv;
-        const int kv = static_cast<int>(in_row / nt);
+        const int kv = static_cast<int>(quotient(in_row, nt));
         int t = static_cast<int>(in_row - kv * nt);
         const int *pages = a.table + static_cast<int64_t>(b) * a.table_ld;
         bool over;
@@ -457,7 +485,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
         f0 = piece * per;
         f1 = f0 + per < W ? f0 + per : W;
         first = by_warp ? f0 : f0 + warp;
-        my_n = f1 > first ? static_cast<int>((f1 - first + stride - 1) / stride) : 0;
+        my_n = f1 > first ? static_cast<int>((f1 - first + stride - 1) >> (by_warp ? 0 : 3)) : 0;
 #pragma unroll 1
         for (int j = 0; j < NS; ++j) {
             if (j < my_n) issue(j);
@@ -465,7 +493,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
         }
         int i = 0, b = row_of(f0);
         int64_t nt = s_start[b + 1] - s_start[b];  // tiles of the row's items
-        int kv = static_cast<int>((f0 - s_start[b] * Hkv) / nt);
+        int kv = static_cast<int>(quotient(f0 - s_start[b] * Hkv, nt));
         int64_t end = s_start[b] * Hkv + (kv + 1) * nt;  // end of this item
         load_q(b, kv);
         for (int64_t f = f0; f < f1;) {
@@ -635,8 +663,8 @@ __global__ void __launch_bounds__(kParts * 64, 16 / kParts) paged_combine_kernel
     const float2 *own_ml = a.own_ml;
     const float *own_o = a.own_o;
     if (nt > 0) {
-        const int64_t f = s0 * Hkv + kv * nt, p0 = f / per;
-        n_own = static_cast<int>((f + nt - 1) / per - p0) + 1;
+        const int64_t f = s0 * Hkv + kv * nt, p0 = quotient(f, per);
+        n_own = static_cast<int>(quotient(f + nt - 1, per) - p0) + 1;
         const int64_t slot = p0 + static_cast<int64_t>(b) * Hkv + kv;
         own_ml += slot * 8 + h;
         own_o += (slot * (D / 4) + d4) * 32 + h * 4;
