@@ -1,4 +1,6 @@
 // Appending to a paged key-value cache and attending over it.
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace moe {
@@ -314,49 +316,56 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
         }
         __syncthreads();
     } else {
-        // four rows a thread, then a scan
-        int64_t n[4], sum = 0;
-        int filled = 0;
+        // one or four rows a thread, then a scan
+        auto scan_rows = [&](auto each) {
+            constexpr int R = decltype(each)::value;
+            int64_t n[R], sum = 0;
+            int filled = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int b = tid * 4 + i;
-            n[i] = 0;
-            if (b < a.B) {
-                bool over;
-                const int len = own_len(a, b, over);
-                n[i] = a.seq_len[b] < 0 ? 0 : ntp + tiles16(len);
-                if (over && blockIdx.x == 0) record_status(a.status, MOE_ERR_PAGE);
+            for (int i = 0; i < R; ++i) {
+                const int b = tid * R + i;
+                n[i] = 0;
+                if (b < a.B) {
+                    bool over;
+                    const int len = own_len(a, b, over);
+                    n[i] = a.seq_len[b] < 0 ? 0 : ntp + tiles16(len);
+                    if (over && blockIdx.x == 0) record_status(a.status, MOE_ERR_PAGE);
+                }
+                sum += n[i];
+                filled += n[i] > 0;
             }
-            sum += n[i];
-            filled += n[i] > 0;
-        }
-        int64_t scan = sum;
+            int64_t scan = sum;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, scan, off);
-            if (lane >= off) scan += v;
-            filled += __shfl_xor_sync(0xffffffffu, filled, off);
-        }
-        if (lane == 31) {
-            s_warp[warp] = scan;
-            s_rows[warp] = filled;
-        }
-        __syncthreads();
-        scan -= sum;
-        for (int w = 0; w < warp; ++w) scan += s_warp[w];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int b = tid * 4 + i;
-            if (b <= a.B) {
-                s_start[b] = scan;
-                if (blockIdx.x == 0) a.starts[b] = scan;
+            for (int off = 1; off < 32; off <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, scan, off);
+                if (lane >= off) scan += v;
             }
-            scan += n[i];
-        }
-        if (tid == kOwnThreads - 1 && a.B == kMaxRows) {
-            s_start[kMaxRows] = scan;
-            if (blockIdx.x == 0) a.starts[kMaxRows] = scan;
-        }
+            filled = __reduce_add_sync(0xffffffffu, filled);
+            if (lane == 31) {
+                s_warp[warp] = scan;
+                s_rows[warp] = filled;
+            }
+            __syncthreads();
+            scan -= sum;
+            for (int w = 0; w < warp; ++w) scan += s_warp[w];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int b = tid * R + i;
+                if (b <= a.B) {
+                    s_start[b] = scan;
+                    if (blockIdx.x == 0) a.starts[b] = scan;
+                }
+                scan += n[i];
+            }
+            if (tid == kOwnThreads - 1 && a.B == R * kOwnThreads) {
+                s_start[a.B] = scan;
+                if (blockIdx.x == 0) a.starts[a.B] = scan;
+            }
+        };
+        if (a.B <= kOwnThreads)
+            scan_rows(std::integral_constant<int, 1>());
+        else
+            scan_rows(std::integral_constant<int, kMaxRows / kOwnThreads>());
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < kOwnWarps; ++w) items += s_rows[w];

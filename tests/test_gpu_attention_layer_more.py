@@ -184,3 +184,43 @@ def test_linear_few_tokens_tiles_and_shares(B, K, N, G):
     y = moe.linear(m, x, dtype=torch.float32)
     assert ((y.double() - want).abs() <= err).all()
     assert torch.equal(y, moe.linear(m, x, dtype=torch.float32))
+
+
+@pytest.mark.parametrize("B", [1, 2, 30, 31, 32, 33, 255, 256, 257, 1023, 1024])
+@pytest.mark.parametrize("prefix", [0, 40])
+def test_attend_numbers_of_rows(B, prefix):
+    """Row counts at which the rows' tiles are counted another way, with rows that
+    are empty, padding, or full."""
+    g = torch.Generator(device="cuda").manual_seed(B + prefix)
+    Hq, Hkv, D, page, ld = 4, 2, 64, 16, 3
+    cache = attention.PagedCache.empty(B * ld + 3, Hkv, page, D)
+    cache.k.copy_(torch.randn(cache.k.shape, generator=g, device="cuda"))
+    cache.v.copy_(torch.randn(cache.v.shape, generator=g, device="cuda"))
+    pages = torch.randperm(B * ld + 3, generator=g, device="cuda").to(torch.int32)
+    table, shared = pages[:B * ld].view(B, ld), pages[B * ld:]
+    lens = torch.randint(-1, ld * page + 1, (B,), generator=g, device="cuda").to(torch.int32)
+    lens[-1] = ld * page if B % 2 else -1
+    lens[0] = 0 if B % 3 else lens[0]
+    q = torch.randn(B, Hq, D, generator=g, device="cuda").to(torch.bfloat16)
+    out = torch.full_like(q, 9.0)
+    cache.attend(q, table, lens, shared if prefix else None, prefix, out=out)
+    assert int(cache.status[0]) == 0
+
+    def gather(pool, t):  # [.., n pages] -> [.., Hkv, positions, D]
+        return pool[t.long()].transpose(-4, -3).flatten(-3, -2).double()
+    k, v = gather(cache.k, table), gather(cache.v, table)
+    s = torch.einsum("bgrd,bgnd->bgrn", q.double().view(B, Hkv, 2, D), k) / D ** 0.5
+    s = s.masked_fill(torch.arange(ld * page, device="cuda") >= lens.view(B, 1, 1, 1), -float("inf"))
+    if prefix:
+        pk, pv = gather(cache.k, shared)[:, :prefix], gather(cache.v, shared)[:, :prefix]
+        sp = torch.einsum("bgrd,gnd->bgrn", q.double().view(B, Hkv, 2, D), pk) / D ** 0.5
+        s, v = torch.cat((sp, s), -1), torch.cat((pv.expand(B, -1, -1, -1), v), 2)
+    p = s.softmax(-1).nan_to_num(0.0)
+    want = torch.einsum("bgrn,bgnd->bgrd", p, v).reshape(B, Hq, D)
+    # weights rounded to bf16, each 2^-8 of itself at most, a hundredth more for the
+    # fp32 arithmetic; then the output's rounding
+    tol = BF16 * 1.01 * (torch.einsum("bgrn,bgnd->bgrd", p, v.abs()).reshape(B, Hq, D) * 2 + want.abs()) + 1e-6
+    real = lens >= 0
+    assert ((out.double() - want).abs() <= tol)[real].all()
+    assert (out[~real] == 9.0).all()
+    assert prefix or (out[lens == 0] == 0).all()
