@@ -440,21 +440,30 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
     };
     const uint32_t ring = smem_u32(smem) + warp * NS * STAGE;
     // tile i into stage i % NS: keys then values, chunk ch of row r at
-    // ch ^ (r & 7); rows past the last position are zeros
+    // ch ^ (r & 7); rows past the last position are zeros.  Lane l copies chunk
+    // l % CH of rows l / CH, + RS, + 2 RS, ..  (A tile lies within a page, so that
+    // the addresses of all its rows are inside the pool; those of a tile without
+    // a page are page 0's, and nothing is read)
+    constexpr int RS = 32 / CH;
+    const int r0 = lane / CH;
+    const int64_t from = (r0 * a.c.pos_stride + lane % CH * 8) * 2, row_bytes = a.c.pos_stride * (2 * RS);
+    const int64_t to_v = reinterpret_cast<const char *>(a.c.v) - reinterpret_cast<const char *>(a.c.k);
+    const uint32_t at_row = r0 * ROW, at_chunk = (lane % CH ^ r0) << 4;
     auto issue = [&](int i) {
         if ((i & 31) == 0) describe(i + lane);
         const int64_t at = __shfl_sync(0xffffffffu, d_at, i & 31);
         const int valid = __shfl_sync(0xffffffffu, d_valid, i & 31);
-        const uint32_t st = ring + (i % NS) * STAGE;
+        const uint32_t st = ring + (i % NS) * STAGE + at_row;
         if (lane == 0) s_valid[warp * NS + i % NS] = valid;
+        const char *src = reinterpret_cast<const char *>(a.c.k + at) + from;
 #pragma unroll
-        for (int j = lane; j < kPosTile * CH; j += 32) {
-            const int r = j / CH, ch = j % CH;
-            const bool ok = r < valid;
-            const int64_t src = ok ? at + r * a.c.pos_stride + ch * 8 : 0;
-            const uint32_t dst = st + r * ROW + ((ch ^ (r & 7)) << 4);
-            cp16_or_zero(dst, a.c.k + src, ok);
-            cp16_or_zero(dst + kPosTile * ROW, a.c.v + src, ok);
+        for (int j = 0; j < kPosTile / RS; ++j) {
+            const bool ok = r0 + j * RS < valid;
+            // (r0 and j RS have no bit in common)
+            const uint32_t dst = st + j * RS * ROW + (at_chunk ^ (j * RS & 7) << 4);
+            cp16_or_zero(dst, src, ok);
+            cp16_or_zero(dst + kPosTile * ROW, src + to_v, ok);
+            src += row_bytes;
         }
     };
     // ldmatrix lane roles: matrix mi = lane / 8, row rr = lane % 8
