@@ -202,9 +202,9 @@ cudaError_t launch_append(const AppendArgs &a, int num_sms, cudaStream_t s) {
 //            rounded values, so that a weight's rounding cancels where one
 //            position dominates
 // Measured, with the merge: 8 rows of up to 32768 positions (134 MB of keys and
-// values) 30 us, 4.5 TB/s, of which the merge's launch and the start (lengths,
-// pages, first tiles: three dependent reads) are 9; 128 rows of up to 512 13 us;
-// one row of 1000 10 us, all of it latency.
+// values) 29 us, 4.6 TB/s, of which the merge's launch and the start (lengths,
+// pages, first tiles: three dependent reads) are 8; 128 rows of up to 512 12.4 us;
+// one row of 1000 9.3 us, all of it latency.
 constexpr int kOwnWarps = 8;
 constexpr int kOwnThreads = kOwnWarps * 32;
 constexpr int kPosTile = 16;
@@ -657,8 +657,10 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
 // the online merge over its partials, four at a time (their loads
 // independent), the shares meet in shared memory.  Bound by latency, so there
 // are as many shares as keep the GPU's threads busy: 128 rows without a prefix
-// take 13 us in all with 2 shares and 18 with 8, one row of 32768 positions 21
-// and 14.
+// took 13 us in all with 2 shares and 18 with 8, one row of 32768 positions 21
+// and 14.  (A merge by the last block to finish an item, in the kernel above,
+// took 1 to 4 us more: its fence, its atomic and one block's reads cost more than
+// this launch.)
 constexpr int kBatch = 4;
 
 template <int kParts>
