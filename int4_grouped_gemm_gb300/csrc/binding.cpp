@@ -49,6 +49,14 @@ int32_t int32(PyObject *o, const char *name) {
     return static_cast<int32_t>(v);
 }
 
+// The cache's description, by its address.
+const gqa_pages *pages_at(PyObject *o) {
+    const void *p = PyLong_AsVoidPtr(o);
+    if (!p && PyErr_Occurred()) throw Raised{};
+    if (!p) value_error("no cache");
+    return static_cast<const gqa_pages *>(p);
+}
+
 // A size as the C calls take it; what is too large for them stays too large.
 int32_t size32(int64_t n) { return static_cast<int32_t>(n < INT32_MAX ? n : INT32_MAX); }
 
@@ -140,8 +148,9 @@ int linear(PyObject *const *v) {
 // pos_offset, interleaved, q_out | None, stream | None
 int append(PyObject *const *v) {
     const int dev = device_of_cache("append", v[1]);
-    const auto *pages = static_cast<const gqa_pages *>(PyLong_AsVoidPtr(v[0]));
+    const gqa_pages *pages = pages_at(v[0]);
     auto *status = static_cast<int32_t *>(PyLong_AsVoidPtr(v[2]));
+    if (!status && PyErr_Occurred()) throw Raised{};
     const at::Tensor &k = tensor(v[4], "k"), &val = tensor(v[5], "v");
     const int64_t T = k.dim() ? k.size(0) : 0;
     const int64_t ks = heads_of(k, "k", T, pages->Hkv, pages->D, dev), vs = heads_of(val, "v", T, pages->Hkv, pages->D, dev);
@@ -182,7 +191,7 @@ int append(PyObject *const *v) {
 // pages, device, q, page_table, seq_len, prefix_pages | None, prefix_len, scale, out, ws, stream | None
 int attend(PyObject *const *v) {
     const int dev = device_of_cache("attend", v[1]);
-    const auto *pages = static_cast<const gqa_pages *>(PyLong_AsVoidPtr(v[0]));
+    const gqa_pages *pages = pages_at(v[0]);
     const at::Tensor &q = tensor(v[2], "q");
     const int64_t B = q.dim() ? q.size(0) : 0, qs = heads_of(q, "q", B, -1, pages->D, dev);
     const at::Tensor &table = tensor(v[3], "page_table");

@@ -136,6 +136,20 @@ def test_the_module_checks_numbers_and_their_count():
         n.linear(w.q, w.scale, w.bias, 1 << 70, 128, 64, x, torch.zeros(2, 64), None, None)
 
 
+def test_the_module_takes_addresses_only():
+    n, c = _lib.native(), cache()
+    k = torch.zeros(3, 2, 64, dtype=BF)
+    rest = (None, k, k, ints(3), ints(3), ints(1, 4), None, 0, False, None, None)
+    for pages, status, error in ((0, 0, ValueError), (None, 0, TypeError), (c._at, "x", TypeError), (c.desc, 0, TypeError)):
+        with pytest.raises(error):
+            n.append(pages, 0, status, *rest)
+    for pages, error in ((0, ValueError), ("x", TypeError)):
+        with pytest.raises(error):
+            n.attend(pages, 0, k, ints(3, 4), ints(3), None, 0, 1.0, k, k, None)
+    with pytest.raises(TypeError):
+        n.attend(c._at, "x", k, ints(3, 4), ints(3), None, 0, 1.0, k, k, None)
+
+
 def test_the_module_and_the_binding_share_one_library():
     """The module is linked to the library beside it, which ctypes has loaded:
     one set of limits and device state in the process."""
