@@ -224,3 +224,35 @@ def test_attend_numbers_of_rows(B, prefix):
     assert ((out.double() - want).abs() <= tol)[real].all()
     assert (out[~real] == 9.0).all()
     assert prefix or (out[lens == 0] == 0).all()
+
+
+def test_the_c_calls_of_the_binding_agree_with_the_helpers():
+    """The calls under their C names on raw descriptors, as for the other operators."""
+    m, _, x = case(5, 512, 300, 64, 1)
+    m.scale[:, 8:] = 0
+    y = torch.empty(5, 300, device="cuda")
+    _lib.int4_linear(m.as_c(), 300, 512, 64, x, y)
+    assert torch.equal(y, moe.linear(m, x, dtype=torch.float32))
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q, k, v = (torch.randn(4, h, 64, generator=g, device="cuda").to(torch.bfloat16) for h in (6, 2, 2))
+    seq = torch.arange(4, dtype=torch.int32, device="cuda")
+    index = torch.tensor([0, 5, 17, 31], dtype=torch.int32, device="cuda")
+    table = torch.arange(8, dtype=torch.int32, device="cuda").view(4, 2)
+    shared = torch.tensor([8, 9], dtype=torch.int32, device="cuda")
+    freq = 100.0 ** (-torch.arange(16, device="cuda") / 16)
+    results = []
+    for raw in (False, True):
+        cache = attention.PagedCache.empty(10, 2, 16, 64)
+        cache.k.copy_(torch.randn(cache.k.shape, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda"))
+        cache.v.copy_(cache.k * 2)
+        turned, out = torch.empty_like(q), torch.empty_like(q)
+        if raw:
+            _lib.gqa_append(cache.desc, q, k, v, seq, index, table, 20, freq, True, turned, cache.status)
+            ws = torch.zeros(_lib.gqa_paged_workspace_bytes(4, 6, 2, 64, 20), dtype=torch.uint8, device="cuda")
+            _lib.gqa_paged_attention(cache.desc, turned, shared, 20, table, index + 1, 0.125, out, ws)
+        else:
+            cache.append(q, k, v, seq, index, table, freq, 20, True, q_out=turned)
+            cache.attend(turned, table, index + 1, shared, 20, out=out)
+        results.append((turned, cache.k, cache.v, out))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
