@@ -198,9 +198,10 @@ cudaError_t launch_append(const AppendArgs &a, int num_sms, cudaStream_t s) {
 // that come late find nothing left and go.  (Which block took a piece does not
 // show in the result.)
 //   scores   mma.sync m16n8k16, the heads as M, 16 positions as N
-//   output   O += P V, P from the score registers, rounded to bf16; l sums the
-//            rounded values, so that a weight's rounding cancels where one
-//            position dominates
+//   output   O += P V, P from the score registers as two bf16 parts (|p - hi -
+//            lo| <= 2^-17 p): the heads fill only half of the MMA's 16 rows, the
+//            upper parts are rows 0-7 and the lower ones rows 8-15, and the two
+//            results are added when the item is through.  l sums the fp32 values
 // Measured, with the merge: 8 rows of up to 32768 positions (134 MB of keys and
 // values) 29 us, 4.6 TB/s, of which the merge's launch and the start (lengths,
 // pages, first tiles: three dependent reads) are 8; 128 rows of up to 512 12.4 us;
@@ -545,17 +546,26 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
                     tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
                     const float m_new = fmaxf(m_run, tmax);  // finite: the tile has a position
                     const float corr = exp2f(m_run - m_new);
-                    const uint32_t p01 = bf16_pair(exp2f(sc[0] - m_new), exp2f(sc[1] - m_new));
-                    const uint32_t p23 = bf16_pair(exp2f(sc[2] - m_new), exp2f(sc[3] - m_new));
-                    l_run = l_run * corr + ((__uint_as_float(p01 << 16) + __uint_as_float(p01 & 0xFFFF0000u)) +
-                                            (__uint_as_float(p23 << 16) + __uint_as_float(p23 & 0xFFFF0000u)));
+                    float p[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) p[j] = exp2f(sc[j] - m_new);
+                    l_run = l_run * corr + ((p[0] + p[1]) + (p[2] + p[3]));
                     m_run = m_new;
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         o[n][0] *= corr;
                         o[n][1] *= corr;
+                        o[n][2] *= corr;
+                        o[n][3] *= corr;
                     }
-                    const uint32_t pa[4] = {p01, 0u, p23, 0u};
+                    uint32_t pa[4];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t hi = bf16_pair(p[2 * j], p[2 * j + 1]);
+                        pa[2 * j] = hi;
+                        pa[2 * j + 1] = bf16_pair(p[2 * j] - __uint_as_float(hi << 16),
+                                                  p[2 * j + 1] - __uint_as_float(hi & 0xFFFF0000u));
+                    }
 #pragma unroll
                     for (int jt = 0; jt < NT / 2; ++jt) {
                         uint32_t bm[4];
@@ -583,6 +593,12 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
                 load_q(b, kv);
             }
 
+            // both parts of the weights
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                o[n][0] += o[n][2];
+                o[n][1] += o[n][3];
+            }
             float l_sum = l_run + __shfl_xor_sync(0xffffffffu, l_run, 1);
             l_sum += __shfl_xor_sync(0xffffffffu, l_sum, 2);
             if (by_warp) {
