@@ -15,10 +15,15 @@
 //            its softmax, the tensor core works for the other.  Up to 128 rows
 //            in all: one sub-tile; slot 0 takes the even and slot 1 the odd
 //            tiles, each with a partial of its own
-//   S, P, O  in tensor memory: S (fp32, 128 columns) and P (bf16, over S's
-//            first 64) and O (fp32, D columns) per slot, 512 columns in all at
-//            D = 128.  P is an operand straight from tensor memory, so that the
-//            second product's shared-memory reads are V alone
+//   S, P, O  in tensor memory: S (fp32, 128 columns), P over it, and O (fp32, D
+//            columns) per slot, 512 columns in all at D = 128.  P is an operand
+//            straight from tensor memory, so that the second product's
+//            shared-memory reads are V alone.  A weight is two bf16 parts (|p -
+//            hi - lo| <= 2^-17 p; of each 64 positions the upper ones over the
+//            first half of their scores' columns, the lower ones over the other),
+//            each with MMAs of its own: with one part, rounded by up to 2^-8, a
+//            call with 128 rows behind 131072 positions took 106 us instead of
+//            129, and rows lost accuracy by sharing their prefix
 //   softmax  one thread per row: no exchange between threads.  m need not be the
 //            maximum, only a reference that keeps 2^(s - m) in range, the same in
 //            l and O: fp32 and bf16 hold a weight of 2^32 as exactly as one of
@@ -294,8 +299,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                             tc_fence_after();
 #pragma unroll
                             for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                                umma_bf16_ts(sO, sS + kk * 8, sdesc_mn128(v_addr + kk * 2048), id_o,
+                                umma_bf16_ts(sO, sS + half * 32 + kk * 8, sdesc_mn128(v_addr + kk * 2048), id_o,
                                              (n < next ? 0 : 1) | kk);
+#pragma unroll
+                            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                                umma_bf16_ts(sO, sS + half * 32 + 32 + kk * 8, sdesc_mn128(v_addr + kk * 2048), id_o, 1);
                         }
                         if (!ok) break;
                         if (n + next < steps) scores(n + next);
@@ -321,7 +329,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         const int slot = warp >> 2, r = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t sS = (tmem + slot * 128) | lanes, sO = (tmem + 256 + slot * D) | lanes;
-        uint32_t mine = 0, it = 0, nq = 0, blocks = 0;
+        uint32_t it = 0;
+        uint32_t turn = 0;                             // parities: blocks of rows (1), of those with tiles (2), this slot's tiles (4)
         bool ok = true;
         int t = tile0;
         for (int j = 0, item = item0; j < count && ok; ++item, t = 0) {
@@ -333,10 +342,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             // The slots have seen the scores of the previous block's last tile and
             // the issuers are past it, so that nothing reads the old ones
             mbar_arrive(&s->q_free);
-            ok = prefix_wait(&s->q_free, nq & 1, a, s, 32);
+            ok = prefix_wait(&s->q_free, turn & 1, a, s, 32);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            ++nq;
+            turn ^= 1;
             {
                 // all copies in flight together (as plain loads and stores they cost
                 // 10 of the 18 us of a short prefix)
@@ -375,7 +384,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             for (int n = 0; j < end; ++j, ++t, ++n, it += 2) {
                 if (!active || (!two && (n & 1) != slot)) continue;
                 const int valid = a.prefix_len - t * kPos;
-                ok = prefix_wait(&s->s_full[slot], mine & 1, a, s, 28);
+                ok = prefix_wait(&s->s_full[slot], turn >> 2, a, s, 28);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -383,7 +392,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     mbar_arrive(&s->p_full[slot][0]);
                     mbar_arrive(&s->p_full[slot][1]);
                     any = true;
-                    ++mine;
+                    turn ^= 4;
                     continue;
                 }
                 uint32_t xa[32], xb[32], xc[32];
@@ -453,20 +462,26 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                         }
                     }
                 };
-                // weights, rounded to bf16 for the product; l sums them unrounded
+                // weights, in two bf16 parts for the product; l sums them in fp32
+                const uint64_t minus1 = pack2(0xBF800000u, 0xBF800000u);
                 const uint64_t scale2 = pack2(__float_as_uint(a.scale_log2), __float_as_uint(a.scale_log2));
                 auto weigh = [&](const uint32_t *y, int n0) {
                     const uint64_t neg_m = pack2(__float_as_uint(-m), __float_as_uint(-m));
-                    uint32_t p[16];
+                    uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         float2 w = unpack2(fma2(pack2(y[2 * e], y[2 * e + 1]), scale2, neg_m));
                         w.x = ex2(w.x);
                         w.y = ex2(w.y);
-                        p[e] = bf162_as_u32(__floats2bfloat162_rn(w.x, w.y));
-                        l2[e & 1] = add2(l2[e & 1], pack2(__float_as_uint(w.x), __float_as_uint(w.y)));
+                        const uint64_t w2 = pack2(__float_as_uint(w.x), __float_as_uint(w.y));
+                        hi[e] = bf162_as_u32(__floats2bfloat162_rn(w.x, w.y));
+                        const float2 r = unpack2(fma2(pack2(hi[e] << 16, hi[e] & 0xFFFF0000u), minus1, w2));
+                        lo[e] = bf162_as_u32(__floats2bfloat162_rn(r.x, r.y));
+                        l2[e & 1] = add2(l2[e & 1], w2);
                     }
-                    tmem_st16(sS + n0 / 2, p);
+                    // (positions 64 on have their columns from 64 on)
+                    tmem_st16(sS + n0 / 2 + n0 / 64 * 32, hi);
+                    tmem_st16(sS + n0 / 2 + n0 / 64 * 32 + 32, lo);
                 };
                 tmem_wait32(xa);
                 tmem_wait32(xb);
@@ -486,7 +501,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 mask(xc, 64);
                 mask(xa, 96);
                 tm = top(xc, xa);
-                if (__any_sync(0xffffffffu, tm > m + kRaise)) raise(tm, 32);
+                if (__any_sync(0xffffffffu, tm > m + kRaise)) raise(tm, 64);
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(&s->p_full[slot][0]);
@@ -498,14 +513,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 const float2 lsum = unpack2(add2(l2[0], l2[1]));
                 l += lsum.x + lsum.y;
                 any = true;
-                ++mine;
+                turn ^= 4;
             }
             if (!ok) break;
             // this piece's partial of the block
             if (active) {
                 const int64_t part = (static_cast<int64_t>(blockIdx.x) + item) * 2 + slot;
                 if (any) {  // also without rows: the next block's first tile comes after this
-                    ok = prefix_wait(&s->o_full[slot], blocks++ & 1, a, s, 31);
+                    ok = prefix_wait(&s->o_full[slot], turn >> 1 & 1, a, s, 31);
+                    turn ^= 2;
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();

@@ -54,6 +54,9 @@ def reference(q, k, v, scale):
     (3, 16, 2, 16, 0, 46),       # pieces by warp
     (1, 16, 2, 64, 0, 1100),     # by block
     (1, 16, 2, 16, 90, 30),      # one row reads the prefix as its own
+    (5, 16, 2, 16, 130, 0),      # 128 rows of the prefix at most
+    (40, 8, 1, 32, 300, 0),      # 256-row blocks
+    (33, 16, 4, 16, 100, 20),    # both parts in one softmax
 ])
 def test_weights_are_not_rounded_to_bf16(B, Hq, Hkv, page, prefix, own, D):
     g = torch.Generator().manual_seed(B + prefix + own + D)
