@@ -555,7 +555,8 @@ size_t gqa_paged_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, 
  *   out[b][h] = softmax(scale * q[b][h] . keys) values     fp32, bf16 out.
  * The prefix is read once for the whole batch.  A row without any position
  * (seq_len 0, no prefix) gives zeros; a row with seq_len < 0 is padding, its
- * out is left as it was.  What the pages hold behind a sequence's last
+ * out is left as it was.  A score of minus infinity weighs nothing; a NaN one,
+ * one of plus infinity, or no other than minus infinity, makes its row's head NaN.  What the pages hold behind a sequence's last
  * position has no influence, NaN included.  Several rows may name the same
  * pages (draft tokens of one sequence: the same table row, growing lengths).
  * q, out: rows of Hq heads of D at the given row strides; out may be q.

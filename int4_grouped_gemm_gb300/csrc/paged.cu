@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
                     float tmax = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
                     tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
                     tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
-                    const float m_new = fmaxf(m_run, tmax);  // finite: the tile has a position
+                    const float m_new = fmaxf(fmaxf(m_run, tmax), kLeastRef);
                     const float corr = exp2f(m_run - m_new);
                     float p[4];
 #pragma unroll

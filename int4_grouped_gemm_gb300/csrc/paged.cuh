@@ -28,6 +28,11 @@ struct AppendArgs {
     int T, Hq, n_seq, table_ld, pos_offset, rot, interleaved;
 };
 
+// A part's reference m (log2 units) is never below this, so that a part with
+// positions differs from one without (-inf): scores of -inf weigh nothing, and
+// NaN, which a maximum passes over, stays in the sums.
+constexpr float kLeastRef = -3.402823466e38f;
+
 // Partial results of the attention, merged by the combine kernel.  A list of
 // tiles is cut into pieces of `per` tiles; piece c and item i of the list (a
 // row's key-value head, or a block of rows of the prefix) that meet have

@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 mask(xb, 32);
                 float tm = top(xa, xb);
                 if (!any)
-                    m = ceilf(tm);
+                    m = fmaxf(ceilf(tm), kLeastRef);
                 else if (__any_sync(0xffffffffu, tm > m + kRaise))
                     raise(tm, 0);
                 tmem_ld32(sS + 64, xc);
