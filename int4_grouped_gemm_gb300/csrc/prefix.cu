@@ -28,8 +28,8 @@
 //            maximum, only a reference that keeps 2^(s - m) in range, the same in
 //            l and O: fp32 and bf16 hold a weight of 2^32 as exactly as one of
 //            1.  So m stays as it is until a score exceeds it by more than 32
-//            (an integer step then, which scales O, l and the tile's weights
-//            exactly), and the weights need not wait for the tile's maximum
+//            (to the next integer then, which scales O, l and the tile's weights
+//            by a power of two), and the weights need not wait for the tile's maximum
 //
 //   warps 0-3, 4-7   softmax of slot 0, 1 (warp w: rows 32 (w % 4) ..)
 //   warp 8           loads: 64-dimension boxes of page rows by TMA, 128-byte
@@ -432,7 +432,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 // much (the warp's 32 rows together; p: weights of this tile so
                 // far, in words): rare but for a block's first tile
                 auto raise = [&](float tm, int p) {
-                    const float m_new = tm > m + kRaise ? m + ceilf(tm - m) : m;
+                    // (the next integer itself: a step from m would lose it if m is far away)
+                    const float m_new = tm > m + kRaise ? ceilf(tm) : m;
                     const float corr = ex2(m - m_new);
                     m = m_new;
                     l *= corr;

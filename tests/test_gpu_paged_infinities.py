@@ -131,3 +131,21 @@ def test_nan_and_infinite_scores_are_not_dropped(shape, value):
     hit = s.B if first < s.prefix else 1        # the prefix is everybody's
     assert torch.isnan(out[:hit]).all()
     assert torch.equal(out[hit:], clean[hit:])
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_scores_far_below_others_in_front_of_them(shape):
+    """The first half scores -8e11 (log2 units), the second 47,000 throughout: the
+    mean of the second half's values."""
+    s = Batch(*shape)
+    n = s.prefix + s.own
+    s.q.zero_()
+    s.q[..., 0] = 2.0 ** 20
+    for b in range(s.B):
+        s.set_keys(b, s.prefix if b and s.prefix else 0, n // 2, -2.0 ** 22)
+        s.set_keys(b, max(n // 2, s.prefix if b and s.prefix else 0), n, 0.25)
+    out = s.run(0.125)
+    for b in range(s.B):
+        want, top = s.want(b, 0.125)
+        err = (out[b].double() - want).abs()
+        assert (err <= top * 2.0 ** -11 + want.abs() * BF16).all(), b
