@@ -199,7 +199,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) gqa_attention_kernel(const __
         float tmax = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
         tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
         tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
-        const float m_new = fmaxf(m_run, tmax);   // finite: a tile holds at least one position of the range
+        // never below the least finite value: scores of -inf weigh nothing, and NaN,
+        // which a maximum passes over, stays in the sums
+        const float m_new = fmaxf(fmaxf(m_run, tmax), -3.402823466e38f);
         const float corr = expf(m_run - m_new);   // 0 on the warp's first tile (m_run = -inf)
         float p[4];
 #pragma unroll
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(256) gqa_combine_kernel(const __grid_constant_
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (mr[i] == -INFINITY) continue;  // past the ranges (every real range has a finite maximum)
+            if (mr[i] == -INFINITY) continue;  // past the ranges (every real range has a maximum above that)
             const float mn = fmaxf(m, mr[i]);
             const float c0 = expf(m - mn), c1 = expf(mr[i] - mn);
             num = num * c0 + orr[i] * c1;

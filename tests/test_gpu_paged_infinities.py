@@ -149,3 +149,35 @@ def test_scores_far_below_others_in_front_of_them(shape):
         want, top = s.want(b, 0.125)
         err = (out[b].double() - want).abs()
         assert (err <= top * 2.0 ** -11 + want.abs() * BF16).all(), b
+
+
+@pytest.mark.parametrize("L", [40, 1000, 30000])
+def test_one_sequence_call_with_infinite_and_nan_scores(L):
+    """gqa_decode_attention likewise."""
+    Hq, Hkv, D = 16, 2, 128
+    g = torch.Generator(device="cuda").manual_seed(L)
+    q, k, v = (torch.randn(h, *n, D, generator=g, device="cuda").to(torch.bfloat16) for h, n in ((Hq, ()), (Hkv, (L,)), (Hkv, (L,))))
+    q[:, 0] = 1.0
+    out = torch.empty(Hq, D, dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(_lib.gqa_attention_workspace_bytes(Hq, Hkv, D, L), dtype=torch.uint8, device="cuda")
+
+    def run():
+        _lib.gqa_decode_attention(q, k, v, L, 1 / math.sqrt(D), out, ws)
+        return out.clone()
+    clean = run()
+    keep = k.clone()
+    k[:, :L // 3, 0] = -INF
+    got = run()
+    p = torch.softmax(q.double().view(Hkv, 8, D) @ k.double().transpose(1, 2) / math.sqrt(D), -1)
+    want = (p @ v.double()).view(Hq, D)
+    assert ((got.double() - want).abs() <= float(v.abs().max()) * 2.0 ** -11 + want.abs() * BF16).all()
+    k.copy_(keep)
+    k[0, L // 2:L // 2 + 20] = NAN
+    got = run()
+    assert torch.isnan(got[:8]).all() and torch.equal(got[8:], clean[8:])
+    k.copy_(keep)
+    q[3, 5] = NAN
+    got = run()
+    assert torch.isnan(got[3]).all()
+    got[3] = clean[3]
+    assert torch.equal(got, clean)
