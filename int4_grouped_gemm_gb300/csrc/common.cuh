@@ -120,6 +120,38 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, long l
     return true;
 }
 
+// Whether the phase with the given parity has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// One role's wait for another of its block: until the phase has completed, or an
+// earlier wait of the block has run out (*abort), or `limit` cycles have passed,
+// which is recorded and ends the block.  The limit is looked at before the thread
+// is suspended, so that with a limit of one cycle every wait that has to wait at
+// all runs out.
+__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, long long limit, int *status, int *abort, int site) {
+    if (mbar_test(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (;;) {
+        if (clock64() - t0 >= limit) {
+            record_status(status, MOE_ERR_TIMEOUT - site);
+            *reinterpret_cast<volatile int *>(abort) = 1;
+            return false;
+        }
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*reinterpret_cast<volatile int *>(abort)) return false;
+    }
+}
+
 // A block's wait for its own copies and MMAs in flight before it ends: about two
 // milliseconds at least, however short the caller's limit is, since what lands
 // after the block has gone would land in another one's shared memory.

@@ -118,17 +118,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 __device__ __forceinline__ bool prefix_wait(uint64_t *bar, uint32_t parity, const PagedArgs &a, PrefixCtl *s, int site) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!mbar_try_wait(bar, parity)) {
-        if (*reinterpret_cast<volatile int *>(&s->abort)) return false;
-        if (clock64() - t0 > a.wait_limit) {
-            record_status(a.status, MOE_ERR_TIMEOUT - site);
-            *reinterpret_cast<volatile int *>(&s->abort) = 1;
-            return false;
-        }
-    }
-    return true;
+    return role_wait(bar, parity, a.wait_limit, a.status, &s->abort, site);
 }
 
 template <int D>
