@@ -393,7 +393,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     const uint32_t vi = (it + 1) % kKvStages;
                     ok = prefix_wait(&s->kv_full[vi], ((it + 1) / kKvStages) & 1, a, s, 30);
                     ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
+                    if (!ok) {
+                        // (no load is under way when tensor memory is freed)
+                        tmem_wait32(xa);
+                        tmem_wait32(xb);
+                        break;
+                    }
                     for (int i = valid * 8 + r; i < kPos * 8; i += kRows)
 #pragma unroll
                         for (int h = 0; h < HALVES; ++h)
