@@ -570,6 +570,13 @@ int gqa_paged_attention(const gqa_pages *cache, const void *q, int64_t q_stride,
                         const int32_t *seq_len, float scale, void *out, int64_t out_stride, void *ws, size_t ws_bytes,
                         cudaStream_t stream);
 
+/* The same with errors recorded at *status (any zeroed int32, device) instead of
+ * the workspace's first word: for workspaces that do not outlive their call. */
+int gqa_paged_attention_status(const gqa_pages *cache, const void *q, int64_t q_stride, int32_t B, int32_t Hq,
+                               const int32_t *prefix_pages, int32_t prefix_len, const int32_t *page_table,
+                               int32_t table_ld, const int32_t *seq_len, float scale, void *out, int64_t out_stride,
+                               void *ws, size_t ws_bytes, int32_t *status, cudaStream_t stream);
+
 /* Human-readable text for a status code. */
 const char *moe_status_string(int code);
 

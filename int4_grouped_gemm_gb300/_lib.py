@@ -107,6 +107,8 @@ SIGNATURES = {
     "gqa_paged_workspace_bytes": (c_sz, [c_i32, c_i32, c_i32, c_i32, c_i32]),
     "gqa_paged_attention": (ctypes.c_int, [c_p, c_p, c_i64, c_i32, c_i32, c_p, c_i32, c_p, c_i32, c_p, ctypes.c_float,
                                            c_p, c_i64, c_p, c_sz, c_p]),
+    "gqa_paged_attention_status": (ctypes.c_int, [c_p, c_p, c_i64, c_i32, c_i32, c_p, c_i32, c_p, c_i32, c_p,
+                                                  ctypes.c_float, c_p, c_i64, c_p, c_sz, c_p, c_p]),
 }
 
 

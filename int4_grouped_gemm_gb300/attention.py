@@ -38,7 +38,8 @@ class PagedCache:
         self.desc = _lib.gqa_pages(k.data_ptr(), v.data_ptr(), self.n_pages, self.page_size, self.Hkv, self.D, page,
                                    head, pos)
         self._device = k.get_device()
-        # where append records errors found on the device
+        # where append, attend without a workspace and the projections of a
+        # decoding step record errors found on the device (moe_read_device_status)
         self.status = torch.zeros(4, dtype=torch.int32, device=k.device)
         self._at, self._status_at = ctypes.addressof(self.desc), self.status.data_ptr()
         self._scale = 1.0 / math.sqrt(self.D)
@@ -67,26 +68,34 @@ class PagedCache:
     def workspace(self, B: int, Hq: int, prefix_len: int = 0) -> torch.Tensor:
         """Scratch of attend for up to B rows, Hq heads and prefix_len shared
         positions; calls that may overlap take one each."""
+        return torch.zeros(self._workspace_bytes(B, Hq, prefix_len), dtype=torch.uint8, device=self.k.device)
+
+    def _workspace_bytes(self, B: int, Hq: int, prefix_len: int) -> int:
         n = _lib.gqa_paged_workspace_bytes(B, Hq, self.Hkv, self.D, prefix_len)
         if n == 0:
             raise _lib.MoEError(_lib.MOE_ERR_SHAPE, "gqa_paged_workspace_bytes")
-        return torch.zeros(n, dtype=torch.uint8, device=self.k.device)
+        return n
 
     def attend(self, q: torch.Tensor, page_table: torch.Tensor, seq_len: torch.Tensor,
                prefix_pages: Optional[torch.Tensor] = None, prefix_len: int = 0, scale: Optional[float] = None,
                out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """out [B, Hq, D]: row b's query attends to the shared prefix (read
         once for all rows), then to the first seq_len[b] positions of
-        page_table[b].  scale: 1 / sqrt(D) unless given."""
+        page_table[b].  scale: 1 / sqrt(D) unless given.  Errors found on the
+        device are recorded in the first word of ws, without ws (scratch of the
+        call's own is then allocated) in `status`."""
         if stream is not None and (out is None or ws is None):
             with _lib.on_stream(stream):
                 return self.attend(q, page_table, seq_len, prefix_pages, prefix_len, scale, out, ws)
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        status = None
         if ws is None:
-            ws = self.workspace(q.shape[0], q.shape[1], prefix_len)
+            ws = torch.empty(self._workspace_bytes(q.shape[0], q.shape[1], prefix_len), dtype=torch.uint8,
+                             device=self.k.device)
+            status = self._status_at
         rc = _lib.native().attend(self._at, self._device, q, page_table, seq_len, prefix_pages, prefix_len,
-                                  self._scale if scale is None else scale, out, ws, _lib.handle(stream))
+                                  self._scale if scale is None else scale, out, ws, _lib.handle(stream), status)
         if rc:
             raise _lib.MoEError(rc, "gqa_paged_attention")
         return out
@@ -102,9 +111,10 @@ class AttentionLayer:
         self.qkv, self.out, self.Hq, self.Hkv, self.D = qkv, out, Hq, Hkv, D
         self.inv_freq, self.interleaved = inv_freq, interleaved
 
-    def project(self, x: torch.Tensor, stream=None):
-        """Queries, keys and values [T, heads, D] of 1 to 64 tokens (views of one buffer)."""
-        return self._split(linear(self.qkv, x, stream=stream))
+    def project(self, x: torch.Tensor, stream=None, status: Optional[torch.Tensor] = None):
+        """Queries, keys and values [T, heads, D] of 1 to 64 tokens (views of one buffer).
+        status: as for moe.linear (a cache's `status`, for instance)."""
+        return self._split(linear(self.qkv, x, status=status, stream=stream))
 
     def _split(self, y: torch.Tensor):
         y = y.view(y.shape[0], self.Hq + 2 * self.Hkv, self.D)
@@ -117,13 +127,14 @@ class AttentionLayer:
         new token goes to position index[b] of page table row seq[b]; it
         attends to the prefix and the first seq_len[b] positions of row b
         (seq_len = index + 1 for a plain step; both negative: padding, whose
-        attn row means nothing)."""
+        attn row means nothing).  1 to 64 rows.  Errors found on the device are
+        recorded in cache.status, the attention's in the first word of ws."""
         if stream is not None:
             with _lib.on_stream(stream):
                 return self.decode(x, cache, seq, index, page_table, seq_len, ws, prefix_pages, prefix_len)
-        qkv = linear(self.qkv, x)
+        qkv = linear(self.qkv, x, status=cache.status)
         q, k, v = self._split(qkv)
         # queries, rotated queries and the attention's output share their place
         cache.append(q, k, v, seq, index, page_table, self.inv_freq, prefix_len, self.interleaved, q_out=q)
         cache.attend(q, page_table, seq_len, prefix_pages, prefix_len, out=q, ws=ws)
-        return linear(self.out, qkv[:, :self.Hq * self.D])
+        return linear(self.out, qkv[:, :self.Hq * self.D], status=cache.status)

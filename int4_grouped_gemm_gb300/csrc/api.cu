@@ -925,11 +925,19 @@ int gqa_paged_attention(const gqa_pages *cache, const void *q, int64_t q_stride,
                         const int32_t *prefix_pages, int32_t prefix_len, const int32_t *page_table, int32_t table_ld,
                         const int32_t *seq_len, float scale, void *out, int64_t out_stride, void *ws, size_t ws_bytes,
                         cudaStream_t stream) {
+    return gqa_paged_attention_status(cache, q, q_stride, B, Hq, prefix_pages, prefix_len, page_table, table_ld, seq_len,
+                                      scale, out, out_stride, ws, ws_bytes, static_cast<int32_t *>(ws), stream);
+}
+
+int gqa_paged_attention_status(const gqa_pages *cache, const void *q, int64_t q_stride, int32_t B, int32_t Hq,
+                               const int32_t *prefix_pages, int32_t prefix_len, const int32_t *page_table,
+                               int32_t table_ld, const int32_t *seq_len, float scale, void *out, int64_t out_stride,
+                               void *ws, size_t ws_bytes, int32_t *status, cudaStream_t stream) {
     PagedArgs a{};
     int rc = check_pages(cache, a.c);
     if (rc) return rc;
     if ((rc = check_ptr(q)) || (rc = check_ptr4(page_table)) || (rc = check_ptr4(seq_len)) || (rc = check_ptr(out)) ||
-        (rc = check_ptr(ws)))
+        (rc = check_ptr(ws)) || (rc = check_ptr4(status)))
         return rc;
     if ((rc = check_paged_shape(B, Hq, a.c.Hkv, a.c.D, prefix_len))) return rc;
     if (prefix_len > 0 && (rc = check_ptr4(prefix_pages))) return rc;
@@ -950,7 +958,7 @@ int gqa_paged_attention(const gqa_pages *cache, const void *q, int64_t q_stride,
     a.prefix_pages = prefix_pages;
     a.table = page_table;
     a.seq_len = seq_len;
-    a.status = static_cast<int *>(ws);
+    a.status = status;
     a.B = B;
     a.Hq = Hq;
     a.group = Hq / a.c.Hkv;

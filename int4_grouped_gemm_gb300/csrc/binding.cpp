@@ -188,7 +188,8 @@ int append(PyObject *const *v) {
                       stream_of(v[13], dev));
 }
 
-// pages, device, q, page_table, seq_len, prefix_pages | None, prefix_len, scale, out, ws, stream | None
+// pages, device, q, page_table, seq_len, prefix_pages | None, prefix_len, scale, out, ws, stream | None and,
+// where the workspace is this call's own (its control block is then cleared first), the address for errors
 int attend(PyObject *const *v) {
     const int dev = device_of_cache("attend", v[1]);
     const gqa_pages *pages = pages_at(v[0]);
@@ -210,19 +211,31 @@ int attend(PyObject *const *v) {
     const at::Tensor &out = tensor(v[8], "out"), &ws = tensor(v[9], "ws");
     const int64_t os = heads_of(out, "out", B, q.size(1), pages->D, dev);
     if (ws.get_device() != dev || !ws.is_contiguous()) value_error("ws: contiguous, on the current device");
-    return gqa_paged_attention(pages, q.data_ptr(), qs, size32(B), size32(q.size(1)), prefix, prefix_len, at,
-                               size32(table.size(1)), lens, static_cast<float>(scale), out.data_ptr(), os, ws.data_ptr(),
-                               static_cast<size_t>(ws.numel()) * ws.element_size(), stream_of(v[10], dev));
+    const size_t bytes = static_cast<size_t>(ws.numel()) * ws.element_size();
+    const cudaStream_t stream = stream_of(v[10], dev);
+    auto *status = static_cast<int32_t *>(ws.data_ptr());
+    if (v[11] != Py_None) {
+        status = static_cast<int32_t *>(PyLong_AsVoidPtr(v[11]));
+        if (!status && PyErr_Occurred()) throw Raised{};
+        const int rc = moe_workspace_init(ws.data_ptr(), bytes, stream);
+        if (rc) return rc;
+    }
+    return gqa_paged_attention_status(pages, q.data_ptr(), qs, size32(B), size32(q.size(1)), prefix, prefix_len, at,
+                                      size32(table.size(1)), lens, static_cast<float>(scale), out.data_ptr(), os,
+                                      ws.data_ptr(), bytes, status, stream);
 }
 
-template <int (*CALL)(PyObject *const *), int ARGS>
+// ARGS arguments, and up to MORE that are None if they are left out.
+template <int (*CALL)(PyObject *const *), int ARGS, int MORE>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    if (n != ARGS) {
+    if (n < ARGS || n > ARGS + MORE) {
         PyErr_Format(PyExc_TypeError, "%d arguments, not %zd", ARGS, n);
         return nullptr;
     }
+    PyObject *all[ARGS + MORE];
+    for (Py_ssize_t i = 0; i < ARGS + MORE; ++i) all[i] = i < n ? args[i] : Py_None;
     try {
-        return PyLong_FromLong(CALL(args));
+        return PyLong_FromLong(CALL(all));
     } catch (const Raised &) {
     } catch (const std::exception &e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
@@ -230,14 +243,14 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return nullptr;
 }
 
-template <int (*CALL)(PyObject *const *), int ARGS>
+template <int (*CALL)(PyObject *const *), int ARGS, int MORE = 0>
 PyCFunction fast() {
-    return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<CALL, ARGS>));
+    return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<CALL, ARGS, MORE>));
 }
 
 PyMethodDef methods[] = {{"linear", fast<linear, 10>(), METH_FASTCALL, "int4_linear"},
                          {"append", fast<append, 14>(), METH_FASTCALL, "gqa_append"},
-                         {"attend", fast<attend, 11>(), METH_FASTCALL, "gqa_paged_attention"},
+                         {"attend", fast<attend, 11, 1>(), METH_FASTCALL, "gqa_paged_attention"},
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "The attention sub-layer's calls on torch tensors.", -1, methods,
