@@ -4,16 +4,20 @@ Each .cu file compiles to an object in parallel, then one link step makes
 the shared library next to this file.  No cmake, no torch extension machinery:
 the library has a plain C ABI and is loaded with ctypes.  Beside it stands
 _native.so, a Python module that makes the attention sub-layer's calls on torch
-tensors (host code against torch's headers and libraries).
+tensors (host code against torch's headers and libraries); where there is no
+torch, the library alone is built.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
+import importlib.util
 import os
 import platform
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -41,19 +45,21 @@ def _stale(obj: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _binding_flags():
-    """Flags of the compile and of the link of the Python module."""
-    import importlib.util
-    import sysconfig
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
-    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+def _torch_root():
+    """torch's folder, or None."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def _binding_flags(torch: str):
+    """Flags of the compile and of the link of the Python module (nvcc's, which
+    brings a host compiler with it)."""
     # (torch's and CUDA's headers as system headers: their warnings are theirs)
-    compile_ = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-I" + os.path.join(ROOT, "include"),
+    compile_ = ["-O2", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "-I" + os.path.join(ROOT, "include"),
                 "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(torch, "include"),
-                "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
-                "-isystem", os.path.join(cuda, "include")]
-    link = ["-L" + HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(torch, "lib"),
-            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+                "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include")]
+    link = ["-cudart", "none", "-L" + HERE, "-Xlinker", "-l:" + os.path.basename(LIB), "-Xlinker", "-rpath=$ORIGIN",
+            "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     return compile_, link
 
 
@@ -77,13 +83,15 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if force or _stale(o, [s, *headers, __file__]):
             jobs.append([nvcc(), *ARCH, *NVCC_FLAGS, *extra_flags, "-c", s, "-o", o])
 
-    # (of one torch version, like the module made from it)
-    import importlib.metadata
-    src = os.path.join(CSRC, "binding.cpp")
-    binding_obj = os.path.join(BUILD_DIR, "binding-" + importlib.metadata.version("torch") + ".o")
-    compile_, link = _binding_flags()
-    if force or _stale(binding_obj, [src, headers[-1], __file__]):
-        jobs.append(["g++", *compile_, "-c", src, "-o", binding_obj])
+    torch = _torch_root()
+    binding = None
+    if torch:
+        # (of one torch version, like the module made from it)
+        src = os.path.join(CSRC, "binding.cpp")
+        binding_obj = os.path.join(BUILD_DIR, "binding-" + importlib.metadata.version("torch") + ".o")
+        compile_, link = _binding_flags(torch)
+        if force or _stale(binding_obj, [src, headers[-1], __file__]):
+            binding = [nvcc(), *compile_, "-c", src, "-o", binding_obj]
 
     def run(cmd):
         if verbose:
@@ -94,6 +102,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        # (the library does not wait for the module, nor depend on it)
+        module = ex.submit(run, binding) if binding else None
         for err in ex.map(run, jobs):
             if verbose and err:
                 print(err, file=sys.stderr)
@@ -101,9 +111,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"])
         os.replace(tmp, LIB)
-    if force or _stale(BINDING, [binding_obj, LIB]):
+    if module:
+        module.result()
+    if torch and (force or _stale(BINDING, [binding_obj, LIB])):
         tmp = BINDING + f".tmp{os.getpid()}"
-        run(["g++", "-shared", "-o", tmp, binding_obj, *link])
+        run([nvcc(), *ARCH, "-shared", "-o", tmp, binding_obj, *link])
         os.replace(tmp, BINDING)
     return LIB
 
