@@ -45,6 +45,13 @@ def _stale(obj: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _read(path: str) -> str:
+    if not os.path.exists(path):
+        return ""
+    with open(path) as f:
+        return f.read().strip()
+
+
 def _torch_root():
     """torch's folder, or None."""
     spec = importlib.util.find_spec("torch")
@@ -68,7 +75,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     # objects built on another machine type are never reused
     stamp = os.path.join(BUILD_DIR, "host.txt")
     host = platform.machine()
-    if not os.path.exists(stamp) or open(stamp).read().strip() != host:
+    if _read(stamp) != host:
         force = True
         with open(stamp, "w") as f:
             f.write(host + "\n")
@@ -86,9 +93,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     torch = _torch_root()
     binding = None
     if torch:
-        # (of one torch version, like the module made from it)
+        # object and module are of one torch and one Python version; the object has them
+        # in its name, the module in the note beside the objects
         src = os.path.join(CSRC, "binding.cpp")
-        binding_obj = os.path.join(BUILD_DIR, "binding-" + importlib.metadata.version("torch") + ".o")
+        versions = importlib.metadata.version("torch") + (sysconfig.get_config_var("EXT_SUFFIX") or "")
+        binding_obj = os.path.join(BUILD_DIR, "binding-" + versions + ".o")
+        made_for = os.path.join(BUILD_DIR, "binding.txt")
         compile_, link = _binding_flags(torch)
         if force or _stale(binding_obj, [src, headers[-1], __file__]):
             binding = [nvcc(), *compile_, "-c", src, "-o", binding_obj]
@@ -113,10 +123,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         os.replace(tmp, LIB)
     if module:
         module.result()
-    if torch and (force or _stale(BINDING, [binding_obj, LIB])):
+    if torch and (force or _stale(BINDING, [binding_obj, LIB]) or _read(made_for) != versions):
         tmp = BINDING + f".tmp{os.getpid()}"
         run([nvcc(), *ARCH, "-shared", "-o", tmp, binding_obj, *link])
         os.replace(tmp, BINDING)
+        with open(made_for, "w") as f:
+            f.write(versions + "\n")
     return LIB
 
 

@@ -68,3 +68,32 @@ def test_the_library_is_made_even_if_the_module_is_not(steps):
     with pytest.raises(RuntimeError, match="refused"):
         steps()
     assert os.path.exists(build.LIB) and not os.path.exists(build.BINDING)
+
+
+def test_the_module_follows_the_torch_version(steps, monkeypatch):
+    """Back at a version whose object is there already, older than the module of the
+    version between: linked again, and nothing is compiled."""
+    current = ["2.9.1"]
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: current[0])
+
+    def linked():
+        with open(build.BINDING) as f:
+            return f.read()
+    steps()
+    first = linked()
+    assert "2.9.1" in first
+    current[0] = "2.11.0"
+    made = steps()
+    assert len(made) == 2 and "2.11.0" in linked()          # its object and the module
+    current[0] = "2.9.1"
+    made = steps()
+    assert len(made) == 1 and "2.9.1" in linked() and "2.11.0" not in linked()
+    assert steps() == []
+
+
+def test_the_module_follows_the_python_version(steps, monkeypatch):
+    steps()
+    get = build.sysconfig.get_config_var
+    monkeypatch.setattr(build.sysconfig, "get_config_var", lambda n: ".cpython-399-none.so" if n == "EXT_SUFFIX" else get(n))
+    assert len(steps()) == 2
+    assert steps() == []
