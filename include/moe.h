@@ -518,8 +518,8 @@ typedef struct {
  * page_table[seq][index / page_size] (int32 [n_seq][table_ld], device), row
  * index % page_size.  Its rotary position is p = index[t] + pos_offset (the
  * length of a shared prefix, or 0), and with angles a_i = p * inv_freq[i]
- * (inv_freq fp32 [rot / 2], device; the product taken exactly, far positions
- * included) the pairs (x_i, x_{i + rot/2}) of each head, or with
+ * (inv_freq fp32 [rot / 2], device, below 2^63; the product taken exactly, far
+ * positions included) the pairs (x_i, x_{i + rot/2}) of each head, or with
  * interleaved = 1 (x_{2i}, x_{2i+1}), become
  *   (x cos a - y sin a, y cos a + x sin a)    fp32, rounded once to bf16;
  * dimensions rot .. D-1 stay.  Keys go to the cache rotated, values as they

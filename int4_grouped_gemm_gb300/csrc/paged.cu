@@ -6,14 +6,37 @@
 namespace moe {
 
 // The rotation angle pos * f as the cosine and sine of its fraction of a turn.
-// f / 2 pi, less whole turns, is kept as a 64-bit fraction (made in fp64, off by
-// 2^-53 of a turn at most for f below 2 pi), so that its product with a position
-// loses whole turns by itself and is off by 2^-22 of a turn at position 2^31, and
-// at any nearer position by less than the fp32 fraction's own rounding.
+// f / 2 pi, less whole turns, is kept as a 64-bit fraction, so that its product
+// with a position loses whole turns by itself.  The fraction is made from f's 24
+// bits times 128 bits of 1 / 2 pi in integers and is off by less than 2^-62 for any
+// f below 2^63, so that the angle is off by 2^-30 of a turn at position 2^32, less than
+// its own rounding to fp32.  (A product in fp64 loses what stands before the
+// point: with f = 100 it was off by 2^-20 of a turn at position 2^30.)
 __device__ __forceinline__ uint64_t turn_fraction(float f) {
-    double r = static_cast<double>(f) * 0.15915494309189533577;
-    r -= rint(r);
-    return static_cast<uint64_t>(__double2ll_rn(r * 18446744073709551616.0));  // 2^64
+    constexpr uint32_t kInv2Pi[4] = {0x7D4D3770u, 0x7F09D5F4u, 0x9391054Au, 0x28BE60DBu};  // 2^128 / 2 pi, from the lowest
+    const uint32_t u = __float_as_uint(f), biased = u >> 23 & 255u;
+    const uint32_t m = (u & 0x7FFFFFu) | (biased ? 0x800000u : 0u);  // f = m 2^(e - 150)
+    const int e = biased ? biased : 1;
+    uint32_t w[5];
+    uint64_t carry = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        carry += static_cast<uint64_t>(m) * kInv2Pi[i];
+        w[i] = static_cast<uint32_t>(carry);
+        carry >>= 32;
+    }
+    w[4] = static_cast<uint32_t>(carry);
+    // the 64 bits below the point: the product shifted down by 128 + 150 - 64 - e
+    const int s = max(214 - e, 0), at = s >> 5;
+    uint32_t lo = 0, mid = 0, hi = 0;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+        lo = i == at ? w[i] : lo;
+        mid = i == at + 1 ? w[i] : mid;
+        hi = i == at + 2 ? w[i] : hi;
+    }
+    const uint64_t frac = static_cast<uint64_t>(__funnelshift_r(mid, hi, s)) << 32 | __funnelshift_r(lo, mid, s);
+    return u >> 31 ? 0 - frac : frac;
 }
 __device__ __forceinline__ float2 angle_cs(uint32_t pos, uint64_t f) {
     const uint32_t frac = __umulhi(static_cast<uint32_t>(f), pos) + static_cast<uint32_t>(f >> 32) * pos;
@@ -24,9 +47,8 @@ __device__ __forceinline__ float2 angle_cs(uint32_t pos, uint64_t f) {
 
 // A block takes a few tokens (one when there are few, so that every SM has a
 // share, up to eight).  First the tokens' places and their angles' cosines and
-// sines into shared memory, one per thread and pair, shared by all heads (fp64
-// only once per pair and block: its rate is 1/64 of fp32's, and with a product
-// per angle a prompt of 8192 tokens took 1.4 us more); then 16-byte pieces: of a
+// sines into shared memory, one per thread and pair, shared by all heads (the
+// frequencies' fractions of a turn once per pair and block); then 16-byte pieces: of a
 // rotated head the pair of pieces whose elements turn into one another (halves:
 // pieces j and j + rot / 16 of the head; interleaved: a piece by itself),
 // otherwise plain copies.  Bound by the bytes, each read and written once, and at
