@@ -486,13 +486,22 @@ static cudaError_t launch_g(const LinearArgs &a, int num_sms, cudaStream_t s) {
     // (8 tokens 4096 -> 4096: one tile 10.6 us, two 10.2, eight 7.1; 8192 -> 4096:
     // 19, 19, 10).  Else one if all blocks run at once, two if they do then, and
     // eight for many rows (one token 2048 -> 3500, 6000, 16384: one tile 4.0, 5.7,
-    // 10.2; two 3.9, 5.4, 8.7; eight 4.5, 5.8, 7.4).  Where the tokens leave no room
-    // for two blocks of eight warps on a SM, very many rows take one of sixteen
+    // 10.2; two 3.9, 5.4, 8.7; eight 4.5, 5.8, 7.4).  (The border for long tokens: 131
+    // rows of 8 x 32768 eight 17, one 10.7; 700 of 8 x 16384 and 8 x 32768 eight 10.0 and
+    // 17.2, one 18.4 and 31; 700 of 8 x 4096 6.1 and 6.2; 700 of 1 x 8192 6.3 and 5.2.)
+    //
+    // A block of sixteen warps converts a chunk of the tokens for twice the rows: for
+    // very many rows whose tokens do not fit at once (80000 rows, 8 x 16384 in groups
+    // of 32 and 64: 294 and 330 us with eight warps, 247 and 235 with sixteen; 8 x
+    // 32768: 598, 490).  Where they do, sixteen are slower (4 x 16384: 192 and 222,
+    // 8 x 4096: 51 and 54, 1 x 32768: 329 and 585), and so they are in groups of 128
+    // (6 x 32768: 515 and 628)
     const int tiles = (a.N + 15) / 16, units = (a.K + kUnit - 1) / kUnit;
-    const bool room = smem_map<G, 8, 8>(a.B, units, 1).total <= kHalfSmem;
-    if (tiles >= 8 * 4 * num_sms && !room) return launch_t<G, 16, 16>(a, num_sms, s);
-    const int slots = num_sms * (room ? 2 : 1);
-    const bool tokens = a.B * a.K >= 8192 && tiles >= num_sms / 4;  // (for 131 rows of 32768: eight 17, one 10.7)
+    const int whole = smem_map<G, 8, 8>(a.B, units, 1).total;
+    if constexpr (G < 128)
+        if (tiles >= 8 * 4 * num_sms && whole > kMaxSmem) return launch_t<G, 16, 16>(a, num_sms, s);
+    const int slots = num_sms * (whole <= kHalfSmem ? 2 : 1);
+    const bool tokens = a.B * a.K >= 8192 && tiles >= num_sms / 4;
     if (tokens || tiles > 2 * slots) return launch_t<G, 8, 8>(a, num_sms, s);
     if (tiles > slots) return launch_t<G, 8, 2>(a, num_sms, s);
     return launch_t<G, 8, 1>(a, num_sms, s);

@@ -21,6 +21,8 @@ CASES = [  # B, K, N, group
     (9, 32, 40, 32), (12, 4224, 19500, 32), (16, 4096, 3001, 64), (20, 16640, 8600, 128), (33, 160, 515, 32),
     (37, 2080, 5003, 32), (40, 32768, 2000, 128), (48, 4096, 20000, 64), (64, 8320, 8600, 64), (64, 32768, 130, 32),
     (64, 2048, 24000, 64),
+    # very many rows: tokens that fit at once, and in chunks (blocks of sixteen warps)
+    (2, 8192, 78001, 64), (8, 14336, 78001, 32), (7, 16384, 77900, 64), (6, 20480, 77900, 128),
 ]
 
 
