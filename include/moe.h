@@ -478,7 +478,7 @@ int gqa_decode_attention_per_head(const void *q, const void *k_cache, const void
  * pack_int4 (scale and bias rows at the padded pitch).  The weights are not
  * rounded to bf16; sums in fp32, y rounded once to bf16 (y_fp32 = 0) or
  * written as fp32 (y_fp32 = 1); group sums and products stay finite for any
- * finite token, and a token with an infinity or NaN leaves its own row of y
+ * finite token and scales and biases below 2^90, and a token with an infinity or NaN leaves its own row of y
  * infinite or NaN and the other rows alone.  x: [B] rows of K bf16, row stride x_stride
  * (>= K); y: [B] rows of N, row stride y_stride (>= N, any).  y must not
  * overlap x.  1 <= N <= 2^30, group in {32, 64, 128}, K % group == 0, K <= 32768,
