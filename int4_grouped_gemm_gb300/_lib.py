@@ -365,13 +365,6 @@ def gqa_decode_attention(q, k_cache, v_cache, L: int, scale: float, out, ws, per
 # calls as they stand, on raw descriptors.
 
 
-def stream_on(stream, device: int) -> int:
-    if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(device)
-    return int(getattr(stream, "cuda_stream", stream))
-
-
 def handle(stream):
     """The raw handle of a torch stream (or of a handle); None stays None."""
     return stream if stream is None else int(getattr(stream, "cuda_stream", stream))
@@ -387,11 +380,6 @@ def on_stream(stream):
     return torch.cuda.stream(stream)
 
 
-def check(rc: int, what: str):
-    if rc:
-        raise MoEError(rc, what)
-
-
 def _row(t) -> int:
     """Elements from one row of t to the next (a single row has no next: its own length)."""
     n = t.shape[0]
@@ -400,9 +388,9 @@ def _row(t) -> int:
 
 def int4_linear(w: moe_qweight, N: int, K: int, group: int, x, y, status=None, stream=None):
     """y [B, N] (bf16 or fp32) = x [B, K] (bf16) times the int4 matrix w [N, K] transposed, 1 <= B <= 64."""
-    check(load().int4_linear(ctypes.byref(w), N, K, group, x.data_ptr(), _row(x), x.shape[0], y.data_ptr(), _row(y),
-                            y.element_size() == 4, None if status is None else status.data_ptr(),
-                            stream_on(stream, x.get_device())), "int4_linear")
+    _check(load().int4_linear(ctypes.byref(w), N, K, group, x.data_ptr(), _row(x), x.shape[0], y.data_ptr(), _row(y),
+                             y.element_size() == 4, None if status is None else status.data_ptr(),
+                             _stream(stream)), "int4_linear")
 
 
 def gqa_append(cache: gqa_pages, q, k, v, seq, index, page_table, pos_offset: int, inv_freq, interleaved: bool, q_out,
@@ -410,13 +398,13 @@ def gqa_append(cache: gqa_pages, q, k, v, seq, index, page_table, pos_offset: in
     """q [T, Hq, D] or None, k, v [T, Hkv, D] bf16; seq, index [T], page_table [n_seq, ld] int32; inv_freq fp32
     [rot / 2] or None; q_out [T, Hq, D] or None; status: an int32-aligned device tensor or None."""
     n_seq, ld = page_table.shape
-    check(load().gqa_append(ctypes.byref(cache), None if q is None else q.data_ptr(), 0 if q is None else _row(q),
-                           k.data_ptr(), _row(k), v.data_ptr(), _row(v), k.shape[0], 0 if q is None else q.shape[1],
-                           seq.data_ptr(), index.data_ptr(), page_table.data_ptr(), n_seq, ld, pos_offset,
-                           None if inv_freq is None else inv_freq.data_ptr(),
-                           0 if inv_freq is None else 2 * inv_freq.shape[0], interleaved,
-                           None if q_out is None else q_out.data_ptr(), 0 if q_out is None else _row(q_out),
-                           None if status is None else status.data_ptr(), stream_on(stream, k.get_device())), "gqa_append")
+    _check(load().gqa_append(ctypes.byref(cache), None if q is None else q.data_ptr(), 0 if q is None else _row(q),
+                            k.data_ptr(), _row(k), v.data_ptr(), _row(v), k.shape[0], 0 if q is None else q.shape[1],
+                            seq.data_ptr(), index.data_ptr(), page_table.data_ptr(), n_seq, ld, pos_offset,
+                            None if inv_freq is None else inv_freq.data_ptr(),
+                            0 if inv_freq is None else 2 * inv_freq.shape[0], interleaved,
+                            None if q_out is None else q_out.data_ptr(), 0 if q_out is None else _row(q_out),
+                            None if status is None else status.data_ptr(), _stream(stream)), "gqa_append")
 
 
 def gqa_paged_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, prefix_len: int) -> int:
@@ -427,8 +415,8 @@ def gqa_paged_attention(cache: gqa_pages, q, prefix_pages, prefix_len: int, page
                         ws, stream=None):
     """q, out [B, Hq, D] bf16; prefix_pages int32 or None; page_table [B, ld], seq_len [B] int32."""
     B, Hq, _ = q.shape
-    check(load().gqa_paged_attention(ctypes.byref(cache), q.data_ptr(), _row(q), B, Hq,
-                                    None if prefix_pages is None else prefix_pages.data_ptr(), prefix_len,
-                                    page_table.data_ptr(), page_table.shape[1], seq_len.data_ptr(), scale,
-                                    out.data_ptr(), _row(out), ws.data_ptr(), ws.numel() * ws.element_size(),
-                                    stream_on(stream, q.get_device())), "gqa_paged_attention")
+    _check(load().gqa_paged_attention(ctypes.byref(cache), q.data_ptr(), _row(q), B, Hq,
+                                     None if prefix_pages is None else prefix_pages.data_ptr(), prefix_len,
+                                     page_table.data_ptr(), page_table.shape[1], seq_len.data_ptr(), scale,
+                                     out.data_ptr(), _row(out), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                     _stream(stream)), "gqa_paged_attention")

@@ -67,30 +67,6 @@ static_assert(kAttnWarps * (kHeads * attn_merge_pitch(128) + 2 * kHeads) * 4 <= 
 static_assert(kAttnWarps * (kHeads * attn_merge_pitch(64) + 2 * kHeads) * 4 <= attn_smem_bytes(64), "merge buffer fits");
 static_assert(attn_smem_bytes(128) <= 227 * 1024 && attn_smem_bytes(64) <= 227 * 1024, "one block per SM");
 
-__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-
-__device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-
-// 16 bytes from global to shared memory, or zeros when `valid` is false (the
-// source is then not read).
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool valid) {
-    const int n = valid ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-
-__device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-
 template <int D>
 __global__ void __launch_bounds__(kAttnThreads, 1) gqa_attention_kernel(const __grid_constant__ GqaArgs a) {
     static_assert(D == 64 || D == 128, "head dimension 64 or 128");

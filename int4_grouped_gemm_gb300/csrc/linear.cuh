@@ -36,6 +36,28 @@ struct LinearArgs {
     }
 };
 
+// (w & mask) | set in one instruction (written plainly, with two immediates, it
+// becomes two)
+__device__ __forceinline__ uint32_t mask_set(uint32_t w, uint32_t mask, uint32_t set) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(set));
+    return r;
+}
+
+// A float of another block of the cluster, at this block's own address of it.
+__device__ __forceinline__ float dsmem_ld(uint32_t addr, uint32_t rank) {
+    uint32_t remote;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // 1 to 8 tokens.
 cudaError_t launch_linear_few(const LinearArgs &a, int num_sms, cudaStream_t s);
 // 9 to 64 tokens; maps: codes (u32, boxes of linear_code_words(G, B) x 128 rows,

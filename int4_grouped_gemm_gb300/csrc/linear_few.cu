@@ -50,9 +50,6 @@ __host__ __device__ constexpr int ring_bytes(int warps) { return warps * stages(
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async_zfill16(uint32_t dst, const void *src, bool valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
 template <int BYTES>
 __device__ __forceinline__ void cp_async_scales(uint32_t dst, const void *src) {
     if constexpr (BYTES == 16)
@@ -80,14 +77,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// (w & mask) | set in one instruction (written plainly, with two immediates, it
-// becomes two)
-__device__ __forceinline__ uint32_t mask_set(uint32_t w, uint32_t mask, uint32_t set) {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(set));
-    return r;
-}
-
 // The eight codes of a word as fp16 pairs (0 1), (2 3), (4 5), (6 7).
 __device__ __forceinline__ void unpack8(uint32_t w, uint32_t (&q)[4]) {
     const __half2 low = __half2half2(__ushort_as_half(0x6400));          // 1024
@@ -102,19 +91,6 @@ __device__ __forceinline__ void unpack8(uint32_t w, uint32_t (&q)[4]) {
         const __half2 r = i & 1 ? __hfma2(h, sixteenth, minus64) : __hsub2(h, low);
         q[i] = *reinterpret_cast<const uint32_t *>(&r);
     }
-}
-
-__device__ __forceinline__ float dsmem_ld(uint32_t addr, uint32_t rank) {
-    uint32_t remote;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 constexpr int kMaxSmem = 226 * 1024, kHalfSmem = 113 * 1024;  // a SM's, and what lets two blocks share it
@@ -175,13 +151,12 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) linear_few_kernel(cons
     // p ^ (2 (r & 3) + (r >> 2 & 1)): the pairs of pieces that a fragment load of
     // four rows meets, and the single ones of eight rows, fall on different banks
     const int ldw = a.K / 8;
-    int n_rb = first_block, n_ch = 0, n_u, n_to, n_rows = 0;  // n_rows: rows of the tile
+    int n_rb = first_block, n_ch = 0, n_u, n_to;
     share(0, n_u, n_to);
     const uint32_t *n_q[4];
     const uint16_t *n_s = nullptr;
     auto aim = [&]() {
         const int row = (n_rb * RW + rw) * 16;
-        n_rows = a.N - row;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             n_q[i] = a.q + static_cast<int64_t>(min(row + (lane >> 3) + 4 * i, a.N - 1)) * ldw + n_u * (kUnit / 8) +
@@ -215,7 +190,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) linear_few_kernel(cons
             const bool ok = n_u * kUnit + 32 * (lane & 7) < a.K;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                cp_async_zfill16((i & 1 ? d_q1 : d_q0) + (i >> 1) * 8 * kRowBytes + off, ok ? n_q[i] : a.q, ok);
+                cp_async16_zfill((i & 1 ? d_q1 : d_q0) + (i >> 1) * 8 * kRowBytes + off, ok ? n_q[i] : a.q, ok);
         }
         cp_async_scales<GU * 2>(d_s + off, n_s);
 #pragma unroll

@@ -248,26 +248,10 @@ __host__ __device__ constexpr int own_smem_bytes(int D) {
 static_assert(kOwnWarps == 8, "a shift by 3 divides by the warps");
 static_assert(own_smem_bytes(128) <= 227 * 1024 && own_smem_bytes(64) <= 227 * 1024, "one block per SM");
 
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-
-__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-
 // a / b of two numbers that are not negative: nearly always both fit 32 bits,
 // where a division takes a fraction of the instructions.
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     return (a | b) >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
-}
-
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-    return bf162_as_u32(__floats2bfloat162_rn(lo, hi));
 }
 
 __host__ __device__ __forceinline__ int tiles16(int n) { return (n + kPosTile - 1) / kPosTile; }
@@ -484,8 +468,8 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
             const bool ok = r0 + j * RS < valid;
             // (r0 and j RS have no bit in common)
             const uint32_t dst = st + j * RS * ROW + (at_chunk ^ (j * RS & 7) << 4);
-            cp16_or_zero(dst, src, ok);
-            cp16_or_zero(dst + kPosTile * ROW, src + to_v, ok);
+            cp_async16_zfill(dst, src, ok);
+            cp_async16_zfill(dst + kPosTile * ROW, src + to_v, ok);
             src += row_bytes;
         }
     };
@@ -554,7 +538,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
 #pragma unroll
                     for (int kd = 0; kd < KD; ++kd) {
                         uint32_t bm[4];
-                        ldsm4(bm, sk + kpos * ROW + (((2 * kd + kch) ^ (kpos & 7)) << 4));
+                        ldsm_x4(bm, sk + kpos * ROW + (((2 * kd + kch) ^ (kpos & 7)) << 4));
                         const uint32_t af[4] = {qa[kd][0], 0u, qa[kd][1], 0u};
                         mma_16816(s0[kd & 1], af, bm[0], bm[1]);
                         mma_16816(s1[kd & 1], af, bm[2], bm[3]);
@@ -583,15 +567,15 @@ __global__ void __launch_bounds__(kOwnThreads, 1) paged_own_kernel(const __grid_
                     uint32_t pa[4];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const uint32_t hi = bf16_pair(p[2 * j], p[2 * j + 1]);
+                        const uint32_t hi = pack2_bf16(p[2 * j], p[2 * j + 1]);
                         pa[2 * j] = hi;
-                        pa[2 * j + 1] = bf16_pair(p[2 * j] - __uint_as_float(hi << 16),
+                        pa[2 * j + 1] = pack2_bf16(p[2 * j] - __uint_as_float(hi << 16),
                                                   p[2 * j + 1] - __uint_as_float(hi & 0xFFFF0000u));
                     }
 #pragma unroll
                     for (int jt = 0; jt < NT / 2; ++jt) {
                         uint32_t bm[4];
-                        ldsm4_trans(bm, sv + vpos * ROW + (((2 * jt + vch) ^ (vpos & 7)) << 4));
+                        ldsm_x4_trans(bm, sv + vpos * ROW + (((2 * jt + vch) ^ (vpos & 7)) << 4));
                         mma_16816(o[2 * jt], pa, bm[0], bm[1]);
                         mma_16816(o[2 * jt + 1], pa, bm[2], bm[3]);
                     }
@@ -810,8 +794,8 @@ __global__ void __launch_bounds__(kParts * 64, 16 / kParts) paged_combine_kernel
         }
         const float inv = mx == -INFINITY ? 0.f : 1.0f / den;  // no position at all: zeros
         uint2 r;
-        r.x = bf16_pair(acc.x * inv, acc.y * inv);
-        r.y = bf16_pair(acc.z * inv, acc.w * inv);
+        r.x = pack2_bf16(acc.x * inv, acc.y * inv);
+        r.y = pack2_bf16(acc.z * inv, acc.w * inv);
         *reinterpret_cast<uint2 *>(a.out + b * a.out_stride + static_cast<int64_t>(kv * a.group + h) * D + d4 * 4) = r;
     }
 }

@@ -64,11 +64,6 @@ struct PagedArgs {
     float scale_log2;                // |scale| log2(e)
 };
 
-// 16 bytes from global to shared memory, or zeros (the source is then not read).
-__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void *src, bool valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-
 cudaError_t launch_append(const AppendArgs &a, int num_sms, cudaStream_t s);
 cudaError_t launch_prefix(const CUtensorMap &k, const CUtensorMap &v, const PagedArgs &a, cudaStream_t s);
 bool paged_joins(int B, int prefix_len);  // the prefix is read per row instead of by the prefix kernel

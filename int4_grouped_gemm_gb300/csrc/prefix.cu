@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 for (int row = tid / CH; row < per_block; row += 256 / CH) {
                     const int g = blk * per_block + row;
                     const int b = g < rows ? static_cast<int>((g * recip) >> 16) : 0, h = g < rows ? g - b * a.group : 0;
-                    cp16_or_zero(smem_u32(dst + (row / kRows) * QSUB + (row % kRows) * 128 + (((ch % 8) ^ (row & 7)) << 4)),
+                    cp_async16_zfill(smem_u32(dst + (row / kRows) * QSUB + (row % kRows) * 128 + (((ch % 8) ^ (row & 7)) << 4)),
                                  a.q + b * a.q_stride + static_cast<int64_t>(h0 + h) * D + ch * 8, g < rows);
                 }
                 cp_async_wait_all();
