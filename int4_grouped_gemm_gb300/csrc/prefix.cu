@@ -26,8 +26,8 @@
 //            129, and rows lost accuracy by sharing their prefix
 //   softmax  one thread per row: no exchange between threads.  m need not be the
 //            maximum, only a reference that keeps 2^(s - m) in range, the same in
-//            l and O: fp32 and bf16 hold a weight of 2^32 as exactly as one of
-//            1.  So m stays as it is until a score exceeds it by more than 32
+//            l and O: fp32 and bf16 hold a weight of 2^8 as exactly as one of
+//            1.  So m stays as it is until a score exceeds it by more than 8
 //            (to the next integer then, which scales O, l and the tile's weights
 //            by a power of two), and the weights need not wait for the tile's maximum
 //
@@ -57,7 +57,10 @@ constexpr int kRows = 128;               // rows of a sub-tile (MMA M)
 constexpr int kPos = 128;                // positions of a tile
 constexpr int kKvStages = 4;             // key or value tiles in flight
 constexpr int kPrefixThreads = 11 * 32;
-constexpr float kRaise = 32.f;           // excess of a score over the reference (log2) that moves the reference
+// Excess of a score over the reference (log2) that moves the reference.  Weights of
+// up to 2^9 leave the values and their sums most of fp32's range (with 32, values
+// of 2^95 gave infinities); a larger one saves no time on scores of ordinary spread.
+constexpr float kRaise = 8.f;
 
 __host__ __device__ constexpr int tile_bytes(int D) { return kPos * D * 2; }
 
