@@ -26,10 +26,11 @@
 //            129, and rows lost accuracy by sharing their prefix
 //   softmax  one thread per row: no exchange between threads.  m need not be the
 //            maximum, only a reference that keeps 2^(s - m) in range, the same in
-//            l and O: fp32 and bf16 hold a weight of 2^8 as exactly as one of
-//            1.  So m stays as it is until a score exceeds it by more than 8
-//            (to the next integer then, which scales O, l and the tile's weights
-//            by a power of two), and the weights need not wait for the tile's maximum
+//            l and O: fp32 and bf16 hold a weight of 2^-24 as exactly as one of
+//            1.  So m starts 24 above the first scores and stays as it is until
+//            one exceeds it by more than 8 (it goes to the integer 24 above that
+//            one then, which scales O, l and the tile's weights by a power of
+//            two), and the weights need not wait for the tile's maximum
 //
 //   warps 0-3, 4-7   softmax of slot 0, 1 (warp w: rows 32 (w % 4) ..)
 //   warp 8           loads: 64-dimension boxes of page rows by TMA, 128-byte
@@ -57,10 +58,12 @@ constexpr int kRows = 128;               // rows of a sub-tile (MMA M)
 constexpr int kPos = 128;                // positions of a tile
 constexpr int kKvStages = 4;             // key or value tiles in flight
 constexpr int kPrefixThreads = 11 * 32;
-// Excess of a score over the reference (log2) that moves the reference.  Weights of
-// up to 2^9 leave the values and their sums most of fp32's range (with 32, values
-// of 2^95 gave infinities); a larger one saves no time on scores of ordinary spread.
-constexpr float kRaise = 8.f;
+// How far the reference is set above a score, and which excess of a score over it
+// moves it (log2).  Together the 32 by which scores may rise before O has to be
+// scaled: with 8 alone a call whose scores spread by 4 took 147 us instead of 130,
+// by 8 154.  Weights of up to 2^9 leave values of up to 2^105 and down to 2^-90 and
+// their sums in fp32's range (with 0 and 32 values of 2^95 gave infinities).
+constexpr float kAbove = 24.f, kRaise = 8.f;
 
 __host__ __device__ constexpr int tile_bytes(int D) { return kPos * D * 2; }
 
@@ -430,8 +433,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 // much (the warp's 32 rows together; p: weights of this tile so
                 // far, in words): rare but for a block's first tile
                 auto raise = [&](float tm, int p) {
-                    // (the next integer itself: a step from m would lose it if m is far away)
-                    const float m_new = tm > m + kRaise ? ceilf(tm) : m;
+                    // (from the score itself: a step from m would lose it if m is far away)
+                    const float m_new = tm > m + kRaise ? ceilf(tm) + kAbove : m;
                     const float corr = ex2(m - m_new);
                     m = m_new;
                     l *= corr;
@@ -488,7 +491,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 mask(xb, 32);
                 float tm = top(xa, xb);
                 if (!any)
-                    m = fmaxf(ceilf(tm), kLeastRef);
+                    m = fmaxf(ceilf(tm) + kAbove, kLeastRef);
                 else if (__any_sync(0xffffffffu, tm > m + kRaise))
                     raise(tm, 0);
                 tmem_ld32(sS + 64, xc);

@@ -1,5 +1,5 @@
-"""Values near the top of bf16's range: what the reference of the softmax leaves above
-1 in the weights must not take the sums out of fp32."""
+"""Values near the ends of bf16's range: what the reference of the softmax leaves above
+or below 1 in the weights must not take the sums out of fp32."""
 import pytest
 import torch
 
@@ -11,16 +11,18 @@ BF16 = torch.finfo(torch.bfloat16).eps / 2
 
 
 @pytest.mark.parametrize("B, Hq, Hkv, D, prefix", [(2, 16, 2, 128, 900), (20, 8, 1, 64, 2000), (60, 16, 2, 128, 1300)])
+@pytest.mark.parametrize("power", [104, -87])
 @pytest.mark.parametrize("step", [6.0, 14.0, 28.0])
-def test_values_up_to_2_to_the_105(B, Hq, Hkv, D, prefix, step):
+def test_values_up_to_2_to_the_105(B, Hq, Hkv, D, prefix, step, power):
     """Scores (log2 units) of 0 at first, then `step`, then step + 1, 900 to 2000 positions
-    of values up to 2^105: no partial sum of weights of at most 2^9 passes 2^126."""
+    of values up to 2^105: no partial sum of weights of at most 2^9 passes 2^126.  And of
+    values about 2^-87: with weights of 2^-24 their sums stay 2^15 above fp32's least."""
     page = 64
     g = torch.Generator(device="cuda").manual_seed(B)
     n = -(-prefix // page)
     cache = attention.PagedCache.empty(n + 1, Hkv, page, D)
     cache.k.zero_()
-    v = torch.randn(cache.v.shape, generator=g, device="cuda").clamp(-2, 2) * 2.0 ** 104
+    v = torch.randn(cache.v.shape, generator=g, device="cuda").clamp(-2, 2) * 2.0 ** power
     cache.v.copy_(v)
     score = torch.zeros(prefix, device="cuda")
     score[100:prefix // 2] = step
