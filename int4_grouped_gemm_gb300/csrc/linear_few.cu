@@ -27,10 +27,11 @@
 // their group sums are made once per block if they fit in shared memory, else
 // chunk by chunk for each block of rows.
 //
-// Measured: 131072 x 4096 with one token 55 us, 5.2 TB/s of the 285 MB (ALU 51 %,
-// issue 66 % of their peaks; eight warps a SM and more in flight gain nothing);
-// 2560 x 2048 with one token 4.1 us and 2048 x 2048 with eight 4.9, which is the
-// tokens' way through shared memory, the ring's first stages and the cluster's sum.
+// Measured, calls: 131072 x 4096 with one token 56 us, 5.1 TB/s of the 285 MB (ALU
+// 51 %, issue 66 % of their peaks; eight warps a SM and more in flight gain
+// nothing); 2560 x 2048 with one token 4.0 us and 2048 x 2048 with eight 5.1, which
+// is the tokens' way through shared memory, the ring's first stages and the cluster's
+// sum.
 #include <cuda_fp16.h>
 
 #include <algorithm>

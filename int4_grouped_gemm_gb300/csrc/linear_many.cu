@@ -34,8 +34,8 @@
 // the unpacking warps, the buffer of sums given back by the epilogue), all that
 // waits for them on one other (`done`).
 //
-// Measured: 64 x 2048 x 131072 60 us, 576 TFLOP/s and 2.8 TB/s, 16 x 4096 x 32768
-// 30.5 us, 37 x 2080 x 5003 12.  Neither the tensor pipe (27 % busy) nor the bytes
+// Measured, calls: 64 x 2048 x 131072 59.5 us, 577 TFLOP/s and 2.8 TB/s, 16 x 4096 x
+// 32768 29.3 us, 37 x 2080 x 5003 12.1.  Neither the tensor pipe (27 % busy) nor the bytes
 // bound it, but a step's round through the roles, whose warps share the issue
 // slots (65 % of them used).
 //

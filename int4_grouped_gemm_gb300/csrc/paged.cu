@@ -52,8 +52,9 @@ __device__ __forceinline__ float2 angle_cs(uint32_t pos, uint64_t f) {
 // rotated head the pair of pieces whose elements turn into one another (halves:
 // pieces j and j + rot / 16 of the head; interleaved: a piece by itself),
 // otherwise plain copies.  Bound by the bytes, each read and written once, and at
-// few tokens by the three dependent reads (index, page, piece): 8192 tokens of
-// 16 + 2 x 2 heads of 128 take 17.9 us (84 MB, 4.7 TB/s), 8 tokens 2.1.
+// few tokens by the three dependent reads (index, page, piece): a call with 8192
+// tokens of 16 + 2 x 2 heads of 128 takes 18.3 us (84 MB, 4.6 TB/s), one with 8
+// tokens 2.9, its host side included.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendTokens = 8;
 
@@ -224,10 +225,11 @@ cudaError_t launch_append(const AppendArgs &a, int num_sms, cudaStream_t s) {
 //            lo| <= 2^-17 p): the heads fill only half of the MMA's 16 rows, the
 //            upper parts are rows 0-7 and the lower ones rows 8-15, and the two
 //            results are added when the item is through.  l sums the fp32 values
-// Measured, with the merge: 8 rows of up to 32768 positions (134 MB of keys and
-// values) 29 us, 4.6 TB/s, of which the merge's launch and the start (lengths,
-// pages, first tiles: three dependent reads) are 8; 128 rows of up to 512 12.4 us;
-// one row of 1000 9.3 us, all of it latency.
+// Measured, calls with the merge: 8 rows of up to 32768 positions (134 MB of keys
+// and values) 31 us, 4.3 TB/s, of which the merge's launch and the start (lengths,
+// pages, first tiles: three dependent reads) are 8 (this kernel alone 28.5, the
+// merge 5); 128 rows of up to 512 13.1 us; one row of 1000 9.5 to 9.8, all of it
+// latency.
 constexpr int kOwnWarps = 8;
 constexpr int kOwnThreads = kOwnWarps * 32;
 constexpr int kPosTile = 16;
@@ -859,8 +861,9 @@ cudaError_t launch_paged(PagedArgs &a, const CUtensorMap *maps, float scale, voi
         a.prefix_blocks = prefix_row_blocks(rows);
         a.prefix_tiles = (a.prefix_len + 127) / 128;
         const int64_t tiles = static_cast<int64_t>(a.c.Hkv) * a.prefix_blocks * a.prefix_tiles;
-        // (short pieces one tile longer: that costs 1.4 us and leaves SMs for the
-        // rows' own positions)
+        // (short pieces one tile longer, which leaves SMs for the rows' own positions: 32
+        // rows behind 65536 positions 30.3 us instead of 35.8, 64 behind 32768 31.8 and
+        // 36.0; 32 of short rows behind 32749 26.6 instead of 22.9)
         a.prefix_per = static_cast<int>((tiles + num_sms - 1) / num_sms);
         if (a.prefix_per >= 2 && a.prefix_per <= 8) ++a.prefix_per;
         a.prefix_ncta = static_cast<int>((tiles + a.prefix_per - 1) / a.prefix_per);

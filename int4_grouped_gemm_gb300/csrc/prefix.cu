@@ -39,14 +39,16 @@
 //                    the slot's next first one.  A token goes to and fro between
 //                    the two, so that the slots stay half a period apart (left
 //                    alone they fell into step, both in their softmax or both
-//                    at the tensor core: 5,300 cycles for a tile of both) and
+//                    at the tensor core: with weights of one part 5,300 cycles
+//                    for a tile of both instead of 3,400) and
 //                    one's barrier waits and commits pass while the other issues
 //
-// Measured: 128 rows of 16 heads behind 131072 positions 97 us, 1.4 PFLOP/s (the
-// tensor pipe 67 % busy; the rest is each slot's wait from its scores to its first
-// weights, which the other slot's products do not quite cover); 32 rows behind
-// 32749 positions 13 us, where a piece has 1 or 2 tiles and its start and partial
-// are most of the time.
+// Measured, this kernel alone: 128 rows of 16 heads behind 131072 positions 119 us,
+// 1.15 PFLOP/s and the tensor pipe 81 % busy, the lower parts of the weights a
+// third of it (the rest is each slot's wait from its scores to its first weights,
+// which the other slot's products do not quite cover); 32 rows behind 32749
+// positions 22 us: 103 pieces of five tiles of about 3 us, then two partials of
+// 64 KB each.
 //
 // A position outside the pool is loaded as zeros (the page coordinate lies
 // past the tensor map) and recorded.  Every wait is bounded.
