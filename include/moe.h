@@ -74,6 +74,7 @@ enum {
     MOE_ERR_TENSOR_MAP = -7,    /* TMA descriptor could not be encoded */
     MOE_ERR_DEVICE = -8,        /* current device is not an sm_103 GPU */
     MOE_ERR_PAGE = -9,          /* device: a page, sequence or position outside the paged cache */
+    MOE_ERR_TOKEN_ID = -10,     /* device: a token id outside the vocabulary */
     MOE_ERR_TIMEOUT = -100      /* device: a bounded wait ran out (-100 - site) */
 };
 
@@ -576,6 +577,88 @@ int gqa_paged_attention_status(const gqa_pages *cache, const void *q, int64_t q_
                                const int32_t *prefix_pages, int32_t prefix_len, const int32_t *page_table,
                                int32_t table_ld, const int32_t *seq_len, float scale, void *out, int64_t out_stride,
                                void *ws, size_t ws_bytes, int32_t *status, cudaStream_t stream);
+
+/* ------------------------------------------------------------- prompts
+ * The operators of a prompt, whose tokens are worked through together: the
+ * attention sub-layer for the rows that moe_prefill_block takes, and what is
+ * read from an output head's scores (the pages check "teacher-forced" log
+ * probabilities of given tokens).  Types, strides, alignment and streams as in
+ * the attention sub-layer above.
+ */
+
+/*
+ * int4_linear for any number of tokens 1 <= T <= 2^20 (for 64 and fewer
+ * int4_linear is made): y[t][n] = sum_k x[t][k] (scale q + bias), products of
+ * tokens and weights exact, sums in fp32, y rounded once to bf16 or written as
+ * fp32.  Products stay finite for tokens and weights below 2^60, and a token with an
+ * infinity or NaN leaves its own row of y without finite numbers and the other rows
+ * alone.  Within a row of x, and a row of the matrix, what is 2^-30 of the
+ * row's largest value counts with an error of that size.  Other arguments and
+ * their limits as int4_linear's.  The workspace (int4_linear_prompt_workspace_bytes, 0
+ * if unsupported; no initialisation needed) is this call's alone while it runs.
+ */
+size_t int4_linear_prompt_workspace_bytes(int32_t N, int32_t K, int32_t group, int32_t T);
+int int4_linear_prompt(const moe_qweight *w, int32_t N, int32_t K, int32_t group, const void *x, int64_t x_stride,
+                       int32_t T, void *y, int64_t y_stride, int32_t y_fp32, void *ws, size_t ws_bytes,
+                       int32_t *status, cudaStream_t stream);
+
+/*
+ * Causal attention of n_seq packed sequences of query tokens.  Rows
+ * q_start[b] .. q_start[b + 1] - 1 of q (q_start int32 [n_seq + 1], device, not
+ * decreasing, within 0 .. T) are the last tokens of sequence b, which has
+ * seq_len[b] positions in the pages of page_table[b] (int32, device; their own
+ * keys and values among them, by gqa_append): the last row stands at position
+ * seq_len[b] - 1, the others before it.  A row sees the prefix_len positions of
+ * prefix_pages (shared by all sequences, NULL if prefix_len is 0) and its own
+ * sequence's positions up to its own, and
+ *   out[t][h] = softmax(scale * q[t][h] . keys) values     fp32, bf16 out
+ * with key-value head h / (Hq / Hkv) for query head h.  A whole prompt
+ * (seq_len = its rows), a further piece of one (seq_len larger) and single
+ * tokens may be packed together; pages of several rows of the table may be the
+ * same.  A row that sees no position (more rows than positions, no prefix) gives
+ * zeros; a sequence without rows or with seq_len < 0 is padding, and rows of no
+ * sequence (before q_start[0], from q_start[n_seq] on) and of padding are left as
+ * they were.  Scores of minus infinity, NaN and plus infinity as in
+ * gqa_paged_attention; what the pages hold at positions that a row does not see
+ * has no influence on it, NaN and infinities included.  Page numbers, q_start and
+ * seq_len are checked on the device: one out of range is not followed and
+ * MOE_ERR_PAGE recorded at *status (the first word of the workspace or any zeroed
+ * int32, or NULL), the rows concerned are then undefined.
+ * q, out: T rows of Hq heads of D at the given row strides; out may be q.
+ * Supported: Hq % Hkv == 0, Hq / Hkv <= 8, Hq <= 256 (MOE_ERR_SHAPE), 1 <= T <=
+ * 2^22, 1 <= n_seq <= 65536, prefix_len 0 .. 2^26, table_ld >= 1 with table_ld *
+ * page_size <= 2^26 (MOE_ERR_TOKENS).  The workspace
+ * (gqa_prompt_workspace_bytes, 0 if unsupported; its first word zero if it is the
+ * status, else no initialisation) is this call's alone while it runs.
+ */
+size_t gqa_prompt_workspace_bytes(int32_t T, int32_t n_seq, int32_t Hq, int32_t Hkv, int32_t D);
+int gqa_prompt_attention(const gqa_pages *cache, const void *q, int64_t q_stride, int32_t T, int32_t Hq,
+                         const int32_t *q_start, int32_t n_seq, const int32_t *prefix_pages, int32_t prefix_len,
+                         const int32_t *page_table, int32_t table_ld, const int32_t *seq_len, float scale, void *out,
+                         int64_t out_stride, void *ws, size_t ws_bytes, int32_t *status, cudaStream_t stream);
+
+/*
+ * Of rows of scores x[T][V] (fp32, or bf16 with logits_fp32 = 0; row stride in
+ * elements, >= V, any; 4- or 2-byte aligned), with lse = log sum_i exp x[i]:
+ *   logprob[t]          x[targets[t]] - lse      (targets int32 [T], or NULL with logprob NULL)
+ *   entropy[t]          -sum_i p_i log p_i, p_i = exp(x[i] - lse)   (or NULL)
+ *   top_ids[t][n_top]   the ids of the largest scores in descending order, equal
+ *                       ones by lower id (NaN before all); 0 <= n_top <= 32
+ *   top_logprobs        [T][n_top], their x - lse
+ * all device memory, 4-byte aligned, contiguous; sums in fp32.  A score of minus
+ * infinity (a masked token) weighs nothing; a row with a NaN, a plus infinity
+ * or nothing but minus infinity has no distribution: its logprob, entropy and
+ * top_logprobs are NaN.  A row with targets[t] < 0 is padding: nothing of it is
+ * read or written.  A target >= V gives NaN and MOE_ERR_TOKEN_ID at *status (or NULL).
+ * 1 <= T <= 2^24 (MOE_ERR_TOKENS), 1 <= V <= 2^28, n_top <= V, stride below 2^39
+ * (MOE_ERR_SHAPE).  The workspace (token_logprobs_workspace_bytes, 0 if unsupported;
+ * its first word zero if it is the status, else no initialisation) is this call's
+ * alone while it runs.
+ */
+size_t token_logprobs_workspace_bytes(int32_t T, int32_t V, int32_t n_top);
+int token_logprobs(const void *logits, int64_t stride, int32_t logits_fp32, int32_t T, int32_t V,
+                   const int32_t *targets, float *logprob, float *entropy, int32_t n_top, int32_t *top_ids,
+                   float *top_logprobs, void *ws, size_t ws_bytes, int32_t *status, cudaStream_t stream);
 
 /* Human-readable text for a status code. */
 const char *moe_status_string(int code);

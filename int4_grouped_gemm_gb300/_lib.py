@@ -24,6 +24,7 @@ MOE_ERR_CUDA = -6
 MOE_ERR_TENSOR_MAP = -7
 MOE_ERR_DEVICE = -8
 MOE_ERR_PAGE = -9
+MOE_ERR_TOKEN_ID = -10
 MOE_ERR_TIMEOUT = -100
 
 
@@ -109,6 +110,15 @@ SIGNATURES = {
                                            c_p, c_i64, c_p, c_sz, c_p]),
     "gqa_paged_attention_status": (ctypes.c_int, [c_p, c_p, c_i64, c_i32, c_i32, c_p, c_i32, c_p, c_i32, c_p,
                                                   ctypes.c_float, c_p, c_i64, c_p, c_sz, c_p, c_p]),
+    "int4_linear_prompt_workspace_bytes": (c_sz, [c_i32, c_i32, c_i32, c_i32]),
+    "int4_linear_prompt": (ctypes.c_int, [c_p, c_i32, c_i32, c_i32, c_p, c_i64, c_i32, c_p, c_i64, c_i32, c_p, c_sz, c_p,
+                                          c_p]),
+    "gqa_prompt_workspace_bytes": (c_sz, [c_i32, c_i32, c_i32, c_i32, c_i32]),
+    "gqa_prompt_attention": (ctypes.c_int, [c_p, c_p, c_i64, c_i32, c_i32, c_p, c_i32, c_p, c_i32, c_p, c_i32, c_p,
+                                            ctypes.c_float, c_p, c_i64, c_p, c_sz, c_p, c_p]),
+    "token_logprobs_workspace_bytes": (c_sz, [c_i32, c_i32, c_i32]),
+    "token_logprobs": (ctypes.c_int, [c_p, c_i64, c_i32, c_i32, c_i32, c_p, c_p, c_p, c_i32, c_p, c_p, c_p, c_sz, c_p,
+                                      c_p]),
 }
 
 
@@ -420,3 +430,46 @@ def gqa_paged_attention(cache: gqa_pages, q, prefix_pages, prefix_len: int, page
                                      page_table.data_ptr(), page_table.shape[1], seq_len.data_ptr(), scale,
                                      out.data_ptr(), _row(out), ws.data_ptr(), ws.numel() * ws.element_size(),
                                      _stream(stream)), "gqa_paged_attention")
+
+
+# ---------------------------------------------------------------- prompts
+
+
+def int4_linear_prompt_workspace_bytes(N: int, K: int, group: int, T: int) -> int:
+    return int(load().int4_linear_prompt_workspace_bytes(N, K, group, T))
+
+
+def int4_linear_prompt(w: moe_qweight, N: int, K: int, group: int, x, y, ws, status=None, stream=None):
+    """int4_linear for any number of tokens."""
+    _check(load().int4_linear_prompt(ctypes.byref(w), N, K, group, x.data_ptr(), _row(x), x.shape[0], y.data_ptr(),
+                                    _row(y), y.element_size() == 4, ws.data_ptr(), ws.numel() * ws.element_size(),
+                                    _ptr(status), _stream(stream)), "int4_linear_prompt")
+
+
+def gqa_prompt_workspace_bytes(T: int, n_seq: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(load().gqa_prompt_workspace_bytes(T, n_seq, Hq, Hkv, D))
+
+
+def gqa_prompt_attention(cache: gqa_pages, q, q_start, prefix_pages, prefix_len: int, page_table, seq_len, scale: float,
+                         out, ws, status=None, stream=None):
+    """q, out [T, Hq, D] bf16; q_start [n_seq + 1], page_table [n_seq, ld], seq_len [n_seq] int32; prefix_pages int32
+    or None; status: an int32-aligned device tensor or None."""
+    T, Hq, _ = q.shape
+    _check(load().gqa_prompt_attention(ctypes.byref(cache), q.data_ptr(), _row(q), T, Hq, q_start.data_ptr(),
+                                      seq_len.shape[0], _ptr(prefix_pages), prefix_len, page_table.data_ptr(),
+                                      page_table.shape[1], seq_len.data_ptr(), scale, out.data_ptr(), _row(out),
+                                      ws.data_ptr(), ws.numel() * ws.element_size(), _ptr(status), _stream(stream)),
+           "gqa_prompt_attention")
+
+
+def token_logprobs_workspace_bytes(T: int, V: int, n_top: int) -> int:
+    return int(load().token_logprobs_workspace_bytes(T, V, n_top))
+
+
+def token_logprobs(logits, targets, logprob, entropy, n_top: int, top_ids, top_logprobs, ws, status=None, stream=None):
+    """logits [T, V] fp32 or bf16; targets int32 [T] and logprob fp32 [T], or both None; entropy fp32 [T] or None;
+    top_ids int32 and top_logprobs fp32 [T, n_top]."""
+    T, V = logits.shape
+    _check(load().token_logprobs(logits.data_ptr(), _row(logits), logits.element_size() == 4, T, V, _ptr(targets),
+                                _ptr(logprob), _ptr(entropy), n_top, _ptr(top_ids), _ptr(top_logprobs), ws.data_ptr(),
+                                ws.numel() * ws.element_size(), _ptr(status), _stream(stream)), "token_logprobs")

@@ -1,8 +1,9 @@
-"""The attention sub-layer of a decoding step, on top of the C ABI.
+"""The attention sub-layer of a decoding step and of a prompt, on top of the C ABI.
 
-``PagedCache`` wraps two page pools (``gqa_append``, ``gqa_paged_attention``);
-``AttentionLayer`` puts int4 projections (``moe.linear``) around it, and its
-result is the ``attn`` of ``PackedLayer.decode_batch_block``.
+``PagedCache`` wraps two page pools (``gqa_append``, ``gqa_paged_attention``,
+``gqa_prompt_attention``); ``AttentionLayer`` puts int4 projections
+(``moe.linear``, ``moe.linear_prompt``) around it, and its result is the
+``attn`` of ``PackedLayer.decode_batch_block`` and ``PackedLayer.prefill_block``.
 """
 from __future__ import annotations
 
@@ -13,7 +14,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .moe import QMatrix, linear
+from .moe import QMatrix, linear, linear_prompt
 
 
 def _need(ok: bool, what: str):
@@ -101,6 +102,45 @@ class PagedCache:
         return out
 
 
+    def prompt_workspace(self, T: int, n_seq: int, Hq: int) -> torch.Tensor:
+        """Scratch of attend_prompt for up to T rows of n_seq sequences; calls
+        that may overlap take one each."""
+        return torch.zeros(self._prompt_bytes(T, n_seq, Hq), dtype=torch.uint8, device=self.k.device)
+
+    def _prompt_bytes(self, T: int, n_seq: int, Hq: int) -> int:
+        n = _lib.gqa_prompt_workspace_bytes(T, n_seq, Hq, self.Hkv, self.D)
+        if n == 0:
+            raise _lib.MoEError(_lib.MOE_ERR_SHAPE, "gqa_prompt_workspace_bytes")
+        return n
+
+    def attend_prompt(self, q: torch.Tensor, q_start: torch.Tensor, page_table: torch.Tensor, seq_len: torch.Tensor,
+                      prefix_pages: Optional[torch.Tensor] = None, prefix_len: int = 0, scale: Optional[float] = None,
+                      out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """out [T, Hq, D]: causal attention of packed sequences.  Rows
+        q_start[b] .. q_start[b + 1] - 1 of q are the last tokens of sequence b,
+        whose first seq_len[b] positions are in page_table[b] (their own among
+        them): each attends to the shared prefix and its sequence's positions up
+        to its own.  scale: 1 / sqrt(D) unless given.  Errors found on the device
+        are recorded in the first word of ws, without ws (scratch of the call's own
+        is then allocated) in `status`."""
+        if stream is not None and (out is None or ws is None):
+            with _lib.on_stream(stream):
+                return self.attend_prompt(q, q_start, page_table, seq_len, prefix_pages, prefix_len, scale, out, ws)
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        status = None
+        if ws is None:
+            ws = torch.empty(self._prompt_bytes(q.shape[0], seq_len.shape[0], q.shape[1]), dtype=torch.uint8,
+                             device=self.k.device)
+            status = self._status_at
+        rc = _lib.native().attend_prompt(self._at, self._device, q, q_start, page_table, seq_len, prefix_pages,
+                                         prefix_len, self._scale if scale is None else scale, out, ws,
+                                         _lib.handle(stream), status)
+        if rc:
+            raise _lib.MoEError(rc, "gqa_prompt_attention")
+        return out
+
+
 class AttentionLayer:
     """int4 projections around a paged cache: qkv [(Hq + 2 Hkv) D, H] and
     out [H, Hq D], both QMatrix (pack_matrix), and the rotation."""
@@ -138,3 +178,23 @@ class AttentionLayer:
         cache.append(q, k, v, seq, index, page_table, self.inv_freq, prefix_len, self.interleaved, q_out=q)
         cache.attend(q, page_table, seq_len, prefix_pages, prefix_len, out=q, ws=ws)
         return linear(self.out, qkv[:, :self.Hq * self.D], status=cache.status)
+
+    def prefill(self, x: torch.Tensor, cache: PagedCache, seq: torch.Tensor, index: torch.Tensor,
+                q_start: torch.Tensor, page_table: torch.Tensor, seq_len: torch.Tensor,
+                prefix_pages: Optional[torch.Tensor] = None, prefix_len: int = 0,
+                ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Packed prompts (or pieces of them): x [T, H] (normalised) -> attn
+        [T, H], which PackedLayer.prefill_block takes.  Token t goes to position
+        index[t] of page table row seq[t]; rows q_start[b] .. q_start[b + 1] - 1
+        are the last tokens of sequence b, of seq_len[b] positions with them
+        (attend_prompt; ws is its workspace).  Errors found on the device are
+        recorded in cache.status, the attention's in the first word of ws if it is given."""
+        if stream is not None:
+            with _lib.on_stream(stream):
+                return self.prefill(x, cache, seq, index, q_start, page_table, seq_len, prefix_pages, prefix_len, ws)
+        qkv = linear_prompt(self.qkv, x, status=cache.status)
+        q, k, v = self._split(qkv)
+        # queries, rotated queries and the attention's output share their place
+        cache.append(q, k, v, seq, index, page_table, self.inv_freq, prefix_len, self.interleaved, q_out=q)
+        cache.attend_prompt(q, q_start, page_table, seq_len, prefix_pages, prefix_len, out=q, ws=ws)
+        return linear_prompt(self.out, qkv[:, :self.Hq * self.D], status=cache.status)

@@ -27,7 +27,8 @@ BINDING = os.path.join(HERE, "_native.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.cu", "pack.cu", "routing.cu", "grouped_gemm.cu", "decode.cu", "small_batch.cu", "block.cu",
-           "attention.cu", "linear_few.cu", "linear_many.cu", "paged.cu", "prefix.cu"]
+           "attention.cu", "linear_few.cu", "linear_many.cu", "paged.cu", "prefix.cu", "prompt.cu", "linear_prompt.cu",
+           "scores.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "-I" + os.path.join(ROOT, "include")]

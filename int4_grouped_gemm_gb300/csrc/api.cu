@@ -10,6 +10,8 @@
 #include "kernels.cuh"
 #include "linear.cuh"
 #include "paged.cuh"
+#include "prompt.cuh"
+#include "scores.cuh"
 #include "small_batch.cuh"
 
 
@@ -775,24 +777,27 @@ int gqa_decode_attention_per_head(const void *q, const void *k_cache, const void
 
 // ------------------------------------------------ attention sub-layer
 
-int int4_linear(const moe_qweight *w, int32_t N, int32_t K, int32_t group, const void *x, int64_t x_stride, int32_t B,
-                void *y, int64_t y_stride, int32_t y_fp32, int32_t *status, cudaStream_t stream) {
+static bool linear_shape(int32_t N, int32_t K, int32_t group) {
+    // (N: rows of a last tile past it still count in 32 bits)
+    return (group == 32 || group == 64 || group == 128) && N >= 1 && N <= (1 << 30) && K >= group && K <= kLinearMaxK &&
+           K % group == 0;
+}
+
+// The checks of a linear call, and its arguments as the launches take them.
+static int linear_args(LinearArgs &a, const moe_qweight *w, int32_t N, int32_t K, int32_t group, const void *x,
+                       int64_t x_stride, int32_t B, int32_t B_max, void *y, int64_t y_stride, int32_t y_fp32,
+                       int32_t *status) {
     if (!w) return MOE_ERR_NULL;
     int rc;
     if ((rc = check_ptr(w->q)) || (rc = check_ptr(w->scale)) || (rc = check_ptr(w->bias)) || (rc = check_ptr(x)) ||
         (rc = check_ptr(y)))
         return rc;
-    if (group != 32 && group != 64 && group != 128) return MOE_ERR_SHAPE;
-    // (N: rows of a last tile past it still count in 32 bits)
-    if (N < 1 || N > (1 << 30) || K < group || K > kLinearMaxK || K % group != 0) return MOE_ERR_SHAPE;
+    if (!linear_shape(N, K, group)) return MOE_ERR_SHAPE;
     if (x_stride < K || x_stride % 8 != 0 || x_stride >= (int64_t(1) << 39) || y_stride < N ||
         y_stride >= (int64_t(1) << 39) || (y_fp32 != 0 && y_fp32 != 1))
         return MOE_ERR_SHAPE;
-    if (B < 1 || B > kLinearMaxB) return MOE_ERR_TOKENS;
+    if (B < 1 || B > B_max) return MOE_ERR_TOKENS;
     if (status && (reinterpret_cast<uintptr_t>(status) & 3u)) return MOE_ERR_ALIGN;
-    DeviceInfo *dev = nullptr;
-    if ((rc = current_device(dev))) return rc;
-    LinearArgs a{};
     a.q = w->q;
     a.s = w->scale;
     a.b = w->bias;
@@ -808,6 +813,16 @@ int int4_linear(const moe_qweight *w, int32_t N, int32_t K, int32_t group, const
     a.y_fp32 = y_fp32;
     a.status = status;
     a.wait_limit = g_wait_limit;
+    return MOE_OK;
+}
+
+int int4_linear(const moe_qweight *w, int32_t N, int32_t K, int32_t group, const void *x, int64_t x_stride, int32_t B,
+                void *y, int64_t y_stride, int32_t y_fp32, int32_t *status, cudaStream_t stream) {
+    LinearArgs a{};
+    int rc = linear_args(a, w, N, K, group, x, x_stride, B, kLinearMaxB, y, y_stride, y_fp32, status);
+    if (rc) return rc;
+    DeviceInfo *dev = nullptr;
+    if ((rc = current_device(dev))) return rc;
     if (B <= kFewTokens) return cuda_rc(launch_linear_few(a, dev->num_sms, stream));
     CUtensorMap maps[4];
     const auto SW0 = CU_TENSOR_MAP_SWIZZLE_NONE;
@@ -973,6 +988,131 @@ int gqa_paged_attention_status(const gqa_pages *cache, const void *q, int64_t q_
     return cuda_rc(launch_paged(a, maps, scale, ws, dev->num_sms, stream));
 }
 
+// ------------------------------------------------------------- prompts
+
+size_t int4_linear_prompt_workspace_bytes(int32_t N, int32_t K, int32_t group, int32_t T) {
+    if (!linear_shape(N, K, group) || T < 1 || T > kLinearPromptMaxT) return 0;
+    return linear_prompt_workspace_bytes(N, K, group, T);
+}
+
+int int4_linear_prompt(const moe_qweight *w, int32_t N, int32_t K, int32_t group, const void *x, int64_t x_stride,
+                       int32_t T, void *y, int64_t y_stride, int32_t y_fp32, void *ws, size_t ws_bytes,
+                       int32_t *status, cudaStream_t stream) {
+    LinearArgs a{};
+    int rc = linear_args(a, w, N, K, group, x, x_stride, T, kLinearPromptMaxT, y, y_stride, y_fp32, status);
+    if (rc) return rc;
+    if ((rc = check_ptr(ws))) return rc;
+    if (ws_bytes < linear_prompt_workspace_bytes(N, K, group, T)) return MOE_ERR_WORKSPACE;
+    DeviceInfo *dev = nullptr;
+    if ((rc = current_device(dev))) return rc;
+    return cuda_rc(launch_linear_prompt(a, ws, dev->num_sms, stream));
+}
+
+static int check_prompt_shape(int32_t T, int32_t n_seq, int32_t Hq, int32_t Hkv, int32_t D) {
+    if (D != 64 && D != 128) return MOE_ERR_SHAPE;
+    if (Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > 8 || Hq > 256) return MOE_ERR_SHAPE;
+    if (T < 1 || T > (1 << 22) || n_seq < 1 || n_seq > 65536) return MOE_ERR_TOKENS;
+    return MOE_OK;
+}
+
+size_t gqa_prompt_workspace_bytes(int32_t T, int32_t n_seq, int32_t Hq, int32_t Hkv, int32_t D) {
+    if (check_prompt_shape(T, n_seq, Hq, Hkv, D) != MOE_OK) return 0;
+    return prompt_workspace_bytes(T, n_seq, Hq, Hkv, D, kGqaMaxSms);
+}
+
+int gqa_prompt_attention(const gqa_pages *cache, const void *q, int64_t q_stride, int32_t T, int32_t Hq,
+                         const int32_t *q_start, int32_t n_seq, const int32_t *prefix_pages, int32_t prefix_len,
+                         const int32_t *page_table, int32_t table_ld, const int32_t *seq_len, float scale, void *out,
+                         int64_t out_stride, void *ws, size_t ws_bytes, int32_t *status, cudaStream_t stream) {
+    PromptArgs a{};
+    int rc = check_pages(cache, a.c);
+    if (rc) return rc;
+    if ((rc = check_ptr(q)) || (rc = check_ptr4(q_start)) || (rc = check_ptr4(page_table)) ||
+        (rc = check_ptr4(seq_len)) || (rc = check_ptr(out)) || (rc = check_ptr(ws)))
+        return rc;
+    if ((rc = check_prompt_shape(T, n_seq, Hq, a.c.Hkv, a.c.D))) return rc;
+    if (prefix_len < 0 || prefix_len > (1 << 26)) return MOE_ERR_TOKENS;
+    if (prefix_len > 0 && (rc = check_ptr4(prefix_pages))) return rc;
+    if (status && (rc = check_ptr4(status))) return rc;
+    if (table_ld < 1 || static_cast<int64_t>(table_ld) * cache->page_size > (1 << 26)) return MOE_ERR_TOKENS;
+    if (!good_stride(q_stride, static_cast<int64_t>(Hq) * a.c.D) ||
+        !good_stride(out_stride, static_cast<int64_t>(Hq) * a.c.D))
+        return MOE_ERR_SHAPE;
+    if (q == out && q_stride != out_stride) return MOE_ERR_SHAPE;
+    if (!(scale == scale) || scale > 1e30f || scale < -1e30f) return MOE_ERR_SHAPE;
+    if (ws_bytes < prompt_workspace_bytes(T, n_seq, Hq, a.c.Hkv, a.c.D, kGqaMaxSms)) return MOE_ERR_WORKSPACE;
+    DeviceInfo *dev = nullptr;
+    if ((rc = current_device(dev))) return rc;
+    if (dev->num_sms > kGqaMaxSms) return MOE_ERR_DEVICE;
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.out = static_cast<__nv_bfloat16 *>(out);
+    a.q_stride = q_stride;
+    a.out_stride = out_stride;
+    a.q_start = q_start;
+    a.prefix_pages = prefix_pages;
+    a.table = page_table;
+    a.seq_len = seq_len;
+    a.status = status;
+    a.T = T;
+    a.Hq = Hq;
+    a.group = Hq / a.c.Hkv;
+    a.n_seq = n_seq;
+    a.prefix_len = prefix_len;
+    a.table_ld = table_ld;
+    a.scale = scale;
+    a.wait_limit = g_wait_limit;
+    CUtensorMap maps[2];
+    const uint32_t rows = cache->page_size < 128 ? cache->page_size : 128;
+    if ((rc = encode_pages(&maps[0], a.c.k, a.c, rows)) || (rc = encode_pages(&maps[1], a.c.v, a.c, rows))) return rc;
+    return cuda_rc(launch_prompt(a, maps, ws, dev->num_sms, stream));
+}
+
+static int check_scores_shape(int32_t T, int32_t V, int32_t n_top) {
+    if (V < 1 || V > (1 << 28) || n_top < 0 || n_top > kMaxTop || n_top > V) return MOE_ERR_SHAPE;
+    if (T < 1 || T > (1 << 24)) return MOE_ERR_TOKENS;
+    return MOE_OK;
+}
+
+size_t token_logprobs_workspace_bytes(int32_t T, int32_t V, int32_t n_top) {
+    if (check_scores_shape(T, V, n_top) != MOE_OK) return 0;
+    return scores_workspace_bytes(T, V, n_top, kGqaMaxSms);
+}
+
+int token_logprobs(const void *logits, int64_t stride, int32_t logits_fp32, int32_t T, int32_t V,
+                   const int32_t *targets, float *logprob, float *entropy, int32_t n_top, int32_t *top_ids,
+                   float *top_logprobs, void *ws, size_t ws_bytes, int32_t *status, cudaStream_t stream) {
+    int rc;
+    if (!logits) return MOE_ERR_NULL;
+    if (logits_fp32 != 0 && logits_fp32 != 1) return MOE_ERR_SHAPE;
+    if (reinterpret_cast<uintptr_t>(logits) & (logits_fp32 ? 3u : 1u)) return MOE_ERR_ALIGN;
+    if ((targets == nullptr) != (logprob == nullptr)) return MOE_ERR_NULL;
+    if (targets && ((rc = check_ptr4(targets)) || (rc = check_ptr4(logprob)))) return rc;
+    if (entropy && (rc = check_ptr4(entropy))) return rc;
+    if ((rc = check_scores_shape(T, V, n_top))) return rc;
+    if (n_top && ((rc = check_ptr4(top_ids)) || (rc = check_ptr4(top_logprobs)))) return rc;
+    if (stride < V || stride >= (int64_t(1) << 39)) return MOE_ERR_SHAPE;
+    if (status && (rc = check_ptr4(status))) return rc;
+    if ((rc = check_ptr(ws))) return rc;
+    if (ws_bytes < scores_workspace_bytes(T, V, n_top, kGqaMaxSms)) return MOE_ERR_WORKSPACE;
+    DeviceInfo *dev = nullptr;
+    if ((rc = current_device(dev))) return rc;
+    if (dev->num_sms > kGqaMaxSms) return MOE_ERR_DEVICE;
+    ScoresArgs a{};
+    a.x = logits;
+    a.stride = stride;
+    a.targets = targets;
+    a.logprob = logprob;
+    a.entropy = entropy;
+    a.top_ids = top_ids;
+    a.top_logprobs = top_logprobs;
+    a.status = status;
+    a.T = T;
+    a.V = V;
+    a.n_top = n_top;
+    a.fp32 = logits_fp32;
+    return cuda_rc(launch_scores(a, ws, dev->num_sms, stream));
+}
+
 const char *moe_status_string(int code) {
     switch (code) {
         case MOE_OK: return "ok";
@@ -985,6 +1125,7 @@ const char *moe_status_string(int code) {
         case MOE_ERR_TENSOR_MAP: return "TMA descriptor could not be encoded";
         case MOE_ERR_DEVICE: return "current device is not an sm_103 GPU";
         case MOE_ERR_PAGE: return "device: a page, sequence or position outside the paged cache";
+        case MOE_ERR_TOKEN_ID: return "device: a token id outside the vocabulary";
         default: break;
     }
     if (code <= MOE_ERR_TIMEOUT && code > MOE_ERR_TIMEOUT - 100) return "device: a bounded wait ran out";

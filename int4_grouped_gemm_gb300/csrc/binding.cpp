@@ -1,5 +1,5 @@
-// Python entry points of the attention sub-layer: torch tensors in, checked, the
-// C calls of moe.h out.
+// Python entry points of the attention sub-layer and the prompt calls: torch
+// tensors in, checked, the C calls of moe.h out.
 //
 // These operators run for a few microseconds, and of the 10 that an append of 8
 // tokens took through ctypes, 7.5 were the reading of eight tensors' shapes and
@@ -13,7 +13,9 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <climits>
+#include <initializer_list>
 #include <string>
+#include <utility>
 
 #include "moe.h"
 
@@ -107,41 +109,79 @@ int device_of_cache(const char *what, PyObject *device) {
     return dev;
 }
 
+// What the linear calls share: q, scale, bias, rows, K, group, x, y from v[0] on.
+struct Linear {
+    moe_qweight w;
+    int32_t N, K, group;
+    int64_t B, x_stride, y_stride;
+    const void *x;
+    void *y;
+    bool fp32;
+    int dev;
+
+    explicit Linear(PyObject *const *v) {
+        const at::Tensor &q = tensor(v[0], "linear: codes"), &s = tensor(v[1], "linear: scales"), &b = tensor(v[2], "linear: biases");
+        N = int32(v[3], "rows");
+        K = int32(v[4], "K");
+        group = int32(v[5], "group");
+        const at::Tensor &xt = tensor(v[6], "linear: x"), &yt = tensor(v[7], "linear: y");
+        if (xt.dim() != 2 || xt.size(1) != K || xt.scalar_type() != at::kBFloat16 || xt.stride(1) != 1)
+            value_error("linear: x [B, " + std::to_string(K) + "] in bf16, its rows contiguous");
+        if (q.numel() * 8 != static_cast<int64_t>(N) * K) value_error("linear: one matrix [N, K], not a stack");
+        const int64_t pitch = group > 0 ? (K / group + 7) / 8 * 8 : 0;
+        if (q.scalar_type() != at::kInt || !q.is_contiguous()) value_error("linear: codes in int32, contiguous");
+        for (const at::Tensor *t : {&s, &b})
+            if (t->element_size() != 2 || !t->is_contiguous() || t->numel() != N * pitch)
+                value_error("linear: scales and biases [N, " + std::to_string(pitch) + "] in 16 bits, contiguous");
+        B = xt.size(0);
+        fp32 = yt.scalar_type() == at::kFloat;
+        if (yt.dim() != 2 || yt.size(0) != B || yt.size(1) != N || !(fp32 || yt.scalar_type() == at::kBFloat16) ||
+            (N > 1 && yt.stride(1) != 1))
+            value_error("linear: y [B, " + std::to_string(N) + "] in bf16 or fp32, its rows contiguous");
+        dev = current_device();
+        on_device(xt, "linear: x", dev);
+        on_device(yt, "linear: y", dev);
+        on_device(q, "linear: codes", dev);
+        on_device(s, "linear: scales", dev);
+        on_device(b, "linear: biases", dev);
+        w = {static_cast<const uint32_t *>(q.data_ptr()), static_cast<const uint16_t *>(s.data_ptr()),
+             static_cast<const uint16_t *>(b.data_ptr())};
+        x = xt.data_ptr();
+        y = yt.data_ptr();
+        x_stride = B > 1 ? xt.stride(0) : K;
+        y_stride = B > 1 ? yt.stride(0) : N;
+    }
+};
+
+// An int32 tensor for errors found on the device, or None.
+int32_t *status_of(PyObject *o, const char *name, int dev) {
+    if (o == Py_None) return nullptr;
+    const at::Tensor &t = tensor(o, name);
+    on_device(t, name, dev);
+    if (t.scalar_type() != at::kInt || t.numel() < 1) value_error(std::string(name) + " in int32");
+    return static_cast<int32_t *>(t.data_ptr());
+}
+
+// A call's scratch and its bytes.
+std::pair<void *, size_t> scratch_of(PyObject *o, int dev) {
+    const at::Tensor &ws = tensor(o, "ws");
+    if (ws.get_device() != dev || !ws.is_contiguous()) value_error("ws: contiguous, on the current device");
+    return {ws.data_ptr(), static_cast<size_t>(ws.numel()) * ws.element_size()};
+}
+
 // q, scale, bias, rows, K, group, x, y, status | None, stream | None
 int linear(PyObject *const *v) {
-    const at::Tensor &q = tensor(v[0], "linear: codes"), &s = tensor(v[1], "linear: scales"), &b = tensor(v[2], "linear: biases");
-    const int32_t N = int32(v[3], "rows"), K = int32(v[4], "K"), group = int32(v[5], "group");
-    const at::Tensor &x = tensor(v[6], "linear: x"), &y = tensor(v[7], "linear: y");
-    if (x.dim() != 2 || x.size(1) != K || x.scalar_type() != at::kBFloat16 || x.stride(1) != 1)
-        value_error("linear: x [B, " + std::to_string(K) + "] in bf16, its rows contiguous");
-    if (q.numel() * 8 != static_cast<int64_t>(N) * K) value_error("linear: one matrix [N, K], not a stack");
-    const int64_t pitch = group > 0 ? (K / group + 7) / 8 * 8 : 0;
-    if (q.scalar_type() != at::kInt || !q.is_contiguous()) value_error("linear: codes in int32, contiguous");
-    for (const at::Tensor *t : {&s, &b})
-        if (t->element_size() != 2 || !t->is_contiguous() || t->numel() != N * pitch)
-            value_error("linear: scales and biases [N, " + std::to_string(pitch) + "] in 16 bits, contiguous");
-    const int64_t B = x.size(0);
-    const bool fp32 = y.scalar_type() == at::kFloat;
-    if (y.dim() != 2 || y.size(0) != B || y.size(1) != N || !(fp32 || y.scalar_type() == at::kBFloat16) ||
-        (N > 1 && y.stride(1) != 1))
-        value_error("linear: y [B, " + std::to_string(N) + "] in bf16 or fp32, its rows contiguous");
-    const int dev = current_device();
-    on_device(x, "linear: x", dev);
-    on_device(y, "linear: y", dev);
-    on_device(q, "linear: codes", dev);
-    on_device(s, "linear: scales", dev);
-    on_device(b, "linear: biases", dev);
-    int32_t *status = nullptr;
-    if (v[8] != Py_None) {
-        const at::Tensor &t = tensor(v[8], "linear: status");
-        on_device(t, "linear: status", dev);
-        if (t.scalar_type() != at::kInt || t.numel() < 1) value_error("linear: status in int32");
-        status = static_cast<int32_t *>(t.data_ptr());
-    }
-    const moe_qweight w{static_cast<const uint32_t *>(q.data_ptr()), static_cast<const uint16_t *>(s.data_ptr()),
-                        static_cast<const uint16_t *>(b.data_ptr())};
-    return int4_linear(&w, N, K, group, x.data_ptr(), B > 1 ? x.stride(0) : K, size32(B), y.data_ptr(),
-                       B > 1 ? y.stride(0) : N, fp32, status, stream_of(v[9], dev));
+    const Linear l(v);
+    return int4_linear(&l.w, l.N, l.K, l.group, l.x, l.x_stride, size32(l.B), l.y, l.y_stride, l.fp32,
+                       status_of(v[8], "linear: status", l.dev), stream_of(v[9], l.dev));
+}
+
+// q, scale, bias, rows, K, group, x, y, ws, status | None, stream | None
+int linear_prompt(PyObject *const *v) {
+    const Linear l(v);
+    const auto [ws, bytes] = scratch_of(v[8], l.dev);
+    return int4_linear_prompt(&l.w, l.N, l.K, l.group, l.x, l.x_stride, size32(l.B), l.y, l.y_stride, l.fp32, ws, bytes,
+                              status_of(v[9], "linear: status", l.dev), stream_of(v[10], l.dev));
 }
 
 // pages, device, status (addresses and a number), q | None, k, v, seq, index, page_table, inv_freq | None,
@@ -188,6 +228,16 @@ int append(PyObject *const *v) {
                       stream_of(v[13], dev));
 }
 
+// The pages of prefix_len shared positions (NULL if there are none).
+const int32_t *prefix_of(PyObject *o, int32_t prefix_len, const gqa_pages *pages, int dev) {
+    if (!prefix_len) return nullptr;
+    if (o == Py_None) value_error("prefix_len without prefix_pages");
+    const at::Tensor &t = tensor(o, "prefix_pages");
+    const int32_t *at = ints_of(t, "prefix_pages", -1, 1, dev);
+    if (prefix_len > t.size(0) * pages->page_size) value_error("prefix_pages: too few for prefix_len");
+    return at;
+}
+
 // pages, device, q, page_table, seq_len, prefix_pages | None, prefix_len, scale, out, ws, stream | None and,
 // where the workspace is this call's own (its control block is then cleared first), the address for errors
 int attend(PyObject *const *v) {
@@ -199,30 +249,87 @@ int attend(PyObject *const *v) {
     const int32_t *at = ints_of(table, "page_table", B, 2, dev);
     const int32_t *lens = ints_of(tensor(v[4], "seq_len"), "seq_len", B, 1, dev);
     const int32_t prefix_len = int32(v[6], "prefix_len");
-    const int32_t *prefix = nullptr;
-    if (prefix_len) {
-        if (v[5] == Py_None) value_error("prefix_len without prefix_pages");
-        const at::Tensor &t = tensor(v[5], "prefix_pages");
-        prefix = ints_of(t, "prefix_pages", -1, 1, dev);
-        if (prefix_len > t.size(0) * pages->page_size) value_error("prefix_pages: too few for prefix_len");
-    }
+    const int32_t *prefix = prefix_of(v[5], prefix_len, pages, dev);
     const double scale = PyFloat_AsDouble(v[7]);
     if (scale == -1.0 && PyErr_Occurred()) throw Raised{};
-    const at::Tensor &out = tensor(v[8], "out"), &ws = tensor(v[9], "ws");
+    const at::Tensor &out = tensor(v[8], "out");
     const int64_t os = heads_of(out, "out", B, q.size(1), pages->D, dev);
-    if (ws.get_device() != dev || !ws.is_contiguous()) value_error("ws: contiguous, on the current device");
-    const size_t bytes = static_cast<size_t>(ws.numel()) * ws.element_size();
+    const auto [ws, bytes] = scratch_of(v[9], dev);
     const cudaStream_t stream = stream_of(v[10], dev);
-    auto *status = static_cast<int32_t *>(ws.data_ptr());
+    auto *status = static_cast<int32_t *>(ws);
     if (v[11] != Py_None) {
         status = static_cast<int32_t *>(PyLong_AsVoidPtr(v[11]));
         if (!status && PyErr_Occurred()) throw Raised{};
-        const int rc = moe_workspace_init(ws.data_ptr(), bytes, stream);
+        const int rc = moe_workspace_init(ws, bytes, stream);
         if (rc) return rc;
     }
     return gqa_paged_attention_status(pages, q.data_ptr(), qs, size32(B), size32(q.size(1)), prefix, prefix_len, at,
                                       size32(table.size(1)), lens, static_cast<float>(scale), out.data_ptr(), os,
-                                      ws.data_ptr(), bytes, status, stream);
+                                      ws, bytes, status, stream);
+}
+
+// pages, device, q, q_start, page_table, seq_len, prefix_pages | None, prefix_len, scale, out, ws, stream | None,
+// and the address for errors where it is not the workspace
+int attend_prompt(PyObject *const *v) {
+    const int dev = device_of_cache("attend_prompt", v[1]);
+    const gqa_pages *pages = pages_at(v[0]);
+    const at::Tensor &q = tensor(v[2], "q");
+    const int64_t T = q.dim() ? q.size(0) : 0, qs = heads_of(q, "q", T, -1, pages->D, dev);
+    const at::Tensor &lens = tensor(v[5], "seq_len");
+    const int32_t *len = ints_of(lens, "seq_len", -1, 1, dev);
+    const int64_t n_seq = lens.size(0);
+    const int32_t *start = ints_of(tensor(v[3], "q_start"), "q_start", n_seq + 1, 1, dev);
+    const at::Tensor &table = tensor(v[4], "page_table");
+    const int32_t *at = ints_of(table, "page_table", n_seq, 2, dev);
+    const int32_t prefix_len = int32(v[7], "prefix_len");
+    const int32_t *prefix = prefix_of(v[6], prefix_len, pages, dev);
+    const double scale = PyFloat_AsDouble(v[8]);
+    if (scale == -1.0 && PyErr_Occurred()) throw Raised{};
+    const at::Tensor &out = tensor(v[9], "out");
+    const int64_t os = heads_of(out, "out", T, q.size(1), pages->D, dev);
+    const auto [ws, bytes] = scratch_of(v[10], dev);
+    auto *status = static_cast<int32_t *>(ws);
+    if (v[12] != Py_None) {
+        status = static_cast<int32_t *>(PyLong_AsVoidPtr(v[12]));
+        if (!status && PyErr_Occurred()) throw Raised{};
+    }
+    return gqa_prompt_attention(pages, q.data_ptr(), qs, size32(T), size32(q.size(1)), start, size32(n_seq), prefix,
+                                prefix_len, at, size32(table.size(1)), len, static_cast<float>(scale), out.data_ptr(),
+                                os, ws, bytes, status, stream_of(v[11], dev));
+}
+
+// A contiguous result of token_logprobs, or None: its address.
+template <typename E>
+E *result_of(PyObject *o, const char *name, at::ScalarType type, std::initializer_list<int64_t> shape, int dev) {
+    if (o == Py_None) return nullptr;
+    const at::Tensor &t = tensor(o, name);
+    if (t.scalar_type() != type || !t.is_contiguous() || t.sizes() != at::IntArrayRef(shape))
+        value_error(std::string(name) + ": " + (type == at::kFloat ? "fp32" : "int32") + ", contiguous, a value a row" +
+                    (shape.size() > 1 ? " and alternative" : ""));
+    on_device(t, name, dev);
+    return static_cast<E *>(t.data_ptr());
+}
+
+// logits, targets | None, logprob | None, entropy | None, n_top, top_ids | None, top_logprobs | None, ws,
+// status | None (errors then go to the workspace), stream | None
+int scores(PyObject *const *v) {
+    const int dev = current_device();
+    const at::Tensor &x = tensor(v[0], "logits");
+    const bool fp32 = x.scalar_type() == at::kFloat;
+    if (x.dim() != 2 || !(fp32 || x.scalar_type() == at::kBFloat16) || (x.size(1) > 1 && x.stride(1) != 1))
+        value_error("logits: [T, V] in fp32 or bf16, its rows contiguous");
+    on_device(x, "logits", dev);
+    const int64_t T = x.size(0), V = x.size(1);
+    const int32_t n_top = int32(v[4], "n_top");
+    const int32_t *targets = v[1] == Py_None ? nullptr : ints_of(tensor(v[1], "targets"), "targets", T, 1, dev);
+    float *logprob = result_of<float>(v[2], "logprob", at::kFloat, {T}, dev);
+    float *entropy = result_of<float>(v[3], "entropy", at::kFloat, {T}, dev);
+    int32_t *ids = n_top > 0 ? result_of<int32_t>(v[5], "top_ids", at::kInt, {T, n_top}, dev) : nullptr;
+    float *top = n_top > 0 ? result_of<float>(v[6], "top_logprobs", at::kFloat, {T, n_top}, dev) : nullptr;
+    const auto [ws, bytes] = scratch_of(v[7], dev);
+    int32_t *status = v[8] == Py_None ? static_cast<int32_t *>(ws) : status_of(v[8], "status", dev);
+    return token_logprobs(x.data_ptr(), T > 1 ? x.stride(0) : V, fp32, size32(T), size32(V), targets, logprob, entropy,
+                          n_top, ids, top, ws, bytes, status, stream_of(v[9], dev));
 }
 
 // ARGS arguments, and up to MORE that are None if they are left out.
@@ -251,9 +358,12 @@ PyCFunction fast() {
 PyMethodDef methods[] = {{"linear", fast<linear, 10>(), METH_FASTCALL, "int4_linear"},
                          {"append", fast<append, 14>(), METH_FASTCALL, "gqa_append"},
                          {"attend", fast<attend, 11, 1>(), METH_FASTCALL, "gqa_paged_attention"},
+                         {"linear_prompt", fast<linear_prompt, 11>(), METH_FASTCALL, "int4_linear_prompt"},
+                         {"attend_prompt", fast<attend_prompt, 12, 1>(), METH_FASTCALL, "gqa_prompt_attention"},
+                         {"scores", fast<scores, 10>(), METH_FASTCALL, "token_logprobs"},
                          {nullptr, nullptr, 0, nullptr}};
 
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "The attention sub-layer's calls on torch tensors.", -1, methods,
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "The attention sub-layer's and the prompt's calls on torch tensors.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

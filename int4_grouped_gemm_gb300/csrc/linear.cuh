@@ -6,11 +6,13 @@
 #include <stddef.h>
 
 #include "common.cuh"
+#include "layout.cuh"
 
 namespace moe {
 
 constexpr int kLinearMaxB = 64;      // tokens of one call
 constexpr int kLinearMaxK = 32768;
+constexpr int kLinearPromptMaxT = 1 << 20;
 constexpr int kFewTokens = 8;        // up to here launch_linear_few
 
 struct LinearArgs {
@@ -66,5 +68,8 @@ cudaError_t launch_linear_few(const LinearArgs &a, int num_sms, cudaStream_t s);
 int linear_token_rows(int B);
 int linear_code_words(int G, int B);
 cudaError_t launch_linear_many(const CUtensorMap *maps, const LinearArgs &a, int num_sms, cudaStream_t s);
+// Any number of tokens.
+size_t linear_prompt_workspace_bytes(int N, int K, int G, int T);
+cudaError_t launch_linear_prompt(const LinearArgs &a, void *ws, int num_sms, cudaStream_t s);
 
 }  // namespace moe

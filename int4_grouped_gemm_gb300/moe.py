@@ -65,6 +65,37 @@ def linear(w: QMatrix, x: torch.Tensor, y: Optional[torch.Tensor] = None, dtype=
     return y
 
 
+def linear_prompt_workspace(w: QMatrix, T: int) -> torch.Tensor:
+    """Scratch of linear_prompt for up to T tokens; calls that may overlap take one each."""
+    return torch.empty(_linear_prompt_bytes(w, T), dtype=torch.uint8, device=w.q.device)
+
+
+def _linear_prompt_bytes(w: QMatrix, T: int) -> int:
+    n = _lib.int4_linear_prompt_workspace_bytes(w.rows, w.K, w.group, T)
+    if n == 0:
+        raise _lib.MoEError(_lib.MOE_ERR_SHAPE, "int4_linear_prompt_workspace_bytes")
+    return n
+
+
+def linear_prompt(w: QMatrix, x: torch.Tensor, y: Optional[torch.Tensor] = None, dtype=torch.bfloat16,
+                  ws: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """linear for any number of tokens, a prompt's (int4_linear_prompt; `linear`
+    is made for 64 and fewer).  ws: linear_prompt_workspace, or None for scratch
+    of the call's own."""
+    if stream is not None and (y is None or ws is None):
+        with _lib.on_stream(stream):
+            return linear_prompt(w, x, y, dtype, ws, status)
+    if y is None:
+        y = torch.empty(x.shape[0], w.rows, dtype=dtype, device=x.device)
+    if ws is None:
+        ws = torch.empty(_linear_prompt_bytes(w, x.shape[0]), dtype=torch.uint8, device=x.device)
+    rc = _lib.native().linear_prompt(w.q, w.scale, w.bias, w.rows, w.K, w.group, x, y, ws, status,
+                                     _lib.handle(stream))
+    if rc:
+        raise _lib.MoEError(rc, "int4_linear_prompt")
+    return y
+
+
 class PackedLayer:
     def __init__(self, E: int, k: int, H: int, I: int, group: int, has_shared: bool,
                  router_w: torch.Tensor, router_bias: Optional[torch.Tensor],
