@@ -15,22 +15,10 @@
 //            its softmax, the tensor core works for the other.  Up to 128 rows
 //            in all: one sub-tile; slot 0 takes the even and slot 1 the odd
 //            tiles, each with a partial of its own
-//   S, P, O  in tensor memory: S (fp32, 128 columns), P over it, and O (fp32, D
-//            columns) per slot, 512 columns in all at D = 128.  P is an operand
-//            straight from tensor memory, so that the second product's
-//            shared-memory reads are V alone.  A weight is two bf16 parts (|p -
-//            hi - lo| <= 2^-17 p; of each 64 positions the upper ones over the
-//            first half of their scores' columns, the lower ones over the other),
-//            each with MMAs of its own: with one part, rounded by up to 2^-8, a
-//            call with 128 rows behind 131072 positions took 106 us instead of
+//   tile     per slot as in attn_tile.cuh; S and O of both take 512 columns of
+//            tensor memory at D = 128.  With weights of one bf16 part instead of
+//            two a call with 128 rows behind 131072 positions took 106 us instead of
 //            129, and rows lost accuracy by sharing their prefix
-//   softmax  one thread per row: no exchange between threads.  m need not be the
-//            maximum, only a reference that keeps 2^(s - m) in range, the same in
-//            l and O: fp32 and bf16 hold a weight of 2^-24 as exactly as one of
-//            1.  So m starts 24 above the first scores and stays as it is until
-//            one exceeds it by more than 8 (it goes to the integer 24 above that
-//            one then, which scales O, l and the tile's weights by a power of
-//            two), and the weights need not wait for the tile's maximum
 //
 //   warps 0-3, 4-7   softmax of slot 0, 1 (warp w: rows 32 (w % 4) ..)
 //   warp 8           loads: 64-dimension boxes of page rows by TMA, 128-byte
@@ -52,23 +40,12 @@
 //
 // A position outside the pool is loaded as zeros (the page coordinate lies
 // past the tensor map) and recorded.  Every wait is bounded.
-#include "paged.cuh"
+#include "attn_tile.cuh"
 
 namespace moe {
 
-constexpr int kRows = 128;               // rows of a sub-tile (MMA M)
-constexpr int kPos = 128;                // positions of a tile
 constexpr int kKvStages = 4;             // key or value tiles in flight
 constexpr int kPrefixThreads = 11 * 32;
-// How far the reference is set above a score, and which excess of a score over it
-// moves it (log2).  Together the 32 by which scores may rise before O has to be
-// scaled: with 8 alone a call whose scores spread by 4 took 147 us instead of 130,
-// by 8 154.  Weights of up to 2^9 leave values of up to 2^105 and down to 2^-90 and
-// their sums in fp32's range (with 0 and 32 values of 2^95 gave infinities).
-constexpr float kAbove = 24.f, kRaise = 8.f;
-
-__host__ __device__ constexpr int tile_bytes(int D) { return kPos * D * 2; }
-
 struct PrefixCtl {
     uint64_t kv_full[kKvStages], kv_empty[kKvStages];
     uint64_t q_free;         // every role is past the previous block of rows
@@ -86,44 +63,6 @@ __host__ __device__ constexpr int prefix_smem_bytes(int D) {
     return 2 * kRows * D * 2 + kKvStages * tile_bytes(D) + 1024 + static_cast<int>(sizeof(PrefixCtl));
 }
 static_assert(prefix_smem_bytes(128) <= 227 * 1024, "one block per SM");
-
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2,
-                                            int c3) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-        : "memory");
-}
-
-// Descriptor of values as the MN-major B operand (dimensions contiguous, 128-byte
-// swizzle): 64 dimensions x 8 positions are 1024 bytes; the next 64 dimensions
-// are a half tile (kPos x 128 bytes) away, the next 8 positions 1024 bytes.
-__device__ __forceinline__ uint64_t sdesc_mn128(uint32_t saddr) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>((kPos * 128) >> 4) << 16;
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
-}
-
-constexpr uint32_t kBTransposed = 1u << 16;  // instruction descriptor: B is MN-major
-
-// 2^x by the hardware's approximation (relative error about 2^-22; results
-// below 2^-126 are zero).
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
 
 __device__ __forceinline__ bool prefix_wait(uint64_t *bar, uint32_t parity, const PagedArgs &a, PrefixCtl *s, int site) {
     return role_wait(bar, parity, a.wait_limit, a.status, &s->abort, site);
@@ -204,16 +143,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             const int boxes = ((left < kPos ? left : kPos) + box_rows - 1) / box_rows;
             // lane j: half j % HALVES of box j / HALVES (at most 16 boxes of 2 halves)
             const int bx = lane / HALVES, half = lane % HALVES;
-            int page = 0, row = 0;
-            if (bx < boxes) {
-                const int p = p0 + bx * box_rows;
-                page = a.prefix_pages[p >> ps];
-                row = p & ((1 << ps) - 1);
-                if (page < 0 || page >= a.c.n_pages) {
-                    record_status(a.status, MOE_ERR_PAGE);
-                    page = a.c.n_pages;  // past the map: zeros
-                }
-            }
+            TileBox at{0, 0};
+            if (bx < boxes) at = tile_box(a.c, a.prefix_pages, p0 + bx * box_rows, a.status);
             for (int m = 0; m < 2 && ok; ++m, ++it) {  // keys, then values
                 const int st = it % kKvStages;
                 ok = prefix_wait(&s->kv_empty[st], ((it / kKvStages) & 1) ^ 1, a, s, 21);
@@ -223,7 +154,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 __syncwarp();
                 if (bx < boxes)
                     tma_load_4d(smem_u32(sKV + st * TILE + half * HALF + bx * box_rows * 128), m ? &tm_v : &tm_k,
-                                &s->kv_full[st], half * 64, row, kv, page);
+                                &s->kv_full[st], half * 64, at.row, kv, at.page);
             }
         }
         // no copy of this block is in flight when it ends
@@ -235,7 +166,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         // then keeps the descriptors in uniform registers, and eight MMAs issue
         // in 450 instead of 680 cycles)
         if (elect_one()) {
-            constexpr uint32_t id_s = idesc_bf16(kRows, kPos), id_o = idesc_bf16(kRows, D) | kBTransposed;
             const int slot = __shfl_sync(__activemask(), warp, 0) - 9;
             const uint32_t sS = tmem + slot * 128, sO = tmem + 256 + slot * D;
             const uint32_t q_addr = smem_u32(sQ + (two ? slot * QSUB : 0)), kv_addr = smem_u32(sKV);
@@ -259,12 +189,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     ok = prefix_wait(&s->kv_full[st], (e / kKvStages) & 1, a, s, 25);
                     if (!ok) return;
                     tc_fence_after();
-                    const uint32_t k_addr = kv_addr + st * TILE;
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk / 4) * HALF + (kk % 4) * 32;
-                        umma_bf16(sS, sdesc_k128(q_addr + off), sdesc_k128(k_addr + off), id_s, kk != 0);
-                    }
+                    tile_scores<D>(sS, q_addr, kv_addr + st * TILE);
                 };
                 // (s_full also says that the previous tile's second product is complete)
                 auto scores_end = [&](int n) {
@@ -295,13 +220,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                             ok = ok && prefix_wait(&s->p_full[slot][half], done & 1, a, s, 27);
                             if (!ok) break;
                             tc_fence_after();
-#pragma unroll
-                            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                                umma_bf16_ts(sO, sS + half * 32 + kk * 8, sdesc_mn128(v_addr + kk * 2048), id_o,
-                                             (n < next ? 0 : 1) | kk);
-#pragma unroll
-                            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                                umma_bf16_ts(sO, sS + half * 32 + 32 + kk * 8, sdesc_mn128(v_addr + kk * 2048), id_o, 1);
+                            tile_values<D>(sO, sS, v_addr, half, n < next ? 0 : 1);
                         }
                         if (!ok) break;
                         if (n + next < steps) scores(n + next);
@@ -393,27 +312,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                     turn ^= 4;
                     continue;
                 }
-                uint32_t xa[32], xb[32], xc[32];
-                tmem_ld32(sS, xa);
-                tmem_ld32(sS + 32, xb);
-                if (valid < kPos) {
-                    // value rows past the prefix's end may hold anything: zeros
-                    const uint32_t vi = (it + 1) % kKvStages;
-                    ok = prefix_wait(&s->kv_full[vi], ((it + 1) / kKvStages) & 1, a, s, 30);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) {
-                        // (no load is under way when tensor memory is freed)
-                        tmem_wait32(xa);
-                        tmem_wait32(xb);
-                        break;
-                    }
-                    for (int i = valid * 8 + r; i < kPos * 8; i += kRows)
-#pragma unroll
-                        for (int h = 0; h < HALVES; ++h)
-                            *reinterpret_cast<uint4 *>(sKV + vi * TILE + h * HALF + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    fence_proxy_async_smem();
-                }
-                uint64_t l2[2] = {0, 0};
                 // scores past the prefix's end have no weight
                 auto mask = [&](uint32_t *y, int n0) {
                     if (n0 + 32 > valid) {
@@ -422,100 +320,21 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                             if (n0 + e >= valid) y[e] = 0xFF800000u;
                     }
                 };
-                auto top = [&](const uint32_t *y, const uint32_t *z) {
-                    float t[2] = {-INFINITY, -INFINITY};
+                auto meanwhile = [&]() {
+                    if (valid >= kPos) return true;
+                    // value rows past the prefix's end may hold anything: zeros
+                    const uint32_t vi = (it + 1) % kKvStages;
+                    if (!__all_sync(0xffffffffu, prefix_wait(&s->kv_full[vi], ((it + 1) / kKvStages) & 1, a, s, 30)))
+                        return false;
+                    for (int i = valid * 8 + r; i < kPos * 8; i += kRows)
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        t[0] = max3(t[0], __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
-                        t[1] = max3(t[1], __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
-                    }
-                    return fmaxf(t[0], t[1]) * a.scale_log2;
+                        for (int h = 0; h < HALVES; ++h)
+                            *reinterpret_cast<uint4 *>(sKV + vi * TILE + h * HALF + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                    return true;
                 };
-                // Move the reference of the rows whose score exceeds it by too
-                // much (the warp's 32 rows together; p: weights of this tile so
-                // far, in words): rare but for a block's first tile
-                auto raise = [&](float tm, int p) {
-                    // (from the score itself: a step from m would lose it if m is far away)
-                    const float m_new = tm > m + kRaise ? ceilf(tm) + kAbove : m;
-                    const float corr = ex2(m - m_new);
-                    m = m_new;
-                    l *= corr;
-                    const uint64_t c2 = pack2(__float_as_uint(corr), __float_as_uint(corr));
-                    l2[0] = fma2(l2[0], c2, 0);
-                    l2[1] = fma2(l2[1], c2, 0);
-                    if (p) {
-                        tmem_st_wait();
-                        const __nv_bfloat162 cb = __float2bfloat162_rn(corr);
-#pragma unroll 1
-                        for (int d = 0; d < p; d += 16) {
-                            uint32_t v[16];
-                            tmem_ld16_now(sS + d, v);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) v[e] = bf162_as_u32(__hmul2(u32_as_bf162(v[e]), cb));
-                            tmem_st16(sS + d, v);
-                        }
-                    }
-                    if (any) {
-#pragma unroll 1
-                        for (int d = 0; d < D; d += 16) {
-                            uint32_t v[16];
-                            tmem_ld16_now(sO + d, v);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * corr);
-                            tmem_st16(sO + d, v);
-                        }
-                    }
-                };
-                // weights, in two bf16 parts for the product; l sums them in fp32
-                const uint64_t minus1 = pack2(0xBF800000u, 0xBF800000u);
-                const uint64_t scale2 = pack2(__float_as_uint(a.scale_log2), __float_as_uint(a.scale_log2));
-                auto weigh = [&](const uint32_t *y, int n0) {
-                    const uint64_t neg_m = pack2(__float_as_uint(-m), __float_as_uint(-m));
-                    uint32_t hi[16], lo[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float2 w = unpack2(fma2(pack2(y[2 * e], y[2 * e + 1]), scale2, neg_m));
-                        w.x = ex2(w.x);
-                        w.y = ex2(w.y);
-                        const uint64_t w2 = pack2(__float_as_uint(w.x), __float_as_uint(w.y));
-                        hi[e] = bf162_as_u32(__floats2bfloat162_rn(w.x, w.y));
-                        const float2 r = unpack2(fma2(pack2(hi[e] << 16, hi[e] & 0xFFFF0000u), minus1, w2));
-                        lo[e] = bf162_as_u32(__floats2bfloat162_rn(r.x, r.y));
-                        l2[e & 1] = add2(l2[e & 1], w2);
-                    }
-                    // (positions 64 on have their columns from 64 on)
-                    tmem_st16(sS + n0 / 2 + n0 / 64 * 32, hi);
-                    tmem_st16(sS + n0 / 2 + n0 / 64 * 32 + 32, lo);
-                };
-                tmem_wait32(xa);
-                tmem_wait32(xb);
-                mask(xa, 0);
-                mask(xb, 32);
-                float tm = top(xa, xb);
-                if (!any)
-                    m = fmaxf(ceilf(tm) + kAbove, kLeastRef);
-                else if (__any_sync(0xffffffffu, tm > m + kRaise))
-                    raise(tm, 0);
-                tmem_ld32(sS + 64, xc);
-                weigh(xa, 0);
-                tmem_ld32(sS + 96, xa);
-                weigh(xb, 32);
-                tmem_wait32(xc);
-                tmem_wait32(xa);
-                mask(xc, 64);
-                mask(xa, 96);
-                tm = top(xc, xa);
-                if (__any_sync(0xffffffffu, tm > m + kRaise)) raise(tm, 64);
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(&s->p_full[slot][0]);
-                weigh(xc, 64);
-                weigh(xa, 96);
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(&s->p_full[slot][1]);
-                const float2 lsum = unpack2(add2(l2[0], l2[1]));
-                l += lsum.x + lsum.y;
+                ok = tile_softmax<D>(sS, sO, a.scale_log2, m, l, any, s->p_full[slot], mask, meanwhile);
+                if (!ok) break;
                 any = true;
                 turn ^= 4;
             }

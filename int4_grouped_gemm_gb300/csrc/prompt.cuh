@@ -5,6 +5,20 @@
 
 namespace moe {
 
+// A block of rows of one sequence: up to 2 x tq tokens (tq = 128 / group) with all
+// heads of a key-value head each.
+struct PromptBlock {
+    int seq, row0;   // sequence, first row of q
+    int pos0, ntok;  // own position of that token (negative: none), tokens
+};
+
+// What the plan kernel leaves for the others.
+struct PromptPlan {
+    int64_t tiles;   // of all blocks of one key-value head
+    int64_t per;     // tiles of a piece
+    int nblocks;
+};
+
 struct PromptArgs {
     Pages c;
     const __nv_bfloat16 *q;          // [T][Hq][D], row stride q_stride
@@ -16,6 +30,19 @@ struct PromptArgs {
     int T, Hq, group, n_seq, prefix_len, table_ld;
     float scale;
     long long wait_limit;
+    // filled in by the launch
+    int tq;                          // tokens of a sub-tile of 128 rows
+    int ncta;                        // pieces
+    int max_blocks;                  // that the workspace has room for
+    int negate, zero_q;              // scale < 0: the queries' signs are flipped instead; 0: zero queries, scale_log2 = 1
+    float scale_log2;                // |scale| log2(e)
+    PromptPlan *plan;
+    int *seq_blocks;                 // [n_seq + 1]: blocks of the sequences before
+    int64_t *start;                  // [blocks + 1]: tiles of the blocks before (of one key-value head)
+    PromptBlock *blocks;
+    int *piece_block;                // [ncta]: block of a piece's first tile
+    float2 *part_ml;                 // [piece][it began before, it ends later][sub-tile][128 rows]
+    float *part_o;                   // same, [D / 4][128 rows][4]
 };
 
 // (max_sms: for any GPU of up to so many)
