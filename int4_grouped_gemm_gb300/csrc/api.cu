@@ -81,6 +81,19 @@ static int encode_pages(CUtensorMap *map, const void *ptr, const Pages &c, uint3
     return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_TENSOR_MAP;
 }
 
+// Rows of heads as a tensor (dimension, head, row), in boxes of 64 dimensions,
+// `heads` heads and `rows` rows.
+static int encode_heads(CUtensorMap *map, const void *ptr, int D, int H, int T, int64_t stride, uint32_t heads, uint32_t rows) {
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(T)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2};
+    cuuint32_t box[3] = {64, heads, rows};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_TENSOR_MAP;
+}
+
 static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 static int check_ptr(const void *p) {
@@ -1017,7 +1030,7 @@ static int check_prompt_shape(int32_t T, int32_t n_seq, int32_t Hq, int32_t Hkv,
 
 size_t gqa_prompt_workspace_bytes(int32_t T, int32_t n_seq, int32_t Hq, int32_t Hkv, int32_t D) {
     if (check_prompt_shape(T, n_seq, Hq, Hkv, D) != MOE_OK) return 0;
-    return prompt_workspace_bytes(T, n_seq, Hq, Hkv, D, kGqaMaxSms);
+    return prompt_workspace_bytes(D, kGqaMaxSms);
 }
 
 int gqa_prompt_attention(const gqa_pages *cache, const void *q, int64_t q_stride, int32_t T, int32_t Hq,
@@ -1040,7 +1053,7 @@ int gqa_prompt_attention(const gqa_pages *cache, const void *q, int64_t q_stride
         return MOE_ERR_SHAPE;
     if (q == out && q_stride != out_stride) return MOE_ERR_SHAPE;
     if (!(scale == scale) || scale > 1e30f || scale < -1e30f) return MOE_ERR_SHAPE;
-    if (ws_bytes < prompt_workspace_bytes(T, n_seq, Hq, a.c.Hkv, a.c.D, kGqaMaxSms)) return MOE_ERR_WORKSPACE;
+    if (ws_bytes < prompt_workspace_bytes(a.c.D, kGqaMaxSms)) return MOE_ERR_WORKSPACE;
     DeviceInfo *dev = nullptr;
     if ((rc = current_device(dev))) return rc;
     if (dev->num_sms > kGqaMaxSms) return MOE_ERR_DEVICE;
@@ -1061,9 +1074,11 @@ int gqa_prompt_attention(const gqa_pages *cache, const void *q, int64_t q_stride
     a.table_ld = table_ld;
     a.scale = scale;
     a.wait_limit = g_wait_limit;
-    CUtensorMap maps[2];
+    CUtensorMap maps[3];
     const uint32_t rows = cache->page_size < 128 ? cache->page_size : 128;
-    if ((rc = encode_pages(&maps[0], a.c.k, a.c, rows)) || (rc = encode_pages(&maps[1], a.c.v, a.c, rows))) return rc;
+    if ((rc = encode_heads(&maps[0], q, a.c.D, Hq, T, q_stride, a.group, prompt_tokens(a.group))) ||
+        (rc = encode_pages(&maps[1], a.c.k, a.c, rows)) || (rc = encode_pages(&maps[2], a.c.v, a.c, rows)))
+        return rc;
     return cuda_rc(launch_prompt(a, maps, ws, dev->num_sms, stream));
 }
 

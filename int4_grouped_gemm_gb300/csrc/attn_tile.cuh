@@ -57,6 +57,7 @@ __device__ __forceinline__ uint64_t sdesc_mn128(uint32_t saddr) {
 }
 
 constexpr uint32_t kBTransposed = 1u << 16;  // instruction descriptor: B is MN-major
+constexpr uint32_t kANegated = 1u << 13;     // A's signs are flipped
 
 // 2^x by the hardware's approximation (relative error about 2^-22; results
 // below 2^-126 are zero).
@@ -87,10 +88,10 @@ __device__ __forceinline__ TileBox tile_box(const Pages &c, const int *pages, in
     return b;
 }
 
-// S = Q K^T of a tile: q and k K-major in halves of 64 dimensions.
+// S = Q K^T of a tile: q and k K-major in halves of 64 dimensions; flags: kANegated or 0.
 template <int D>
-__device__ __forceinline__ void tile_scores(uint32_t sS, uint32_t q_addr, uint32_t k_addr) {
-    constexpr uint32_t id_s = idesc_bf16(kRows, kPos);
+__device__ __forceinline__ void tile_scores(uint32_t sS, uint32_t q_addr, uint32_t k_addr, uint32_t flags = 0) {
+    const uint32_t id_s = idesc_bf16(kRows, kPos) | flags;
     constexpr int HALF = kPos * 128;
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {

@@ -5,18 +5,11 @@
 
 namespace moe {
 
-// A block of rows of one sequence: up to 2 x tq tokens (tq = 128 / group) with all
-// heads of a key-value head each.
-struct PromptBlock {
-    int seq, row0;   // sequence, first row of q
-    int pos0, ntok;  // own position of that token (negative: none), tokens
-};
-
-// What the plan kernel leaves for the others.
-struct PromptPlan {
-    int64_t tiles;   // of all blocks of one key-value head
-    int64_t per;     // tiles of a piece
-    int nblocks;
+// What the combine kernel needs of a block of rows that a cut between two pieces
+// runs through; pieces: how many it lies in (0: nothing to join at this cut).
+struct PromptCut {
+    int pieces, kv, row0, ntok;
+    int pos0, pad[3];
 };
 
 struct PromptArgs {
@@ -33,20 +26,17 @@ struct PromptArgs {
     // filled in by the launch
     int tq;                          // tokens of a sub-tile of 128 rows
     int ncta;                        // pieces
-    int max_blocks;                  // that the workspace has room for
-    int negate, zero_q;              // scale < 0: the queries' signs are flipped instead; 0: zero queries, scale_log2 = 1
+    int negate;                      // scale < 0: the queries are taken with their signs flipped
     float scale_log2;                // |scale| log2(e)
-    PromptPlan *plan;
-    int *seq_blocks;                 // [n_seq + 1]: blocks of the sequences before
-    int64_t *start;                  // [blocks + 1]: tiles of the blocks before (of one key-value head)
-    PromptBlock *blocks;
-    int *piece_block;                // [ncta]: block of a piece's first tile
-    float2 *part_ml;                 // [piece][it began before, it ends later][sub-tile][128 rows]
+    PromptCut *cuts;                 // [ncta]: at a piece's beginning
+    float2 *part_ml;                 // [piece][its block began before, it ends later][sub-tile][128 rows]
     float *part_o;                   // same, [D / 4][128 rows][4]
 };
 
 // (max_sms: for any GPU of up to so many)
-size_t prompt_workspace_bytes(int T, int n_seq, int Hq, int Hkv, int D, int max_sms);
+size_t prompt_workspace_bytes(int D, int max_sms);
+// maps: queries (boxes of 64 x group x tq in (D, Hq, T)), keys, values.
+inline int prompt_tokens(int group) { return 128 / group; }  // of a sub-tile
 cudaError_t launch_prompt(PromptArgs &a, const CUtensorMap *maps, void *ws, int num_sms, cudaStream_t s);
 
 }  // namespace moe
