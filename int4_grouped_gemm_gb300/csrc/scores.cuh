@@ -19,6 +19,11 @@ struct ScoresArgs {
     float *top_logprobs;     // [T][n_top]
     int *status;             // may be NULL
     int T, V, n_top, fp32;
+    // filled in by the launch
+    int parts;               // of a row, each a block
+    int part_batches;        // batches of 256 scores of a part
+    float4 *part_sums;       // [T][parts]: reference, sum, weighted sum
+    unsigned long long *part_top;  // [T][parts][32]
 };
 
 // (max_sms: for any GPU of up to so many)
