@@ -8,6 +8,7 @@
 // comes back as its return code.
 #include <Python.h>
 
+#include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -310,30 +311,65 @@ E *result_of(PyObject *o, const char *name, at::ScalarType type, std::initialize
     return static_cast<E *>(t.data_ptr());
 }
 
+// Rows of scores and the tokens given for them.
+struct Scores {
+    const at::Tensor &x;
+    bool fp32;
+    int dev;
+    int64_t T, V;
+    int32_t n_top;
+    const int32_t *targets;
+
+    Scores(PyObject *logits, PyObject *given, PyObject *n) : x(tensor(logits, "logits")), dev(current_device()) {
+        fp32 = x.scalar_type() == at::kFloat;
+        if (x.dim() != 2 || !(fp32 || x.scalar_type() == at::kBFloat16) || (x.size(1) > 1 && x.stride(1) != 1))
+            value_error("logits: [T, V] in fp32 or bf16, its rows contiguous");
+        on_device(x, "logits", dev);
+        T = x.size(0);
+        V = x.size(1);
+        n_top = int32(n, "n_top");
+        targets = given == Py_None ? nullptr : ints_of(tensor(given, "targets"), "targets", T, 1, dev);
+    }
+    int call(float *logprob, float *entropy, int32_t *ids, float *top, PyObject *ws_, PyObject *status_, PyObject *stream) const {
+        const auto [ws, bytes] = scratch_of(ws_, dev);
+        int32_t *status = status_ == Py_None ? static_cast<int32_t *>(ws) : status_of(status_, "status", dev);
+        return token_logprobs(x.data_ptr(), T > 1 ? x.stride(0) : V, fp32, size32(T), size32(V), targets, logprob, entropy,
+                              n_top, ids, top, ws, bytes, status, stream_of(stream, dev));
+    }
+};
+
 // logits, targets | None, logprob | None, entropy | None, n_top, top_ids | None, top_logprobs | None, ws,
 // status | None (errors then go to the workspace), stream | None
 int scores(PyObject *const *v) {
-    const int dev = current_device();
-    const at::Tensor &x = tensor(v[0], "logits");
-    const bool fp32 = x.scalar_type() == at::kFloat;
-    if (x.dim() != 2 || !(fp32 || x.scalar_type() == at::kBFloat16) || (x.size(1) > 1 && x.stride(1) != 1))
-        value_error("logits: [T, V] in fp32 or bf16, its rows contiguous");
-    on_device(x, "logits", dev);
-    const int64_t T = x.size(0), V = x.size(1);
-    const int32_t n_top = int32(v[4], "n_top");
-    const int32_t *targets = v[1] == Py_None ? nullptr : ints_of(tensor(v[1], "targets"), "targets", T, 1, dev);
-    float *logprob = result_of<float>(v[2], "logprob", at::kFloat, {T}, dev);
-    float *entropy = result_of<float>(v[3], "entropy", at::kFloat, {T}, dev);
-    int32_t *ids = n_top > 0 ? result_of<int32_t>(v[5], "top_ids", at::kInt, {T, n_top}, dev) : nullptr;
-    float *top = n_top > 0 ? result_of<float>(v[6], "top_logprobs", at::kFloat, {T, n_top}, dev) : nullptr;
-    const auto [ws, bytes] = scratch_of(v[7], dev);
-    int32_t *status = v[8] == Py_None ? static_cast<int32_t *>(ws) : status_of(v[8], "status", dev);
-    return token_logprobs(x.data_ptr(), T > 1 ? x.stride(0) : V, fp32, size32(T), size32(V), targets, logprob, entropy,
-                          n_top, ids, top, ws, bytes, status, stream_of(v[9], dev));
+    const Scores s(v[0], v[1], v[4]);
+    float *logprob = result_of<float>(v[2], "logprob", at::kFloat, {s.T}, s.dev);
+    float *entropy = result_of<float>(v[3], "entropy", at::kFloat, {s.T}, s.dev);
+    int32_t *ids = s.n_top > 0 ? result_of<int32_t>(v[5], "top_ids", at::kInt, {s.T, s.n_top}, s.dev) : nullptr;
+    float *top = s.n_top > 0 ? result_of<float>(v[6], "top_logprobs", at::kFloat, {s.T, s.n_top}, s.dev) : nullptr;
+    return s.call(logprob, entropy, ids, top, v[7], v[8], v[9]);
 }
 
+// logits, targets | None, n_top, ws, status | None, stream | None: scores with results of its own (made in
+// Python they took longer than one row's kernels): (rc, logprob | None, entropy, top_ids, top_logprobs)
+PyObject *scores_new(PyObject *const *v) {
+    const Scores s(v[0], v[1], v[2]);
+    if (s.n_top < 0) value_error("n_top: 0 at least");
+    const auto f = s.x.options().dtype(at::kFloat);
+    const at::Tensor logprob = s.targets ? at::empty({s.T}, f) : at::Tensor(), entropy = at::empty({s.T}, f),
+                     ids = at::empty({s.T, s.n_top}, f.dtype(at::kInt)), top = at::empty({s.T, s.n_top}, f);
+    const int rc = s.call(s.targets ? static_cast<float *>(logprob.data_ptr()) : nullptr, static_cast<float *>(entropy.data_ptr()),
+                          s.n_top ? static_cast<int32_t *>(ids.data_ptr()) : nullptr,
+                          s.n_top ? static_cast<float *>(top.data_ptr()) : nullptr, v[3], v[4], v[5]);
+    // (N takes the references; a missing one has set an exception)
+    PyObject *given = s.targets ? THPVariable_Wrap(logprob) : Py_NewRef(Py_None);
+    return Py_BuildValue("(iNNNN)", rc, given, THPVariable_Wrap(entropy), THPVariable_Wrap(ids), THPVariable_Wrap(top));
+}
+
+PyObject *as_object(int rc) { return PyLong_FromLong(rc); }
+PyObject *as_object(PyObject *o) { return o; }
+
 // ARGS arguments, and up to MORE that are None if they are left out.
-template <int (*CALL)(PyObject *const *), int ARGS, int MORE>
+template <auto CALL, int ARGS, int MORE>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n < ARGS || n > ARGS + MORE) {
         PyErr_Format(PyExc_TypeError, "%d arguments, not %zd", ARGS, n);
@@ -342,7 +378,7 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     PyObject *all[ARGS + MORE];
     for (Py_ssize_t i = 0; i < ARGS + MORE; ++i) all[i] = i < n ? args[i] : Py_None;
     try {
-        return PyLong_FromLong(CALL(all));
+        return as_object(CALL(all));
     } catch (const Raised &) {
     } catch (const std::exception &e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
@@ -350,7 +386,7 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return nullptr;
 }
 
-template <int (*CALL)(PyObject *const *), int ARGS, int MORE = 0>
+template <auto CALL, int ARGS, int MORE = 0>
 PyCFunction fast() {
     return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<CALL, ARGS, MORE>));
 }
@@ -361,6 +397,7 @@ PyMethodDef methods[] = {{"linear", fast<linear, 10>(), METH_FASTCALL, "int4_lin
                          {"linear_prompt", fast<linear_prompt, 11>(), METH_FASTCALL, "int4_linear_prompt"},
                          {"attend_prompt", fast<attend_prompt, 12, 1>(), METH_FASTCALL, "gqa_prompt_attention"},
                          {"scores", fast<scores, 10>(), METH_FASTCALL, "token_logprobs"},
+                         {"scores_new", fast<scores_new, 6>(), METH_FASTCALL, "token_logprobs"},
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "The attention sub-layer's and the prompt's calls on torch tensors.", -1, methods,

@@ -56,15 +56,16 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     if stream is not None and (out is None or ws is None):
         with _lib.on_stream(stream):
             return token_logprobs(logits, targets, n_top, out, ws, status)
-    if logits.dim() != 2:
-        raise ValueError("token_logprobs: logits [T, V]")
-    T, V = logits.shape
-    if out is None:
-        out = TokenScores.empty(T, n_top, targets is not None, logits.device)
     if ws is None:
-        ws = torch.empty(_bytes(T, V, n_top), dtype=torch.uint8, device=logits.device)
-    rc = _lib.native().scores(logits, targets, out.logprob, out.entropy, n_top, out.top_ids, out.top_logprobs, ws,
-                              status, _lib.handle(stream))
+        if logits.dim() != 2:
+            raise ValueError("token_logprobs: logits [T, V]")
+        ws = torch.empty(_bytes(*logits.shape, n_top), dtype=torch.uint8, device=logits.device)
+    if out is None:
+        rc, *made = _lib.native().scores_new(logits, targets, n_top, ws, status, None)
+        out = TokenScores._make(made)
+    else:
+        rc = _lib.native().scores(logits, targets, out.logprob, out.entropy, n_top, out.top_ids, out.top_logprobs, ws,
+                                  status, _lib.handle(stream))
     if rc:
         raise _lib.MoEError(rc, "token_logprobs")
     return out
