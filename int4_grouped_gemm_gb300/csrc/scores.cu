@@ -7,13 +7,15 @@
 //            moves only when a score exceeds it by 8 (S and U are then scaled): e^8
 //            costs nothing of fp32's accuracy, and a running maximum would be moved
 //            in most batches by one of a warp's lanes
-//   top      each warp keeps the 32 best scores so far, sorted, a lane each, as one
-//            64-bit number of value and id.  Of a batch of 256 scores it looks at the
-//            lanes' maxima only, which the sums need anyway; where one exceeds the
-//            n-th best, the scores that do go to a buffer, and 32 of them are
-//            sorted and merged with the list by exchanges between lanes (15 + 6
-//            steps).  For scores in random order that is n log(V / 8n) of V / 8 scores a
-//            warp; in rising order every score is sorted
+//   top      the pass keeps, of each lane's scores, the maximum of every eighth part
+//            (the sums need the maxima anyway).  At its end the warps' ceil(n / warps)-th
+//            largest of these maxima, the least of them, is a value that n scores at least
+//            reach; the few eighths that reach it are read again, 1 to 2 n of the row's
+//            256 to 2048, their scores that reach it sorted 32 at a time and merged with
+//            the list of the 32 best, a lane each, by exchanges between lanes (15 + 6
+//            steps).  (A list kept during the pass, by each warp, took as many
+//            instructions as the sums in long rows, and several times as many in short
+//            ones: 257 x 50021 with 5 alternatives 39 us)
 //   work     a row is cut into parts where there are too few rows for the GPU, a
 //            block of eight warps each, whose sums and lists are merged through shared
 //            memory; scores_merge_kernel merges the parts.  Short rows of many are a
@@ -31,16 +33,18 @@ typedef unsigned long long u64;
 constexpr int kWarps = 8;             // of a block
 constexpr int kBatch = 256;           // scores that a warp takes at a time, eight a lane
 constexpr int kPartBatches = 16;      // of a part at least
+constexpr int kEighths = 8;           // parts of a lane's scores whose maxima are kept
 constexpr float kLogRaise = 8.f;
 constexpr float kLeast = -3.402823466e38f;
 
 // A score's place in the order of alternatives: larger scores first, NaN before
-// all, equal ones (zeros of both signs too) by lower id; 0: none.
-__device__ __forceinline__ u64 rank_key(float x, int id) {
+// all, zeros of both signs equal; never 0.
+__device__ __forceinline__ uint32_t order_of(float x) {
     const uint32_t u = x != x ? 0x7FFFFFFFu : __float_as_uint(x + 0.f);
-    const uint32_t up = u & 0x80000000u ? ~u : u | 0x80000000u;
-    return static_cast<u64>(up) << 32 | ~static_cast<uint32_t>(id);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+// ... and equal ones by lower id; 0: none.
+__device__ __forceinline__ u64 rank_key(uint32_t order, int id) { return static_cast<u64>(order) << 32 | ~static_cast<uint32_t>(id); }
 __device__ __forceinline__ float key_score(u64 k) {
     const uint32_t up = static_cast<uint32_t>(k >> 32);
     return __uint_as_float(up & 0x80000000u ? up & 0x7FFFFFFFu : ~up);
@@ -103,55 +107,32 @@ __device__ __forceinline__ u64 merge32(u64 a, u64 b, int lane) {
     return bitonic_merge(larger(a, __shfl_sync(0xffffffffu, b, 31 - lane)), lane);
 }
 
-// The float before x (plus infinity or finite): y > before(x) where y >= x; NaN for
-// minus infinity.
-__device__ __forceinline__ float before(float x) {
-    const uint32_t u = __float_as_uint(x);
-    return __uint_as_float(u == 0 || u == 0x80000000u ? 0x80000001u : u & 0x80000000u ? u + 1 : u - 1);
-}
-
-// The 32 best of a warp's scores so far.
+// The 32 best of the scores that a warp looks at, which are those of `least` (an
+// order) at least.
 struct Best {
-    u64 list = 0;           // this lane's
-    float above = NAN;      // a score that is not `<=` this may be among the n best
-    int waiting = 0;        // scores in the buffer
+    u64 list = 0, nth = 0;  // this lane's; the n-th
+    uint32_t least;
+    int waiting = 0;        // scores in the buffer (of 64)
 
-    // equal: a score equal to the n-th best may still have a lower id, which is so
-    // within a batch, but not from one to the next
-    __device__ __forceinline__ void set_above(int n, bool equal) {
-        const u64 k = __shfl_sync(0xffffffffu, list, n - 1);
-        const float x = key_score(k), y = x != x ? INFINITY : x;
-        // fewer than n: NaN, which takes all; the n-th a NaN: only NaN comes before it
-        above = k == 0 ? NAN : equal ? before(y) : y;
-    }
-    __device__ __forceinline__ void sort_in(const u64 *buffer, int n, int lane) {
+    __device__ __forceinline__ void sort_in(u64 *buffer, int n, int lane) {
         __syncwarp();
         const u64 k = lane < waiting ? buffer[lane] : 0;
         const u64 rest = 32 + lane < waiting ? buffer[32 + lane] : 0;
         __syncwarp();
         list = merge32(list, sort32(k, lane), lane);
-        if (waiting > 32) const_cast<u64 *>(buffer)[lane] = rest;
+        if (waiting > 32) buffer[lane] = rest;
         waiting = waiting > 32 ? waiting - 32 : 0;
-        set_above(n, true);
+        nth = __shfl_sync(0xffffffffu, list, n - 1);
+        least = larger(least, static_cast<uint32_t>(nth >> 32));
     }
     __device__ __forceinline__ void offer(float x, int id, bool real, u64 *buffer, int n, int lane) {
-        const bool take = real && !(x <= above);
+        const uint32_t o = order_of(x);
+        if (!__any_sync(0xffffffffu, real && o >= least)) return;
+        const u64 key = rank_key(o, id);
+        const bool take = real && o >= least && key > nth;
         const unsigned m = __ballot_sync(0xffffffffu, take);
-        if (!m) return;
-        if (take) buffer[waiting + __popc(m & ((1u << lane) - 1))] = rank_key(x, id);
+        if (take) buffer[waiting + __popc(m & ((1u << lane) - 1))] = key;
         waiting += __popc(m);
-        if (waiting >= 32) sort_in(buffer, n, lane);
-    }
-    // Scores of one lane alone.
-    template <typename F>
-    __device__ __forceinline__ void offer_lane(const float (&x)[8], int of, F id, u64 *buffer, int n, int lane) {
-        int k = 0;
-        if (lane == of) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (!(x[i] <= above) && id(i) >= 0) buffer[waiting + k++] = rank_key(x[i], id(i));
-        }
-        waiting += __shfl_sync(0xffffffffu, k, of);
         if (waiting >= 32) sort_in(buffer, n, lane);
     }
 };
@@ -245,45 +226,47 @@ struct Ring {
     static constexpr int VEC = 16 / sizeof(E), N = 8 / VEC, STAGES = 8 / N;
     uint4 *mine;  // [stage][N][32 lanes], this lane's
 
+    // The vector from score e of the row on, minus infinity where there is no score.
+    __device__ __forceinline__ static uint4 edge(const E *row, int64_t e, int64_t hi) {
+        auto at = [&](int64_t k) { return k >= 0 && k < hi ? __float_as_uint(score(row + k)) : 0xFF800000u; };
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = sizeof(E) == 4 ? at(e + j) : at(e + 2 * j) >> 16 | at(e + 2 * j + 1);
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ static void unpack(float *x, const uint4 &v) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (sizeof(E) == 4) {
+                x[j] = __uint_as_float(w[j]);
+            } else {
+                x[2 * j] = __uint_as_float(w[j] << 16);
+                x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+            }
+        }
+    }
+    __device__ __forceinline__ static void fetch(float *x, const E *row, int64_t e, int64_t hi) {
+        unpack(x, e >= 0 && e + VEC <= hi ? __ldcg(reinterpret_cast<const uint4 *>(row + e)) : edge(row, e, hi));
+    }
     // first: index in the row of the batch's first score; hi: the row's end (0: no batch)
     __device__ __forceinline__ void load(int stage, const E *row, int64_t first, int64_t hi, int lane) const {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int64_t e = first + (i * 32 + lane) * VEC;
             uint4 *to = mine + (stage * N + i) * 32;
-            if (e >= 0 && e + VEC <= hi) {
+            if (e >= 0 && e + VEC <= hi)
                 cp_async<16>(to, row + e);
-            } else if (hi > 0) {
-                // minus infinity where there is no score
-                uint32_t w[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    auto at = [&](int64_t k) { return k >= 0 && k < hi ? __float_as_uint(score(row + k)) : 0xFF800000u; };
-                    w[j] = sizeof(E) == 4 ? at(e + j) : at(e + 2 * j) >> 16 | at(e + 2 * j + 1);
-                }
-                *to = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            else if (hi > 0)
+                *to = edge(row, e, hi);
         }
         cp_async_commit();
     }
     __device__ __forceinline__ void read(int stage, float (&x)[8]) const {
         cp_async_wait<STAGES - 1>();
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const uint4 v = mine[(stage * N + i) * 32];
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if constexpr (sizeof(E) == 4) {
-                    x[i * 4 + j] = __uint_as_float(w[j]);
-                } else {
-                    x[2 * j] = __uint_as_float(w[j] << 16);
-                    x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-                }
-            }
-        }
+        for (int i = 0; i < N; ++i) unpack(x + i * VEC, mine[(stage * N + i) * 32]);
     }
-    __device__ __forceinline__ static int index(int i, int lane) { return (i / VEC * 32 + lane) * VEC + i % VEC; }
 };
 
 // ROWS: rows of a block, each for 8 / ROWS warps.
@@ -291,6 +274,7 @@ template <typename E, bool TOP, int ROWS>
 __global__ void __launch_bounds__(kWarps * 32, 4) scores_kernel(const __grid_constant__ ScoresArgs a) {
     constexpr int WPR = kWarps / ROWS;
     __shared__ u64 buffers[TOP ? kWarps : 1][TOP ? 64 : 1];
+    __shared__ uint32_t maxima[TOP ? kWarps : 1][kEighths][32], shares[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
@@ -312,29 +296,12 @@ __global__ void __launch_bounds__(kWarps * 32, 4) scores_kernel(const __grid_con
     int b = (ROWS > 1 ? 0 : part * a.part_batches) + mine;
 
     Sums s{kLeast, 0.f, 0.f};
-    Best best;
     u64 S2 = 0, U2 = 0;  // pairs of partial sums
     const u64 log2e = pack2(0x3FB8AA3Bu, 0x3FB8AA3Bu);
-    // the warps' ceil(n / warps)-th best: n scores at least are not below the least of them
-    __shared__ u64 quantiles[kWarps];
-    const int nth_share = TOP ? (a.n_top + WPR - 1) / WPR - 1 : 0;
-    if (TOP && WPR > 1) {
-        if (threadIdx.x < kWarps) quantiles[threadIdx.x] = 0;
-        __syncthreads();
-    }
-    // what the block's warps together leave of `above`
-    auto share = [&]() {
-        if (WPR == 1) return;
-        const u64 nth = __shfl_sync(0xffffffffu, best.list, nth_share);
-        if (lane == 0) *const_cast<volatile u64 *>(quantiles + warp) = nth;
-        u64 q = *const_cast<volatile u64 *>(quantiles + warp - mine + lane % WPR);
-#pragma unroll
-        for (int i = WPR / 2; i; i >>= 1) q = smaller(q, __shfl_xor_sync(0xffffffffu, q, i));
-        // (zero: a warp has too few yet; before(minus infinity) and a NaN among the best
-        // take all, as NaN)
-        const float y = before(key_score(q));
-        if (q && y == y && !(y <= best.above)) best.above = y;
-    };
+    const int b0 = b, own = b < b1 ? (b1 - b + WPR - 1) / WPR : 0;  // this warp's first batch and their number
+    const int eighth = max(1, (own + kEighths - 1) / kEighths);
+    float most = -INFINITY;  // of the eighth
+    int left = eighth, done = 0;
     const Ring<E> ring{&ring_at[warp][0][lane]};
     constexpr int STAGES = Ring<E>::STAGES;
     auto load = [&](int stage, int b) { ring.load(stage, row, off + static_cast<int64_t>(b) * kBatch, b < b1 ? a.V : 0, lane); };
@@ -342,7 +309,6 @@ __global__ void __launch_bounds__(kWarps * 32, 4) scores_kernel(const __grid_con
     for (int i = 0; i < STAGES; ++i) load(i, b + i * WPR);
     bool first = true;
     for (int stage = 0; b < b1; b += WPR, stage = (stage + 1) % STAGES) {
-        const int at = off + b * kBatch;
         float x[8];
         ring.read(stage, x);
         const float top = max3_nan(max3_nan(x[0], x[1], x[2]), max3_nan(x[3], x[4], x[5]), max_nan(x[6], x[7]));
@@ -369,38 +335,83 @@ __global__ void __launch_bounds__(kWarps * 32, 4) scores_kernel(const __grid_con
         }
         load(stage, b + STAGES * WPR);  // (its scores are in registers)
         if (TOP) {
-            if (first && at >= 0 && at + kBatch <= a.V) {
-                // the n-th of the lanes' maxima is not above the n-th best
-                const uint32_t k = sort32(static_cast<uint32_t>(rank_key(top, 0) >> 32), lane);
-                const float nth = key_score(static_cast<u64>(__shfl_sync(0xffffffffu, k, a.n_top - 1)) << 32);
-                if (nth > -INFINITY) best.above = before(nth);
-            }
-            const unsigned lanes = __ballot_sync(0xffffffffu, !(top <= best.above));
-            if (lanes) {
-                auto id_of = [&](int i) {
-                    const int id = at + Ring<E>::index(i, lane);
-                    return id < a.V ? id : -1;
-                };
-                if ((lanes & (lanes - 1)) == 0) {
-                    best.offer_lane(x, __ffs(lanes) - 1, id_of, buffer, a.n_top, lane);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) best.offer(x[i], id_of(i), id_of(i) >= 0, buffer, a.n_top, lane);
-                }
-                if (first && best.waiting) best.sort_in(buffer, a.n_top, lane);
-                best.set_above(a.n_top, false);
-                share();
+            most = max_nan(most, top);
+            if (--left == 0) {
+                maxima[warp][done++][lane] = order_of(most);
+                left = eighth;
+                most = -INFINITY;
             }
         }
         first = false;
-    }
-    if (TOP) {
-        while (best.waiting) best.sort_in(buffer, a.n_top, lane);
     }
     const float2 S1 = unpack2(S2), U1 = unpack2(U2);
     s.S = S1.x + S1.y;
     s.U = U1.x + U1.y;
     merge_lanes(s);
+    Best best;
+    if (TOP) {
+        if (left < eighth) maxima[warp][done++][lane] = order_of(most);
+        // the share-th largest of the warp's maxima
+        const int batches_here = ROWS > 1 ? batches : max(0, b1 - part * a.part_batches);
+        const int with = min(WPR, max(1, batches_here)), share = (a.n_top + with - 1) / with;
+        uint32_t m[kEighths], mx = 0, nth = 0;
+#pragma unroll
+        for (int i = 0; i < kEighths; ++i) m[i] = i < done ? maxima[warp][i][lane] : 0;
+#pragma unroll
+        for (int i = 0; i < kEighths; ++i) mx = larger(mx, m[i]);
+        if (share > 4) {
+            // (of the lanes' own maxima: lower, but in few steps)
+            nth = __shfl_sync(0xffffffffu, sort32(mx, lane), share - 1);
+        } else {
+            for (int k = 0;;) {
+                nth = __reduce_max_sync(0xffffffffu, mx);
+                if (++k == share) break;
+                // one of them, of the first lane that has it, goes
+                bool goes = lane == __ffs(__ballot_sync(0xffffffffu, mx == nth)) - 1;
+                mx = 0;
+#pragma unroll
+                for (int i = 0; i < kEighths; ++i) {
+                    if (goes && m[i] == nth) {
+                        m[i] = 0;
+                        goes = false;
+                    }
+                    mx = larger(mx, m[i]);
+                }
+            }
+        }
+        if (WPR > 1) {
+            // (a warp without batches has no say)
+            if (lane == 0) shares[warp] = own ? nth : 0xFFFFFFFFu;
+            __syncthreads();
+            nth = shares[warp - mine + lane % WPR];
+#pragma unroll
+            for (int i = WPR / 2; i; i >>= 1) nth = smaller(nth, __shfl_xor_sync(0xffffffffu, nth, i));
+        }
+        best.least = nth;
+        // the eighths that reach it
+        auto look = [&](int at, int hi) {
+            float x[Ring<E>::VEC];
+            Ring<E>::fetch(x, row, at, hi);
+#pragma unroll
+            for (int j = 0; j < Ring<E>::VEC; ++j)
+                best.offer(x[j], at + j, at + j >= 0 && at + j < hi, buffer, a.n_top, lane);
+        };
+        for (int i = 0; i < done; ++i) {
+            unsigned lanes = __ballot_sync(0xffffffffu, maxima[warp][i][lane] >= nth);
+            const int first_b = b0 + i * eighth * WPR, vectors = min(eighth, own - i * eighth) * Ring<E>::N;
+            auto vector = [&](int v, int of) {
+                return off + (first_b + v / Ring<E>::N * WPR) * kBatch + (v % Ring<E>::N * 32 + of) * Ring<E>::VEC;
+            };
+            if (__popc(lanes) * ((vectors + 31) / 32) >= vectors) {
+                // many lanes of a short eighth: all of it
+                for (int v = 0; v < vectors; ++v) look(vector(v, lane), a.V);
+            } else {
+                for (; lanes; lanes &= lanes - 1)
+                    for (int v = lane; v - lane < vectors; v += 32) look(vector(v, __ffs(lanes) - 1), v < vectors ? a.V : 0);
+            }
+        }
+        if (best.waiting) best.sort_in(buffer, a.n_top, lane);
+    }
     merge_warps<WPR>(s, best.list, TOP, warp, lane);
     if (mine || target < 0) return;
     if (a.parts == 1) {
@@ -437,10 +448,12 @@ __global__ void __launch_bounds__(kWarps * 32) scores_merge_kernel(const __grid_
 
 // ------------------------------------------------------------------- host
 
-// Parts of a row: as many as leave each SM its four blocks, of 4096 scores at least.
+// Parts of a row: as many as give each SM two blocks, of 4096 scores at least.  (With
+// more, a block's beginning and end and the merge cost more than they bring: 257 rows
+// of 50021 in two parts 33 us instead of 20.)
 static int row_parts(int T, int V, int sms) {
     const int most = std::max(1, V / (kBatch * kPartBatches));
-    return std::max(1, std::min(4 * sms / T, most));
+    return std::max(1, std::min(2 * sms / T, most));
 }
 
 size_t scores_workspace_bytes(int T, int V, int n_top, int max_sms) {
@@ -458,13 +471,13 @@ template <typename E, bool TOP>
 static cudaError_t launch_e(ScoresArgs &a, void *ws, int num_sms, cudaStream_t s) {
     a.parts = row_parts(a.T, a.V, num_sms);
     if (a.parts == 1) {
-        // the fewer warps a row has, the fewer lists are made and merged: as few as
-        // leave each SM its 32 warps, or as the row has batches for
-        const int most = 4 * num_sms * kWarps / a.T, need = a.V / kBatch;
+        // a warp has 16 batches, or fewer where there are not 32 warps for each SM
+        const int batches = a.V / kBatch, fill = 4 * num_sms * kWarps / a.T;
+        const int warps = std::max(batches / 16, std::min(fill, batches / 2));
         a.part_batches = 1 << 30;
-        if (most < 2 || need < 2) return launch_rows<E, TOP, 8>(a, s);
-        if (most < 4 || need < 4) return launch_rows<E, TOP, 4>(a, s);
-        if (most < 8 || need < 8) return launch_rows<E, TOP, 2>(a, s);
+        if (warps < 2) return launch_rows<E, TOP, 8>(a, s);
+        if (warps < 4) return launch_rows<E, TOP, 4>(a, s);
+        if (warps < 8) return launch_rows<E, TOP, 2>(a, s);
         return launch_rows<E, TOP, 1>(a, s);
     }
     // (up to a vector before the row counts with it)
