@@ -829,6 +829,25 @@ static int linear_args(LinearArgs &a, const moe_qweight *w, int32_t N, int32_t K
     return MOE_OK;
 }
 
+// A linear call of up to kLinearMaxB tokens.
+static int linear_run(const LinearArgs &a, const DeviceInfo *dev, cudaStream_t stream) {
+    if (a.B <= kFewTokens) return cuda_rc(launch_linear_few(a, dev->num_sms, stream));
+    int rc;
+    CUtensorMap maps[4];
+    const auto SW0 = CU_TENSOR_MAP_SWIZZLE_NONE;
+    const int words = linear_code_words(a.G, a.B);
+    if ((rc = encode_2d(&maps[0], CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, a.q, a.K / 8, a.N, words, 128,
+                        words == 8    ? CU_TENSOR_MAP_SWIZZLE_32B
+                        : words == 16 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                      : CU_TENSOR_MAP_SWIZZLE_128B)) ||
+        (rc = encode_2d(&maps[1], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.s, a.K / a.G, a.N, 16, 128, SW0, a.ldg)) ||
+        (rc = encode_2d(&maps[2], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.b, a.K / a.G, a.N, 16, 128, SW0, a.ldg)) ||
+        (rc = encode_2d(&maps[3], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.x, a.K, a.B, 64, linear_token_rows(a.B),
+                        CU_TENSOR_MAP_SWIZZLE_128B, a.x_stride)))
+        return rc;
+    return cuda_rc(launch_linear_many(maps, a, dev->num_sms, stream));
+}
+
 int int4_linear(const moe_qweight *w, int32_t N, int32_t K, int32_t group, const void *x, int64_t x_stride, int32_t B,
                 void *y, int64_t y_stride, int32_t y_fp32, int32_t *status, cudaStream_t stream) {
     LinearArgs a{};
@@ -836,20 +855,7 @@ int int4_linear(const moe_qweight *w, int32_t N, int32_t K, int32_t group, const
     if (rc) return rc;
     DeviceInfo *dev = nullptr;
     if ((rc = current_device(dev))) return rc;
-    if (B <= kFewTokens) return cuda_rc(launch_linear_few(a, dev->num_sms, stream));
-    CUtensorMap maps[4];
-    const auto SW0 = CU_TENSOR_MAP_SWIZZLE_NONE;
-    const int words = linear_code_words(group, B);
-    if ((rc = encode_2d(&maps[0], CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, w->q, K / 8, N, words, 128,
-                        words == 8    ? CU_TENSOR_MAP_SWIZZLE_32B
-                        : words == 16 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                      : CU_TENSOR_MAP_SWIZZLE_128B)) ||
-        (rc = encode_2d(&maps[1], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->scale, K / group, N, 16, 128, SW0, a.ldg)) ||
-        (rc = encode_2d(&maps[2], CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, w->bias, K / group, N, 16, 128, SW0, a.ldg)) ||
-        (rc = encode_2d(&maps[3], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, K, B, 64, linear_token_rows(B),
-                        CU_TENSOR_MAP_SWIZZLE_128B, x_stride)))
-        return rc;
-    return cuda_rc(launch_linear_many(maps, a, dev->num_sms, stream));
+    return linear_run(a, dev, stream);
 }
 
 // int32 and fp32 arrays of the paged calls: element-aligned, so that slices of
@@ -1018,7 +1024,21 @@ int int4_linear_prompt(const moe_qweight *w, int32_t N, int32_t K, int32_t group
     if (ws_bytes < linear_prompt_workspace_bytes(N, K, group, T)) return MOE_ERR_WORKSPACE;
     DeviceInfo *dev = nullptr;
     if ((rc = current_device(dev))) return rc;
-    return cuda_rc(launch_linear_prompt(a, ws, dev->num_sms, stream));
+    // (as two calls for few tokens: 10 us instead of FEW_MEASURED for 65 x 2048 x 2560)
+    if (T <= 2 * kLinearMaxB) {
+        LinearArgs b = a;
+        a.B = (T + 1) / 2;
+        b.B = T - a.B;
+        b.x += a.B * x_stride;
+        b.y = static_cast<char *>(b.y) + a.B * y_stride * (y_fp32 ? 4 : 2);
+        if ((rc = linear_run(a, dev, stream)) || !b.B) return rc;
+        return linear_run(b, dev, stream);
+    }
+    const LinearMap encode = [](CUtensorMap *map, const void *ptr, int inner, int rows, int box_inner, int box_rows) {
+        return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, ptr, inner, rows, box_inner, box_rows,
+                         CU_TENSOR_MAP_SWIZZLE_128B) == MOE_OK;
+    };
+    return cuda_rc(launch_linear_prompt(a, encode, ws, dev->num_sms, stream));
 }
 
 static int check_prompt_shape(int32_t T, int32_t n_seq, int32_t Hq, int32_t Hkv, int32_t D) {
