@@ -14,17 +14,23 @@
 //            at 2^8, which keeps sums of 128 in fp16's range
 //
 // linear_operands_kernel writes both operands, rows of P = K + 3 K / G columns (each
-// part rounded up to 64, zeros between), and the rows' powers; matrices larger than
-// the L2 are worked through in pieces of rows, so that the fp16 weights are read
-// back from the L2.  (Unpacked in the product's kernel, a code is unpacked again for
-// every 256 tokens: that kernel of the experts' products runs at 41 % of the tensor
-// rate.)
+// part rounded up to 64, zeros between), and the rows' powers; large matrices are
+// worked through in pieces of rows, so that the fp16 weights are read back from the
+// L2, and the next piece is unpacked while one is multiplied.  (Unpacked in the
+// product's kernel, a code is unpacked again for every 256 tokens: that kernel of the
+// experts' products runs at 41 % of the tensor rate.)
 //
-// linear_prompt_kernel: tiles of 128 weight rows (M) by up to 256 tokens (N, a multiple
-// of 16 picked for even rounds over the SMs), one block per SM, tiles in turn:
+// linear_prompt_kernel: pairs of blocks, on two SMs, work on tiles of 256 weight rows
+// by up to 256 tokens (a multiple of 32 picked for even rounds over the pairs) with
+// tcgen05.mma across both: a block holds its 128 rows and half of the tokens, so
+// that each SM fetches 32 KB for 512 cycles of MMA.  (One block alone, 128 rows by
+// 192 to 256 tokens, fetches 40 to 48 KB in the time, more than the 64 bytes a
+// cycle that reach a SM: 4096 x 2048 x 2560 45 us instead of PAIR_MEASURED.)
 //
-//   warp 0           loads: 64 columns of both operands a stage, 128-byte swizzle
-//   warp 1           MMA issue; two accumulators in tensor memory in turn
+//   warp 0           loads: 64 columns of both operands a stage, 128-byte swizzle;
+//                    both blocks' loads complete on the first one's barrier
+//   warp 1           MMA issue, in the pair's first block; two accumulators in
+//                    tensor memory in turn
 //   warps 4-11       epilogue: a lane is a weight row, so that a warp writes 32
 //                    neighbouring results of a token at a time, whatever y's stride;
 //                    powers of two put back
@@ -39,7 +45,8 @@
 namespace moe {
 namespace prompt {
 
-constexpr int kRows = 128;                 // weight rows of a tile
+constexpr int kRows = 128;                 // weight rows of a block, of a tile
+constexpr int kPairRows = 2 * kRows;
 constexpr int kMaxTok = 256;               // tokens of a tile
 constexpr int kStep = 64;                  // columns of a stage
 constexpr int kMaxStages = 8;
@@ -47,7 +54,7 @@ constexpr int kEpiWarp = 4, kEpiWarps = 8;
 constexpr int kThreads = (kEpiWarp + kEpiWarps) * 32;
 constexpr int kWBytes = kRows * kStep * 2;
 constexpr int kMaxT = 16384;               // tokens whose operands are held at a time
-constexpr size_t kWeightBytes = 40 << 20;  // of fp16 weights held at a time, about
+constexpr size_t kWeightBytes = 40 << 20;  // of fp16 weights of a piece, about; two are held
 
 // Columns of an operand's row.
 struct Columns {
@@ -57,10 +64,11 @@ struct Columns {
 
 struct Args {
     LinearArgs l;
-    __half *xh, *wh;      // [tokens here][P], [rows here][P]
+    __half *xh, *wh;      // [tokens here][P], [rows of this piece][P]
     int *xe, *we;         // their powers
     int t0, nt, n0, nn;   // tokens and rows of this launch
-    int x_blocks;         // operands: blocks that make tokens
+    int x_blocks;         // operands: blocks that make tokens (0: not the first piece)
+    int gshift;           // log2 of the group
     int tok, t_tiles, n_tiles, stages;
 };
 
@@ -90,20 +98,26 @@ __device__ __forceinline__ void zero_columns(__half *row, int from, int to, int 
 constexpr int kOpThreads = 256;
 
 // Blocks 0 .. x_blocks - 1: a token each.  The others: a weight row a warp.
-__global__ void __launch_bounds__(kOpThreads) linear_operands_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kOpThreads, 6) linear_operands_kernel(const __grid_constant__ Args a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Columns c(a.l.K, a.l.G);
     const int G = a.l.G, ng = c.groups;
     __shared__ uint32_t tops[kOpThreads / 32];
-    pdl_wait();
+    // A later piece's weights go to the place that the piece before the last one had,
+    // whose product is over: the product that runs now waited for the last piece's
+    // operands, and these (below) for that product.  Nothing else is written
+    const bool first = a.x_blocks > 0;
+    if (first) pdl_wait();
     pdl_trigger();
     if (static_cast<int>(blockIdx.x) < a.x_blocks) {
         const int t = blockIdx.x;
         const uint4 *x = reinterpret_cast<const uint4 *>(a.l.x + (a.t0 + t) * a.l.x_stride);
         __half *row = a.xh + static_cast<int64_t>(t) * c.P;
         uint32_t top = 0;
+        uint4 v0 = make_uint4(0u, 0u, 0u, 0u);
         for (int i = tid; i < c.K / 8; i += kOpThreads) {
-            const uint4 v = __ldg(x + i);
+            const uint4 v = __ldcg(x + i);
+            if (i == tid) v0 = v;
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, w[j] >> 16 & 0x7FFFu));
@@ -120,7 +134,7 @@ __global__ void __launch_bounds__(kOpThreads) linear_operands_kernel(const __gri
             const int i = i0 + tid;
             float sum = 0.f;
             if (i < c.K / 8) {
-                const uint4 v = __ldg(x + i);
+                const uint4 v = i0 ? __ldcg(x + i) : v0;
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                 uint4 o;
                 uint32_t *ow = reinterpret_cast<uint32_t *>(&o);
@@ -150,7 +164,10 @@ __global__ void __launch_bounds__(kOpThreads) linear_operands_kernel(const __gri
         return;
     }
     const int r = (blockIdx.x - a.x_blocks) * (kOpThreads / 32) + warp;
-    if (r >= a.nn) return;
+    if (r >= a.nn) {
+        if (!first) pdl_wait();
+        return;
+    }
     const int64_t n = a.n0 + r;
     const uint16_t *s = a.l.s + n * a.l.ldg, *z = a.l.b + n * a.l.ldg;
     const uint32_t *q = a.l.q + n * (c.K / 8);
@@ -161,9 +178,10 @@ __global__ void __launch_bounds__(kOpThreads) linear_operands_kernel(const __gri
         top = fmaxf(top, fmaxf(8.f * fabsf(sg), 256.f * fabsf(cg)));
     }
     const int up = 14 - power_of(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
+#pragma unroll 4
     for (int i = lane; i < c.K / 8; i += 32) {
         const uint32_t w = __ldcs(q + i);
-        const __half2 sg = __half2half2(__float2half_rn(times_power(bf16_bits_to_float(__ldg(s + i * 8 / G)), up)));
+        const __half2 sg = __half2half2(__float2half_rn(times_power(bf16_bits_to_float(__ldg(s + (i * 8 >> a.gshift))), up)));
         const __half2 c1032 = __half2half2(__ushort_as_half(0x6408));
         uint4 o;
         uint32_t *ow = reinterpret_cast<uint32_t *>(&o);
@@ -187,35 +205,74 @@ __global__ void __launch_bounds__(kOpThreads) linear_operands_kernel(const __gri
     zero_columns(row, c.K, c.Kp, lane, 32);
     zero_columns(row, c.Kp + 3 * ng, c.P, lane, 32);
     if (lane == 0) a.we[r] = -up;
+    // this kernel is over when the product before it is
+    if (!first) pdl_wait();
 }
 
 // -------------------------------------------------------------- product
 
 struct Ctl {
-    uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t acc_full[2], acc_empty[2];
+    uint64_t full[kMaxStages], empty[kMaxStages];  // (full: of both blocks' loads, in the first one)
+    uint64_t acc_full[2], acc_empty[2];            // (acc_empty: of both, in the first one)
     uint64_t drain;
     uint32_t tmem;
     int abort;
 };
 
-__host__ __device__ constexpr int stage_bytes(int tok) { return kWBytes + tok * kStep * 2; }
+__host__ __device__ constexpr int stage_bytes(int tok) { return kWBytes + tok / 2 * kStep * 2; }
 __host__ __device__ constexpr int stages_for(int tok) {
-    const int n = (kBlockSmem - 1024 - static_cast<int>(sizeof(Ctl))) / stage_bytes(tok);
+    // (8 KB stay free for blocks that unpack the next piece)
+    const int n = (kBlockSmem - 9 * 1024 - static_cast<int>(sizeof(Ctl))) / stage_bytes(tok);
     return n < kMaxStages ? n : kMaxStages;
 }
 __host__ __device__ constexpr int smem_bytes(int tok) {
-    return stages_for(tok) * stage_bytes(tok) + 1024 + static_cast<int>(sizeof(Ctl));
+    // (more than half of a SM's: one block at a time, since each takes all of the tensor memory)
+    const int n = stages_for(tok) * stage_bytes(tok) + 1024 + static_cast<int>(sizeof(Ctl));
+    return n > kBlockSmem / 2 + 1024 ? n : kBlockSmem / 2 + 1024;
 }
-static_assert(stages_for(kMaxTok) >= 4 && smem_bytes(kMaxTok) <= kBlockSmem, "stages");
+static_assert(stages_for(kMaxTok) >= 4 && smem_bytes(kMaxTok) <= kBlockSmem && smem_bytes(32) <= kBlockSmem, "stages");
 
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, const Args &a, Ctl *s, int site) {
     return role_wait(bar, parity, a.l.wait_limit, a.l.status, &s->abort, site);
 }
 
-// Instruction descriptor: fp16 x fp16 -> fp32, A and B K-major, shape 128 x tok.
+// Instruction descriptor: fp16 x fp16 -> fp32, A and B K-major, shape 256 x tok over a pair.
 __device__ __forceinline__ uint32_t idesc_f16(int tok) {
-    return (1u << 4) | (static_cast<uint32_t>(tok >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24);
+    return (1u << 4) | (static_cast<uint32_t>(tok >> 3) << 17) | (static_cast<uint32_t>(kPairRows >> 4) << 24);
+}
+
+// Of a pair of blocks: the address of the first block's copy of a shared variable.
+__device__ __forceinline__ uint32_t in_first(const void *p) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+    return r;
+}
+__device__ __forceinline__ void pair_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// A box into this block's shared memory, complete on a barrier of the pair.
+__device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive on `bar` of both blocks when every MMA issued so far by this thread is done.
+__device__ __forceinline__ void pair_commit(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -227,6 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ctl *s = reinterpret_cast<Ctl *>(base + stages * stage);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tiles = a.t_tiles * a.n_tiles, steps = Columns(a.l.K, a.l.G).P / kStep;
+    const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (tid == 0) {
         for (int i = 0; i < stages; ++i) {
@@ -235,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s->acc_full[i], 1);
-            mbar_init(&s->acc_empty[i], kEpiWarps);
+            mbar_init(&s->acc_empty[i], 2 * kEpiWarps);
         }
         mbar_init(&s->drain, 1);
         s->abort = 0;
@@ -244,11 +302,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&tm_x);
     }
     if (warp == 1) {
-        tmem_alloc(&s->tmem, 512);
-        tmem_relinquish();
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s->tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // both blocks' barriers are there
     tc_fence_after();
     const uint32_t tmem = s->tmem;
     pdl_wait();
@@ -258,29 +317,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
             uint32_t it = 0;
             bool ok = true;
-            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-                const int n0 = tile % a.n_tiles * kRows, t0 = tile / a.n_tiles * a.tok;
+            for (int tile = pair; tile < tiles && ok; tile += pairs) {
+                const int n0 = tile % a.n_tiles * kPairRows + rank * kRows, t0 = tile / a.n_tiles * a.tok + rank * (a.tok / 2);
                 for (int k = 0; k < steps && ok; ++k, ++it) {
                     const int st = it % stages;
                     ok = wait(&s->empty[st], ((it / stages) & 1) ^ 1, a, s, 61);
                     if (!ok) break;
-                    uint8_t *at = base + st * stage;
-                    mbar_arrive_expect_tx(&s->full[st], stage);
-                    tma_load_2d(at, &tm_w, &s->full[st], k * kStep, n0);
-                    tma_load_2d(at + kWBytes, &tm_x, &s->full[st], k * kStep, t0);
+                    const uint32_t at = smem_u32(base + st * stage), bar = in_first(&s->full[st]);
+                    // (the other block's bytes may come before they are expected: the phase
+                    // cannot end before this arrival)
+                    if (rank == 0) mbar_arrive_expect_tx(&s->full[st], 2 * stage);
+                    pair_load_2d(at, &tm_w, bar, k * kStep, n0);
+                    pair_load_2d(at + kWBytes, &tm_x, bar, k * kStep, t0);
                 }
             }
-            // no copy of this block is in flight when it ends
+            // no copy of this block is in flight when it ends: the MMAs that read the last
+            // ones are complete, or two milliseconds have passed for each
             for (uint32_t i = it > static_cast<uint32_t>(stages) ? it - stages : 0; i < it; ++i)
-                mbar_drain(&s->full[i % stages], (i / stages) & 1, a.l.wait_limit);
+                mbar_wait(&s->empty[i % stages], (i / stages) & 1, 1 << 22);
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (elect_one()) {
+        if (rank == 0 && elect_one()) {
             const uint32_t idesc = idesc_f16(a.tok);
             uint32_t it = 0, nt = 0;
             bool ok = true;
-            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++nt) {
+            for (int tile = pair; tile < tiles && ok; tile += pairs, ++nt) {
                 const uint32_t acc = tmem + (nt & 1) * 256;
                 ok = wait(&s->acc_empty[nt & 1], ((nt >> 1) & 1) ^ 1, a, s, 62);
                 if (!ok) break;
@@ -293,13 +355,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t w_at = smem_u32(base) + st * stage, x_at = w_at + kWBytes;
 #pragma unroll
                     for (int j = 0; j < kStep / 16; ++j)
-                        umma_bf16(acc, sdesc_k128(w_at + j * 32), sdesc_k128(x_at + j * 32), idesc, k | j);
-                    umma_commit(&s->empty[st]);
+                        pair_mma(acc, sdesc_k128(w_at + j * 32), sdesc_k128(x_at + j * 32), idesc, k | j);
+                    pair_commit(&s->empty[st]);
                 }
-                if (ok) umma_commit(&s->acc_full[nt & 1]);
+                if (ok) pair_commit(&s->acc_full[nt & 1]);
             }
             // every MMA issued here is complete before tensor memory is freed
-            umma_commit(&s->drain);
+            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&s->drain))
+                         : "memory");
             mbar_drain(&s->drain, 0, a.l.wait_limit);
         }
         __syncwarp();
@@ -307,8 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quarter = warp & 3, half = (warp - kEpiWarp) >> 2;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         uint32_t nt = 0;
-        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++nt) {
-            const int n = tile % a.n_tiles * kRows + quarter * 32 + lane, t0 = tile / a.n_tiles * a.tok;
+        for (int tile = pair; tile < tiles; tile += pairs, ++nt) {
+            const int n = tile % a.n_tiles * kPairRows + rank * kRows + quarter * 32 + lane, t0 = tile / a.n_tiles * a.tok;
             const int we = n < a.nn ? __ldcg(a.we + n) : 0;
             const bool ok = __all_sync(0xffffffffu, wait(&s->acc_full[nt & 1], (nt >> 1) & 1, a, s, 64));
             if (!ok) break;
@@ -328,15 +391,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s->acc_empty[nt & 1]);
+            if (lane == 0) pair_arrive(in_first(&s->acc_empty[nt & 1]));
         }
     }
 
+    // neither block goes while the other may still reach its shared or tensor memory
     tc_fence_before();
     __syncthreads();
+    cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
 }
 
@@ -344,32 +409,37 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 struct Layout {
     size_t xe, we, xh, wh, total;
-    int rows;  // weight rows held at a time
+    size_t we_piece, wh_piece;  // bytes from one piece's place to the other's
+    int rows;                   // weight rows of a piece
 };
 
 static Layout layout(int N, int K, int G, int T) {
     auto up = [](size_t n) { return (n + 1023) / 1024 * 1024; };
     const size_t P = Columns(K, G).P;
     Layout L{};
-    const size_t most = std::max<size_t>(kWeightBytes / (P * 2) / kRows * kRows, kRows);
+    const size_t most = std::max<size_t>(kWeightBytes / (P * 2) / kPairRows * kPairRows, kPairRows);
     L.rows = static_cast<int>(std::min<size_t>(N, most));
+    const size_t places = N > L.rows ? 2 : 1;
+    L.we_piece = up(L.rows * sizeof(int));
+    L.wh_piece = up(L.rows * P * 2);
     L.xe = kCtrlBytes;
     L.we = L.xe + up(std::min(T, kMaxT) * sizeof(int));
-    L.xh = up(L.we + L.rows * sizeof(int));
+    L.xh = L.we + places * L.we_piece;
     L.wh = L.xh + up(std::min(T, kMaxT) * P * 2);
-    L.total = L.wh + L.rows * P * 2;
+    L.total = L.wh + places * L.wh_piece;
     return L;
 }
 
-// Tokens of a tile: as many as make the rounds over the SMs cheapest, a round's cost
-// being its tokens and 32 more (weights are fetched for few tokens as for many).
-static int tile_tokens(int N, int T, int sms) {
-    const int n_tiles = (N + kRows - 1) / kRows;
+// Tokens of a tile: as many as make the rounds over the pairs of SMs cheapest, a
+// round's cost being its tokens and 32 more (weights are fetched for few tokens as
+// for many).
+static int tile_tokens(int N, int T, int pairs) {
+    const int n_tiles = (N + kPairRows - 1) / kPairRows;
     int best = kMaxTok;
     int64_t least = INT64_MAX;
-    for (int tok = kMaxTok; tok >= 32; tok -= 16) {
+    for (int tok = kMaxTok; tok >= 32; tok -= 32) {
         const int64_t tiles = static_cast<int64_t>(n_tiles) * ((T + tok - 1) / tok);
-        const int64_t cost = (tiles + sms - 1) / sms * (tok + 32);
+        const int64_t cost = (tiles + pairs - 1) / pairs * (tok + 32);
         if (cost < least) {
             least = cost;
             best = tok;
@@ -389,31 +459,43 @@ cudaError_t launch_linear_prompt(const LinearArgs &l, LinearMap encode, void *ws
     char *w = static_cast<char *>(ws);
     Args a{};
     a.l = l;
+    a.gshift = l.G == 32 ? 5 : l.G == 64 ? 6 : 7;
     a.xe = reinterpret_cast<int *>(w + L.xe);
-    a.we = reinterpret_cast<int *>(w + L.we);
     a.xh = reinterpret_cast<__half *>(w + L.xh);
-    a.wh = reinterpret_cast<__half *>(w + L.wh);
     cudaError_t e = allow_smem<linear_prompt_kernel>();
     if (e != cudaSuccess) return e;
     for (a.t0 = 0; a.t0 < l.B; a.t0 += kMaxT) {
         a.nt = std::min(l.B - a.t0, kMaxT);
-        for (a.n0 = 0; a.n0 < l.N; a.n0 += L.rows) {
+        int place = 0;
+        for (a.n0 = 0; a.n0 < l.N; a.n0 += L.rows, place ^= 1) {
             a.nn = std::min(l.N - a.n0, L.rows);
+            a.we = reinterpret_cast<int *>(w + L.we + place * L.we_piece);
+            a.wh = reinterpret_cast<__half *>(w + L.wh + place * L.wh_piece);
             a.x_blocks = a.n0 ? 0 : a.nt;
             const int w_blocks = (a.nn + kOpThreads / 32 - 1) / (kOpThreads / 32);
             if ((e = launch_dependent(linear_operands_kernel, dim3(a.x_blocks + w_blocks), dim3(kOpThreads), 0, s, a)) != cudaSuccess)
                 return e;
-            a.tok = tile_tokens(a.nn, a.nt, num_sms);
+            a.tok = tile_tokens(a.nn, a.nt, num_sms / 2);
             a.stages = stages_for(a.tok);
-            a.n_tiles = (a.nn + kRows - 1) / kRows;
+            a.n_tiles = (a.nn + kPairRows - 1) / kPairRows;
             a.t_tiles = (a.nt + a.tok - 1) / a.tok;
             CUtensorMap mw, mx;
-            if (!encode(&mw, a.wh, c.P, a.nn, kStep, kRows) || !encode(&mx, a.xh, c.P, a.nt, kStep, a.tok))
+            if (!encode(&mw, a.wh, c.P, a.nn, kStep, kRows) || !encode(&mx, a.xh, c.P, a.nt, kStep, a.tok / 2))
                 return cudaErrorInvalidValue;
-            const int tiles = a.n_tiles * a.t_tiles;
-            if ((e = launch_dependent(linear_prompt_kernel, dim3(std::min(tiles, num_sms)), dim3(kThreads), smem_bytes(a.tok),
-                                      s, mw, mx, a)) != cudaSuccess)
-                return e;
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(2 * std::min(a.n_tiles * a.t_tiles, num_sms / 2));
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = smem_bytes(a.tok);
+            cfg.stream = s;
+            cudaLaunchAttribute attr[2];
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            attr[1].id = cudaLaunchAttributeClusterDimension;
+            attr[1].val.clusterDim.x = 2;
+            attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 2;
+            if ((e = cudaLaunchKernelEx(&cfg, linear_prompt_kernel, mw, mx, a)) != cudaSuccess) return e;
         }
     }
     return cudaSuccess;
