@@ -95,14 +95,14 @@ __device__ __forceinline__ void zero_columns(__half *row, int from, int to, int 
     for (int c = from + i; c < to; c += n) row[c] = __float2half_rn(0.f);
 }
 
-constexpr int kOpThreads = 256;
+constexpr int kOpThreads = 256, kOpRows = kOpThreads / 32;
+constexpr int kHeld = 8;  // of a token's vectors of eight, those that a lane keeps between the passes
 
-// Blocks 0 .. x_blocks - 1: a token each.  The others: a weight row a warp.
-__global__ void __launch_bounds__(kOpThreads, 6) linear_operands_kernel(const __grid_constant__ Args a) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+// A row a warp: blocks 0 .. x_blocks - 1 tokens, the others weights.
+__global__ void __launch_bounds__(kOpThreads, 4) linear_operands_kernel(const __grid_constant__ Args a) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Columns c(a.l.K, a.l.G);
-    const int G = a.l.G, ng = c.groups;
-    __shared__ uint32_t tops[kOpThreads / 32];
+    const int ng = c.groups;
     // A later piece's weights go to the place that the piece before the last one had,
     // whose product is over: the product that runs now waited for the last piece's
     // operands, and these (below) for that product.  Nothing else is written
@@ -110,46 +110,43 @@ __global__ void __launch_bounds__(kOpThreads, 6) linear_operands_kernel(const __
     if (first) pdl_wait();
     pdl_trigger();
     if (static_cast<int>(blockIdx.x) < a.x_blocks) {
-        const int t = blockIdx.x;
+        const int t = blockIdx.x * kOpRows + warp, n = c.K / 8;
+        if (t >= a.nt) return;
         const uint4 *x = reinterpret_cast<const uint4 *>(a.l.x + (a.t0 + t) * a.l.x_stride);
         __half *row = a.xh + static_cast<int64_t>(t) * c.P;
+        uint4 held[kHeld];
         uint32_t top = 0;
-        uint4 v0 = make_uint4(0u, 0u, 0u, 0u);
-        for (int i = tid; i < c.K / 8; i += kOpThreads) {
-            const uint4 v = __ldcg(x + i);
-            if (i == tid) v0 = v;
+        auto look = [&](const uint4 &v) {
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, w[j] >> 16 & 0x7FFFu));
-        }
+        };
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) held[i] = i * 32 + lane < n ? __ldcg(x + i * 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) look(held[i]);
+#pragma unroll 4
+        for (int i = kHeld * 32 + lane; i < n; i += 32) look(__ldcg(x + i));
         top = __reduce_max_sync(0xffffffffu, top);
-        if (lane == 0) tops[warp] = top;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kOpThreads / 32; ++i) top = max(top, tops[i]);
         // (a row with an infinity or NaN keeps it)
-        const int e = power_of(__uint_as_float(top << 16)), up = 14 - e;
-        const int lanes = G / 8;  // of a group
-        for (int i0 = 0; i0 < c.K / 8; i0 += kOpThreads) {
-            const int i = i0 + tid;
+        const int up = 14 - power_of(__uint_as_float(top << 16));
+        const int lanes = a.l.G / 8;  // of a group
+        auto put = [&](const uint4 &v, int i) {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t o[4];
             float sum = 0.f;
-            if (i < c.K / 8) {
-                const uint4 v = i0 ? __ldcg(x + i) : v0;
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                uint4 o;
-                uint32_t *ow = reinterpret_cast<uint32_t *>(&o);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const __half2 h = __floats2half2_rn(times_power(__uint_as_float(w[j] << 16), up),
-                                                        times_power(__uint_as_float(w[j] & 0xFFFF0000u), up));
-                    ow[j] = *reinterpret_cast<const uint32_t *>(&h);
-                    const float2 f = __half22float2(h);
-                    sum += f.x + f.y;
-                }
-                reinterpret_cast<uint4 *>(row)[i] = o;
+            for (int j = 0; j < 4; ++j) {
+                const __half2 h = __floats2half2_rn(times_power(__uint_as_float(w[j] << 16), up),
+                                                    times_power(__uint_as_float(w[j] & 0xFFFF0000u), up));
+                o[j] = *reinterpret_cast<const uint32_t *>(&h);
+                const float2 f = __half22float2(h);
+                sum += f.x + f.y;
             }
             for (int j = 1; j < lanes; j <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, j);
-            if (i < c.K / 8 && i % lanes == 0) {
+            if (i >= n) return;
+            reinterpret_cast<uint4 *>(row)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+            if (i % lanes == 0) {
                 const int g = i / lanes;
                 __half h1, h2;
                 split(sum * 0x1p-8f, h1, h2);
@@ -157,13 +154,17 @@ __global__ void __launch_bounds__(kOpThreads, 6) linear_operands_kernel(const __
                 row[c.Kp + ng + g] = h2;
                 row[c.Kp + 2 * ng + g] = h1;
             }
-        }
-        zero_columns(row, c.K, c.Kp, tid, kOpThreads);
-        zero_columns(row, c.Kp + 3 * ng, c.P, tid, kOpThreads);
-        if (tid == 0) a.xe[t] = -up;
+        };
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            if (i * 32 < n) put(held[i], i * 32 + lane);
+        for (int i = kHeld * 32; i < n; i += 32) put(i + lane < n ? __ldcg(x + i + lane) : make_uint4(0u, 0u, 0u, 0u), i + lane);
+        zero_columns(row, c.K, c.Kp, lane, 32);
+        zero_columns(row, c.Kp + 3 * ng, c.P, lane, 32);
+        if (lane == 0) a.xe[t] = -up;
         return;
     }
-    const int r = (blockIdx.x - a.x_blocks) * (kOpThreads / 32) + warp;
+    const int r = (blockIdx.x - a.x_blocks) * kOpRows + warp;
     if (r >= a.nn) {
         if (!first) pdl_wait();
         return;
@@ -376,17 +377,49 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool ok = __all_sync(0xffffffffu, wait(&s->acc_full[nt & 1], (nt >> 1) & 1, a, s, 64));
             if (!ok) break;
             tc_fence_after();
-            // sixteen tokens at a time, the halves in turn
-            for (int c = half * 16; c < a.tok; c += 32) {
-                float v[16];
-                tmem_ld16((tmem + (nt & 1) * 256 + c) | lanes, v);
+            // 32 tokens at a time, the halves in turn; the powers as two factors where they
+            // are near enough to one that neither leaves fp32's range
+            for (int c = half * 32; c < a.tok; c += 64) {
                 const int left = a.nt - t0 - c;
                 if (left <= 0) break;
-                const int xe = lane < 16 && lane < left ? __ldcg(a.xe + t0 + c + lane) : 0;
+                uint32_t v[32];
+                tmem_ld32((tmem + (nt & 1) * 256 + c) | lanes, v);
+                const int xe = lane < left ? __ldcg(a.xe + t0 + c + lane) : 0;
+                const bool near = __all_sync(0xffffffffu, abs(xe) <= 60 && abs(we) <= 60);
+                const float xf = near ? __int_as_float((xe + 127) << 23) : 0.f, wf = __int_as_float(((near ? we : 0) + 127) << 23);
+                tmem_wait32(v);
+                char *at = static_cast<char *>(a.l.y) + ((a.t0 + t0 + c) * a.l.y_stride + a.n0 + n) * (a.l.y_fp32 ? 4 : 2);
+                auto write = [&](auto put) {
+                    if (left >= 32) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float y = times_power(v[j], max(-250, min(250, we + __shfl_sync(0xffffffffu, xe, j))));
-                    if (j < left && n < a.nn) a.l.store(a.t0 + t0 + c + j, a.n0 + n, y);
+                        for (int j = 0; j < 32; ++j) put(j);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < left) put(j);
+                    }
+                };
+                auto scaled = [&](int j) { return __uint_as_float(v[j]) * __shfl_sync(0xffffffffu, xf, j) * wf; };
+                if (!near) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const int e = max(-250, min(250, we + __shfl_sync(0xffffffffu, xe, j)));
+                        if (j < left && n < a.nn) a.l.store(a.t0 + t0 + c + j, a.n0 + n, times_power(__uint_as_float(v[j]), e));
+                    }
+                } else if (a.l.y_fp32) {
+                    const int64_t step = a.l.y_stride * 4;
+                    write([&](int j) {
+                        const float y = scaled(j);
+                        if (n < a.nn) *reinterpret_cast<float *>(at) = y;
+                        at += step;
+                    });
+                } else {
+                    const int64_t step = a.l.y_stride * 2;
+                    write([&](int j) {
+                        const float y = scaled(j);
+                        if (n < a.nn) *reinterpret_cast<__nv_bfloat16 *>(at) = __float2bfloat16_rn(y);
+                        at += step;
+                    });
                 }
             }
             tc_fence_before();
@@ -430,6 +463,18 @@ static Layout layout(int N, int K, int G, int T) {
     return L;
 }
 
+// Lets blocks of the operands kernel run on SMs that the product's have: only kernels
+// with the same division of shared memory and L1 run on one together.
+static cudaError_t beside_product() {
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_acquire))) return e;
+    e = cudaFuncSetAttribute(linear_operands_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_release);
+    return e;
+}
+
 // Tokens of a tile: as many as make the rounds over the pairs of SMs cheapest, a
 // round's cost being its tokens and 32 more (weights are fetched for few tokens as
 // for many).
@@ -464,6 +509,7 @@ cudaError_t launch_linear_prompt(const LinearArgs &l, LinearMap encode, void *ws
     a.xh = reinterpret_cast<__half *>(w + L.xh);
     cudaError_t e = allow_smem<linear_prompt_kernel>();
     if (e != cudaSuccess) return e;
+    if (l.N > L.rows && (e = beside_product()) != cudaSuccess) return e;
     for (a.t0 = 0; a.t0 < l.B; a.t0 += kMaxT) {
         a.nt = std::min(l.B - a.t0, kMaxT);
         int place = 0;
@@ -471,8 +517,8 @@ cudaError_t launch_linear_prompt(const LinearArgs &l, LinearMap encode, void *ws
             a.nn = std::min(l.N - a.n0, L.rows);
             a.we = reinterpret_cast<int *>(w + L.we + place * L.we_piece);
             a.wh = reinterpret_cast<__half *>(w + L.wh + place * L.wh_piece);
-            a.x_blocks = a.n0 ? 0 : a.nt;
-            const int w_blocks = (a.nn + kOpThreads / 32 - 1) / (kOpThreads / 32);
+            a.x_blocks = a.n0 ? 0 : (a.nt + kOpRows - 1) / kOpRows;
+            const int w_blocks = (a.nn + kOpRows - 1) / kOpRows;
             if ((e = launch_dependent(linear_operands_kernel, dim3(a.x_blocks + w_blocks), dim3(kOpThreads), 0, s, a)) != cudaSuccess)
                 return e;
             a.tok = tile_tokens(a.nn, a.nt, num_sms / 2);
