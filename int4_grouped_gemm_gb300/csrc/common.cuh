@@ -357,6 +357,14 @@ __device__ __forceinline__ void tmem_wait32(uint32_t *r) {
                  : "memory");
 }
 
+__device__ __forceinline__ void tmem_wait16(uint32_t *r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
 // Load of 16 columns, complete on return.
 __device__ __forceinline__ void tmem_ld16_now(uint32_t taddr, uint32_t *r) {
     asm volatile(

@@ -68,9 +68,9 @@ cudaError_t launch_linear_few(const LinearArgs &a, int num_sms, cudaStream_t s);
 int linear_token_rows(int B);
 int linear_code_words(int G, int B);
 cudaError_t launch_linear_many(const CUtensorMap *maps, const LinearArgs &a, int num_sms, cudaStream_t s);
-// Many tokens; encode: the map of a row-major fp16 matrix in boxes of box_inner x box_rows, 128-byte
-// swizzle (false: none can be made).
-using LinearMap = bool (*)(CUtensorMap *map, const void *ptr, int inner, int rows, int box_inner, int box_rows);
+// Many tokens; encode: the map of a row-major matrix of fp16 (half; 128-byte swizzle) or 32-bit words
+// (32-byte swizzle) in boxes of box_inner x box_rows (false: none can be made).
+using LinearMap = bool (*)(CUtensorMap *map, const void *ptr, bool half, int inner, int rows, int box_inner, int box_rows);
 size_t linear_prompt_workspace_bytes(int N, int K, int G, int T);
 cudaError_t launch_linear_prompt(const LinearArgs &a, LinearMap encode, void *ws, int num_sms, cudaStream_t s);
 

@@ -1,8 +1,7 @@
 // y[t][n] = sum_k x[t][k] (s[n][k/G] q[n][k] + z[n][k/G]) for a prompt's many tokens, on
 // the fifth-generation tensor cores.
 //
-// With so many tokens the unpacking is done once, by a kernel of its own, and the
-// product is a plain one of fp16 operands, no product of which is rounded:
+// The product is a plain one of fp16 operands, no product of which is rounded:
 //
 //   weights  s (q - 8): eight bits by four with a sign are eleven, exact in fp16, at a
 //            power of two of the row's own
@@ -13,24 +12,35 @@
 //            parts (h1, h2, h1) times c as two (c1, c1, c2), 22 bits each; X at 2^-8 and c
 //            at 2^8, which keeps sums of 128 in fp16's range
 //
-// linear_operands_kernel writes both operands, rows of P = K + 3 K / G columns (each
-// part rounded up to 64, zeros between), and the rows' powers; large matrices are
-// worked through in pieces of rows, so that the fp16 weights are read back from the
-// L2, and the next piece is unpacked while one is multiplied.  (Unpacked in the
-// product's kernel, a code is unpacked again for every 256 tokens: that kernel of the
-// experts' products runs at 41 % of the tensor rate.)
+// linear_operands_kernel makes the tokens' operand, rows of P = K + 3 K / G columns
+// (each part rounded up to 64, zeros between), the rows' powers, and of the weights
+// the bias columns and the scales in fp16.  The codes themselves are unpacked
+//   of large matrices (more than kPieceBytes in fp16) for few tiles of tokens by the
+//   product's kernel, again for each tile: the matrix is then read as it is;
+//   else by the operands kernel, once, into rows of P columns too, large matrices a
+//   piece of rows at a time, so that they are read back from the L2.
+// (512 x 2048 x 131072 266 us the first way, 496 the second; 1024 x 2048 x 2560 26.6 and
+// 22.9.)
 //
 // linear_prompt_kernel: pairs of blocks, on two SMs, work on tiles of 256 weight rows
 // by up to 256 tokens (a multiple of 32 picked for even rounds over the pairs) with
 // tcgen05.mma across both: a block holds its 128 rows and half of the tokens, so
 // that each SM fetches 32 KB for 512 cycles of MMA.  (One block alone, 128 rows by
 // 192 to 256 tokens, fetches 40 to 48 KB in the time, more than the 64 bytes a
-// cycle that reach a SM: 4096 x 2048 x 2560 45 us instead of PAIR_MEASURED.)
+// cycle that reach a SM: the product of
+// 4096 x 4096 x 4096 took 99 us so, 90 in pairs.)
 //
 //   warp 0           loads: 64 columns of both operands a stage, 128-byte swizzle;
 //                    both blocks' loads complete on the first one's barrier
 //   warp 1           MMA issue, in the pair's first block; two accumulators in
 //                    tensor memory in turn
+//   warp 3           loads of packed codes, a ring of their own
+//   warps 12-19      unpacking: a thread a row's 64 codes of a stage, two sets of four
+//                    warps in turn
+//   warp 2           tells the pair's first block what was unpacked here: an arrival
+//                    across blocks waits for all of its thread's memory operations
+//                    (done by the unpacking threads, which fetched codes themselves
+//                    then, a stage took 1.1 us)
 //   warps 4-11       epilogue: a lane is a weight row, so that a warp writes 32
 //                    neighbouring results of a token at a time, whatever y's stride;
 //                    powers of two put back
@@ -51,23 +61,31 @@ constexpr int kMaxTok = 256;               // tokens of a tile
 constexpr int kStep = 64;                  // columns of a stage
 constexpr int kMaxStages = 8;
 constexpr int kEpiWarp = 4, kEpiWarps = 8;
-constexpr int kThreads = (kEpiWarp + kEpiWarps) * 32;
+constexpr int kDeqWarp = kEpiWarp + kEpiWarps, kSets = 4, kSetWarps = 4, kDeqWarps = kSets * kSetWarps;
+constexpr int kQ = 8, kQBytes = kRows * kStep / 2;  // stages of packed codes
+constexpr int threads(bool codes) { return (codes ? kDeqWarp + kDeqWarps : kDeqWarp) * 32; }
+constexpr int kFewTiles = 8;               // of tokens, up to which the product's kernel unpacks large matrices
 constexpr int kWBytes = kRows * kStep * 2;
 constexpr int kMaxT = 16384;               // tokens whose operands are held at a time
-constexpr size_t kWeightBytes = 40 << 20;  // of fp16 weights of a piece, about; two are held
+constexpr size_t kPieceBytes = 80 << 20;   // of what is made of the weights for a piece of rows, about
 
-// Columns of an operand's row.
+// Columns of an operand's row: codes up to Kp, then biases.
 struct Columns {
     int K, Kp, groups, P;
-    __host__ __device__ Columns(int K_, int G) : K(K_), Kp((K_ + 63) / 64 * 64), groups(K_ / G), P(Kp + (3 * groups + 63) / 64 * 64) {}
+    int Gp;  // scales of a row in fp16, up to a multiple of 8
+    __host__ __device__ Columns(int K_, int G)
+        : K(K_), Kp((K_ + 63) / 64 * 64), groups(K_ / G), P(Kp + (3 * groups + 63) / 64 * 64), Gp((groups + 7) / 8 * 8) {}
 };
 
 struct Args {
     LinearArgs l;
-    __half *xh, *wh;      // [tokens here][P], [rows of this piece][P]
+    __half *xh;           // [tokens here][P]
+    __half *wh;           // [rows of this piece][P - code_steps 64]
+    __half *sh;           // [rows of this piece][Gp]: scales, where the product unpacks
     int *xe, *we;         // their powers
     int t0, nt, n0, nn;   // tokens and rows of this launch
-    int x_blocks;         // operands: blocks that make tokens (0: not the first piece)
+    int x_blocks;         // operands: blocks that make tokens
+    int code_steps;       // of a tile's steps, the first ones whose weights the product unpacks
     int gshift;           // log2 of the group
     int tok, t_tiles, n_tiles, stages;
 };
@@ -95,19 +113,29 @@ __device__ __forceinline__ void zero_columns(__half *row, int from, int to, int 
     for (int c = from + i; c < to; c += n) row[c] = __float2half_rn(0.f);
 }
 
+// Eight codes times their scale, (q - 8) s, exact.
+__device__ __forceinline__ uint4 unpack8(uint32_t w, __half2 s) {
+    const __half2 c1032 = __half2half2(__ushort_as_half(0x6408));
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        // 1024 + q by a mask-and-set a pair
+        const uint32_t b = mask_set(w >> (4 * j), 0x000F000Fu, 0x64006400u);
+        const __half2 p = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&b), c1032), s);
+        o[j] = *reinterpret_cast<const uint32_t *>(&p);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 constexpr int kOpThreads = 256, kOpRows = kOpThreads / 32;
 constexpr int kHeld = 8;  // of a token's vectors of eight, those that a lane keeps between the passes
 
 // A row a warp: blocks 0 .. x_blocks - 1 tokens, the others weights.
-__global__ void __launch_bounds__(kOpThreads, 4) linear_operands_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kOpThreads, 3) linear_operands_kernel(const __grid_constant__ Args a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Columns c(a.l.K, a.l.G);
     const int ng = c.groups;
-    // A later piece's weights go to the place that the piece before the last one had,
-    // whose product is over: the product that runs now waited for the last piece's
-    // operands, and these (below) for that product.  Nothing else is written
-    const bool first = a.x_blocks > 0;
-    if (first) pdl_wait();
+    pdl_wait();
     pdl_trigger();
     if (static_cast<int>(blockIdx.x) < a.x_blocks) {
         const int t = blockIdx.x * kOpRows + warp, n = c.K / 8;
@@ -165,55 +193,44 @@ __global__ void __launch_bounds__(kOpThreads, 4) linear_operands_kernel(const __
         return;
     }
     const int r = (blockIdx.x - a.x_blocks) * kOpRows + warp;
-    if (r >= a.nn) {
-        if (!first) pdl_wait();
-        return;
-    }
+    if (r >= a.nn) return;
     const int64_t n = a.n0 + r;
     const uint16_t *s = a.l.s + n * a.l.ldg, *z = a.l.b + n * a.l.ldg;
     const uint32_t *q = a.l.q + n * (c.K / 8);
-    __half *row = a.wh + static_cast<int64_t>(r) * c.P;
+    const int codes = c.Kp - a.code_steps * kStep;  // columns of codes here: all or none
+    __half *row = a.wh + static_cast<int64_t>(r) * (codes + c.P - c.Kp), *bias = row + codes;
     float top = 0.f;
     for (int g = lane; g < ng; g += 32) {
         const float sg = bf16_bits_to_float(__ldg(s + g)), cg = bf16_bits_to_float(__ldg(z + g)) + 8.f * sg;
         top = fmaxf(top, fmaxf(8.f * fabsf(sg), 256.f * fabsf(cg)));
     }
     const int up = 14 - power_of(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
-#pragma unroll 4
-    for (int i = lane; i < c.K / 8; i += 32) {
-        const uint32_t w = __ldcs(q + i);
-        const __half2 sg = __half2half2(__float2half_rn(times_power(bf16_bits_to_float(__ldg(s + (i * 8 >> a.gshift))), up)));
-        const __half2 c1032 = __half2half2(__ushort_as_half(0x6408));
-        uint4 o;
-        uint32_t *ow = reinterpret_cast<uint32_t *>(&o);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            // 1024 + q by a mask-and-set a pair
-            const uint32_t b = mask_set(w >> (4 * j), 0x000F000Fu, 0x64006400u);
-            const __half2 p = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&b), c1032), sg);
-            ow[j] = *reinterpret_cast<const uint32_t *>(&p);
-        }
-        reinterpret_cast<uint4 *>(row)[i] = o;
-    }
     for (int g = lane; g < ng; g += 32) {
         const float sg = bf16_bits_to_float(__ldg(s + g)), cg = bf16_bits_to_float(__ldg(z + g)) + 8.f * sg;
         __half c1, c2;
         split(times_power(cg, up) * 256.f, c1, c2);
-        row[c.Kp + g] = c1;
-        row[c.Kp + ng + g] = c1;
-        row[c.Kp + 2 * ng + g] = c2;
+        bias[g] = c1;
+        bias[ng + g] = c1;
+        bias[2 * ng + g] = c2;
+        if (!codes) a.sh[static_cast<int64_t>(r) * c.Gp + g] = __float2half_rn(times_power(sg, up));
+    }
+    zero_columns(bias, 3 * ng, c.P - c.Kp, lane, 32);
+    if (lane == 0) a.we[r] = -up;
+    if (!codes) return;
+#pragma unroll 4
+    for (int i = lane; i < c.K / 8; i += 32) {
+        const __half sg = __float2half_rn(times_power(bf16_bits_to_float(__ldg(s + (i * 8 >> a.gshift))), up));
+        reinterpret_cast<uint4 *>(row)[i] = unpack8(__ldcs(q + i), __half2half2(sg));
     }
     zero_columns(row, c.K, c.Kp, lane, 32);
-    zero_columns(row, c.Kp + 3 * ng, c.P, lane, 32);
-    if (lane == 0) a.we[r] = -up;
-    // this kernel is over when the product before it is
-    if (!first) pdl_wait();
 }
 
 // -------------------------------------------------------------- product
 
 struct Ctl {
     uint64_t full[kMaxStages], empty[kMaxStages];  // (full: of both blocks' loads, in the first one)
+    uint64_t q_full[kQ], q_empty[kQ];              // packed codes
+    uint64_t unpacked[kMaxStages];                 // codes of the stage are in their place
     uint64_t acc_full[2], acc_empty[2];            // (acc_empty: of both, in the first one)
     uint64_t drain;
     uint32_t tmem;
@@ -221,17 +238,21 @@ struct Ctl {
 };
 
 __host__ __device__ constexpr int stage_bytes(int tok) { return kWBytes + tok / 2 * kStep * 2; }
-__host__ __device__ constexpr int stages_for(int tok) {
-    // (8 KB stay free for blocks that unpack the next piece)
-    const int n = (kBlockSmem - 9 * 1024 - static_cast<int>(sizeof(Ctl))) / stage_bytes(tok);
+__host__ __device__ constexpr int fixed_bytes(bool codes) {
+    return 1024 + static_cast<int>(sizeof(Ctl)) + (codes ? kQ * kQBytes : 0);
+}
+__host__ __device__ constexpr int stages_for(int tok, bool codes) {
+    const int n = (kBlockSmem - fixed_bytes(codes)) / stage_bytes(tok);
     return n < kMaxStages ? n : kMaxStages;
 }
-__host__ __device__ constexpr int smem_bytes(int tok) {
+__host__ __device__ constexpr int smem_bytes(int tok, bool codes) {
     // (more than half of a SM's: one block at a time, since each takes all of the tensor memory)
-    const int n = stages_for(tok) * stage_bytes(tok) + 1024 + static_cast<int>(sizeof(Ctl));
+    const int n = stages_for(tok, codes) * stage_bytes(tok) + fixed_bytes(codes);
     return n > kBlockSmem / 2 + 1024 ? n : kBlockSmem / 2 + 1024;
 }
-static_assert(stages_for(kMaxTok) >= 4 && smem_bytes(kMaxTok) <= kBlockSmem && smem_bytes(32) <= kBlockSmem, "stages");
+static_assert(stages_for(kMaxTok, true) >= 4 && smem_bytes(kMaxTok, true) <= kBlockSmem &&
+                  smem_bytes(kMaxTok, false) <= kBlockSmem && smem_bytes(32, true) <= kBlockSmem,
+              "stages");
 
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, const Args &a, Ctl *s, int site) {
     return role_wait(bar, parity, a.l.wait_limit, a.l.status, &s->abort, site);
@@ -249,7 +270,7 @@ __device__ __forceinline__ uint32_t in_first(const void *p) {
     return r;
 }
 __device__ __forceinline__ void pair_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // A box into this block's shared memory, complete on a barrier of the pair.
 __device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1) {
@@ -276,25 +297,101 @@ __device__ __forceinline__ void pair_commit(uint64_t *bar) {
         : "memory");
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+// The unpacking warps' part: set 0 and 1 take a block's stages in turn, a thread its
+// row of 128.
+__device__ __forceinline__ void unpack_role(const Args &a, Ctl *s, uint8_t *base, int stage, int steps, int tiles, int rank,
+                                            int pair, int pairs) {
+    const Columns c(a.l.K, a.l.G);
+    const int set = (threadIdx.x / 32 - kDeqWarp) / kSetWarps, r = (threadIdx.x - kDeqWarp * 32) % kRows, lane = threadIdx.x & 31;
+    const int stages = a.stages;
+    const uint32_t row = smem_u32(base) + r * 128, packed = smem_u32(base) + stages * stage + r * 32, turn = (r >> 2 & 1) << 4;
+    // the set's next stage with codes, whose scales are fetched one ahead: tile and step
+    int next_tile = pair, next_k = set, before = 0;  // (stages of the tiles before, modulo kSets)
+    __half2 ahead = __half2half2(__ushort_as_half(0));
+    auto fetch = [&]() {
+        // (a tile may have fewer stages with codes than there are sets)
+        while (next_k >= a.code_steps && next_tile < tiles) {
+            next_tile += pairs;
+            before = (before + steps) % kSets;
+            next_k = (set - before + kSets) % kSets;
+        }
+        if (next_tile >= tiles) return;
+        const int n = min(next_tile % a.n_tiles * kPairRows + rank * kRows + r, a.nn - 1);
+        const __half *at = a.sh + static_cast<int64_t>(n) * c.Gp + (next_k * kStep >> a.gshift);
+        // (a stage's one or two scales)
+        ahead = a.gshift == 5 ? __ldcg(reinterpret_cast<const __half2 *>(at)) : __half2half2(__ldcg(at));
+        next_k += kSets;
+    };
+    fetch();
+    uint32_t it = 0, nq = 0;  // stages so far, of them with codes
+    bool ok = true;
+    for (int tile = pair; tile < tiles && ok; tile += pairs) {
+        for (int k = 0; k < steps && ok; ++k, ++it) {
+            const bool codes = k < a.code_steps;
+            const uint32_t qi = nq;
+            nq += codes;
+            if (static_cast<int>(it % kSets) != set) continue;
+            const int st = it % stages;
+            if (codes) {
+                const __half2 sg = ahead;
+                fetch();
+                ok = __all_sync(0xffffffffu, wait(&s->q_full[qi % kQ], (qi / kQ) & 1, a, s, 65));
+                if (!ok) break;
+                uint32_t w[8];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[4 * h]), "=r"(w[4 * h + 1]), "=r"(w[4 * h + 2]), "=r"(w[4 * h + 3])
+                                 : "r"(packed + qi % kQ * kQBytes + ((h << 4) ^ turn))
+                                 : "memory");
+                ok = __all_sync(0xffffffffu, wait(&s->empty[st], ((it / stages) & 1) ^ 1, a, s, 66));
+                if (!ok) break;
+                const __half2 s0 = __low2half2(sg), s1 = __high2half2(sg);
+                const bool half_step = k * kStep + kStep > c.K;  // only 32 of the codes are there
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint4 v = j >= 4 && half_step ? make_uint4(0u, 0u, 0u, 0u) : unpack8(w[j], j < 4 ? s0 : s1);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + st * stage + ((j ^ (r & 7)) << 4)), "r"(v.x),
+                                 "r"(v.y), "r"(v.z), "r"(v.w)
+                                 : "memory");
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s->q_empty[qi % kQ]);
+            } else {
+                ok = __all_sync(0xffffffffu, wait(&s->empty[st], ((it / stages) & 1) ^ 1, a, s, 67));
+            }
+            if (ok && lane == 0) mbar_arrive(&s->unpacked[st]);
+        }
+    }
+}
+
+// CODES: the first code_steps steps' weights are unpacked here.
+template <bool CODES>
+__global__ void __launch_bounds__(threads(CODES), 1)
     linear_prompt_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
-                         const __grid_constant__ Args a) {
+                         const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ Args a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int stage = stage_bytes(a.tok), stages = a.stages;
-    Ctl *s = reinterpret_cast<Ctl *>(base + stages * stage);
+    Ctl *s = reinterpret_cast<Ctl *>(base + stages * stage + (CODES ? kQ * kQBytes : 0));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tiles = a.t_tiles * a.n_tiles, steps = Columns(a.l.K, a.l.G).P / kStep;
     const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (tid == 0) {
         for (int i = 0; i < stages; ++i) {
-            mbar_init(&s->full[i], 1);
+            mbar_init(&s->full[i], CODES ? 3 : 1);  // (the loads' and both blocks' unpacking's)
             mbar_init(&s->empty[i], 1);
+            mbar_init(&s->unpacked[i], kSetWarps);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s->acc_full[i], 1);
             mbar_init(&s->acc_empty[i], 2 * kEpiWarps);
+        }
+        for (int i = 0; i < kQ; ++i) {
+            mbar_init(&s->q_full[i], 1);
+            mbar_init(&s->q_empty[i], kSetWarps);
         }
         mbar_init(&s->drain, 1);
         s->abort = 0;
@@ -327,8 +424,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t at = smem_u32(base + st * stage), bar = in_first(&s->full[st]);
                     // (the other block's bytes may come before they are expected: the phase
                     // cannot end before this arrival)
-                    if (rank == 0) mbar_arrive_expect_tx(&s->full[st], 2 * stage);
-                    pair_load_2d(at, &tm_w, bar, k * kStep, n0);
+                    const bool codes = CODES && k < a.code_steps;
+                    if (rank == 0) mbar_arrive_expect_tx(&s->full[st], 2 * (codes ? stage - kWBytes : stage));
+                    if (!codes) pair_load_2d(at, &tm_w, bar, (CODES ? k - a.code_steps : k) * kStep, n0);
                     pair_load_2d(at + kWBytes, &tm_x, bar, k * kStep, t0);
                 }
             }
@@ -367,6 +465,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_drain(&s->drain, 0, a.l.wait_limit);
         }
         __syncwarp();
+    } else if (warp == 2) {
+        if (CODES && elect_one()) {
+            const int total = pair < tiles ? (tiles - pair + pairs - 1) / pairs * steps : 0;
+            for (int it = 0; it < total; ++it) {
+                if (!wait(&s->unpacked[it % stages], (it / stages) & 1, a, s, 68)) break;
+                pair_arrive(in_first(&s->full[it % stages]));
+            }
+        }
+        __syncwarp();
+    } else if (warp == 3) {
+        if (CODES && elect_one()) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int tile = pair; tile < tiles && ok; tile += pairs) {
+                const int n0 = a.n0 + tile % a.n_tiles * kPairRows + rank * kRows;
+                for (int k = 0; k < a.code_steps && ok; ++k, ++it) {
+                    ok = wait(&s->q_empty[it % kQ], ((it / kQ) & 1) ^ 1, a, s, 69);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&s->q_full[it % kQ], kQBytes);
+                    tma_load_2d(base + stages * stage + it % kQ * kQBytes, &tm_q, &s->q_full[it % kQ], k * (kStep / 8), n0);
+                }
+            }
+            for (uint32_t i = it > kQ ? it - kQ : 0; i < it; ++i) mbar_drain(&s->q_full[i % kQ], (i / kQ) & 1, a.l.wait_limit);
+        }
+        __syncwarp();
+    } else if (warp >= kDeqWarp) {
+        if (CODES) unpack_role(a, s, base, stage, steps, tiles, rank, pair, pairs);
     } else if (warp >= kEpiWarp) {
         const int quarter = warp & 3, half = (warp - kEpiWarp) >> 2;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
@@ -377,32 +502,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool ok = __all_sync(0xffffffffu, wait(&s->acc_full[nt & 1], (nt >> 1) & 1, a, s, 64));
             if (!ok) break;
             tc_fence_after();
-            // 32 tokens at a time, the halves in turn; the powers as two factors where they
+            // some tokens at a time, the halves in turn; the powers as two factors where they
             // are near enough to one that neither leaves fp32's range
-            for (int c = half * 32; c < a.tok; c += 64) {
+            constexpr int E = CODES ? 16 : 32;
+            for (int c = half * E; c < a.tok; c += 2 * E) {
                 const int left = a.nt - t0 - c;
                 if (left <= 0) break;
-                uint32_t v[32];
-                tmem_ld32((tmem + (nt & 1) * 256 + c) | lanes, v);
-                const int xe = lane < left ? __ldcg(a.xe + t0 + c + lane) : 0;
+                uint32_t v[E];
+                const uint32_t from = (tmem + (nt & 1) * 256 + c) | lanes;
+                if constexpr (CODES)
+                    tmem_ld16_issue(from, v);
+                else
+                    tmem_ld32(from, v);
+                const int xe = lane < E && lane < left ? __ldcg(a.xe + t0 + c + lane) : 0;
                 const bool near = __all_sync(0xffffffffu, abs(xe) <= 60 && abs(we) <= 60);
                 const float xf = near ? __int_as_float((xe + 127) << 23) : 0.f, wf = __int_as_float(((near ? we : 0) + 127) << 23);
-                tmem_wait32(v);
+                if constexpr (CODES)
+                    tmem_wait16(v);
+                else
+                    tmem_wait32(v);
                 char *at = static_cast<char *>(a.l.y) + ((a.t0 + t0 + c) * a.l.y_stride + a.n0 + n) * (a.l.y_fp32 ? 4 : 2);
                 auto write = [&](auto put) {
-                    if (left >= 32) {
+                    if (left >= E) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) put(j);
+                        for (int j = 0; j < E; ++j) put(j);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
+                        for (int j = 0; j < E; ++j)
                             if (j < left) put(j);
                     }
                 };
                 auto scaled = [&](int j) { return __uint_as_float(v[j]) * __shfl_sync(0xffffffffu, xf, j) * wf; };
                 if (!near) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
+                    for (int j = 0; j < E; ++j) {
                         const int e = max(-250, min(250, we + __shfl_sync(0xffffffffu, xe, j)));
                         if (j < left && n < a.nn) a.l.store(a.t0 + t0 + c + j, a.n0 + n, times_power(__uint_as_float(v[j]), e));
                     }
@@ -441,38 +574,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ----------------------------------------------------------------- host
 
 struct Layout {
-    size_t xe, we, xh, wh, total;
-    size_t we_piece, wh_piece;  // bytes from one piece's place to the other's
-    int rows;                   // weight rows of a piece
+    size_t xe, we, xh, sh, wh, total;
+    int rows;        // weight rows of a piece
+    int code_steps;  // (0: codes are unpacked before the product)
 };
 
 static Layout layout(int N, int K, int G, int T) {
     auto up = [](size_t n) { return (n + 1023) / 1024 * 1024; };
-    const size_t P = Columns(K, G).P;
+    const Columns c(K, G);
     Layout L{};
-    const size_t most = std::max<size_t>(kWeightBytes / (P * 2) / kPairRows * kPairRows, kPairRows);
+    L.code_steps = T <= kFewTiles * kMaxTok && static_cast<size_t>(N) * c.P * sizeof(__half) > kPieceBytes ? c.Kp / kStep : 0;
+    const size_t width = (c.P - L.code_steps * kStep) * sizeof(__half);  // of a row of wh
+    const size_t most = std::max<size_t>(kPieceBytes / width / kPairRows * kPairRows, kPairRows);
     L.rows = static_cast<int>(std::min<size_t>(N, most));
-    const size_t places = N > L.rows ? 2 : 1;
-    L.we_piece = up(L.rows * sizeof(int));
-    L.wh_piece = up(L.rows * P * 2);
     L.xe = kCtrlBytes;
     L.we = L.xe + up(std::min(T, kMaxT) * sizeof(int));
-    L.xh = L.we + places * L.we_piece;
-    L.wh = L.xh + up(std::min(T, kMaxT) * P * 2);
-    L.total = L.wh + places * L.wh_piece;
+    L.xh = L.we + up(L.rows * sizeof(int));
+    L.sh = L.xh + up(std::min(T, kMaxT) * static_cast<size_t>(c.P) * sizeof(__half));
+    L.wh = L.sh + (L.code_steps ? up(L.rows * static_cast<size_t>(c.Gp) * sizeof(__half)) : 0);
+    L.total = L.wh + L.rows * width;
     return L;
-}
-
-// Lets blocks of the operands kernel run on SMs that the product's have: only kernels
-// with the same division of shared memory and L1 run on one together.
-static cudaError_t beside_product() {
-    static std::atomic<bool> done[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_acquire))) return e;
-    e = cudaFuncSetAttribute(linear_operands_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-    if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_release);
-    return e;
 }
 
 // Tokens of a tile: as many as make the rounds over the pairs of SMs cheapest, a
@@ -495,7 +616,11 @@ static int tile_tokens(int N, int T, int pairs) {
 
 }  // namespace prompt
 
-size_t linear_prompt_workspace_bytes(int N, int K, int G, int T) { return prompt::layout(N, K, G, T).total; }
+// (a call of fewer tokens may take the way that needs more)
+size_t linear_prompt_workspace_bytes(int N, int K, int G, int T) {
+    const size_t few = prompt::layout(N, K, G, std::min(T, prompt::kFewTiles * prompt::kMaxTok)).total;
+    return std::max(few, prompt::layout(N, K, G, T).total);
+}
 
 cudaError_t launch_linear_prompt(const LinearArgs &l, LinearMap encode, void *ws, int num_sms, cudaStream_t s) {
     using namespace prompt;
@@ -507,31 +632,34 @@ cudaError_t launch_linear_prompt(const LinearArgs &l, LinearMap encode, void *ws
     a.gshift = l.G == 32 ? 5 : l.G == 64 ? 6 : 7;
     a.xe = reinterpret_cast<int *>(w + L.xe);
     a.xh = reinterpret_cast<__half *>(w + L.xh);
-    cudaError_t e = allow_smem<linear_prompt_kernel>();
+    const auto kernel = L.code_steps ? linear_prompt_kernel<true> : linear_prompt_kernel<false>;
+    cudaError_t e = L.code_steps ? allow_smem<linear_prompt_kernel<true>>() : allow_smem<linear_prompt_kernel<false>>();
     if (e != cudaSuccess) return e;
-    if (l.N > L.rows && (e = beside_product()) != cudaSuccess) return e;
+    a.we = reinterpret_cast<int *>(w + L.we);
+    a.sh = reinterpret_cast<__half *>(w + L.sh);
+    a.wh = reinterpret_cast<__half *>(w + L.wh);
+    a.code_steps = L.code_steps;
     for (a.t0 = 0; a.t0 < l.B; a.t0 += kMaxT) {
         a.nt = std::min(l.B - a.t0, kMaxT);
-        int place = 0;
-        for (a.n0 = 0; a.n0 < l.N; a.n0 += L.rows, place ^= 1) {
+        for (a.n0 = 0; a.n0 < l.N; a.n0 += L.rows) {
             a.nn = std::min(l.N - a.n0, L.rows);
-            a.we = reinterpret_cast<int *>(w + L.we + place * L.we_piece);
-            a.wh = reinterpret_cast<__half *>(w + L.wh + place * L.wh_piece);
             a.x_blocks = a.n0 ? 0 : (a.nt + kOpRows - 1) / kOpRows;
             const int w_blocks = (a.nn + kOpRows - 1) / kOpRows;
             if ((e = launch_dependent(linear_operands_kernel, dim3(a.x_blocks + w_blocks), dim3(kOpThreads), 0, s, a)) != cudaSuccess)
                 return e;
             a.tok = tile_tokens(a.nn, a.nt, num_sms / 2);
-            a.stages = stages_for(a.tok);
+            a.stages = stages_for(a.tok, a.code_steps > 0);
             a.n_tiles = (a.nn + kPairRows - 1) / kPairRows;
             a.t_tiles = (a.nt + a.tok - 1) / a.tok;
-            CUtensorMap mw, mx;
-            if (!encode(&mw, a.wh, c.P, a.nn, kStep, kRows) || !encode(&mx, a.xh, c.P, a.nt, kStep, a.tok / 2))
+            CUtensorMap mw, mx, mq;
+            if (!encode(&mw, a.wh, true, c.P - a.code_steps * kStep, a.nn, kStep, kRows) ||
+                !encode(&mx, a.xh, true, c.P, a.nt, kStep, a.tok / 2) ||
+                !encode(&mq, l.q, false, c.K / 8, l.N, kStep / 8, kRows))
                 return cudaErrorInvalidValue;
             cudaLaunchConfig_t cfg{};
             cfg.gridDim = dim3(2 * std::min(a.n_tiles * a.t_tiles, num_sms / 2));
-            cfg.blockDim = dim3(kThreads);
-            cfg.dynamicSmemBytes = smem_bytes(a.tok);
+            cfg.blockDim = dim3(threads(a.code_steps > 0));
+            cfg.dynamicSmemBytes = smem_bytes(a.tok, a.code_steps > 0);
             cfg.stream = s;
             cudaLaunchAttribute attr[2];
             attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -541,7 +669,7 @@ cudaError_t launch_linear_prompt(const LinearArgs &l, LinearMap encode, void *ws
             attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
             cfg.attrs = attr;
             cfg.numAttrs = 2;
-            if ((e = cudaLaunchKernelEx(&cfg, linear_prompt_kernel, mw, mx, a)) != cudaSuccess) return e;
+            if ((e = cudaLaunchKernelEx(&cfg, kernel, mw, mx, mq, a)) != cudaSuccess) return e;
         }
     }
     return cudaSuccess;

@@ -170,3 +170,32 @@ def test_linear_prompt_smaller_call_in_a_larger_workspace():
         x = randn(g, T, 256)
         got = moe.linear_prompt(m, x.cuda(), dtype=torch.float32, ws=ws).cpu().double()
         assert ((got - x.double() @ w.t()).abs() <= bound(x, w, 256)).all()
+
+
+@pytest.mark.parametrize("T,K,N,G", [(130, 96, 440000, 32), (257, 64, 330000, 64), (700, 1152, 40000, 128),
+                                     (129, 2080, 20000, 32), (2048, 256, 131000, 64), (300, 4096, 10300, 128),
+                                     (2049, 576, 70000, 64), (150, 32, 330100, 32)])
+def test_linear_prompt_of_large_matrices(T, K, N, G):
+    """More fp16 weights than are held at a time: unpacked by the product's kernel for
+    up to 2048 tokens, in pieces of rows for more; few and odd numbers of steps."""
+    g = torch.Generator(device="cuda").manual_seed(T + N)
+    codes = torch.randint(-2 ** 31, 2 ** 31, (N, K // 8), generator=g, device="cuda", dtype=torch.int32)
+    s = (torch.rand(N, K // G, generator=g, device="cuda") * 0.01 + 0.001).to(torch.bfloat16)
+    z = (torch.randn(N, K // G, generator=g, device="cuda") * 0.03).to(torch.bfloat16)
+    pad = (0, moe.ld_groups(K, G) - K // G)
+    m = moe.QMatrix(codes, torch.nn.functional.pad(s, pad).view(torch.int16), torch.nn.functional.pad(z, pad).view(torch.int16),
+                    N, K, G)
+    x = torch.randn(T, K, generator=g, device="cuda").to(torch.bfloat16)
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    got = moe.linear_prompt(m, x, dtype=torch.float32, status=status)
+    assert _lib.moe_read_device_status(status) == 0
+    assert torch.equal(got, moe.linear_prompt(m, x, dtype=torch.float32))
+    # rows here and there, and the last ones
+    rows = torch.cat((torch.arange(0, N, 997), torch.arange(max(0, N - 600), N))).cuda()
+    words = codes[rows].long() & 0xFFFFFFFF
+    q = torch.empty(len(rows), K, dtype=torch.float64, device="cuda")
+    for e in range(8):
+        q[:, e::8] = ((words >> (4 * (e // 2 + 4 * (e % 2)))) & 15).double()
+    w = q * s[rows].double().repeat_interleave(G, 1) + z[rows].double().repeat_interleave(G, 1)
+    want = x.double() @ w.t()
+    assert ((got[:, rows].double() - want).abs() <= bound(x, w, K)).all()
