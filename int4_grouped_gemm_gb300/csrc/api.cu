@@ -1024,17 +1024,7 @@ int int4_linear_prompt(const moe_qweight *w, int32_t N, int32_t K, int32_t group
     if (ws_bytes < linear_prompt_workspace_bytes(N, K, group, T)) return MOE_ERR_WORKSPACE;
     DeviceInfo *dev = nullptr;
     if ((rc = current_device(dev))) return rc;
-    // (up to here two calls for few tokens are as fast: 65 x 2048 x 2560 16.4 us, 129 tokens
-    // the other way 17.7)
-    if (T <= 2 * kLinearMaxB) {
-        LinearArgs b = a;
-        a.B = (T + 1) / 2;
-        b.B = T - a.B;
-        b.x += a.B * x_stride;
-        b.y = static_cast<char *>(b.y) + a.B * y_stride * (y_fp32 ? 4 : 2);
-        if ((rc = linear_run(a, dev, stream)) || !b.B) return rc;
-        return linear_run(b, dev, stream);
-    }
+    if (T <= kLinearMaxB) return linear_run(a, dev, stream);
     const LinearMap encode = [](CUtensorMap *map, const void *ptr, bool half, int inner, int rows, int box_inner, int box_rows) {
         return encode_2d(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32, half ? 2 : 4, ptr, inner,
                          rows, box_inner, box_rows, half ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_32B) == MOE_OK;

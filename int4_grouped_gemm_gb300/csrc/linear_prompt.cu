@@ -33,14 +33,17 @@
 //   warp 0           loads: 64 columns of both operands a stage, 128-byte swizzle;
 //                    both blocks' loads complete on the first one's barrier
 //   warp 1           MMA issue, in the pair's first block; two accumulators in
-//                    tensor memory in turn
+//                    tensor memory, a tile each in turn.  The MMA cuts sums off towards
+//                    zero, which adds up: 2e-6 of y over 2176 columns, proportional to
+//                    their number.  fp32 results are therefore summed over at most
+//                    kChunk stages at a time: the first chunk stays in one accumulator,
+//                    to which the epilogue's warps add the others, rounded, as they
+//                    come from the other one (7e-7 of y)
 //   warp 3           loads of packed codes, a ring of their own
-//   warps 12-19      unpacking: a thread a row's 64 codes of a stage, two sets of four
+//   warps 12-27      unpacking: a thread a row's 64 codes of a stage, four sets of four
 //                    warps in turn
-//   warp 2           tells the pair's first block what was unpacked here: an arrival
-//                    across blocks waits for all of its thread's memory operations
-//                    (done by the unpacking threads, which fetched codes themselves
-//                    then, a stage took 1.1 us)
+//   warp 2           tells the pair's first block what was unpacked here (of block
+//                    scope; a release of cluster scope took 0.6 us for each stage)
 //   warps 4-11       epilogue: a lane is a weight row, so that a warp writes 32
 //                    neighbouring results of a token at a time, whatever y's stride;
 //                    powers of two put back
@@ -60,6 +63,7 @@ constexpr int kPairRows = 2 * kRows;
 constexpr int kMaxTok = 256;               // tokens of a tile
 constexpr int kStep = 64;                  // columns of a stage
 constexpr int kMaxStages = 8;
+constexpr int kChunk = 13;                 // stages that are summed by MMAs alone, for fp32 results
 constexpr int kEpiWarp = 4, kEpiWarps = 8;
 constexpr int kDeqWarp = kEpiWarp + kEpiWarps, kSets = 4, kSetWarps = 4, kDeqWarps = kSets * kSetWarps;
 constexpr int kQ = 8, kQBytes = kRows * kStep / 2;  // stages of packed codes
@@ -88,6 +92,7 @@ struct Args {
     int code_steps;       // of a tile's steps, the first ones whose weights the product unpacks
     int gshift;           // log2 of the group
     int tok, t_tiles, n_tiles, stages;
+    int chunk;            // stages of a chunk; all of a tile's: no chunks
 };
 
 // ------------------------------------------------------------- operands
@@ -297,14 +302,30 @@ __device__ __forceinline__ void pair_commit(uint64_t *bar) {
         : "memory");
 }
 
-// The unpacking warps' part: set 0 and 1 take a block's stages in turn, a thread its
+// A role's place in the ring of stages.  (By division of a count by the number of
+// stages, which is not a constant, the roles' instructions were twice as many.)
+struct Ring {
+    int at = 0;
+    uint32_t phase = 0;
+
+    __device__ __forceinline__ void advance(int by, int stages) {
+        if ((at += by) >= stages) {
+            at -= stages;
+            phase ^= 1;
+        }
+    }
+};
+
+// The unpacking warps' part: the sets take a block's stages in turn, a thread its
 // row of 128.
 __device__ __forceinline__ void unpack_role(const Args &a, Ctl *s, uint8_t *base, int stage, int steps, int tiles, int rank,
                                             int pair, int pairs) {
     const Columns c(a.l.K, a.l.G);
     const int set = (threadIdx.x / 32 - kDeqWarp) / kSetWarps, r = (threadIdx.x - kDeqWarp * 32) % kRows, lane = threadIdx.x & 31;
     const int stages = a.stages;
-    const uint32_t row = smem_u32(base) + r * 128, packed = smem_u32(base) + stages * stage + r * 32, turn = (r >> 2 & 1) << 4;
+    // (16-byte piece j of the row at j ^ (r % 8) of its 128 bytes)
+    const uint32_t row = smem_u32(base) + r * 128 + ((r & 7) << 4);
+    const uint32_t packed = smem_u32(base) + stages * stage + r * 32 + ((r >> 2 & 1) << 4);
     // the set's next stage with codes, whose scales are fetched one ahead: tile and step
     int next_tile = pair, next_k = set, before = 0;  // (stages of the tiles before, modulo kSets)
     __half2 ahead = __half2half2(__ushort_as_half(0));
@@ -323,45 +344,53 @@ __device__ __forceinline__ void unpack_role(const Args &a, Ctl *s, uint8_t *base
         next_k += kSets;
     };
     fetch();
-    uint32_t it = 0, nq = 0;  // stages so far, of them with codes
+    Ring ring;
+    ring.advance(set, stages);
+    uint32_t codes_before = 0;  // stages with codes of the tiles before
     bool ok = true;
-    for (int tile = pair; tile < tiles && ok; tile += pairs) {
-        for (int k = 0; k < steps && ok; ++k, ++it) {
-            const bool codes = k < a.code_steps;
-            const uint32_t qi = nq;
-            nq += codes;
-            if (static_cast<int>(it % kSets) != set) continue;
-            const int st = it % stages;
-            if (codes) {
-                const __half2 sg = ahead;
-                fetch();
-                ok = __all_sync(0xffffffffu, wait(&s->q_full[qi % kQ], (qi / kQ) & 1, a, s, 65));
-                if (!ok) break;
-                uint32_t w[8];
+    int k = set;
+    for (int tile = pair; tile < tiles && ok; tile += pairs, codes_before += a.code_steps, k -= steps) {
+        for (; k < a.code_steps; k += kSets, ring.advance(kSets, stages)) {
+            const __half2 sg = ahead;
+            fetch();
+            const uint32_t qi = codes_before + k;
+            ok = __all_sync(0xffffffffu, wait(&s->q_full[qi % kQ], (qi / kQ) & 1, a, s, 65));
+            if (!ok) break;
+            uint32_t w[8];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(w[4 * h]), "=r"(w[4 * h + 1]), "=r"(w[4 * h + 2]), "=r"(w[4 * h + 3])
-                                 : "r"(packed + qi % kQ * kQBytes + ((h << 4) ^ turn))
-                                 : "memory");
-                ok = __all_sync(0xffffffffu, wait(&s->empty[st], ((it / stages) & 1) ^ 1, a, s, 66));
-                if (!ok) break;
-                const __half2 s0 = __low2half2(sg), s1 = __high2half2(sg);
-                const bool half_step = k * kStep + kStep > c.K;  // only 32 of the codes are there
+            for (int h = 0; h < 2; ++h)
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[4 * h]), "=r"(w[4 * h + 1]), "=r"(w[4 * h + 2]), "=r"(w[4 * h + 3])
+                             : "r"((packed + qi % kQ * kQBytes) ^ (h << 4))
+                             : "memory");
+            ok = __all_sync(0xffffffffu, wait(&s->empty[ring.at], ring.phase ^ 1, a, s, 66));
+            if (!ok) break;
+            const __half2 s0 = __low2half2(sg), s1 = __high2half2(sg);
+            const uint32_t to = row + ring.at * stage;
+            auto put = [&](int j, const uint4 &v) {
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to ^ (j << 4)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                             : "memory");
+            };
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint4 v = j >= 4 && half_step ? make_uint4(0u, 0u, 0u, 0u) : unpack8(w[j], j < 4 ? s0 : s1);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + st * stage + ((j ^ (r & 7)) << 4)), "r"(v.x),
-                                 "r"(v.y), "r"(v.z), "r"(v.w)
-                                 : "memory");
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s->q_empty[qi % kQ]);
+            for (int j = 0; j < 4; ++j) put(j, unpack8(w[j], s0));
+            if (k * kStep + kStep <= c.K) {
+#pragma unroll
+                for (int j = 4; j < 8; ++j) put(j, unpack8(w[j], s1));
             } else {
-                ok = __all_sync(0xffffffffu, wait(&s->empty[st], ((it / stages) & 1) ^ 1, a, s, 67));
+                // only 32 of the codes are there
+#pragma unroll
+                for (int j = 4; j < 8; ++j) put(j, make_uint4(0u, 0u, 0u, 0u));
             }
-            if (ok && lane == 0) mbar_arrive(&s->unpacked[st]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&s->q_empty[qi % kQ]);
+                mbar_arrive(&s->unpacked[ring.at]);
+            }
+        }
+        for (; k < steps && ok; k += kSets, ring.advance(kSets, stages)) {
+            ok = __all_sync(0xffffffffu, wait(&s->empty[ring.at], ring.phase ^ 1, a, s, 67));
+            if (ok && lane == 0) mbar_arrive(&s->unpacked[ring.at]);
         }
     }
 }
@@ -413,51 +442,68 @@ __global__ void __launch_bounds__(threads(CODES), 1)
 
     if (warp == 0) {
         if (elect_one()) {
-            uint32_t it = 0;
+            Ring ring;
+            int loaded = 0;
             bool ok = true;
             for (int tile = pair; tile < tiles && ok; tile += pairs) {
                 const int n0 = tile % a.n_tiles * kPairRows + rank * kRows, t0 = tile / a.n_tiles * a.tok + rank * (a.tok / 2);
-                for (int k = 0; k < steps && ok; ++k, ++it) {
-                    const int st = it % stages;
-                    ok = wait(&s->empty[st], ((it / stages) & 1) ^ 1, a, s, 61);
+                for (int k = 0; k < steps; ++k, ring.advance(1, stages)) {
+                    ok = wait(&s->empty[ring.at], ring.phase ^ 1, a, s, 61);
                     if (!ok) break;
-                    const uint32_t at = smem_u32(base + st * stage), bar = in_first(&s->full[st]);
+                    const uint32_t at = smem_u32(base + ring.at * stage), bar = in_first(&s->full[ring.at]);
                     // (the other block's bytes may come before they are expected: the phase
                     // cannot end before this arrival)
                     const bool codes = CODES && k < a.code_steps;
-                    if (rank == 0) mbar_arrive_expect_tx(&s->full[st], 2 * (codes ? stage - kWBytes : stage));
+                    if (rank == 0) mbar_arrive_expect_tx(&s->full[ring.at], 2 * (codes ? stage - kWBytes : stage));
                     if (!codes) pair_load_2d(at, &tm_w, bar, (CODES ? k - a.code_steps : k) * kStep, n0);
                     pair_load_2d(at + kWBytes, &tm_x, bar, k * kStep, t0);
+                    loaded = min(loaded + 1, stages);
                 }
             }
             // no copy of this block is in flight when it ends: the MMAs that read the last
             // ones are complete, or two milliseconds have passed for each
-            for (uint32_t i = it > static_cast<uint32_t>(stages) ? it - stages : 0; i < it; ++i)
-                mbar_wait(&s->empty[i % stages], (i / stages) & 1, 1 << 22);
+            ring.at -= loaded;
+            if (ring.at < 0) {
+                ring.at += stages;
+                ring.phase ^= 1;
+            }
+            for (; loaded; --loaded, ring.advance(1, stages)) mbar_wait(&s->empty[ring.at], ring.phase, 1 << 22);
         }
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
             const uint32_t idesc = idesc_f16(a.tok);
-            uint32_t it = 0, nt = 0;
+            Ring ring;
+            uint32_t nt = 0;
             bool ok = true;
+            const bool chunks = a.chunk < steps;
+            uint32_t nc = 0;  // chunks that went to the second accumulator
             for (int tile = pair; tile < tiles && ok; tile += pairs, ++nt) {
-                const uint32_t acc = tmem + (nt & 1) * 256;
-                ok = wait(&s->acc_empty[nt & 1], ((nt >> 1) & 1) ^ 1, a, s, 62);
+                const uint32_t which = chunks ? 0 : nt & 1, uses = chunks ? nt : nt >> 1;
+                uint32_t acc = tmem + which * 256;
+                ok = wait(&s->acc_empty[which], (uses & 1) ^ 1, a, s, 62);
                 if (!ok) break;
                 tc_fence_after();
-                for (int k = 0; k < steps; ++k, ++it) {
-                    const int st = it % stages;
-                    ok = wait(&s->full[st], (it / stages) & 1, a, s, 63);
+                for (int k = 0, in_chunk = 0; k < steps; ++k, ++in_chunk, ring.advance(1, stages)) {
+                    if (in_chunk == a.chunk) {
+                        if (k > a.chunk) pair_commit(&s->acc_full[1]);
+                        in_chunk = 0;
+                        acc = tmem + 256;
+                        ok = wait(&s->acc_empty[1], (nc & 1) ^ 1, a, s, 70);
+                        ++nc;
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    ok = wait(&s->full[ring.at], ring.phase, a, s, 63);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t w_at = smem_u32(base) + st * stage, x_at = w_at + kWBytes;
+                    const uint32_t w_at = smem_u32(base) + ring.at * stage, x_at = w_at + kWBytes;
 #pragma unroll
                     for (int j = 0; j < kStep / 16; ++j)
-                        pair_mma(acc, sdesc_k128(w_at + j * 32), sdesc_k128(x_at + j * 32), idesc, k | j);
-                    pair_commit(&s->empty[st]);
+                        pair_mma(acc, sdesc_k128(w_at + j * 32), sdesc_k128(x_at + j * 32), idesc, in_chunk | j);
+                    pair_commit(&s->empty[ring.at]);
                 }
-                if (ok) pair_commit(&s->acc_full[nt & 1]);
+                if (ok) pair_commit(&s->acc_full[chunks ? 1 : which]);
             }
             // every MMA issued here is complete before tensor memory is freed
             asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&s->drain))
@@ -467,10 +513,10 @@ __global__ void __launch_bounds__(threads(CODES), 1)
         __syncwarp();
     } else if (warp == 2) {
         if (CODES && elect_one()) {
-            const int total = pair < tiles ? (tiles - pair + pairs - 1) / pairs * steps : 0;
-            for (int it = 0; it < total; ++it) {
-                if (!wait(&s->unpacked[it % stages], (it / stages) & 1, a, s, 68)) break;
-                pair_arrive(in_first(&s->full[it % stages]));
+            Ring ring;
+            for (int left = pair < tiles ? (tiles - pair + pairs - 1) / pairs * steps : 0; left; --left, ring.advance(1, stages)) {
+                if (!wait(&s->unpacked[ring.at], ring.phase, a, s, 68)) break;
+                pair_arrive(in_first(&s->full[ring.at]));
             }
         }
         __syncwarp();
@@ -495,32 +541,68 @@ __global__ void __launch_bounds__(threads(CODES), 1)
     } else if (warp >= kEpiWarp) {
         const int quarter = warp & 3, half = (warp - kEpiWarp) >> 2;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        uint32_t nt = 0;
+        const bool chunks = a.chunk < steps;
+        constexpr int E = CODES ? 16 : 32;
+        auto load = [&](uint32_t from, uint32_t (&v)[E]) {
+            if constexpr (CODES)
+                tmem_ld16_issue(from | lanes, v);
+            else
+                tmem_ld32(from | lanes, v);
+        };
+        auto loaded = [&](uint32_t (&v)[E]) {
+            if constexpr (CODES)
+                tmem_wait16(v);
+            else
+                tmem_wait32(v);
+        };
+        uint32_t nt = 0, nc = 0;
+        bool ok = true;
         for (int tile = pair; tile < tiles; tile += pairs, ++nt) {
             const int n = tile % a.n_tiles * kPairRows + rank * kRows + quarter * 32 + lane, t0 = tile / a.n_tiles * a.tok;
             const int we = n < a.nn ? __ldcg(a.we + n) : 0;
-            const bool ok = __all_sync(0xffffffffu, wait(&s->acc_full[nt & 1], (nt >> 1) & 1, a, s, 64));
+            // all chunks but the last one: added to the first
+            for (int k = 2 * a.chunk; chunks && k < steps && ok; k += a.chunk, ++nc) {
+                ok = __all_sync(0xffffffffu, wait(&s->acc_full[1], nc & 1, a, s, 71));
+                if (!ok) break;
+                tc_fence_after();
+                for (int c = half * E; c < a.tok; c += 2 * E) {
+                    uint32_t v[E], u[E];
+                    load(tmem + c, v);
+                    load(tmem + 256 + c, u);
+                    loaded(v);
+                    loaded(u);
+#pragma unroll
+                    for (int j = 0; j < E; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(u[j]));
+#pragma unroll
+                    for (int j = 0; j < E; j += 16) tmem_st16((tmem + c + j) | lanes, v + j);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) pair_arrive(in_first(&s->acc_empty[1]));
+            }
+            if (!ok) break;
+            const uint32_t which = chunks ? 1 : nt & 1;
+            ok = __all_sync(0xffffffffu, wait(&s->acc_full[which], (chunks ? nc++ : nt >> 1) & 1, a, s, 64));
             if (!ok) break;
             tc_fence_after();
             // some tokens at a time, the halves in turn; the powers as two factors where they
             // are near enough to one that neither leaves fp32's range
-            constexpr int E = CODES ? 16 : 32;
             for (int c = half * E; c < a.tok; c += 2 * E) {
                 const int left = a.nt - t0 - c;
                 if (left <= 0) break;
-                uint32_t v[E];
-                const uint32_t from = (tmem + (nt & 1) * 256 + c) | lanes;
-                if constexpr (CODES)
-                    tmem_ld16_issue(from, v);
-                else
-                    tmem_ld32(from, v);
+                uint32_t v[E], u[E];
+                load(tmem + (nt & 1 && !chunks ? 256 : 0) + c, v);
+                if (chunks) load(tmem + 256 + c, u);
                 const int xe = lane < E && lane < left ? __ldcg(a.xe + t0 + c + lane) : 0;
                 const bool near = __all_sync(0xffffffffu, abs(xe) <= 60 && abs(we) <= 60);
                 const float xf = near ? __int_as_float((xe + 127) << 23) : 0.f, wf = __int_as_float(((near ? we : 0) + 127) << 23);
-                if constexpr (CODES)
-                    tmem_wait16(v);
-                else
-                    tmem_wait32(v);
+                loaded(v);
+                if (chunks) {
+                    loaded(u);
+#pragma unroll
+                    for (int j = 0; j < E; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(u[j]));
+                }
                 char *at = static_cast<char *>(a.l.y) + ((a.t0 + t0 + c) * a.l.y_stride + a.n0 + n) * (a.l.y_fp32 ? 4 : 2);
                 auto write = [&](auto put) {
                     if (left >= E) {
@@ -557,7 +639,10 @@ __global__ void __launch_bounds__(threads(CODES), 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) pair_arrive(in_first(&s->acc_empty[nt & 1]));
+            if (lane == 0) {
+                pair_arrive(in_first(&s->acc_empty[which]));
+                if (chunks) pair_arrive(in_first(&s->acc_empty[0]));
+            }
         }
     }
 
@@ -650,6 +735,8 @@ cudaError_t launch_linear_prompt(const LinearArgs &l, LinearMap encode, void *ws
             a.tok = tile_tokens(a.nn, a.nt, num_sms / 2);
             a.stages = stages_for(a.tok, a.code_steps > 0);
             a.n_tiles = (a.nn + kPairRows - 1) / kPairRows;
+            const int steps = c.P / kStep, parts = l.y_fp32 ? (steps + kChunk - 1) / kChunk : 1;
+            a.chunk = (steps + parts - 1) / parts;
             a.t_tiles = (a.nt + a.tok - 1) / a.tok;
             CUtensorMap mw, mx, mq;
             if (!encode(&mw, a.wh, true, c.P - a.code_steps * kStep, a.nn, kStep, kRows) ||
