@@ -49,6 +49,7 @@ constexpr int kThreads = 11 * 32;
 constexpr int kDiag = 3;                 // tiles that a block's own tokens (at most 256) lie in
 constexpr int kItems = 4;                // blocks that the loads may be ahead
 constexpr int kSwitch = 1;               // what changing blocks counts, in tiles
+constexpr int kAhead = 4;                // sequences whose lengths a lane fetches together
 
 // A piece's part of a block: tiles t .. t + n - 1 (n = 0: no more).
 struct Item {
@@ -60,55 +61,39 @@ struct Item {
     int any_broken;
 };
 
-struct PromptCtl {
-    uint64_t kv_full[kStages], kv_empty[kStages];
-    uint64_t item_full[kItems], item_empty[kItems];
-    uint64_t q_full[2], q_empty[2];  // the slot's queries of the block
-    uint64_t s_full[2];      // scores of the slot's tile are in tensor memory
-    uint64_t p_full[2][2];   // weights of its positions 0-63, 64-127 are (and O is ready to be added to)
-    uint64_t o_full[2];      // O of the block of rows is complete
-    uint64_t token[2];       // the slot's issuer may go on
-    uint64_t drain;
-    Item items[kItems];
-    int64_t sums[kThreads / 32];
-    int64_t found_at;        // where the piece's sequence begins in the list
-    int found;               // the sequence
-    uint32_t tmem;
-    int abort;
-};
-
-__host__ __device__ constexpr int prompt_smem_bytes(int D) {
-    return 2 * kRows * D * 2 + kStages * tile_bytes(D) + 1024 + static_cast<int>(sizeof(PromptCtl));
-}
-static_assert(prompt_smem_bytes(128) <= kBlockSmem, "one block per SM");
-
 // ------------------------------------------------------------------ list
 
 __device__ __forceinline__ int tiles_of(int positions) { return (positions + kPos - 1) / kPos; }
 
-// sum_{i < n} floor((a i + b) / m), by the Euclidean algorithm on (a, m).
-__device__ __forceinline__ int64_t floor_sum(int64_t n, uint32_t m, uint32_t a, uint32_t b) {
-    int64_t sum = 0;
-    for (;;) {
-        sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
-        a %= m;
-        b %= m;
-        const uint64_t y = static_cast<uint64_t>(a) * n + b;
-        if (y < m) return sum;
-        n = static_cast<int64_t>(y / m);
-        b = static_cast<uint32_t>(y % m);
-        const uint32_t t = m;
-        m = a;
-        a = t;
-    }
+// sum_{i < n} floor((a i + b) / 128): the terms' own sum less their remainders'.  Those
+// come back after 128 / g terms, g the largest power of two in a (128 at most), and are
+// then b mod g and its steps of g, each once; what is left is at most 63 terms for an
+// even a.
+__device__ __forceinline__ int64_t floor_sum(int n, int a, int64_t b) {
+    static_assert(kPos == 128, "the divisor");
+    const int log_g = min(__ffs(a) - 1, 7), g = 1 << log_g, period = 128 >> log_g;
+    const int once = period * static_cast<int>(b & (g - 1)) + g * (period * (period - 1) / 2);
+    int some = 0, at = static_cast<int>(b & 127);
+#pragma unroll 4
+    for (int left = n & (period - 1); left > 0; --left, at += a) some += at & 127;
+    const int64_t rest = static_cast<int64_t>(n >> (7 - log_g)) * once + some;
+    return (static_cast<int64_t>(n) * (n - 1) / 2 * a + b * n - rest) >> 7;
+}
+
+// a / b for a >= 0, b > 0 (nearly always of 32 bits, whose division is far quicker).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
 }
 
 // A sequence's rows; none for padding and for what is out of range.
 struct Seq {
     int row0, n, pos0;
 
-    __device__ __forceinline__ Seq(const PromptArgs &a, int b) : row0(0), n(0), pos0(0) {
-        const int r0 = __ldcg(a.q_start + b), r1 = __ldcg(a.q_start + b + 1), len = __ldcg(a.seq_len + b);
+    __device__ __forceinline__ Seq() : row0(0), n(0), pos0(0) {}
+    __device__ __forceinline__ Seq(const PromptArgs &a, int b)
+        : Seq(a, __ldcg(a.q_start + b), __ldcg(a.q_start + b + 1), __ldcg(a.seq_len + b)) {}
+    __device__ __forceinline__ Seq(const PromptArgs &a, int r0, int r1, int len) : row0(0), n(0), pos0(0) {
         if (r0 < 0 || r1 < r0 || r1 > a.T || len > static_cast<int64_t>(a.table_ld) << a.c.page_shift) {
             record_status(a.status, MOE_ERR_PAGE);
         } else if (len >= 0) {
@@ -128,95 +113,35 @@ struct Seq {
         const int span = 2 * a.tq, nb = blocks(span), prefix = tiles_of(a.prefix_len);
         int64_t sum = 0;
         if (j == nb && nb > 0) sum = kSwitch + tiles(a, --j);
+        if (j == 0) return sum;
         const int none = pos0 >= 0 ? 0 : min(j, -pos0 / span);  // blocks before the first position
         return sum + static_cast<int64_t>(j) * (kSwitch + prefix) + (prefix ? 0 : none) +
-               floor_sum(j - none, kPos, span, pos0 + (none + 1) * span + kPos - 1);
+               floor_sum(j - none, span, pos0 + (none + 1) * static_cast<int64_t>(span) + kPos - 1);
     }
 };
 
-// Inclusive sum over the block's threads; `total` gets the sum of all.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *sums, int64_t &total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int i = 1; i < 32; i <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, v, i);
-        if (lane >= i) v += o;
-    }
-    __syncthreads();  // the last call's sums have been read
-    if (lane == 31) sums[warp] = v;
-    __syncthreads();
-    int64_t before = 0;
-    total = 0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
-        before += i < warp ? sums[i] : 0;
-        total += sums[i];
-    }
-    return v + before;
-}
-
-// Where in the list the piece is, for the whole block; the sequence that it begins
-// in goes to s->found.
-struct Place {
-    int64_t each, per;  // length of one key-value head's list, of a piece
+struct PromptCtl {
+    uint64_t kv_full[kStages], kv_empty[kStages];
+    uint64_t item_full[kItems], item_empty[kItems];
+    uint64_t q_full[2], q_empty[2];  // the slot's queries of the block
+    uint64_t s_full[2];      // scores of the slot's tile are in tensor memory
+    uint64_t p_full[2][2];   // weights of its positions 0-63, 64-127 are (and O is ready to be added to)
+    uint64_t o_full[2];      // O of the block of rows is complete
+    uint64_t token[2];       // the slot's issuer may go on
+    uint64_t drain;
+    Item items[kItems];
+    uint32_t tmem;
+    int abort;
 };
-__device__ __forceinline__ Place find_piece(const PromptArgs &a, PromptCtl *s) {
-    const int tid = threadIdx.x, span = 2 * a.tq;
-    Place p{0, 0};
-    int64_t mine = 0, upto = 0, rows = 0;
-    for (int b0 = 0; b0 < a.n_seq; b0 += kThreads) {
-        mine = 0;
-        int64_t n = 0, total;
-        if (b0 + tid < a.n_seq) {
-            const Seq q(a, b0 + tid);
-            mine = q.length(a, q.blocks(span));
-            n = q.n;
-        }
-        upto = block_scan(mine, s->sums, total) + p.each;
-        p.each += total;
-        if (a.n_seq > 1) {
-            block_scan(n, s->sums, total);
-            rows += total;
-        }
-    }
-    // (starts that go back may give more rows than there are: none is worked on then)
-    if (rows > a.T) {
-        if (tid == 0) record_status(a.status, MOE_ERR_PAGE);
-        p.each = 0;
-    }
-    const int64_t all = p.each * a.c.Hkv;
-    p.per = (all + a.ncta - 1) / a.ncta;
-    const int64_t f0 = blockIdx.x * p.per;
-    if (f0 < all) {
-        const int64_t at = f0 % p.each;
-        if (a.n_seq <= kThreads) {
-            if (upto - mine <= at && at < upto) {
-                s->found = tid;
-                s->found_at = upto - mine;
-            }
-        } else {
-            int64_t before = 0;
-            for (int b0 = 0; b0 < a.n_seq && before <= at; b0 += kThreads) {
-                int64_t v = 0, total;
-                if (b0 + tid < a.n_seq) {
-                    const Seq q(a, b0 + tid);
-                    v = q.length(a, q.blocks(span));
-                }
-                const int64_t u = block_scan(v, s->sums, total) + before;
-                if (u - v <= at && at < u) {
-                    s->found = b0 + tid;
-                    s->found_at = u - v;
-                }
-                before += total;
-            }
-        }
-    }
-    __syncthreads();
-    return p;
+
+__host__ __device__ constexpr int prompt_smem_bytes(int D) {
+    return 2 * kRows * D * 2 + kStages * tile_bytes(D) + 1024 + static_cast<int>(sizeof(PromptCtl));
 }
+static_assert(prompt_smem_bytes(128) <= kBlockSmem, "one block per SM");
 
 // A warp's way along the list, all lanes alike.
 struct Walk {
+    int64_t per;             // length of a piece
     int64_t left;            // of the piece from here on
     int kv, seq, blk, nb;
     int t, n, of;            // first tile of the block here, tiles of it here, of it at all
@@ -235,26 +160,88 @@ struct Walk {
         left -= at < kSwitch ? kSwitch - at : 0;
         n = static_cast<int>(min(static_cast<int64_t>(of - t), left));
     }
-    // False: nothing (more) for this piece.
-    __device__ __forceinline__ bool first(const PromptArgs &a, const PromptCtl *s, const Place &p) {
-        const int lane = threadIdx.x & 31;
-        const int64_t f0 = blockIdx.x * p.per, rest = p.each * a.c.Hkv - f0;
-        if (rest <= 0) return false;
-        left = min(rest, p.per);
-        kv = static_cast<int>(f0 / p.each);
-        seq = s->found;
-        const int64_t at = f0 - kv * p.each - s->found_at;
-        const Seq q(a, seq);
-        // the last block that begins at `at` or before, by 32 looks at a time
-        int lo = 0, hi = q.blocks(2 * a.tq);
+    // False: nothing (more) for this piece.  Every piece adds up the list for itself,
+    // one lane a run of sequences.
+    __device__ __forceinline__ bool first(const PromptArgs &a) {
+        const int lane = threadIdx.x & 31, span = 2 * a.tq;
+        const int run = (a.n_seq + 31) / 32;
+        int64_t own = 0, rows = 0;
+        Seq q;
+        for (int i = 0; i < run; i += kAhead) {
+            int r[kAhead + 1], len[kAhead];
+#pragma unroll
+            for (int e = 0; e <= kAhead; ++e) {
+                const int b = lane * run + min(i + e, run);
+                r[e] = __ldcg(a.q_start + min(b, a.n_seq));
+                if (e < kAhead) len[e] = __ldcg(a.seq_len + min(b, a.n_seq - 1));
+            }
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) {
+                if (i + e >= run) break;
+                q = lane * run + i + e < a.n_seq ? Seq(a, r[e], r[e + 1], len[e]) : Seq();
+                own += q.length(a, q.blocks(span));
+                rows += q.n;
+            }
+        }
+        int64_t upto = own;
+#pragma unroll
+        for (int i = 1; i < 32; i <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, upto, i);
+            if (lane >= i) upto += o;
+            rows += __shfl_xor_sync(0xffffffffu, rows, i);
+        }
+        int64_t each = __shfl_sync(0xffffffffu, upto, 31);  // length of one key-value head's list
+        // (starts that go back may give more rows than there are: none is worked on then)
+        if (rows > a.T) {
+            record_status(a.status, MOE_ERR_PAGE);
+            each = 0;
+        }
+        per = quotient(each * a.c.Hkv + a.ncta - 1, a.ncta);
+        left = min(each * a.c.Hkv - blockIdx.x * per, per);
+        if (left <= 0) return false;
+        kv = static_cast<int>(quotient(blockIdx.x * per, each));
+        int64_t at = blockIdx.x * per - kv * each;
+        // the sequence: the lane's run, then in it
+        const int l = __ffs(__ballot_sync(0xffffffffu, at < upto)) - 1;
+        at -= __shfl_sync(0xffffffffu, upto - own, l);
+        seq = l * run;
+        int k = l;
+        if (run > 1) {
+            for (;; seq += 32) {
+                if (seq >= a.n_seq) return false;  // (the lengths have changed meanwhile)
+                q = lane < run && seq + lane < a.n_seq ? Seq(a, seq + lane) : Seq();
+                own = upto = q.length(a, q.blocks(span));
+#pragma unroll
+                for (int i = 1; i < 32; i <<= 1) {
+                    const int64_t o = __shfl_up_sync(0xffffffffu, upto, i);
+                    if (lane >= i) upto += o;
+                }
+                const unsigned m = __ballot_sync(0xffffffffu, at < upto);
+                if (m) {
+                    k = __ffs(m) - 1;
+                    at -= __shfl_sync(0xffffffffu, upto - own, k);
+                    seq += k;
+                    break;
+                }
+                at -= __shfl_sync(0xffffffffu, upto, 31);
+            }
+        }
+        q.row0 = __shfl_sync(0xffffffffu, q.row0, k);
+        q.n = __shfl_sync(0xffffffffu, q.n, k);
+        q.pos0 = __shfl_sync(0xffffffffu, q.pos0, k);
+        // its last block that begins at `at` or before, by 32 looks at a time
+        int lo = 0, hi = q.blocks(span);
+        int64_t begin = 0;
         while (hi - lo > 1) {
             const int step = (hi - lo + 31) / 32, j = lo + lane * step;
-            const unsigned ok = __ballot_sync(0xffffffffu, j < hi && q.length(a, j) <= at);
-            lo += (31 - __clz(ok)) * step;
+            const int64_t b = q.length(a, min(j, hi - 1));
+            const int last = 31 - __clz(__ballot_sync(0xffffffffu, j < hi && b <= at));
+            begin = __shfl_sync(0xffffffffu, b, last);
+            lo += last * step;
             hi = min(hi, lo + step);
         }
         blk = lo;
-        block(a, q, at - q.length(a, lo));
+        block(a, q, at - begin);
         return n > 0 || next(a);
     }
     __device__ __forceinline__ bool next(const PromptArgs &a) {
@@ -411,7 +398,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     pdl_wait();
     pdl_trigger();
-    const Place place = find_piece(a, s);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -426,21 +412,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int bx = lane / HALVES, half = lane % HALVES;
         uint32_t it = 0, ni = 0, nq[2] = {0, 0};  // ring entries, blocks, a slot's blocks
         Walk w;
-        bool more = w.first(a, s, place), ok = true;
-        // what there is to join at the piece's beginning: of a block that the piece
-        // before begins, all its pieces
-        if (lane == 0 && blockIdx.x) {
-            PromptCut c{};
-            if (more && w.t > 0 && w.t <= place.per) {
-                const int64_t f0 = blockIdx.x * place.per;
-                c.pieces = static_cast<int>((f0 + w.of - w.t - 1) / place.per) - static_cast<int>(blockIdx.x) + 2;
-                c.kv = w.kv;
-                c.row0 = w.row0;
-                c.ntok = w.ntok;
-                c.pos0 = w.pos0;
-            }
-            a.cuts[blockIdx.x] = c;
-        }
+        bool more = w.first(a), ok = true;
+        // the block that the piece begins in, which may be cut there
+        const bool cut = more && w.t > 0 && w.t <= w.per;
+        const PromptCut here{0, w.kv, w.row0, w.ntok, w.pos0};
+        const int64_t to_end = w.of - w.t;
         for (;; ++ni) {
             Item *k = s->items + ni % kItems;
             ok = warp_wait(&s->item_empty[ni % kItems], (ni / kItems & 1) ^ 1, a, s, 40);
@@ -498,6 +474,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             more = w.next(a);
+        }
+        // what there is to join at the piece's beginning: of a block that the piece
+        // before begins, all its pieces
+        if (lane == 0 && blockIdx.x) {
+            PromptCut c{};
+            if (cut) {
+                c = here;
+                c.pieces = static_cast<int>(quotient(blockIdx.x * w.per + to_end - 1, w.per)) -
+                           static_cast<int>(blockIdx.x) + 2;
+            }
+            a.cuts[blockIdx.x] = c;
         }
         // no copy of this block is in flight when it ends
         for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
@@ -605,9 +592,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!active) it += 2 * item->n;
             for (int t = item->t; active && t < item->t + item->n; ++t, it += 2) {
                 const int pos0 = item->pos0, ntok = item->ntok;
-                ok = warp_wait(&s->s_full[slot], turn >> 1 & 1, a, s, 50);
-                if (!ok) break;
-                tc_fence_after();
                 const bool pre = t < ptiles;
                 const int p0 = (pre ? t : t - ptiles) * kPos;
                 const int left = (pre ? a.prefix_len : pos0 + ntok) - p0;  // positions of the tile
@@ -632,6 +616,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
+                ok = warp_wait(&s->s_full[slot], turn >> 1 & 1, a, s, 50);
+                if (!ok) break;
+                tc_fence_after();
                 if (warp_real) {
                     tile_softmax<D>(sS, sO, a.scale_log2, m, l, m != -INFINITY, s->p_full[slot], mask, []() { return true; });
                 } else {
