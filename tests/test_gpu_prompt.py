@@ -457,3 +457,19 @@ def test_prompt_sublayer_layer_and_scores_together():
     assert (got.entropy.double() + (lp.exp() * lp).sum(-1)).abs().max() <= 2e-5
     top = lp.topk(3, -1)
     assert torch.equal(got.top_ids.long(), top.indices) and (got.top_logprobs.double() - top.values).abs().max() <= 2e-5
+
+
+@pytest.mark.parametrize("n", [32, 33, 400, 1100])
+def test_prompt_of_many_sequences(n):
+    # sequences of one to some tokens, empty ones and padding between them, over more
+    # than a warp's lanes and more than 32 of each
+    g = gen(n)
+    seqs = []
+    for _ in range(n):
+        rows = int(torch.randint(0, 6, (1,), generator=g))
+        seqs.append((0, -1) if rows == 5 else (rows, rows + int(torch.randint(0, 40, (1,), generator=g))))
+    c = Prompt(seqs + [(300, 700)], 2, 1, 64, 16, 0, True, seed=9, lead=3, tail=2)
+    out = torch.full_like(c.q, 7.0)
+    c.run(out=out)
+    c.check(out)
+    assert (out[:3] == 7.0).all() and (out[-2:] == 7.0).all()
