@@ -15,12 +15,12 @@
 // linear_operands_kernel makes the tokens' operand, rows of P = K + 3 K / G columns
 // (each part rounded up to 64, zeros between), the rows' powers, and of the weights
 // the bias columns and the scales in fp16.  The codes themselves are unpacked
-//   of large matrices (more than kPieceBytes in fp16) for few tiles of tokens by the
-//   product's kernel, again for each tile: the matrix is then read as it is;
+//   of large matrices for few tiles of tokens (codes_up_to) by the product's kernel,
+//   again for each tile: the matrix is then read as it is;
 //   else by the operands kernel, once, into rows of P columns too, large matrices a
 //   piece of rows at a time, so that they are read back from the L2.
-// (512 x 2048 x 131072 266 us the first way, 496 the second; 1024 x 2048 x 2560 26.6 and
-// 22.9.)
+// (256 x 2048 x 16384 28 us the first way, 52 the second; 512 x 2048 x 131072 fp32 295
+// and 496; 1024 x 2048 x 8192 38 and 42, 2048 67 and 62; 512 x 2048 x 4096 23 and 20.)
 //
 // linear_prompt_kernel: pairs of blocks, on two SMs, work on tiles of 256 weight rows
 // by up to 256 tokens (a multiple of 32 picked for even rounds over the pairs) with
@@ -68,7 +68,8 @@ constexpr int kEpiWarp = 4, kEpiWarps = 8;
 constexpr int kDeqWarp = kEpiWarp + kEpiWarps, kSets = 4, kSetWarps = 4, kDeqWarps = kSets * kSetWarps;
 constexpr int kQ = 8, kQBytes = kRows * kStep / 2;  // stages of packed codes
 constexpr int threads(bool codes) { return (codes ? kDeqWarp + kDeqWarps : kDeqWarp) * 32; }
-constexpr int kFewTiles = 8;               // of tokens, up to which the product's kernel unpacks large matrices
+constexpr size_t kCodesBytes = 8 << 20;    // of fp16 weights for each tile of tokens, above which the product's
+constexpr int kCodesTiles[2] = {4, 8};     // kernel unpacks them: of the fewest and of the most tiles that count
 constexpr int kWBytes = kRows * kStep * 2;
 constexpr int kMaxT = 16384;               // tokens whose operands are held at a time
 constexpr size_t kPieceBytes = 80 << 20;   // of what is made of the weights for a piece of rows, about
@@ -664,11 +665,18 @@ struct Layout {
     int code_steps;  // (0: codes are unpacked before the product)
 };
 
+// Tokens up to which the product's kernel unpacks the codes: unpacking before it costs
+// as many bytes as the weights have in fp16, unpacking in it some time for every tile.
+static int codes_up_to(int N, const Columns &c) {
+    const size_t tiles = (static_cast<size_t>(N) * c.P * sizeof(__half) - 1) / kCodesBytes;
+    return tiles < kCodesTiles[0] ? 0 : static_cast<int>(std::min<size_t>(tiles, kCodesTiles[1])) * kMaxTok;
+}
+
 static Layout layout(int N, int K, int G, int T) {
     auto up = [](size_t n) { return (n + 1023) / 1024 * 1024; };
     const Columns c(K, G);
     Layout L{};
-    L.code_steps = T <= kFewTiles * kMaxTok && static_cast<size_t>(N) * c.P * sizeof(__half) > kPieceBytes ? c.Kp / kStep : 0;
+    L.code_steps = T <= codes_up_to(N, c) ? c.Kp / kStep : 0;
     const size_t width = (c.P - L.code_steps * kStep) * sizeof(__half);  // of a row of wh
     const size_t most = std::max<size_t>(kPieceBytes / width / kPairRows * kPairRows, kPairRows);
     L.rows = static_cast<int>(std::min<size_t>(N, most));
@@ -703,8 +711,9 @@ static int tile_tokens(int N, int T, int pairs) {
 
 // (a call of fewer tokens may take the way that needs more)
 size_t linear_prompt_workspace_bytes(int N, int K, int G, int T) {
-    const size_t few = prompt::layout(N, K, G, std::min(T, prompt::kFewTiles * prompt::kMaxTok)).total;
-    return std::max(few, prompt::layout(N, K, G, T).total);
+    const size_t all = prompt::layout(N, K, G, T).total;
+    const int few = prompt::codes_up_to(N, prompt::Columns(K, G));  // (these take other room)
+    return few && few < T ? std::max(all, prompt::layout(N, K, G, few).total) : all;
 }
 
 cudaError_t launch_linear_prompt(const LinearArgs &l, LinearMap encode, void *ws, int num_sms, cudaStream_t s) {

@@ -199,3 +199,16 @@ def test_linear_prompt_of_large_matrices(T, K, N, G):
     w = q * s[rows].double().repeat_interleave(G, 1) + z[rows].double().repeat_interleave(G, 1)
     want = x.double() @ w.t()
     assert ((got[:, rows].double() - want).abs() <= bound(x, w, K)).all()
+
+
+@pytest.mark.parametrize("T,K,N,G", [(65, 2048, 8192, 64), (1024, 2048, 8192, 64), (1025, 2048, 8192, 64),
+                                     (300, 1056, 16001, 32), (1281, 2048, 10000, 128)])
+def test_linear_prompt_of_middling_matrices(T, K, N, G):
+    """Around the number of tokens up to which the product's kernel unpacks."""
+    test_linear_prompt_of_large_matrices(T, K, N, G)
+
+
+def test_linear_prompt_workspace_of_more_tokens_serves_fewer():
+    m, _ = make_int4(gen(71), 16384, 2048, 64)
+    sizes = [moe.linear_prompt_workspace(m, T).numel() for T in (1, 64, 65, 1000, 1024, 1025, 2047, 2048, 2049, 5000)]
+    assert sizes == sorted(sizes)
