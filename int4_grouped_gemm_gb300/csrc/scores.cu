@@ -396,19 +396,31 @@ __global__ void __launch_bounds__(kWarps * 32, 4) scores_kernel(const __grid_con
             for (int j = 0; j < Ring<E>::VEC; ++j)
                 best.offer(x[j], at + j, at + j >= 0 && at + j < hi, buffer, a.n_top, lane);
         };
+        const int each = eighth * Ring<E>::N;  // vectors of an eighth
+        auto vector = [&](int i, int v, int of) {
+            return off + (b0 + (i * eighth + v / Ring<E>::N) * WPR) * kBatch + (v % Ring<E>::N * 32 + of) * Ring<E>::VEC;
+        };
+        // (the ring is empty)
+        unsigned char *few = reinterpret_cast<unsigned char *>(&ring_at[warp][0][0]);
+        int n_few = 0;
+        __syncwarp();
         for (int i = 0; i < done; ++i) {
-            unsigned lanes = __ballot_sync(0xffffffffu, maxima[warp][i][lane] >= nth);
-            const int first_b = b0 + i * eighth * WPR, vectors = min(eighth, own - i * eighth) * Ring<E>::N;
-            auto vector = [&](int v, int of) {
-                return off + (first_b + v / Ring<E>::N * WPR) * kBatch + (v % Ring<E>::N * 32 + of) * Ring<E>::VEC;
-            };
+            const bool reaches = maxima[warp][i][lane] >= nth;
+            const unsigned lanes = __ballot_sync(0xffffffffu, reaches);
+            const int vectors = min(eighth, own - i * eighth) * Ring<E>::N;
             if (__popc(lanes) * ((vectors + 31) / 32) >= vectors) {
                 // many lanes of a short eighth: all of it
-                for (int v = 0; v < vectors; ++v) look(vector(v, lane), a.V);
+                for (int v = 0; v < vectors; ++v) look(vector(i, v, lane), a.V);
             } else {
-                for (; lanes; lanes &= lanes - 1)
-                    for (int v = lane; v - lane < vectors; v += 32) look(vector(v, __ffs(lanes) - 1), v < vectors ? a.V : 0);
+                if (reaches) few[n_few + __popc(lanes & ((1u << lane) - 1))] = static_cast<unsigned char>(i * 32 + lane);
+                n_few += __popc(lanes);
             }
+        }
+        __syncwarp();
+        // ... the others together, a lane a vector
+        for (int p = lane; p - lane < n_few * each; p += 32) {
+            const int k = p / each, v = p - k * each, of = k < n_few ? few[k] : 0;
+            look(vector(of >> 5, v, of & 31), k < n_few && (of >> 5) * eighth + v / Ring<E>::N < own ? a.V : 0);
         }
         if (best.waiting) best.sort_in(buffer, a.n_top, lane);
     }
