@@ -45,9 +45,8 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 }
 // ... and equal ones by lower id; 0: none.
 __device__ __forceinline__ u64 rank_key(uint32_t order, int id) { return static_cast<u64>(order) << 32 | ~static_cast<uint32_t>(id); }
-__device__ __forceinline__ float key_score(u64 k) {
-    const uint32_t up = static_cast<uint32_t>(k >> 32);
-    return __uint_as_float(up & 0x80000000u ? up & 0x7FFFFFFFu : ~up);
+__device__ __forceinline__ float score_of(uint32_t order) {
+    return __uint_as_float(order & 0x80000000u ? order & 0x7FFFFFFFu : ~order);
 }
 __device__ __forceinline__ int key_id(u64 k) { return static_cast<int>(~static_cast<uint32_t>(k)); }
 
@@ -125,15 +124,27 @@ struct Best {
         nth = __shfl_sync(0xffffffffu, list, n - 1);
         least = larger(least, static_cast<uint32_t>(nth >> 32));
     }
-    __device__ __forceinline__ void offer(float x, int id, bool real, u64 *buffer, int n, int lane) {
-        const uint32_t o = order_of(x);
-        if (!__any_sync(0xffffffffu, real && o >= least)) return;
-        const u64 key = rank_key(o, id);
-        const bool take = real && o >= least && key > nth;
-        const unsigned m = __ballot_sync(0xffffffffu, take);
-        if (take) buffer[waiting + __popc(m & ((1u << lane) - 1))] = key;
-        waiting += __popc(m);
-        if (waiting >= 32) sort_in(buffer, n, lane);
+    // Each lane's x[0 .. N - 1], of ids at .. at + N - 1 (those in 0 .. hi - 1 count).
+    template <int N>
+    __device__ __forceinline__ void offer(const float (&x)[N], int at, int hi, u64 *buffer, int n, int lane) {
+        const float from = score_of(least);
+        unsigned hits = 0;
+#pragma unroll
+        for (int j = 0; j < N; ++j) hits |= (hi > 0 && !(x[j] < from)) << j;
+        while (__any_sync(0xffffffffu, hits != 0)) {
+            const int j = __ffs(hits) - 1;
+            float y = x[0];
+#pragma unroll
+            for (int i = 1; i < N; ++i) y = i == j ? x[i] : y;
+            const uint32_t o = order_of(y);
+            const u64 key = rank_key(o, at + j);
+            const bool take = hits && at + j >= 0 && at + j < hi && o >= least && key > nth;
+            hits &= hits - 1;
+            const unsigned m = __ballot_sync(0xffffffffu, take);
+            if (take) buffer[waiting + __popc(m & ((1u << lane) - 1))] = key;
+            waiting += __popc(m);
+            if (waiting >= 32) sort_in(buffer, n, lane);
+        }
     }
 };
 
@@ -156,6 +167,16 @@ struct Sums {
         S += b.S;
         U += b.U;
     }
+    // Those of each `of` neighbouring lanes (all with one reference).
+    template <int of>
+    __device__ __forceinline__ void add_lanes() {
+        move(score_of(__reduce_max_sync(0xffffffffu, order_of(r))));
+#pragma unroll
+        for (int i = of / 2; i; i >>= 1) {
+            S += __shfl_xor_sync(0xffffffffu, S, i);
+            U += __shfl_xor_sync(0xffffffffu, U, i);
+        }
+    }
 };
 
 // What a row's sums and list say, by a warp.
@@ -173,37 +194,31 @@ __device__ __forceinline__ void finish_row(const ScoresArgs &a, int t, int targe
     if (lane < a.n_top) {
         const int64_t at = static_cast<int64_t>(t) * a.n_top + lane;
         a.top_ids[at] = key_id(list);
-        a.top_logprobs[at] = (key_score(list) - s.r) - logS;
+        a.top_logprobs[at] = (score_of(static_cast<uint32_t>(list >> 32)) - s.r) - logS;
     }
 }
 
-// Merges the sums and lists of each WPR warps, halves at a time; the first of them
-// returns with all.
+// Merges the sums, and with `top` the lists (halves at a time), of each WPR warps; the
+// first of them returns with all.
 template <int WPR>
 __device__ __forceinline__ void merge_warps(Sums &s, u64 &list, bool top, int warp, int lane) {
     __shared__ Sums sums[kWarps];
     __shared__ u64 lists[kWarps][32];
     const int mine = warp % WPR;
-#pragma unroll
-    for (int half = WPR / 2; half; half >>= 1) {
-        if (mine >= half && mine < 2 * half) {
-            if (lane == 0) sums[warp] = s;
-            if (top) lists[warp][lane] = list;
-        }
+    if (WPR > 1) {
+        if (lane == 0) sums[warp] = s;
         __syncthreads();
-        if (mine < half) {
-            s.add(sums[warp + half]);
-            if (top) list = merge32(list, lists[warp + half][lane], lane);
+        if (mine == 0) {
+            s = sums[warp + lane % WPR];
+            s.add_lanes<WPR>();
         }
     }
-}
-
-__device__ __forceinline__ void merge_lanes(Sums &s) {
+    if (!top) return;
 #pragma unroll
-    for (int i = 16; i; i >>= 1) {
-        const Sums o{__shfl_xor_sync(0xffffffffu, s.r, i), __shfl_xor_sync(0xffffffffu, s.S, i),
-                     __shfl_xor_sync(0xffffffffu, s.U, i)};
-        s.add(o);
+    for (int half = WPR / 2; half; half >>= 1) {
+        if (mine >= half && mine < 2 * half) lists[warp][lane] = list;
+        __syncthreads();
+        if (mine < half) list = merge32(list, lists[warp + half][lane], lane);
     }
 }
 
@@ -250,12 +265,13 @@ struct Ring {
         unpack(x, e >= 0 && e + VEC <= hi ? __ldcg(reinterpret_cast<const uint4 *>(row + e)) : edge(row, e, hi));
     }
     // first: index in the row of the batch's first score; hi: the row's end (0: no batch)
-    __device__ __forceinline__ void load(int stage, const E *row, int64_t first, int64_t hi, int lane) const {
+    __device__ __forceinline__ void load(int stage, const E *row, int first, int hi, int lane) const {
+        const bool inner = first >= 0 && first + kBatch <= hi;  // (all lanes alike)
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int64_t e = first + (i * 32 + lane) * VEC;
+            const int e = first + (i * 32 + lane) * VEC;
             uint4 *to = mine + (stage * N + i) * 32;
-            if (e >= 0 && e + VEC <= hi)
+            if (inner || (e >= 0 && e + VEC <= hi))
                 cp_async<16>(to, row + e);
             else if (hi > 0)
                 *to = edge(row, e, hi);
@@ -304,7 +320,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) scores_kernel(const __grid_con
     int left = eighth, done = 0;
     const Ring<E> ring{&ring_at[warp][0][lane]};
     constexpr int STAGES = Ring<E>::STAGES;
-    auto load = [&](int stage, int b) { ring.load(stage, row, off + static_cast<int64_t>(b) * kBatch, b < b1 ? a.V : 0, lane); };
+    auto load = [&](int stage, int b) { ring.load(stage, row, off + b * kBatch, b < b1 ? a.V : 0, lane); };
 #pragma unroll
     for (int i = 0; i < STAGES; ++i) load(i, b + i * WPR);
     bool first = true;
@@ -347,7 +363,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) scores_kernel(const __grid_con
     const float2 S1 = unpack2(S2), U1 = unpack2(U2);
     s.S = S1.x + S1.y;
     s.U = U1.x + U1.y;
-    merge_lanes(s);
+    s.add_lanes<32>();
     Best best;
     if (TOP) {
         if (left < eighth) maxima[warp][done++][lane] = order_of(most);
@@ -392,9 +408,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) scores_kernel(const __grid_con
         auto look = [&](int at, int hi) {
             float x[Ring<E>::VEC];
             Ring<E>::fetch(x, row, at, hi);
-#pragma unroll
-            for (int j = 0; j < Ring<E>::VEC; ++j)
-                best.offer(x[j], at + j, at + j >= 0 && at + j < hi, buffer, a.n_top, lane);
+            best.offer(x, at, hi, buffer, a.n_top, lane);
         };
         const int each = eighth * Ring<E>::N;  // vectors of an eighth
         auto vector = [&](int i, int v, int of) {
@@ -422,9 +436,36 @@ __global__ void __launch_bounds__(kWarps * 32, 4) scores_kernel(const __grid_con
             const int k = p / each, v = p - k * each, of = k < n_few ? few[k] : 0;
             look(vector(of >> 5, v, of & 31), k < n_few && (of >> 5) * eighth + v / Ring<E>::N < own ? a.V : 0);
         }
-        if (best.waiting) best.sort_in(buffer, a.n_top, lane);
     }
-    merge_warps<WPR>(s, best.list, TOP, warp, lane);
+    bool merged = false;  // the lists are
+    if (TOP && WPR > 1) {
+        // nearly always a row's warps have at most 64 scores that none has sorted yet: the
+        // first of them sorts them all
+        __shared__ int counts[kWarps];
+        if (lane == 0) counts[warp] = best.nth ? 65 : best.waiting;
+        __syncthreads();
+        const int count = counts[lane % kWarps];
+        int of_row = count;
+#pragma unroll
+        for (int i = WPR / 2; i; i >>= 1) of_row += __shfl_xor_sync(0xffffffffu, of_row, i);
+        merged = __all_sync(0xffffffffu, of_row <= 64);
+        if (merged && mine == 0) {
+            u64 k[2] = {0, 0};
+            int at = lane, all = 0;
+#pragma unroll
+            for (int w = 0; w < WPR; ++w) {
+                const int n = __shfl_sync(0xffffffffu, count, warp + w);
+                if (at >= 0 && at < n) k[0] = buffers[warp + w][at];
+                if (at + 32 >= 0 && at + 32 < n) k[1] = buffers[warp + w][at + 32];
+                at -= n;
+                all += n;
+            }
+            best.list = sort32(k[0], lane);
+            if (all > 32) best.list = merge32(best.list, sort32(k[1], lane), lane);
+        }
+    }
+    if (TOP && !merged && best.waiting) best.sort_in(buffer, a.n_top, lane);
+    merge_warps<WPR>(s, best.list, TOP && !merged, warp, lane);
     if (mine || target < 0) return;
     if (a.parts == 1) {
         finish_row(a, t, target, given, s, best.list, lane);
@@ -452,8 +493,9 @@ __global__ void __launch_bounds__(kWarps * 32) scores_merge_kernel(const __grid_
         s.add(Sums{v.x, v.y, v.z});
     }
     if (a.n_top)
+#pragma unroll 4
         for (int p = warp; p < a.parts; p += kWarps) list = merge32(list, __ldcg(a.part_top + (base + p) * 32 + lane), lane);
-    merge_lanes(s);
+    s.add_lanes<32>();
     merge_warps<kWarps>(s, list, a.n_top > 0, warp, lane);
     if (warp == 0) finish_row(a, t, target, given, s, list, lane);
 }
