@@ -19,7 +19,7 @@
 //   again for each tile: the matrix is then read as it is;
 //   else by the operands kernel, once, into rows of P columns too, large matrices a
 //   piece of rows at a time, so that they are read back from the L2.
-// (256 x 2048 x 16384 28 us the first way, 52 the second; 512 x 2048 x 131072 fp32 295
+// (256 x 2048 x 16384 28 us the first way, 52 the second; 512 x 2048 x 131072 fp32 267
 // and 496; 1024 x 2048 x 8192 38 and 42, 2048 67 and 62; 512 x 2048 x 4096 23 and 20.)
 //
 // linear_prompt_kernel: pairs of blocks, on two SMs, work on tiles of 256 weight rows
@@ -134,9 +134,13 @@ __device__ __forceinline__ uint4 unpack8(uint32_t w, __half2 s) {
 }
 
 constexpr int kOpThreads = 256, kOpRows = kOpThreads / 32;
+constexpr int kBareRows = 4;
 constexpr int kHeld = 8;  // of a token's vectors of eight, those that a lane keeps between the passes
 
-// A row a warp: blocks 0 .. x_blocks - 1 tokens, the others weights.
+// A row a warp: blocks 0 .. x_blocks - 1 tokens, the others weights, whose rows without
+// codes are little work each: kBareRows of them a warp (512 x 2048 x 131072 fp32 267 us,
+// one a warp 295).
+template <bool CODES>
 __global__ void __launch_bounds__(kOpThreads, 3) linear_operands_kernel(const __grid_constant__ Args a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Columns c(a.l.K, a.l.G);
@@ -198,37 +202,54 @@ __global__ void __launch_bounds__(kOpThreads, 3) linear_operands_kernel(const __
         if (lane == 0) a.xe[t] = -up;
         return;
     }
-    const int r = (blockIdx.x - a.x_blocks) * kOpRows + warp;
-    if (r >= a.nn) return;
-    const int64_t n = a.n0 + r;
-    const uint16_t *s = a.l.s + n * a.l.ldg, *z = a.l.b + n * a.l.ldg;
-    const uint32_t *q = a.l.q + n * (c.K / 8);
-    const int codes = c.Kp - a.code_steps * kStep;  // columns of codes here: all or none
-    __half *row = a.wh + static_cast<int64_t>(r) * (codes + c.P - c.Kp), *bias = row + codes;
-    float top = 0.f;
-    for (int g = lane; g < ng; g += 32) {
-        const float sg = bf16_bits_to_float(__ldg(s + g)), cg = bf16_bits_to_float(__ldg(z + g)) + 8.f * sg;
-        top = fmaxf(top, fmaxf(8.f * fabsf(sg), 256.f * fabsf(cg)));
+    constexpr int each = CODES ? 1 : kBareRows;  // rows of a warp
+    const int r0 = ((blockIdx.x - a.x_blocks) * kOpRows + warp) * each, codes = CODES ? c.Kp : 0;
+    auto scales = [&](int r, int g, float &sg, float &cg) {
+        const int64_t at = static_cast<int64_t>(a.n0 + r) * a.l.ldg + g;
+        sg = bf16_bits_to_float(__ldg(a.l.s + at));
+        cg = bf16_bits_to_float(__ldg(a.l.b + at)) + 8.f * sg;
+    };
+    float held_s[each], held_c[each];  // those of group `lane`
+#pragma unroll
+    for (int i = 0; i < each; ++i) {
+        held_s[i] = held_c[i] = 0.f;
+        if (r0 + i < a.nn && lane < ng) scales(r0 + i, lane, held_s[i], held_c[i]);
     }
-    const int up = 14 - power_of(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
-    for (int g = lane; g < ng; g += 32) {
-        const float sg = bf16_bits_to_float(__ldg(s + g)), cg = bf16_bits_to_float(__ldg(z + g)) + 8.f * sg;
-        __half c1, c2;
-        split(times_power(cg, up) * 256.f, c1, c2);
-        bias[g] = c1;
-        bias[ng + g] = c1;
-        bias[2 * ng + g] = c2;
-        if (!codes) a.sh[static_cast<int64_t>(r) * c.Gp + g] = __float2half_rn(times_power(sg, up));
-    }
-    zero_columns(bias, 3 * ng, c.P - c.Kp, lane, 32);
-    if (lane == 0) a.we[r] = -up;
-    if (!codes) return;
+#pragma unroll
+    for (int i = 0; i < each; ++i) {
+        const int r = r0 + i;
+        if (r >= a.nn) return;
+        __half *row = a.wh + static_cast<int64_t>(r) * (codes + c.P - c.Kp), *bias = row + codes;
+        float top = fmaxf(8.f * fabsf(held_s[i]), 256.f * fabsf(held_c[i]));
+        for (int g = lane + 32; g < ng; g += 32) {
+            float sg, cg;
+            scales(r, g, sg, cg);
+            top = fmaxf(top, fmaxf(8.f * fabsf(sg), 256.f * fabsf(cg)));
+        }
+        const int up = 14 - power_of(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
+        for (int g = lane; g < ng; g += 32) {
+            float sg = held_s[i], cg = held_c[i];
+            if (g >= 32) scales(r, g, sg, cg);
+            __half c1, c2;
+            split(times_power(cg, up) * 256.f, c1, c2);
+            bias[g] = c1;
+            bias[ng + g] = c1;
+            bias[2 * ng + g] = c2;
+            if (!CODES) a.sh[static_cast<int64_t>(r) * c.Gp + g] = __float2half_rn(times_power(sg, up));
+        }
+        zero_columns(bias, 3 * ng, c.P - c.Kp, lane, 32);
+        if (lane == 0) a.we[r] = -up;
+        if constexpr (CODES) {
+            const uint16_t *s = a.l.s + static_cast<int64_t>(a.n0 + r) * a.l.ldg;
+            const uint32_t *q = a.l.q + static_cast<int64_t>(a.n0 + r) * (c.K / 8);
 #pragma unroll 4
-    for (int i = lane; i < c.K / 8; i += 32) {
-        const __half sg = __float2half_rn(times_power(bf16_bits_to_float(__ldg(s + (i * 8 >> a.gshift))), up));
-        reinterpret_cast<uint4 *>(row)[i] = unpack8(__ldcs(q + i), __half2half2(sg));
+            for (int k = lane; k < c.K / 8; k += 32) {
+                const __half sg = __float2half_rn(times_power(bf16_bits_to_float(__ldg(s + (k * 8 >> a.gshift))), up));
+                reinterpret_cast<uint4 *>(row)[k] = unpack8(__ldcs(q + k), __half2half2(sg));
+            }
+            zero_columns(row, c.K, c.Kp, lane, 32);
+        }
     }
-    zero_columns(row, c.K, c.Kp, lane, 32);
 }
 
 // -------------------------------------------------------------- product
@@ -726,6 +747,7 @@ cudaError_t launch_linear_prompt(const LinearArgs &l, LinearMap encode, void *ws
     a.gshift = l.G == 32 ? 5 : l.G == 64 ? 6 : 7;
     a.xe = reinterpret_cast<int *>(w + L.xe);
     a.xh = reinterpret_cast<__half *>(w + L.xh);
+    const auto operands = L.code_steps ? linear_operands_kernel<false> : linear_operands_kernel<true>;
     const auto kernel = L.code_steps ? linear_prompt_kernel<true> : linear_prompt_kernel<false>;
     cudaError_t e = L.code_steps ? allow_smem<linear_prompt_kernel<true>>() : allow_smem<linear_prompt_kernel<false>>();
     if (e != cudaSuccess) return e;
@@ -738,8 +760,8 @@ cudaError_t launch_linear_prompt(const LinearArgs &l, LinearMap encode, void *ws
         for (a.n0 = 0; a.n0 < l.N; a.n0 += L.rows) {
             a.nn = std::min(l.N - a.n0, L.rows);
             a.x_blocks = a.n0 ? 0 : (a.nt + kOpRows - 1) / kOpRows;
-            const int w_blocks = (a.nn + kOpRows - 1) / kOpRows;
-            if ((e = launch_dependent(linear_operands_kernel, dim3(a.x_blocks + w_blocks), dim3(kOpThreads), 0, s, a)) != cudaSuccess)
+            const int w_rows = kOpRows * (L.code_steps ? kBareRows : 1), w_blocks = (a.nn + w_rows - 1) / w_rows;
+            if ((e = launch_dependent(operands, dim3(a.x_blocks + w_blocks), dim3(kOpThreads), 0, s, a)) != cudaSuccess)
                 return e;
             a.tok = tile_tokens(a.nn, a.nt, num_sms / 2);
             a.stages = stages_for(a.tok, a.code_steps > 0);
