@@ -587,15 +587,18 @@ int gqa_paged_attention_status(const gqa_pages *cache, const void *q, int64_t q_
  */
 
 /*
- * int4_linear for any number of tokens 1 <= T <= 2^20 (for 64 and fewer
- * int4_linear is made): y[t][n] = sum_k x[t][k] (scale q + bias), products of
- * tokens and weights exact, sums in fp32, y rounded once to bf16 or written as
- * fp32.  Products stay finite for tokens and weights below 2^60, and a token with an
- * infinity or NaN leaves its own row of y without finite numbers and the other rows
- * alone.  Within a row of x, and a row of the matrix, what is 2^-30 of the
- * row's largest value counts with an error of that size.  Other arguments and
- * their limits as int4_linear's.  The workspace (int4_linear_prompt_workspace_bytes, 0
- * if unsupported; no initialisation needed) is this call's alone while it runs.
+ * int4_linear for any number of tokens 1 <= T <= 2^20 (64 and fewer are
+ * int4_linear's own): y[t][n] = sum_k x[t][k] (scale q + bias), products of tokens
+ * and weights exact, sums in fp32, y rounded once to bf16 or written as fp32.  Every
+ * token and every row of the matrix has a power of two of its own, so that only a
+ * result beyond fp32 is infinite; a token's elements below 2^-31 of its largest are off
+ * by 2^-39 of that one, a row's scales below 2^-23 of its largest weight by 2^-31.  Sums
+ * are off by about 7e-7 of y's norm (fp32 results) or 1e-9 of it a column (bf16
+ * results, before their rounding).  A token with an infinity or NaN leaves its own
+ * row of y without finite numbers and the other rows alone.  Other arguments and their limits
+ * as int4_linear's.  The workspace (int4_linear_prompt_workspace_bytes, 0 if
+ * unsupported, enough for fewer tokens too; no initialisation needed) is this call's
+ * alone while it runs.
  */
 size_t int4_linear_prompt_workspace_bytes(int32_t N, int32_t K, int32_t group, int32_t T);
 int int4_linear_prompt(const moe_qweight *w, int32_t N, int32_t K, int32_t group, const void *x, int64_t x_stride,
@@ -651,9 +654,9 @@ int gqa_prompt_attention(const gqa_pages *cache, const void *q, int64_t q_stride
  * top_logprobs are NaN.  A row with targets[t] < 0 is padding: nothing of it is
  * read or written.  A target >= V gives NaN and MOE_ERR_TOKEN_ID at *status (or NULL).
  * 1 <= T <= 2^24 (MOE_ERR_TOKENS), 1 <= V <= 2^28, n_top <= V, stride below 2^39
- * (MOE_ERR_SHAPE).  The workspace (token_logprobs_workspace_bytes, 0 if unsupported;
- * its first word zero if it is the status, else no initialisation) is this call's
- * alone while it runs.
+ * (MOE_ERR_SHAPE).  The workspace (token_logprobs_workspace_bytes, 0 if unsupported,
+ * enough for fewer rows too; its first word zero if it is the status, else no
+ * initialisation) is this call's alone while it runs.
  */
 size_t token_logprobs_workspace_bytes(int32_t T, int32_t V, int32_t n_top);
 int token_logprobs(const void *logits, int64_t stride, int32_t logits_fp32, int32_t T, int32_t V,

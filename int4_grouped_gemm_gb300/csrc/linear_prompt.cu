@@ -6,7 +6,7 @@
 //   weights  s (q - 8): eight bits by four with a sign are eleven, exact in fp16, at a
 //            power of two of the row's own
 //   tokens   bf16's eight bits are exact in fp16 at a power of two of the row's own
-//            (largest element in [2^14, 2^15); what is below 2^-31 of it is off by 2^-40)
+//            (largest element in [2^14, 2^15); what is below 2^-31 of it is off by 2^-39)
 //   biases   with c = z + 8 s what is left is sum_g X[t][g] c[n][g], X = sum of the
 //            group's x: three more columns of the product for each group, X as two fp16
 //            parts (h1, h2, h1) times c as two (c1, c1, c2), 22 bits each; X at 2^-8 and c

@@ -505,14 +505,13 @@ __global__ void __launch_bounds__(kWarps * 32) scores_merge_kernel(const __grid_
 // Parts of a row: as many as give each SM two blocks, of 4096 scores at least.  (With
 // more, a block's beginning and end and the merge cost more than they bring: 257 rows
 // of 50021 in two parts 33 us instead of 20.)
-static int row_parts(int T, int V, int sms) {
-    const int most = std::max(1, V / (kBatch * kPartBatches));
-    return std::max(1, std::min(2 * sms / T, most));
-}
+static int most_parts(int V) { return std::max(1, V / (kBatch * kPartBatches)); }
+static int row_parts(int T, int V, int sms) { return std::max(1, std::min(2 * sms / T, most_parts(V))); }
 
+// (also for fewer rows, which have more parts)
 size_t scores_workspace_bytes(int T, int V, int n_top, int max_sms) {
-    const int parts = row_parts(T, V, max_sms);
-    const size_t blocks = parts > 1 ? static_cast<size_t>(T) * parts : 0;
+    const int most = most_parts(V);
+    const size_t blocks = most > 1 ? std::min<size_t>(static_cast<size_t>(T) * most, 2 * max_sms) : 0;
     return kCtrlBytes + blocks * (sizeof(float4) + (n_top ? 32 * sizeof(u64) : 0));
 }
 

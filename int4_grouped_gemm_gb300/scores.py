@@ -38,7 +38,7 @@ def _bytes(T: int, V: int, n_top: int) -> int:
 
 
 def workspace(T: int, V: int, n_top: int, device="cuda") -> torch.Tensor:
-    """Scratch of token_logprobs for T rows of V scores; calls that may overlap
+    """Scratch of token_logprobs for up to T rows of V scores; calls that may overlap
     take one each.  Its first word records errors found on the device
     (moe_read_device_status) unless the call is given a status."""
     return torch.zeros(_bytes(T, V, n_top), dtype=torch.uint8, device=device)
