@@ -15,8 +15,9 @@
 //            that a cut runs through every piece leaves a partial (m, l, O), and
 //            prompt_combine_kernel joins them.  Lengths and starts are on the device
 //            (a captured call is replayed with others): each piece adds up the
-//            list's length from them and finds its beginning (a kernel before this one
-//            that laid the list out took 4 us of a short call)
+//            list's length from them and finds its beginning, in one warp (a kernel
+//            before this one that laid the list out took 4 us of a short call, sums over
+//            the whole block 1)
 //   tile     as in attn_tile.cuh
 //
 //   warps 0-3, 4-7   softmax of slot 0, 1 (warp w: rows 32 (w % 4) ..)
@@ -39,6 +40,15 @@
 //
 // A position outside the pool is loaded as zeros (the page coordinate lies past
 // the tensor map) and recorded.  Every wait is bounded.
+//
+// What bounds it.  D = 128: the tensor core.  16384 tokens of 16 heads on 2 in 950 us
+// are 1160 TFLOP/s, 1740 with the second parts of the weights, and the clock falls
+// to 1.5 GHz.  D = 64: the softmax warps, busy 2700 of a tile's 3660 cycles (8192
+// tokens 215 us).  Two threads a row (16 softmax warps of 96 registers) took 1127 us
+// where this took 980, the scores of each half of the next tile behind this one's
+// values 988 (and 10 % more at D = 64), rows written by way of shared memory 3 %
+// more.  A call of a few tiles is a chain of first steps: 77 tokens 10.4 us, of which the
+// plan 2.2, pages and keys 2, one tile's softmax 1.9, the rows 1.8.
 #include "attn_tile.cuh"
 #include "prompt.cuh"
 
