@@ -41,14 +41,14 @@
 // A position outside the pool is loaded as zeros (the page coordinate lies past
 // the tensor map) and recorded.  Every wait is bounded.
 //
-// What bounds it.  D = 128: the tensor core.  16384 tokens of 16 heads on 2 in 950 us
-// are 1160 TFLOP/s, 1740 with the second parts of the weights, and the clock falls
-// to 1.5 GHz.  D = 64: the softmax warps, busy 2700 of a tile's 3660 cycles (8192
-// tokens 215 us).  Two threads a row (16 softmax warps of 96 registers) took 1127 us
-// where this took 980, the scores of each half of the next tile behind this one's
-// values 988 (and 10 % more at D = 64), rows written by way of shared memory 3 %
-// more.  A call of a few tiles is a chain of first steps: 77 tokens 10.4 us, of which the
-// plan 2.2, pages and keys 2, one tile's softmax 1.9, the rows 1.8.
+// What bounds it.  D = 128: the tensor core.  16384 tokens of 16 heads on 2 in 885 us
+// are 1240 TFLOP/s, 1860 with the second parts of the weights.  D = 64: the softmax
+// warps, busy 2700 of a tile's 3660 cycles (8192 tokens 215 us).  Two threads a row (16
+// softmax warps of 96 registers) took 1127 us where this then took 980, the scores of
+// each half of the next tile behind this one's values 988 (and 10 % more at D = 64);
+// rows written by way of shared memory 1 % less, at D = 64 7 % more.  A call of a few
+// tiles is a chain of first steps: 77 tokens 10.4 us, of which the plan 2.2, pages and
+// keys 2, one tile's softmax 1.9, the rows 1.8.
 #include "attn_tile.cuh"
 #include "prompt.cuh"
 
@@ -58,7 +58,9 @@ constexpr int kStages = 4;               // key or value tiles in flight
 constexpr int kThreads = 11 * 32;
 constexpr int kDiag = 3;                 // tiles that a block's own tokens (at most 256) lie in
 constexpr int kItems = 4;                // blocks that the loads may be ahead
-constexpr int kSwitch = 1;               // what changing blocks counts, in tiles
+// What changing blocks counts, in tiles: with 0, 1, 4 of them 4096 tokens take 115, 89
+// and 79 us, with 2 76.
+constexpr int kSwitch = 2;
 constexpr int kAhead = 4;                // sequences whose lengths a lane fetches together
 
 // A piece's part of a block: tiles t .. t + n - 1 (n = 0: no more).
@@ -166,7 +168,7 @@ struct Walk {
         ntok = min(q.n - blk * span, span);
         pos0 = q.pos0 + blk * span;
         of = q.tiles(a, blk);
-        t = at > kSwitch ? static_cast<int>(at) - kSwitch : 0;
+        t = at > kSwitch ? static_cast<int>(at - kSwitch) : 0;
         left -= at < kSwitch ? kSwitch - at : 0;
         n = static_cast<int>(min(static_cast<int64_t>(of - t), left));
     }
