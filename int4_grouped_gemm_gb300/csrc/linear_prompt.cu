@@ -52,7 +52,7 @@
 // two rounds over the pairs, tensor pipe 62 % busy in its 32 us.  512 x 2048 x 131072
 // fp32 in 267: 29 us for scales, biases and tokens, then 248 in which the tensor pipe is
 // busy for 52 %, the issue slots for 44 %, and every stage waits for its unpacking.  65
-// tokens 15 us: two launches and 36 stages one after another on 30 pairs.
+// tokens 15 us: two launches and 34 stages one after another on 30 pairs.
 //
 // Every wait is bounded.
 #include <cuda_fp16.h>
