@@ -330,15 +330,25 @@ struct Scores {
         n_top = int32(n, "n_top");
         targets = given == Py_None ? nullptr : ints_of(tensor(given, "targets"), "targets", T, 1, dev);
     }
+    // ws_: None for scratch of the call's own
     int call(float *logprob, float *entropy, int32_t *ids, float *top, PyObject *ws_, PyObject *status_, PyObject *stream) const {
-        const auto [ws, bytes] = scratch_of(ws_, dev);
+        at::Tensor own;
+        std::pair<void *, size_t> scratch{nullptr, 0};
+        if (ws_ == Py_None) {
+            scratch.second = token_logprobs_workspace_bytes(size32(T), size32(V), n_top);
+            own = at::empty({static_cast<int64_t>(scratch.second)}, x.options().dtype(at::kByte));
+            scratch.first = own.data_ptr();
+        } else {
+            scratch = scratch_of(ws_, dev);
+        }
+        const auto [ws, bytes] = scratch;
         int32_t *status = status_ == Py_None ? static_cast<int32_t *>(ws) : status_of(status_, "status", dev);
         return token_logprobs(x.data_ptr(), T > 1 ? x.stride(0) : V, fp32, size32(T), size32(V), targets, logprob, entropy,
                               n_top, ids, top, ws, bytes, status, stream_of(stream, dev));
     }
 };
 
-// logits, targets | None, logprob | None, entropy | None, n_top, top_ids | None, top_logprobs | None, ws,
+// logits, targets | None, logprob | None, entropy | None, n_top, top_ids | None, top_logprobs | None, ws | None,
 // status | None (errors then go to the workspace), stream | None
 int scores(PyObject *const *v) {
     const Scores s(v[0], v[1], v[4]);
@@ -349,7 +359,7 @@ int scores(PyObject *const *v) {
     return s.call(logprob, entropy, ids, top, v[7], v[8], v[9]);
 }
 
-// logits, targets | None, n_top, ws, status | None, stream | None: scores with results of its own (made in
+// logits, targets | None, n_top, ws | None, status | None, stream | None: scores with results of its own (made in
 // Python they took longer than one row's kernels): (rc, logprob | None, entropy, top_ids, top_logprobs)
 PyObject *scores_new(PyObject *const *v) {
     const Scores s(v[0], v[1], v[2]);

@@ -452,6 +452,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) scores_kernel(const __grid_con
         for (int i = WPR / 2; i; i >>= 1) of_row += __shfl_xor_sync(0xffffffffu, of_row, i);
         merged = __all_sync(0xffffffffu, of_row <= 64);
         if (merged && mine == 0) {
+            // each lane's two by the number of larger ones among them all
             u64 k[2] = {0, 0};
             int at = lane, all = 0;
 #pragma unroll
@@ -462,8 +463,26 @@ __global__ void __launch_bounds__(kWarps * 32, 4) scores_kernel(const __grid_con
                 at -= n;
                 all += n;
             }
-            best.list = sort32(k[0], lane);
-            if (all > 32) best.list = merge32(best.list, sort32(k[1], lane), lane);
+            u64 *list = buffer;
+            __syncwarp();
+            list[lane] = k[0];
+            list[32 + lane] = k[1];
+            __syncwarp();
+            int rank[2] = {0, 0};
+#pragma unroll 8
+            for (int i = 0; i < all; ++i) {
+                const u64 o = list[i];
+                rank[0] += o > k[0];
+                rank[1] += o > k[1];
+            }
+            __syncwarp();
+            list[lane] = 0;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (k[i] && rank[i] < 32) list[rank[i]] = k[i];
+            __syncwarp();
+            best.list = list[lane];
         }
     }
     if (TOP && !merged && best.waiting) best.sort_in(buffer, a.n_top, lane);

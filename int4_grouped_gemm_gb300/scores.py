@@ -56,10 +56,8 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     if stream is not None and (out is None or ws is None):
         with _lib.on_stream(stream):
             return token_logprobs(logits, targets, n_top, out, ws, status)
-    if ws is None:
-        if logits.dim() != 2:
-            raise ValueError("token_logprobs: logits [T, V]")
-        ws = torch.empty(_bytes(*logits.shape, n_top), dtype=torch.uint8, device=logits.device)
+    if logits.dim() != 2:
+        raise ValueError("token_logprobs: logits [T, V]")
     if out is None:
         rc, *made = _lib.native().scores_new(logits, targets, n_top, ws, status, None)
         out = TokenScores._make(made)
