@@ -11,11 +11,12 @@
 //            (the sums need the maxima anyway).  At its end the warps' ceil(n / warps)-th
 //            largest of these maxima, the least of them, is a value that n scores at least
 //            reach; the few eighths that reach it are read again, 1 to 2 n of the row's
-//            256 to 2048, their scores that reach it sorted 32 at a time and merged with
-//            the list of the 32 best, a lane each, by exchanges between lanes (15 + 6
-//            steps).  (A list kept during the pass, by each warp, took as many
-//            instructions as the sums in long rows, and several times as many in short
-//            ones: 257 x 50021 with 5 alternatives 39 us)
+//            256 to 2048.  At most 64 of their scores reach it nearly always: the row's
+//            first warp puts them in order by counting the larger ones.  More are sorted
+//            32 at a time and merged with the list of the 32 best, a lane each, by
+//            exchanges between lanes (15 + 6 steps).  (A list kept during the pass, by
+//            each warp, took as many instructions as the sums in long rows, and several
+//            times as many in short ones: 257 x 50021 with 5 alternatives 39 us, now 16)
 //   work     a row is cut into parts where there are too few rows for the GPU, a
 //            block of eight warps each, whose sums are merged through shared memory and
 //            whose scores that reach the n are sorted by the first one;
