@@ -588,6 +588,11 @@ __global__ void __launch_bounds__(threads(CODES), 1)
         for (int tile = pair; tile < tiles; tile += pairs, ++nt) {
             const int n = tile % a.n_tiles * kPairRows + rank * kRows + quarter * 32 + lane, t0 = tile / a.n_tiles * a.tok;
             const int we = n < a.nn ? __ldcg(a.we + n) : 0;
+            // tokens' powers, a lane a token, some tokens ahead
+            auto powers = [&](int c) {
+                return lane < E && c + lane < min(a.tok, a.nt - t0) ? __ldcg(a.xe + t0 + c + lane) : 0;
+            };
+            int ahead = powers(half * E);
             // all chunks but the last one: added to the first
             for (int k = 2 * a.chunk; chunks && k < steps && ok; k += a.chunk, ++nc) {
                 ok = __all_sync(0xffffffffu, wait(&s->acc_full[1], nc & 1, a, s, 71));
@@ -622,7 +627,8 @@ __global__ void __launch_bounds__(threads(CODES), 1)
                 uint32_t v[E], u[E];
                 load(tmem + (nt & 1 && !chunks ? 256 : 0) + c, v);
                 if (chunks) load(tmem + 256 + c, u);
-                const int xe = lane < E && lane < left ? __ldcg(a.xe + t0 + c + lane) : 0;
+                const int xe = ahead;
+                ahead = powers(c + 2 * E);
                 const bool near = __all_sync(0xffffffffu, abs(xe) <= 60 && abs(we) <= 60);
                 const float xf = near ? __int_as_float((xe + 127) << 23) : 0.f, wf = __int_as_float(((near ? we : 0) + 127) << 23);
                 loaded(v);

@@ -56,7 +56,7 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
     if stream is not None and (out is None or ws is None):
         with _lib.on_stream(stream):
             return token_logprobs(logits, targets, n_top, out, ws, status)
-    if logits.dim() != 2:
+    if ws is None and logits.dim() != 2:
         raise ValueError("token_logprobs: logits [T, V]")
     if out is None:
         rc, *made = _lib.native().scores_new(logits, targets, n_top, ws, status, None)
