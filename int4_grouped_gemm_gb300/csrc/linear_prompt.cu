@@ -19,7 +19,7 @@
 //   again for each tile: the matrix is then read as it is;
 //   else by the operands kernel, once, into rows of P columns too, large matrices a
 //   piece of rows at a time, so that they are read back from the L2.
-// (256 x 2048 x 16384 28 us the first way, 52 the second; 512 x 2048 x 131072 fp32 267
+// (256 x 2048 x 16384 28 us the first way, 52 the second; 512 x 2048 x 131072 fp32 256
 // and 496; 1024 x 2048 x 8192 38 and 42, 2048 67 and 62; 512 x 2048 x 4096 23 and 20.)
 //
 // linear_prompt_kernel: pairs of blocks, on two SMs, work on tiles of 256 weight rows
@@ -44,13 +44,14 @@
 //                    warps in turn
 //   warp 2           tells the pair's first block what was unpacked here (of block
 //                    scope; a release of cluster scope took 0.6 us for each stage)
-//   warps 4-11       epilogue: a lane is a weight row, so that a warp writes 32
-//                    neighbouring results of a token at a time, whatever y's stride;
-//                    powers of two put back
+//   warps 4-11, 4-15 where nothing is unpacked here (8192 x 256 x 8192 fp32 63 us, with
+//                    eight 67.5): epilogue: a lane is a weight row, so that a warp writes
+//                    32 neighbouring results of a token at a time, whatever y's
+//                    stride; powers of two put back
 //
 // What bounds it.  4096 x 2048 x 2560 in 40 us: the operands, 8 to 9 us, and a product of
 // two rounds over the pairs, tensor pipe 62 % busy in its 32 us.  512 x 2048 x 131072
-// fp32 in 267: 29 us for scales, biases and tokens, then 248 in which the tensor pipe is
+// fp32 in 256: 29 us for scales, biases and tokens, then a product in which the tensor pipe is
 // busy for 52 %, the issue slots for 44 %, and every stage waits for its unpacking.  65
 // tokens 15 us: two launches and 34 stages one after another on 30 pairs.
 //
@@ -70,10 +71,11 @@ constexpr int kMaxTok = 256;               // tokens of a tile
 constexpr int kStep = 64;                  // columns of a stage
 constexpr int kMaxStages = 8;
 constexpr int kChunk = 13;                 // stages that are summed by MMAs alone, for fp32 results
-constexpr int kEpiWarp = 4, kEpiWarps = 8;
-constexpr int kDeqWarp = kEpiWarp + kEpiWarps, kSets = 4, kSetWarps = 4, kDeqWarps = kSets * kSetWarps;
+constexpr int kEpiWarp = 4;
+__host__ __device__ constexpr int epi_warps(bool codes) { return codes ? 8 : 12; }
+constexpr int kDeqWarp = kEpiWarp + epi_warps(true), kSets = 4, kSetWarps = 4, kDeqWarps = kSets * kSetWarps;
 constexpr int kQ = 8, kQBytes = kRows * kStep / 2;  // stages of packed codes
-constexpr int threads(bool codes) { return (codes ? kDeqWarp + kDeqWarps : kDeqWarp) * 32; }
+constexpr int threads(bool codes) { return (codes ? kDeqWarp + kDeqWarps : kEpiWarp + epi_warps(false)) * 32; }
 constexpr size_t kCodesBytes = 8 << 20;    // of fp16 weights for each tile of tokens, above which the product's
 constexpr int kCodesTiles[2] = {4, 8};     // kernel unpacks them: of the fewest and of the most tiles that count
 constexpr int kWBytes = kRows * kStep * 2;
@@ -444,7 +446,7 @@ __global__ void __launch_bounds__(threads(CODES), 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s->acc_full[i], 1);
-            mbar_init(&s->acc_empty[i], 2 * kEpiWarps);
+            mbar_init(&s->acc_empty[i], 2 * epi_warps(CODES));
         }
         for (int i = 0; i < kQ; ++i) {
             mbar_init(&s->q_full[i], 1);
@@ -564,10 +566,11 @@ __global__ void __launch_bounds__(threads(CODES), 1)
             for (uint32_t i = it > kQ ? it - kQ : 0; i < it; ++i) mbar_drain(&s->q_full[i % kQ], (i / kQ) & 1, a.l.wait_limit);
         }
         __syncwarp();
-    } else if (warp >= kDeqWarp) {
-        if (CODES) unpack_role(a, s, base, stage, steps, tiles, rank, pair, pairs);
+    } else if (CODES && warp >= kDeqWarp) {
+        unpack_role(a, s, base, stage, steps, tiles, rank, pair, pairs);
     } else if (warp >= kEpiWarp) {
-        const int quarter = warp & 3, half = (warp - kEpiWarp) >> 2;
+        constexpr int SETS = epi_warps(CODES) / 4;  // of four warps, in turn
+        const int quarter = warp & 3, set = (warp - kEpiWarp) >> 2;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const bool chunks = a.chunk < steps;
         constexpr int E = CODES ? 16 : 32;
@@ -592,13 +595,13 @@ __global__ void __launch_bounds__(threads(CODES), 1)
             auto powers = [&](int c) {
                 return lane < E && c + lane < min(a.tok, a.nt - t0) ? __ldcg(a.xe + t0 + c + lane) : 0;
             };
-            int ahead = powers(half * E);
+            int ahead = powers(set * E);
             // all chunks but the last one: added to the first
             for (int k = 2 * a.chunk; chunks && k < steps && ok; k += a.chunk, ++nc) {
                 ok = __all_sync(0xffffffffu, wait(&s->acc_full[1], nc & 1, a, s, 71));
                 if (!ok) break;
                 tc_fence_after();
-                for (int c = half * E; c < a.tok; c += 2 * E) {
+                for (int c = set * E; c < a.tok; c += SETS * E) {
                     uint32_t v[E], u[E];
                     load(tmem + c, v);
                     load(tmem + 256 + c, u);
@@ -619,16 +622,16 @@ __global__ void __launch_bounds__(threads(CODES), 1)
             ok = __all_sync(0xffffffffu, wait(&s->acc_full[which], (chunks ? nc++ : nt >> 1) & 1, a, s, 64));
             if (!ok) break;
             tc_fence_after();
-            // some tokens at a time, the halves in turn; the powers as two factors where they
+            // some tokens at a time, the sets of warps in turn; the powers as two factors where they
             // are near enough to one that neither leaves fp32's range
-            for (int c = half * E; c < a.tok; c += 2 * E) {
+            for (int c = set * E; c < a.tok; c += SETS * E) {
                 const int left = a.nt - t0 - c;
                 if (left <= 0) break;
                 uint32_t v[E], u[E];
                 load(tmem + (nt & 1 && !chunks ? 256 : 0) + c, v);
                 if (chunks) load(tmem + 256 + c, u);
                 const int xe = ahead;
-                ahead = powers(c + 2 * E);
+                ahead = powers(c + SETS * E);
                 const bool near = __all_sync(0xffffffffu, abs(xe) <= 60 && abs(we) <= 60);
                 const float xf = near ? __int_as_float((xe + 127) << 23) : 0.f, wf = __int_as_float(((near ? we : 0) + 127) << 23);
                 loaded(v);
