@@ -49,11 +49,12 @@
 //                    32 neighbouring results of a token at a time, whatever y's
 //                    stride; powers of two put back
 //
-// What bounds it.  4096 x 2048 x 2560 in 40 us: the operands, 8 to 9 us, and a product of
-// two rounds over the pairs, tensor pipe 62 % busy in its 32 us.  512 x 2048 x 131072
-// fp32 in 256: 29 us for scales, biases and tokens, then a product in which the tensor pipe is
-// busy for 52 %, the issue slots for 44 %, and every stage waits for its unpacking.  65
-// tokens 15 us: two launches and 34 stages one after another on 30 pairs.
+// What bounds it.  4096 x 2048 x 2560 in 38 us: the operands, 6 to 8 us (their bytes:
+// 16384 x 2048 tokens pass at 5.5 TB/s, read and written), and a product of three
+// rounds over the pairs, tensor pipe 62 % busy in its 32 us.  512 x 2048 x 131072 fp32
+// in 256: 29 us for scales, biases and tokens, then a product in which the tensor pipe
+// is busy for 52 %, the issue slots for 44 %, and every stage waits for its unpacking.
+// 65 tokens 15 us: two launches and 34 stages one after another on 30 pairs.
 //
 // Every wait is bounded.
 #include <cuda_fp16.h>
@@ -160,51 +161,69 @@ __global__ void __launch_bounds__(kOpThreads, 3) linear_operands_kernel(const __
         if (t >= a.nt) return;
         const uint4 *x = reinterpret_cast<const uint4 *>(a.l.x + (a.t0 + t) * a.l.x_stride);
         __half *row = a.xh + static_cast<int64_t>(t) * c.P;
+        __shared__ float group_sums[kOpRows][kHeld * 8];
         uint4 held[kHeld];
-        uint32_t top = 0;
+        auto fetch = [&](int from) {
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i)
+                held[i] = from + i * 32 + lane < n ? __ldcg(x + from + i * 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
+        };
+        // (NaN does not count: it stays NaN at any power)
+        __nv_bfloat162 most = u32_as_bf162(0u);
         auto look = [&](const uint4 &v) {
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, w[j] >> 16 & 0x7FFFu));
+            for (int j = 0; j < 4; ++j) most = __hmax2(most, u32_as_bf162(w[j] & 0x7FFF7FFFu));
         };
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) held[i] = i * 32 + lane < n ? __ldcg(x + i * 32 + lane) : make_uint4(0u, 0u, 0u, 0u);
+        fetch(0);
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) look(held[i]);
 #pragma unroll 4
         for (int i = kHeld * 32 + lane; i < n; i += 32) look(__ldcg(x + i));
-        top = __reduce_max_sync(0xffffffffu, top);
-        // (a row with an infinity or NaN keeps it)
-        const int up = 14 - power_of(__uint_as_float(top << 16));
-        const int lanes = a.l.G / 8;  // of a group
-        auto put = [&](const uint4 &v, int i) {
+        const uint32_t tops = bf162_as_u32(most), top = __reduce_max_sync(0xffffffffu, max(tops & 0xFFFFu, tops >> 16));
+        // (a row with an infinity keeps it)
+        const int up = 14 - power_of(__uint_as_float(top << 16)), up1 = min(up, 127);
+        const int lane_shift = a.gshift - 3;  // log2 of a group's lanes
+        const uint32_t f1 = (up1 + 127) << 23, f2 = (up - up1 + 127) << 23;
+        auto put = [&](const uint4 &v, int i, float *to) {
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
             uint32_t o[4];
-            float sum = 0.f;
+            uint64_t sums = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const __half2 h = __floats2half2_rn(times_power(__uint_as_float(w[j] << 16), up),
-                                                    times_power(__uint_as_float(w[j] & 0xFFFF0000u), up));
+                uint64_t y = fma2(pack2(w[j] << 16, w[j] & 0xFFFF0000u), pack2(f1, f1), 0);
+                if (up > 127) y = fma2(y, pack2(f2, f2), 0);
+                const float2 f = unpack2(y);
+                const __half2 h = __floats2half2_rn(f.x, f.y);
                 o[j] = *reinterpret_cast<const uint32_t *>(&h);
-                const float2 f = __half22float2(h);
-                sum += f.x + f.y;
+                sums = add2(sums, y);
             }
-            for (int j = 1; j < lanes; j <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, j);
+            const float2 two = unpack2(sums);
+            float sum = two.x + two.y;
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            if (lane_shift > 2) sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+            if (lane_shift > 3) sum += __shfl_xor_sync(0xffffffffu, sum, 8);
             if (i >= n) return;
             reinterpret_cast<uint4 *>(row)[i] = make_uint4(o[0], o[1], o[2], o[3]);
-            if (i % lanes == 0) {
-                const int g = i / lanes;
-                __half h1, h2;
-                split(sum * 0x1p-8f, h1, h2);
-                row[c.Kp + g] = h1;
-                row[c.Kp + ng + g] = h2;
-                row[c.Kp + 2 * ng + g] = h1;
-            }
+            if ((lane & ((1 << lane_shift) - 1)) == 0) to[lane >> lane_shift] = sum;
         };
+        for (int from = 0; from < n; from += kHeld * 32) {
+            if (from) fetch(from);
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i)
-            if (i * 32 < n) put(held[i], i * 32 + lane);
-        for (int i = kHeld * 32; i < n; i += 32) put(i + lane < n ? __ldcg(x + i + lane) : make_uint4(0u, 0u, 0u, 0u), i + lane);
+            for (int i = 0; i < kHeld; ++i)
+                if (from + i * 32 < n) put(held[i], from + i * 32 + lane, group_sums[warp] + (i * 32 >> lane_shift));
+            __syncwarp();
+            const int g0 = from >> lane_shift, here = min(kHeld * 32, n - from) >> lane_shift;
+            for (int g = lane; g < here; g += 32) {
+                __half h1, h2;
+                split(group_sums[warp][g] * 0x1p-8f, h1, h2);
+                row[c.Kp + g0 + g] = h1;
+                row[c.Kp + ng + g0 + g] = h2;
+                row[c.Kp + 2 * ng + g0 + g] = h1;
+            }
+            __syncwarp();
+        }
         zero_columns(row, c.K, c.Kp, lane, 32);
         zero_columns(row, c.Kp + 3 * ng, c.P, lane, 32);
         if (lane == 0) a.xe[t] = -up;
