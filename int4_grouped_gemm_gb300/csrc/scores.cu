@@ -2,11 +2,15 @@
 // rows of scores, in one pass over the scores.
 //
 //   sums     with a reference r, S = sum e^(x - r) and U = sum e^(x - r) (x - r):
-//            log sum e^x = r + log S, entropy = log S - U / S.  Each thread has a
-//            reference of its own, the maximum of its first eight scores, which it
-//            moves only when a score exceeds it by 8 (S and U are then scaled): e^8
-//            costs nothing of fp32's accuracy, and a running maximum would be moved
-//            in most batches by one of a warp's lanes
+//            log sum e^x = r + log S, entropy = log S - U / S.  r is a warp's largest
+//            score so far, the same in all lanes, so that the row's largest one counts as
+//            exactly 1 at the end and log S and U / S are small where a token is nearly
+//            certain.  (With a reference of each thread's own that scores may exceed by 8,
+//            log S and x - r cancelled: a log probability of -3.4e-4 was off by 7e-7, now by
+//            6e-8.)  It is found by a vote for each batch, and moved (S and U are then
+//            scaled) about log n times in n batches, where the maximum of each lane would
+//            be moved in most of them by one of 32: 4096 x 50021 bf16 96.6 us, with the
+//            threads' own references 95.8, fp32 133.0 and 132.6
 //   top      the pass keeps, of each lane's scores, the maximum of every eighth part
 //            (the sums need the maxima anyway).  At its end the warps' ceil(n / warps)-th
 //            largest of these maxima, the least of them, is a value that n scores at least
@@ -37,7 +41,6 @@ constexpr int kWarps = 8;             // of a block
 constexpr int kBatch = 256;           // scores that a warp takes at a time, eight a lane
 constexpr int kPartBatches = 16;      // of a part at least
 constexpr int kEighths = 8;           // parts of a lane's scores whose maxima are kept
-constexpr float kLogRaise = 8.f;
 constexpr float kLeast = -3.402823466e38f;
 
 // A score's place in the order of alternatives: larger scores first, NaN before
@@ -170,7 +173,7 @@ struct Sums {
         S += b.S;
         U += b.U;
     }
-    // Those of each `of` neighbouring lanes (all with one reference).
+    // Those of each `of` neighbouring lanes (taken to the largest reference of the warp).
     template <int of>
     __device__ __forceinline__ void add_lanes() {
         move(score_of(__reduce_max_sync(0xffffffffu, order_of(r))));
@@ -326,13 +329,14 @@ __global__ void __launch_bounds__(kWarps * 32, 4) scores_kernel(const __grid_con
     auto load = [&](int stage, int b) { ring.load(stage, row, off + b * kBatch, b < b1 ? a.V : 0, lane); };
 #pragma unroll
     for (int i = 0; i < STAGES; ++i) load(i, b + i * WPR);
-    bool first = true;
     for (int stage = 0; b < b1; b += WPR, stage = (stage + 1) % STAGES) {
         float x[8];
         ring.read(stage, x);
         const float top = max3_nan(max3_nan(x[0], x[1], x[2]), max3_nan(x[3], x[4], x[5]), max_nan(x[6], x[7]));
-        if (first || !(top <= s.r + kLogRaise)) {
-            const float to = max_nan(top, kLeast), d = s.r - to, c = exp_of(d);
+        // (NaN goes through: to is NaN then, and stays)
+        if (__any_sync(0xffffffffu, !(top <= s.r))) {
+            const float to = score_of(__reduce_max_sync(0xffffffffu, order_of(max_nan(top, s.r))));
+            const float d = s.r - to, c = exp_of(d);
             const u64 c2 = pack2(__float_as_uint(c), __float_as_uint(c)), d2 = pack2(__float_as_uint(d), __float_as_uint(d));
             const float2 v = unpack2(S2);
             U2 = v.x + v.y > 0.f && c > 0.f ? fma2(c2, fma2(d2, S2, U2), 0) : 0;
@@ -361,7 +365,6 @@ __global__ void __launch_bounds__(kWarps * 32, 4) scores_kernel(const __grid_con
                 most = -INFINITY;
             }
         }
-        first = false;
     }
     const float2 S1 = unpack2(S2), U1 = unpack2(U2);
     s.S = S1.x + S1.y;
