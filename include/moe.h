@@ -592,7 +592,10 @@ int gqa_paged_attention_status(const gqa_pages *cache, const void *q, int64_t q_
  * and weights exact, sums in fp32, y rounded once to bf16 or written as fp32.  Every
  * token and every row of the matrix has a power of two of its own, so that only a
  * result beyond fp32 is infinite; a token's elements below 2^-31 of its largest are off
- * by 2^-39 of that one, a row's scales below 2^-23 of its largest weight by 2^-31.  Sums
+ * by 2^-39 of that one, a row's scales below 2^-23 of its largest weight by 2^-31.  The
+ * biases meet the sums of a token's groups as c = bias + 8 scale, both with 22 bits or more
+ * but for what is below 2^-42 of the token's largest element and 2^-39 of the row's largest c
+ * or scale.  Sums
  * are off by about 7e-7 of y's norm (fp32 results) or 1e-9 of it a column (bf16
  * results, before their rounding).  A token with an infinity or NaN leaves its own
  * row of y without finite numbers and the other rows alone.  Other arguments and their limits

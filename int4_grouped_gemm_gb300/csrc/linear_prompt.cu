@@ -9,8 +9,10 @@
 //            (largest element in [2^14, 2^15); what is below 2^-31 of it is off by 2^-39)
 //   biases   with c = z + 8 s what is left is sum_g X[t][g] c[n][g], X = sum of the
 //            group's x: three more columns of the product for each group, X as two fp16
-//            parts (h1, h2, h1) times c as two (c1, c1, c2), 22 bits each; X at 2^-8 and c
-//            at 2^8, which keeps sums of 128 in fp16's range
+//            parts (h1, 2^11 h2, h1) times c as two (c1, 2^-11 c1, c2), 22 bits each; X at
+//            2^-8 and c at 2^8, which keeps sums of 128 in fp16's range.  h2 at 2^11,
+//            since a group's sum may be far below the token's largest element: its parts
+//            end at 2^-42 of that one so, at 2^-31 without
 //
 // linear_operands_kernel makes the tokens' operand, rows of P = K + 3 K / G columns
 // (each part rounded up to 64, zeros between), the rows' powers, and of the weights
@@ -118,10 +120,11 @@ __device__ __forceinline__ int power_of(float x) {
     return (e ? e : 1) - 127;
 }
 
-// y in two fp16 parts.
-__device__ __forceinline__ void split(float y, __half &hi, __half &lo) {
+// y in two fp16 parts, the lower one `up` times too large.
+constexpr float kLowUp = 0x1p11f;
+__device__ __forceinline__ void split(float y, __half &hi, __half &lo, float up = 1.f) {
     hi = __float2half_rn(y);
-    lo = __float2half_rn(y - __half2float(hi));
+    lo = __float2half_rn((y - __half2float(hi)) * up);
 }
 
 __device__ __forceinline__ void zero_columns(__half *row, int from, int to, int i, int n) {
@@ -217,7 +220,7 @@ __global__ void __launch_bounds__(kOpThreads, 3) linear_operands_kernel(const __
             const int g0 = from >> lane_shift, here = min(kHeld * 32, n - from) >> lane_shift;
             for (int g = lane; g < here; g += 32) {
                 __half h1, h2;
-                split(group_sums[warp][g] * 0x1p-8f, h1, h2);
+                split(group_sums[warp][g] * 0x1p-8f, h1, h2, kLowUp);
                 row[c.Kp + g0 + g] = h1;
                 row[c.Kp + ng + g0 + g] = h2;
                 row[c.Kp + 2 * ng + g0 + g] = h1;
@@ -260,7 +263,7 @@ __global__ void __launch_bounds__(kOpThreads, 3) linear_operands_kernel(const __
             __half c1, c2;
             split(times_power(cg, up) * 256.f, c1, c2);
             bias[g] = c1;
-            bias[ng + g] = c1;
+            bias[ng + g] = __float2half_rn(__half2float(c1) / kLowUp);
             bias[2 * ng + g] = c2;
             if (!CODES) a.sh[static_cast<int64_t>(r) * c.Gp + g] = __float2half_rn(times_power(sg, up));
         }
