@@ -588,7 +588,7 @@ int gqa_paged_attention_status(const gqa_pages *cache, const void *q, int64_t q_
 
 /*
  * int4_linear for any number of tokens 1 <= T <= 2^20 (64 and fewer are
- * int4_linear's own): y[t][n] = sum_k x[t][k] (scale q + bias), products of tokens
+ * int4_linear's own, within its range of scales): y[t][n] = sum_k x[t][k] (scale q + bias), products of tokens
  * and weights exact, sums in fp32, y rounded once to bf16 or written as fp32.  Every
  * token and every row of the matrix has a power of two of its own, so that only a
  * result beyond fp32 is infinite; a token's elements below 2^-31 of its largest are off

@@ -109,7 +109,7 @@ struct Args {
 
 // ------------------------------------------------------------- operands
 
-// 2^e for e in -140 .. 140 times x, without a rounding that the result does not need.
+// 2^e for e in -250 .. 250 times x, without a rounding that the result does not need.
 __device__ __forceinline__ float times_power(float x, int e) {
     const int h = e / 2;
     return x * __int_as_float((h + 127) << 23) * __int_as_float((e - h + 127) << 23);
@@ -118,6 +118,11 @@ __device__ __forceinline__ float times_power(float x, int e) {
 __device__ __forceinline__ int power_of(float x) {
     const int e = static_cast<int>(__float_as_uint(x) >> 23 & 255);
     return (e ? e : 1) - 127;
+}
+// ... of x >= 0, subnormal numbers too (0: -150).
+__device__ __forceinline__ int power_of_any(float x) {
+    const uint32_t u = __float_as_uint(x);
+    return u >> 23 ? power_of(x) : -118 - __clz(u);
 }
 
 // y in two fp16 parts, the lower one `up` times too large.
@@ -234,10 +239,12 @@ __global__ void __launch_bounds__(kOpThreads, 3) linear_operands_kernel(const __
     }
     constexpr int each = CODES ? 1 : kBareRows;  // rows of a warp
     const int r0 = ((blockIdx.x - a.x_blocks) * kOpRows + warp) * each, codes = CODES ? c.Kp : 0;
+    // (c at 2^-16: z, s and 256 c stay within fp32 so, and any bf16 number times that is exact)
+    constexpr int kDown = 16;
     auto scales = [&](int r, int g, float &sg, float &cg) {
         const int64_t at = static_cast<int64_t>(a.n0 + r) * a.l.ldg + g;
         sg = bf16_bits_to_float(__ldg(a.l.s + at));
-        cg = bf16_bits_to_float(__ldg(a.l.b + at)) + 8.f * sg;
+        cg = fmaf(sg, 0x1p-13f, bf16_bits_to_float(__ldg(a.l.b + at)) * 0x1p-16f);
     };
     float held_s[each], held_c[each];  // those of group `lane`
 #pragma unroll
@@ -250,18 +257,18 @@ __global__ void __launch_bounds__(kOpThreads, 3) linear_operands_kernel(const __
         const int r = r0 + i;
         if (r >= a.nn) return;
         __half *row = a.wh + static_cast<int64_t>(r) * (codes + c.P - c.Kp), *bias = row + codes;
-        float top = fmaxf(8.f * fabsf(held_s[i]), 256.f * fabsf(held_c[i]));
+        float top = fmaxf(0x1p-13f * fabsf(held_s[i]), 256.f * fabsf(held_c[i]));
         for (int g = lane + 32; g < ng; g += 32) {
             float sg, cg;
             scales(r, g, sg, cg);
-            top = fmaxf(top, fmaxf(8.f * fabsf(sg), 256.f * fabsf(cg)));
+            top = fmaxf(top, fmaxf(0x1p-13f * fabsf(sg), 256.f * fabsf(cg)));
         }
-        const int up = 14 - power_of(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
+        const int up = 14 - power_of_any(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)))) - kDown;
         for (int g = lane; g < ng; g += 32) {
             float sg = held_s[i], cg = held_c[i];
             if (g >= 32) scales(r, g, sg, cg);
             __half c1, c2;
-            split(times_power(cg, up) * 256.f, c1, c2);
+            split(times_power(cg, up + kDown) * 256.f, c1, c2);
             bias[g] = c1;
             bias[ng + g] = __float2half_rn(__half2float(c1) / kLowUp);
             bias[2 * ng + g] = c2;
