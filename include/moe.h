@@ -601,7 +601,10 @@ int gqa_paged_attention_status(const gqa_pages *cache, const void *q, int64_t q_
  * row of y without finite numbers and the other rows alone.  Other arguments and their limits
  * as int4_linear's.  The workspace (int4_linear_prompt_workspace_bytes, 0 if
  * unsupported, enough for fewer tokens too; no initialisation needed) is this call's
- * alone while it runs.
+ * alone while it runs.  It holds the operands in fp16, 2 (K + 3 K / group) bytes for
+ * each of up to 16384 tokens, and of the matrix up to 80 MB: 29 MB for 4096 x 2048 x 2560,
+ * 1.25 GB at most (K = 32768, groups of 32, 16384 tokens; calls of fewer tokens one
+ * after another need less).  64 and fewer tokens use none of it (256 bytes are asked for).
  */
 size_t int4_linear_prompt_workspace_bytes(int32_t N, int32_t K, int32_t group, int32_t T);
 int int4_linear_prompt(const moe_qweight *w, int32_t N, int32_t K, int32_t group, const void *x, int64_t x_stride,

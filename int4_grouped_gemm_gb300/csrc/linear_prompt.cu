@@ -774,8 +774,10 @@ static int tile_tokens(int N, int T, int pairs) {
 
 }  // namespace prompt
 
-// (a call of fewer tokens may take the way that needs more)
+// (a call of fewer tokens may take the way that needs more; kLinearMaxB and fewer need
+// none, and 0 stands for what is not supported)
 size_t linear_prompt_workspace_bytes(int N, int K, int G, int T) {
+    if (T <= kLinearMaxB) return kCtrlBytes;
     const size_t all = prompt::layout(N, K, G, T).total;
     const int few = prompt::codes_up_to(N, prompt::Columns(K, G));  // (these take other room)
     return few && few < T ? std::max(all, prompt::layout(N, K, G, few).total) : all;
