@@ -11,7 +11,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _lib
-from .moe import QMatrix, linear_prompt
+from .moe import QMatrix, linear_prompt, linear_prompt_workspace
 
 
 class TokenScores(NamedTuple):
@@ -89,9 +89,14 @@ class OutputHead:
         T, V = x.shape[0], self.w.rows
         out = TokenScores.empty(T, n_top, targets is not None, x.device)
         n = max(1, min(T, self.rows))
+        if T == 0:
+            return out
+        # one piece after another, in the same scratch
         y = torch.empty(n, V, dtype=torch.float32, device=x.device)
+        lin_ws = linear_prompt_workspace(self.w, n)
+        ws = torch.empty(_bytes(n, V, n_top), dtype=torch.uint8, device=x.device)
         for a in range(0, T, n):
             b = min(T, a + n)
-            linear_prompt(self.w, x[a:b], y[:b - a], status=status)
-            token_logprobs(y[:b - a], None if targets is None else targets[a:b], n_top, out.rows(a, b), status=status)
+            linear_prompt(self.w, x[a:b], y[:b - a], ws=lin_ws, status=status)
+            token_logprobs(y[:b - a], None if targets is None else targets[a:b], n_top, out.rows(a, b), ws, status)
         return out
