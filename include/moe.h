@@ -669,6 +669,12 @@ int token_logprobs(const void *logits, int64_t stride, int32_t logits_fp32, int3
                    const int32_t *targets, float *logprob, float *entropy, int32_t n_top, int32_t *top_ids,
                    float *top_logprobs, void *ws, size_t ws_bytes, int32_t *status, cudaStream_t stream);
 
+/* The same for results that hold nothing yet: those of padding rows become NaN, and
+ * their ids -1. */
+int token_logprobs_filled(const void *logits, int64_t stride, int32_t logits_fp32, int32_t T, int32_t V,
+                          const int32_t *targets, float *logprob, float *entropy, int32_t n_top, int32_t *top_ids,
+                          float *top_logprobs, void *ws, size_t ws_bytes, int32_t *status, cudaStream_t stream);
+
 /* Human-readable text for a status code. */
 const char *moe_status_string(int code);
 

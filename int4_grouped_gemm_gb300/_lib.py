@@ -119,6 +119,8 @@ SIGNATURES = {
     "token_logprobs_workspace_bytes": (c_sz, [c_i32, c_i32, c_i32]),
     "token_logprobs": (ctypes.c_int, [c_p, c_i64, c_i32, c_i32, c_i32, c_p, c_p, c_p, c_i32, c_p, c_p, c_p, c_sz, c_p,
                                       c_p]),
+    "token_logprobs_filled": (ctypes.c_int, [c_p, c_i64, c_i32, c_i32, c_i32, c_p, c_p, c_p, c_i32, c_p, c_p, c_p, c_sz,
+                                             c_p, c_p]),
 }
 
 

@@ -1104,9 +1104,9 @@ size_t token_logprobs_workspace_bytes(int32_t T, int32_t V, int32_t n_top) {
     return scores_workspace_bytes(T, V, n_top, kGqaMaxSms);
 }
 
-int token_logprobs(const void *logits, int64_t stride, int32_t logits_fp32, int32_t T, int32_t V,
-                   const int32_t *targets, float *logprob, float *entropy, int32_t n_top, int32_t *top_ids,
-                   float *top_logprobs, void *ws, size_t ws_bytes, int32_t *status, cudaStream_t stream) {
+static int run_scores(const void *logits, int64_t stride, int32_t logits_fp32, int32_t T, int32_t V,
+                      const int32_t *targets, float *logprob, float *entropy, int32_t n_top, int32_t *top_ids,
+                      float *top_logprobs, void *ws, size_t ws_bytes, int32_t *status, cudaStream_t stream, bool fill) {
     int rc;
     if (!logits) return MOE_ERR_NULL;
     if (logits_fp32 != 0 && logits_fp32 != 1) return MOE_ERR_SHAPE;
@@ -1136,7 +1136,22 @@ int token_logprobs(const void *logits, int64_t stride, int32_t logits_fp32, int3
     a.V = V;
     a.n_top = n_top;
     a.fp32 = logits_fp32;
+    a.fill = fill;
     return cuda_rc(launch_scores(a, ws, dev->num_sms, stream));
+}
+
+int token_logprobs(const void *logits, int64_t stride, int32_t logits_fp32, int32_t T, int32_t V,
+                   const int32_t *targets, float *logprob, float *entropy, int32_t n_top, int32_t *top_ids,
+                   float *top_logprobs, void *ws, size_t ws_bytes, int32_t *status, cudaStream_t stream) {
+    return run_scores(logits, stride, logits_fp32, T, V, targets, logprob, entropy, n_top, top_ids, top_logprobs, ws,
+                      ws_bytes, status, stream, false);
+}
+
+int token_logprobs_filled(const void *logits, int64_t stride, int32_t logits_fp32, int32_t T, int32_t V,
+                          const int32_t *targets, float *logprob, float *entropy, int32_t n_top, int32_t *top_ids,
+                          float *top_logprobs, void *ws, size_t ws_bytes, int32_t *status, cudaStream_t stream) {
+    return run_scores(logits, stride, logits_fp32, T, V, targets, logprob, entropy, n_top, top_ids, top_logprobs, ws,
+                      ws_bytes, status, stream, true);
 }
 
 const char *moe_status_string(int code) {

@@ -330,8 +330,9 @@ struct Scores {
         n_top = int32(n, "n_top");
         targets = given == Py_None ? nullptr : ints_of(tensor(given, "targets"), "targets", T, 1, dev);
     }
-    // ws_: None for scratch of the call's own
-    int call(float *logprob, float *entropy, int32_t *ids, float *top, PyObject *ws_, PyObject *status_, PyObject *stream) const {
+    // ws_: None for scratch of the call's own; fill: the results hold nothing yet
+    int call(float *logprob, float *entropy, int32_t *ids, float *top, PyObject *ws_, PyObject *status_, PyObject *stream,
+             bool fill) const {
         at::Tensor own;
         std::pair<void *, size_t> scratch{nullptr, 0};
         if (ws_ == Py_None) {
@@ -343,20 +344,21 @@ struct Scores {
         }
         const auto [ws, bytes] = scratch;
         int32_t *status = status_ == Py_None ? static_cast<int32_t *>(ws) : status_of(status_, "status", dev);
-        return token_logprobs(x.data_ptr(), T > 1 ? x.stride(0) : V, fp32, size32(T), size32(V), targets, logprob, entropy,
-                              n_top, ids, top, ws, bytes, status, stream_of(stream, dev));
+        return (fill ? token_logprobs_filled : token_logprobs)(x.data_ptr(), T > 1 ? x.stride(0) : V, fp32, size32(T),
+                                                               size32(V), targets, logprob, entropy, n_top, ids, top, ws,
+                                                               bytes, status, stream_of(stream, dev));
     }
 };
 
 // logits, targets | None, logprob | None, entropy | None, n_top, top_ids | None, top_logprobs | None, ws | None,
-// status | None (errors then go to the workspace), stream | None
+// status | None (errors then go to the workspace), stream | None, and whether padding rows' results are filled in
 int scores(PyObject *const *v) {
     const Scores s(v[0], v[1], v[4]);
     float *logprob = result_of<float>(v[2], "logprob", at::kFloat, {s.T}, s.dev);
     float *entropy = result_of<float>(v[3], "entropy", at::kFloat, {s.T}, s.dev);
     int32_t *ids = s.n_top > 0 ? result_of<int32_t>(v[5], "top_ids", at::kInt, {s.T, s.n_top}, s.dev) : nullptr;
     float *top = s.n_top > 0 ? result_of<float>(v[6], "top_logprobs", at::kFloat, {s.T, s.n_top}, s.dev) : nullptr;
-    return s.call(logprob, entropy, ids, top, v[7], v[8], v[9]);
+    return s.call(logprob, entropy, ids, top, v[7], v[8], v[9], v[10] == Py_True);
 }
 
 // logits, targets | None, n_top, ws | None, status | None, stream | None: scores with results of its own (made in
@@ -369,7 +371,7 @@ PyObject *scores_new(PyObject *const *v) {
                      ids = at::empty({s.T, s.n_top}, f.dtype(at::kInt)), top = at::empty({s.T, s.n_top}, f);
     const int rc = s.call(s.targets ? static_cast<float *>(logprob.data_ptr()) : nullptr, static_cast<float *>(entropy.data_ptr()),
                           s.n_top ? static_cast<int32_t *>(ids.data_ptr()) : nullptr,
-                          s.n_top ? static_cast<float *>(top.data_ptr()) : nullptr, v[3], v[4], v[5]);
+                          s.n_top ? static_cast<float *>(top.data_ptr()) : nullptr, v[3], v[4], v[5], true);
     // (N takes the references; a missing one has set an exception)
     PyObject *given = s.targets ? THPVariable_Wrap(logprob) : Py_NewRef(Py_None);
     return Py_BuildValue("(iNNNN)", rc, given, THPVariable_Wrap(entropy), THPVariable_Wrap(ids), THPVariable_Wrap(top));
@@ -406,7 +408,7 @@ PyMethodDef methods[] = {{"linear", fast<linear, 10>(), METH_FASTCALL, "int4_lin
                          {"attend", fast<attend, 11, 1>(), METH_FASTCALL, "gqa_paged_attention"},
                          {"linear_prompt", fast<linear_prompt, 11>(), METH_FASTCALL, "int4_linear_prompt"},
                          {"attend_prompt", fast<attend_prompt, 12, 1>(), METH_FASTCALL, "gqa_prompt_attention"},
-                         {"scores", fast<scores, 10>(), METH_FASTCALL, "token_logprobs"},
+                         {"scores", fast<scores, 10, 1>(), METH_FASTCALL, "token_logprobs"},
                          {"scores_new", fast<scores_new, 6>(), METH_FASTCALL, "token_logprobs"},
                          {nullptr, nullptr, 0, nullptr}};
 

@@ -204,6 +204,19 @@ __device__ __forceinline__ void finish_row(const ScoresArgs &a, int t, int targe
     }
 }
 
+// A padding row's results, by a warp.
+__device__ __forceinline__ void fill_row(const ScoresArgs &a, int t, int lane) {
+    if (lane == 0) {
+        if (a.logprob) a.logprob[t] = NAN;
+        if (a.entropy) a.entropy[t] = NAN;
+    }
+    if (lane < a.n_top) {
+        const int64_t at = static_cast<int64_t>(t) * a.n_top + lane;
+        a.top_ids[at] = -1;
+        a.top_logprobs[at] = NAN;
+    }
+}
+
 // Merges the sums, and with `top` the lists (halves at a time), of each WPR warps; the
 // first of them returns with all.
 template <int WPR>
@@ -306,6 +319,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) scores_kernel(const __grid_con
     const int mine = warp % WPR;  // of the row's warps
     // (a block's warps stay together until their lists are merged, also without a row)
     const int target = t < a.T ? (a.targets ? a.targets[t] : 0) : -1;
+    if (a.fill && t < a.T && target < 0 && mine == 0 && part == 0) fill_row(a, t, lane);
     if (WPR == 1 && target < 0) return;
     const E *row = static_cast<const E *>(a.x) + t * a.stride;
     const float given = a.logprob && target >= 0 && target < a.V ? score(row + target) : 0.f;

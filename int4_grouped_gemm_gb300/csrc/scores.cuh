@@ -19,6 +19,7 @@ struct ScoresArgs {
     float *top_logprobs;     // [T][n_top]
     int *status;             // may be NULL
     int T, V, n_top, fp32;
+    int fill;                // padding rows' results become NaN and -1 (0: stay as they are)
     // filled in by the launch
     int parts;               // of a row, each a block
     int part_batches;        // batches of 256 scores of a part

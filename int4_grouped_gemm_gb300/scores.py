@@ -49,24 +49,30 @@ def token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
                    status: Optional[torch.Tensor] = None, stream=None) -> TokenScores:
     """Of logits [T, V] (fp32 or bf16): the log probabilities of targets (int32
     [T]; a row with a negative one is padding, its results are left as they
-    were), the entropy, and the n_top (up to 32) most probable tokens.  status: a
-    zeroed int32 device tensor for errors found on the device (a target outside
-    the vocabulary); without it they go to the first word of ws, or nowhere if ws
-    is not given either."""
+    were in out, and without out NaN, ids -1), the entropy, and the n_top (up to 32)
+    most probable tokens.  status: a zeroed int32 device tensor for errors found on
+    the device (a target outside the vocabulary); without it they go to the first
+    word of ws, or nowhere if ws is not given either."""
     if stream is not None and (out is None or ws is None):
         with _lib.on_stream(stream):
             return token_logprobs(logits, targets, n_top, out, ws, status)
     if ws is None and logits.dim() != 2:
         raise ValueError("token_logprobs: logits [T, V]")
-    if out is None:
-        rc, *made = _lib.native().scores_new(logits, targets, n_top, ws, status, None)
-        out = TokenScores._make(made)
-    else:
-        rc = _lib.native().scores(logits, targets, out.logprob, out.entropy, n_top, out.top_ids, out.top_logprobs, ws,
-                                  status, _lib.handle(stream))
+    if out is not None:
+        _write(logits, targets, n_top, out, ws, status, stream)
+        return out
+    rc, *made = _lib.native().scores_new(logits, targets, n_top, ws, status, None)
     if rc:
         raise _lib.MoEError(rc, "token_logprobs")
-    return out
+    return TokenScores._make(made)
+
+
+def _write(logits, targets, n_top, out, ws, status, stream=None, fill=False):
+    """fill: out holds nothing yet."""
+    rc = _lib.native().scores(logits, targets, out.logprob, out.entropy, n_top, out.top_ids, out.top_logprobs, ws,
+                              status, _lib.handle(stream), fill)
+    if rc:
+        raise _lib.MoEError(rc, "token_logprobs")
 
 
 class OutputHead:
@@ -82,7 +88,8 @@ class OutputHead:
                  status: Optional[torch.Tensor] = None, stream=None) -> TokenScores:
         """token_logprobs of x [T, H] (bf16, normalised) times the head, fp32
         scores: the scores of a prompt's tokens are those of the next ones, so
-        that targets[t] is the token after token t."""
+        that targets[t] is the token after token t (negative: padding, whose results
+        are NaN, ids -1)."""
         if stream is not None:
             with _lib.on_stream(stream):
                 return self.logprobs(x, targets, n_top, status)
@@ -98,5 +105,5 @@ class OutputHead:
         for a in range(0, T, n):
             b = min(T, a + n)
             linear_prompt(self.w, x[a:b], y[:b - a], ws=lin_ws, status=status)
-            token_logprobs(y[:b - a], None if targets is None else targets[a:b], n_top, out.rows(a, b), ws, status)
+            _write(y[:b - a], None if targets is None else targets[a:b], n_top, out.rows(a, b), ws, status, fill=True)
         return out
