@@ -83,17 +83,22 @@ class OutputHead:
         if rows < 1:
             raise ValueError("OutputHead: rows >= 1")
         self.w, self.rows = w, rows
+        # where logprobs records errors found on the device if it is given no status
+        # (moe_read_device_status)
+        self.status = torch.zeros(4, dtype=torch.int32, device=w.q.device)
 
     def logprobs(self, x: torch.Tensor, targets: Optional[torch.Tensor] = None, n_top: int = 0,
                  status: Optional[torch.Tensor] = None, stream=None) -> TokenScores:
         """token_logprobs of x [T, H] (bf16, normalised) times the head, fp32
         scores: the scores of a prompt's tokens are those of the next ones, so
         that targets[t] is the token after token t (negative: padding, whose results
-        are NaN, ids -1)."""
+        are NaN, ids -1).  Errors found on the device are recorded in status, a zeroed
+        int32 device tensor, or without it in `self.status`."""
         if stream is not None:
             with _lib.on_stream(stream):
                 return self.logprobs(x, targets, n_top, status)
         T, V = x.shape[0], self.w.rows
+        status = self.status if status is None else status
         out = TokenScores.empty(T, n_top, targets is not None, x.device)
         n = max(1, min(T, self.rows))
         if T == 0:
