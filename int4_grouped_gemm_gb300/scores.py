@@ -98,6 +98,8 @@ class OutputHead:
             with _lib.on_stream(stream):
                 return self.logprobs(x, targets, n_top, status)
         T, V = x.shape[0], self.w.rows
+        if targets is not None and targets.shape != (T,):
+            raise ValueError(f"OutputHead: targets [{T}], a token for each row of x")
         status = self.status if status is None else status
         out = TokenScores.empty(T, n_top, targets is not None, x.device)
         n = max(1, min(T, self.rows))
