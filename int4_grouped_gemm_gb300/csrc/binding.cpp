@@ -366,6 +366,9 @@ int scores(PyObject *const *v) {
 PyObject *scores_new(PyObject *const *v) {
     const Scores s(v[0], v[1], v[2]);
     if (s.n_top < 0) value_error("n_top: 0 at least");
+    // (more alternatives than there can be are refused before memory for them is asked for)
+    if (!token_logprobs_workspace_bytes(size32(s.T), size32(s.V), s.n_top))
+        return Py_BuildValue("(iOOOO)", s.T < 1 || s.T > 1 << 24 ? MOE_ERR_TOKENS : MOE_ERR_SHAPE, Py_None, Py_None, Py_None, Py_None);
     const auto f = s.x.options().dtype(at::kFloat);
     const at::Tensor logprob = s.targets ? at::empty({s.T}, f) : at::Tensor(), entropy = at::empty({s.T}, f),
                      ids = at::empty({s.T, s.n_top}, f.dtype(at::kInt)), top = at::empty({s.T, s.n_top}, f);

@@ -101,14 +101,15 @@ class OutputHead:
         if targets is not None and targets.shape != (T,):
             raise ValueError(f"OutputHead: targets [{T}], a token for each row of x")
         status = self.status if status is None else status
-        out = TokenScores.empty(T, n_top, targets is not None, x.device)
         n = max(1, min(T, self.rows))
+        nbytes = _bytes(n, V, n_top)  # (refuses what there cannot be)
+        out = TokenScores.empty(T, n_top, targets is not None, x.device)
         if T == 0:
             return out
         # one piece after another, in the same scratch
         y = torch.empty(n, V, dtype=torch.float32, device=x.device)
         lin_ws = linear_prompt_workspace(self.w, n)
-        ws = torch.empty(_bytes(n, V, n_top), dtype=torch.uint8, device=x.device)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
         for a in range(0, T, n):
             b = min(T, a + n)
             linear_prompt(self.w, x[a:b], y[:b - a], ws=lin_ws, status=status)
