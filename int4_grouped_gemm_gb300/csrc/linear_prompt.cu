@@ -44,8 +44,7 @@
 //   warp 3           loads of packed codes, a ring of their own
 //   warps 12-27      unpacking: a thread a row's 64 codes of a stage, four sets of four
 //                    warps in turn
-//   warp 2           tells the pair's first block what was unpacked here (of block
-//                    scope; a release of cluster scope took 0.6 us for each stage)
+//   warp 2           tells the pair's first block what was unpacked here (pair_arrive)
 //   warps 4-11, 4-15 where nothing is unpacked here (8192 x 256 x 8192 fp32 63 us, with
 //                    eight 67.5): epilogue: a lane is a weight row, so that a warp writes
 //                    32 neighbouring results of a token at a time, whatever y's
@@ -333,8 +332,21 @@ __device__ __forceinline__ uint32_t in_first(const void *p) {
     asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
     return r;
 }
+// Arrives on a barrier of the pair's first block, whose MMA thread acts on it.  The arrival
+// is of cluster scope, what comes before it is ordered in this block alone: a release
+// of cluster scope waits for all that the thread's block has under way, 0.3 to 0.6 us
+// for each stage (512 x 2048 x 131072 435 us, so 268).  That is enough, because nothing
+// that the MMA thread's own accesses would have to see is handed over:
+//   unpacked codes   lie in this block's shared memory, of which there is one copy, in
+//                    this SM.  Each writer has fenced them for the asynchronous proxy and
+//                    arrived on `unpacked` (release, block scope), the thread here has
+//                    seen that phase end (acquire, block scope): the bytes are in their
+//                    place before the arrival leaves, and the only one to read them is
+//                    this SM's tensor core, for an MMA that is issued behind the arrival
+//   tensor memory    an accumulator's loads and stores of this warp are complete
+//                    (tcgen05.wait) and its values in registers before it arrives
 __device__ __forceinline__ void pair_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("fence.acq_rel.cta;\n\tmbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // A box into this block's shared memory, complete on a barrier of the pair.
 __device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1) {
