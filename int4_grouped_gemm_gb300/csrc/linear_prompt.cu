@@ -50,12 +50,15 @@
 //                    32 neighbouring results of a token at a time, whatever y's
 //                    stride; powers of two put back
 //
-// What bounds it.  4096 x 2048 x 2560 in 38 us: the operands, 6 to 8 us (their bytes:
-// 16384 x 2048 tokens pass at 5.5 TB/s, read and written), and a product of three
-// rounds over the pairs, tensor pipe 62 % busy in its 32 us.  512 x 2048 x 131072 fp32
-// in 256: 29 us for scales, biases and tokens, then a product in which the tensor pipe
-// is busy for 52 %, the issue slots for 44 %, and every stage waits for its unpacking.
-// 65 tokens 15 us: two launches and 34 stages one after another on 30 pairs.
+// What bounds it.  4096 x 2048 x 2560 in 38 to 42 us (by GPU): the operands, 6 to 8 us (their
+// bytes: 16384 x 2048 tokens pass at 5.5 TB/s, read and written), and a product of three
+// rounds over the pairs in 32 us, tensor pipe 63 %.  Its tiles of 192 tokens fetch 28 KB in
+// 384 cycles, 75 bytes a cycle where 64 reach a SM, so that 86 % is the most it could be.
+// 1021 x 2080 x 5003 fp32 in 34 to 42: tiles of 160 tokens, 83 bytes a cycle, and chunks: 42 %
+// of 28 us.  512 x 2048 x 131072 fp32 in 256 to 271: 29 to 31 us for scales, biases and
+// tokens, then a product in which the tensor pipe is busy for 55 %, the issue slots for
+// 48 %, and every stage waits for its unpacking.  65 tokens 14 to 15 us: two launches and
+// 34 stages one after another on 30 pairs; K is not split here.
 //
 // Every wait is bounded.
 #include <cuda_fp16.h>

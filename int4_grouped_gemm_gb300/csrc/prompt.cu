@@ -41,14 +41,17 @@
 // A position outside the pool is loaded as zeros (the page coordinate lies past
 // the tensor map) and recorded.  Every wait is bounded.
 //
-// What bounds it.  D = 128: the tensor core.  16384 tokens of 16 heads on 2 in 885 us
-// are 1240 TFLOP/s, 1860 with the second parts of the weights.  D = 64: the softmax
+// What bounds it.  D = 128: the tensor core.  16384 tokens of 16 heads on 2 in 885 to 971 us
+// (by GPU) are 1130 to 1240 TFLOP/s, half as much again with the second parts of the
+// weights.  D = 64: the softmax
 // warps, busy 2700 of a tile's 3660 cycles (8192 tokens 215 us).  Two threads a row (16
 // softmax warps of 96 registers) took 1127 us where this then took 980, the scores of
 // each half of the next tile behind this one's values 988 (and 10 % more at D = 64);
 // rows written by way of shared memory 1 % less, at D = 64 7 % more.  A call of a few
 // tiles is a chain of first steps: 77 tokens 10.4 us, of which the plan 2.2, pages and
-// keys 2, one tile's softmax 1.9, the rows 1.8.
+// keys 2, one tile's softmax 1.9, the rows 1.8.  Many short sequences cost a block each,
+// and the plan one look at each length a piece: 32768 rows of 512 sequences 97 us, 65536
+// of 4096 283, of 16384 1000, of 65536 3790 (a row each).
 #include "attn_tile.cuh"
 #include "prompt.cuh"
 

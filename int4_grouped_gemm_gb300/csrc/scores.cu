@@ -20,15 +20,15 @@
 //            32 at a time and merged with the list of the 32 best, a lane each, by
 //            exchanges between lanes (15 + 6 steps).  (A list kept during the pass, by
 //            each warp, took as many instructions as the sums in long rows, and several
-//            times as many in short ones: 257 x 50021 with 5 alternatives 39 us, now 16)
+//            times as many in short ones: 257 x 50021 with 5 alternatives 39 us, so 16 to 19)
 //   work     a row is cut into parts where there are too few rows for the GPU, a
 //            block of eight warps each, whose sums are merged through shared memory and
 //            whose scores that reach the n are sorted by the first one;
 //            scores_merge_kernel merges the parts.  Short rows of many are a warp's each
 //
-// Bound by the bytes of fp32 scores: 64 bytes a thread are in flight, 4096 x 131072
-// with 8 alternatives take 325 us, 6.6 TB/s.  bf16 ones are bound by the instructions
-// (issue slots 66 to 75 %): 4096 x 50021 97 us, 4.2 TB/s.
+// Bound by the bytes of fp32 scores: 96 to 128 bytes a thread are in flight, 4096 x 131072
+// with 8 alternatives take 319 to 325 us, 6.6 TB/s.  bf16 ones are bound by the instructions
+// (issue slots 65 %, ALU 57 %): 4096 x 50021 97 us, 4.2 TB/s.
 #include "scores.cuh"
 
 #include <algorithm>
